@@ -3,7 +3,8 @@
 Five operators, in the order in which a layer uses them:
 
 * ``norm``           root-mean-square norm with the residual's addition, written in bf16 or in fp8
-                     (E4M3) with one fp32 scale per row and 128 columns
+                     (E4M3) with one fp32 scale per row and 128 columns; scale (b, i) belongs to
+                     columns 128 b to 128 b + 127 of row (or block of rows) i
 * ``norm_backward``  its gradients
 * ``quantize``       a matrix, or its transpose, in fp8 with a scale per 1 x 128 or 128 x 128 block
 * ``fp8gemm``        the product of two such matrices
@@ -123,13 +124,13 @@ def blocks(n):
 
 
 def spread(s, block, rows, cols):
-    """The scales of a matrix in blocks, one for each of its values."""
-    s = s.repeat_interleave(BLOCK, dim=-1)[..., :cols]
+    """The scales (blocks of columns first) of a matrix, one for each of its values."""
+    s = s.transpose(-1, -2).repeat_interleave(BLOCK, dim=-1)[..., :cols]
     return s.repeat_interleave(BLOCK, dim=-2)[..., :rows, :] if block == "tiles" else s
 
 
 def plain_quantize(x, block):
-    """fp32 values -> (E4M3 values, fp32 scales)."""
+    """fp32 values -> (E4M3 values, fp32 scales, blocks of columns first)."""
     rows, cols = x.shape[-2:]
     pad = torch.nn.functional.pad(x, (0, -cols % BLOCK, 0, -rows % BLOCK if block == "tiles" else 0))
     if block == "tiles":
@@ -137,7 +138,7 @@ def plain_quantize(x, block):
         amax = cut.abs().amax(dim=(-3, -1))
     else:
         amax = pad.unflatten(-1, (-1, BLOCK)).abs().amax(dim=-1)
-    scales = (amax / FP8_MAX).clamp_min(SCALE_MIN)
+    scales = (amax / FP8_MAX).clamp_min(SCALE_MIN).transpose(-1, -2).contiguous()
     v = x / spread(scales, block, rows, cols)
     return v.clamp(-FP8_MAX, FP8_MAX).to(torch.float8_e4m3fn), scales
 
@@ -162,7 +163,7 @@ def prepare(case, seed):
             st["h"] = None if rt is None else torch.empty(rows, dim, dtype=rt, device="cuda")
             if case["out"] == "fp8":
                 st["q"] = padded(rows, dim, torch.float8_e4m3fn)
-                st["scales"] = torch.empty(rows, blocks(dim), device="cuda")
+                st["scales"] = torch.empty(blocks(dim), rows, device="cuda")
             else:
                 st["y"] = torch.empty(rows, dim, dtype=torch.bfloat16, device="cuda")
             return st
@@ -181,7 +182,7 @@ def prepare(case, seed):
         if case["transpose"]:
             rows, cols = cols, rows
         st["q"] = padded(rows, cols, torch.float8_e4m3fn)
-        st["scales"] = torch.empty(blocks(rows) if case["block"] == "tiles" else rows, blocks(cols),
+        st["scales"] = torch.empty(blocks(cols), blocks(rows) if case["block"] == "tiles" else rows,
                                    device="cuda")
         return st
 
@@ -344,14 +345,14 @@ def exact_quantize(x, block):
     cut = cut.view(br, high, bc, BLOCK)
     s = torch.clamp(cut.abs().amax(dim=3).amax(dim=1) / FP8_MAX, min=SCALE_MIN)
     q = exact_e4m3(cut / s[:, None, :, None]).view(br * high, bc * BLOCK)
-    return q[:rows, :cols], s
+    return q[:rows, :cols], s.t()
 
 
 def exact_values(q, s, high):
     """The fp64 values of a matrix in fp8 whose blocks are `high` x 128."""
     i = torch.arange(q.shape[0], device=q.device) // high
     j = torch.arange(q.shape[1], device=q.device) // BLOCK
-    return q.double() * s.double()[i][:, j]
+    return q.double() * s.double().t()[i][:, j]
 
 
 def exact(case, seed):
@@ -388,7 +389,7 @@ def exact(case, seed):
     for g, (lo, hi) in enumerate(zip(ends[:-1], ends[1:])):
         if case["kind"] == "fp8":
             w = exact_values(st["b"][g], st["b_scales"][g], BLOCK).t()
-            d[lo:hi] = exact_values(st["a"][lo:hi], st["a_scales"][lo:hi], 1) @ w
+            d[lo:hi] = exact_values(st["a"][lo:hi], st["a_scales"][:, lo:hi], 1) @ w
         elif case["kind"] == "forward":
             d[lo:hi] = st["a"][lo:hi].double() @ st["b"][g].double()
         else:
