@@ -27,6 +27,10 @@ __all__ = [
     "gemm_status_string", "gemm_check_device_error", "gemm_shutdown", "gemm_release_stream",
     "gemm_select_path", "gemm_split_parts", "gemm_split_cluster", "gemm_quantization", "gemm_version", "sgemm", "bf16gemm",
     "STATUS", "PATHS",
+    "RmsnormArgs", "RmsnormGradArgs", "BLOCK", "gemm_rmsnorm", "gemm_rmsnorm_backward",
+    "gemm_fp8_quantize", "gemm_fp8gemm", "gemm_fp8gemm_grouped", "gemm_bf16gemm_grouped",
+    "gemm_bf16gemm_grouped_wgrad", "rmsnorm", "rmsnorm_backward", "fp8_quantize", "fp8gemm",
+    "fp8gemm_grouped", "bf16gemm_grouped", "bf16gemm_grouped_wgrad",
 ]
 
 STATUS = {
@@ -62,6 +66,32 @@ class GemmOutput(ctypes.Structure):
 class GemmConfig(ctypes.Structure):
     """Mirror of gemm_config_t (include/gemm12.h)."""
     _fields_ = [("kernel", ctypes.c_int), ("split", ctypes.c_int), ("group_m", ctypes.c_int)]
+
+
+class RmsnormArgs(ctypes.Structure):
+    """Mirror of gemm_rmsnorm_t (include/gemm12.h)."""
+    _fields_ = [
+        ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("x_type", ctypes.c_int),
+        ("residual", ctypes.c_void_p), ("ldr", ctypes.c_int64), ("residual_type", ctypes.c_int),
+        ("h", ctypes.c_void_p), ("ldh", ctypes.c_int64), ("h_type", ctypes.c_int),
+        ("weight", ctypes.c_void_p), ("eps", ctypes.c_float),
+        ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64), ("y_type", ctypes.c_int),
+        ("q", ctypes.c_void_p), ("ldq", ctypes.c_int64),
+        ("scales", ctypes.c_void_p), ("ld_scales", ctypes.c_int64), ("rstd", ctypes.c_void_p),
+    ]
+
+
+class RmsnormGradArgs(ctypes.Structure):
+    """Mirror of gemm_rmsnorm_grad_t (include/gemm12.h)."""
+    _fields_ = [
+        ("dy", ctypes.c_void_p), ("lddy", ctypes.c_int64), ("dy_type", ctypes.c_int),
+        ("h", ctypes.c_void_p), ("ldh", ctypes.c_int64), ("h_type", ctypes.c_int),
+        ("weight", ctypes.c_void_p), ("rstd", ctypes.c_void_p),
+        ("residual_grad", ctypes.c_void_p), ("ldrg", ctypes.c_int64),
+        ("residual_grad_type", ctypes.c_int),
+        ("dh", ctypes.c_void_p), ("lddh", ctypes.c_int64), ("dh_type", ctypes.c_int),
+        ("dweight", ctypes.c_void_p),
+    ]
 
 
 KERNELS = {"auto": 0, "single_cta": 1, "cta_pair": 2, "wide": 3}
@@ -140,6 +170,24 @@ def load_library(build_if_missing: bool = False):
         lib.gemm_split_parts.restype = cint
         lib.gemm_split_cluster.argtypes = [cint, i64, i64, i64, cfg_p]
         lib.gemm_split_cluster.restype = cint
+        lib.gemm_rmsnorm.argtypes = [i64, i64, ctypes.POINTER(RmsnormArgs), vp]
+        lib.gemm_rmsnorm.restype = cint
+        lib.gemm_rmsnorm_backward.argtypes = [i64, i64, ctypes.POINTER(RmsnormGradArgs), vp]
+        lib.gemm_rmsnorm_backward.restype = cint
+        lib.gemm_fp8_quantize.argtypes = [i64, i64, vp, i64, cint, cint, cint, vp, i64, vp, i64, vp]
+        lib.gemm_fp8_quantize.restype = cint
+        lib.gemm_fp8gemm.argtypes = [i64, i64, i64, f32, vp, i64, vp, i64, vp, i64, vp, i64, cint,
+                                     f32, vp, i64, cint, vp]
+        lib.gemm_fp8gemm.restype = cint
+        lib.gemm_fp8gemm_grouped.argtypes = [i64, vp, i64, i64, i64, f32, vp, i64, vp, i64, vp, i64,
+                                             i64, vp, i64, i64, cint, f32, vp, i64, cint, vp]
+        lib.gemm_fp8gemm_grouped.restype = cint
+        lib.gemm_bf16gemm_grouped.argtypes = [i64, vp, i64, i64, i64, f32, vp, i64, vp, i64, i64,
+                                              cint, f32, vp, i64, cint, vp]
+        lib.gemm_bf16gemm_grouped.restype = cint
+        lib.gemm_bf16gemm_grouped_wgrad.argtypes = [i64, vp, i64, i64, i64, f32, vp, i64, vp, i64,
+                                                    f32, vp, i64, i64, cint, vp]
+        lib.gemm_bf16gemm_grouped_wgrad.restype = cint
         lib.gemm_version.argtypes = []
         lib.gemm_version.restype = cint
         _lib = lib
@@ -282,6 +330,57 @@ def gemm_version() -> int:
     return load_library().gemm_version()
 
 
+# gemm_block_t: the shape of an fp8 matrix's scaled blocks.
+BLOCK = {"rows": 0, "tiles": 1}
+
+
+def gemm_rmsnorm(rows, dim, args: "RmsnormArgs", stream=0) -> int:
+    """Root-mean-square norm (gemm_rmsnorm_t). Returns the status."""
+    return load_library().gemm_rmsnorm(rows, dim, ctypes.byref(args), stream)
+
+
+def gemm_rmsnorm_backward(rows, dim, args: "RmsnormGradArgs", stream=0) -> int:
+    """Its gradients (gemm_rmsnorm_grad_t). Returns the status."""
+    return load_library().gemm_rmsnorm_backward(rows, dim, ctypes.byref(args), stream)
+
+
+def gemm_fp8_quantize(rows, cols, x, ldx, x_type, block, transpose, q, ldq, scales, ld_scales,
+                      stream=0) -> int:
+    """A matrix or its transpose in fp8 with block scales. Returns the status."""
+    return load_library().gemm_fp8_quantize(rows, cols, x, ldx, x_type, block, transpose, q, ldq,
+                                            scales, ld_scales, stream)
+
+
+def gemm_fp8gemm(M, N, K, alpha, A, lda, a_scales, ld_as, B, ldb, b_scales, ld_bs, b_block, beta, D,
+                 ldd, d_type, stream=0) -> int:
+    """fp8 GEMM with block scales, B given as N x K. Returns the status."""
+    return load_library().gemm_fp8gemm(M, N, K, alpha, A, lda, a_scales, ld_as, B, ldb, b_scales,
+                                       ld_bs, b_block, beta, D, ldd, d_type, stream)
+
+
+def gemm_fp8gemm_grouped(G, offsets, rows, N, K, alpha, A, lda, a_scales, ld_as, B, ldb, stride_b,
+                         b_scales, ld_bs, stride_bs, b_block, beta, D, ldd, d_type,
+                         stream=0) -> int:
+    """fp8 products grouped by expert. Returns the status."""
+    return load_library().gemm_fp8gemm_grouped(G, offsets, rows, N, K, alpha, A, lda, a_scales,
+                                               ld_as, B, ldb, stride_b, b_scales, ld_bs, stride_bs,
+                                               b_block, beta, D, ldd, d_type, stream)
+
+
+def gemm_bf16gemm_grouped(G, offsets, rows, N, K, alpha, A, lda, B, ldb, stride_b, transpose_b,
+                          beta, D, ldd, d_type, stream=0) -> int:
+    """bf16 products grouped by expert. Returns the status."""
+    return load_library().gemm_bf16gemm_grouped(G, offsets, rows, N, K, alpha, A, lda, B, ldb,
+                                                stride_b, transpose_b, beta, D, ldd, d_type, stream)
+
+
+def gemm_bf16gemm_grouped_wgrad(G, offsets, rows, N, K, alpha, A, lda, dD, lddd, beta, dB, ldb,
+                                stride_b, d_type, stream=0) -> int:
+    """Their gradient with respect to B. Returns the status."""
+    return load_library().gemm_bf16gemm_grouped_wgrad(G, offsets, rows, N, K, alpha, A, lda, dD,
+                                                      lddd, beta, dB, ldb, stride_b, d_type, stream)
+
+
 # ------------------------------------------------------------ tensor helpers
 def _row_major_ld(t, name):
     if t.dim() != 2:
@@ -422,3 +521,265 @@ def bf16gemm_fused(A, B, D, C=None, alpha=1.0, beta=0.0, bias=None, act="none", 
     if st != 0:
         raise GemmError(st, "gemm_bf16gemm_fused")
     return D
+
+
+# ------------------------------------------- operators around the GEMMs
+_FLOAT_CODES = None
+
+
+def _float_code(t, name):
+    """gemm_out_t of a float32 or bfloat16 CUDA tensor."""
+    global _FLOAT_CODES
+    if _FLOAT_CODES is None:
+        import torch
+        _FLOAT_CODES = {torch.float32: OUT["f32"], torch.bfloat16: OUT["bf16"]}
+    code = _FLOAT_CODES.get(t.dtype)
+    if code is None or not t.is_cuda:
+        raise TypeError("%s must be a float32 or bfloat16 CUDA tensor" % name)
+    return code
+
+
+def _check_dtype(t, dtype, name):
+    if t.dtype != dtype or not t.is_cuda:
+        raise TypeError("%s must be a %s CUDA tensor" % (name, dtype))
+
+
+def _check_shape(t, shape, name):
+    if tuple(t.shape) != shape:
+        raise ValueError("%s must have shape %s, not %s" % (name, shape, tuple(t.shape)))
+
+
+def _check_vector(t, n, name):
+    import torch
+    _check_dtype(t, torch.float32, name)
+    if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
+        raise ValueError("%s must be a contiguous vector of %d values" % (name, n))
+    return t.data_ptr()
+
+
+def _check_scales(t, shape, name):
+    """Pitch of a matrix of scales: k-blocks x rows (or blocks of rows)."""
+    import torch
+    _check_dtype(t, torch.float32, name)
+    _check_shape(t, shape, name)
+    return _row_major_ld(t, name)
+
+
+def _row_array(t, shape, name):
+    """(address, leading dimension, type) of a row-major float array."""
+    code = _float_code(t, name)
+    _check_shape(t, shape, name)
+    return t.data_ptr(), _row_major_ld(t, name), code
+
+
+def _same_device(device, *tensors):
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError("all tensors must be on %s" % (device,))
+
+
+def rmsnorm(x, weight, eps=1e-6, residual=None, h=None, y=None, q=None, scales=None, rstd=None,
+            stream=None):
+    """h = x + residual; y = h / sqrt(mean(h^2) + eps) * weight over the last dimension of x
+    (rows, dim), into the given outputs: h, y (float32 or bfloat16), q with scales (y in
+    float8_e4m3fn, scales (ceil(dim / 128), rows) float32) and rstd (rows,).  weight is float32.
+    h may be the residual itself and y may be x itself."""
+    import torch
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D")
+    rows, dim = x.shape
+    _same_device(x.device, weight, residual, h, y, q, scales, rstd)
+    a = RmsnormArgs()
+    a.x, a.ldx, a.x_type = _row_array(x, (rows, dim), "x")
+    a.weight, a.eps = _check_vector(weight, dim, "weight"), eps
+    if residual is not None:
+        a.residual, a.ldr, a.residual_type = _row_array(residual, (rows, dim), "residual")
+    if h is not None:
+        a.h, a.ldh, a.h_type = _row_array(h, (rows, dim), "h")
+    if y is not None:
+        a.y, a.ldy, a.y_type = _row_array(y, (rows, dim), "y")
+    if (q is None) != (scales is None):
+        raise ValueError("q and scales come together")
+    if q is not None:
+        _check_dtype(q, torch.float8_e4m3fn, "q")
+        _check_shape(q, (rows, dim), "q")
+        a.q, a.ldq = q.data_ptr(), _row_major_ld(q, "q")
+        a.ld_scales = max(_check_scales(scales, (-(-dim // 128), rows), "scales"), rows)
+        a.scales = scales.data_ptr()
+    if rstd is not None:
+        a.rstd = _check_vector(rstd, rows, "rstd")
+    st = load_library().gemm_rmsnorm(rows, dim, ctypes.byref(a), _stream_handle(stream, x.device))
+    if st != 0:
+        raise GemmError(st, "gemm_rmsnorm")
+
+
+def rmsnorm_backward(dy, h, weight, rstd, dh, dweight=None, residual_grad=None, stream=None):
+    """Gradients of rmsnorm's y: dh <- the gradient with respect to h (and so x and the
+    residual) plus residual_grad, dweight (dim,) <- the one with respect to the weight."""
+    if dy.dim() != 2:
+        raise ValueError("dy must be 2-D")
+    rows, dim = dy.shape
+    _same_device(dy.device, h, weight, rstd, dh, dweight, residual_grad)
+    a = RmsnormGradArgs()
+    a.dy, a.lddy, a.dy_type = _row_array(dy, (rows, dim), "dy")
+    a.h, a.ldh, a.h_type = _row_array(h, (rows, dim), "h")
+    a.dh, a.lddh, a.dh_type = _row_array(dh, (rows, dim), "dh")
+    a.weight, a.rstd = _check_vector(weight, dim, "weight"), _check_vector(rstd, rows, "rstd")
+    if residual_grad is not None:
+        a.residual_grad, a.ldrg, a.residual_grad_type = _row_array(residual_grad, (rows, dim),
+                                                                   "residual_grad")
+    if dweight is not None:
+        a.dweight = _check_vector(dweight, dim, "dweight")
+    st = load_library().gemm_rmsnorm_backward(rows, dim, ctypes.byref(a),
+                                              _stream_handle(stream, dy.device))
+    if st != 0:
+        raise GemmError(st, "gemm_rmsnorm_backward")
+    return dh
+
+
+def fp8_quantize(x, q, scales, block="rows", transpose=False, stream=None):
+    """x (rows, cols), float32 or bfloat16, or its transpose, into q (float8_e4m3fn) with one
+    float32 scale per 1 x 128 ("rows") or 128 x 128 ("tiles") block of q: scales[b, r] is that
+    of columns 128 b .. 128 b + 127 and row (or block of rows) r."""
+    import torch
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D")
+    rows, cols = x.shape
+    _same_device(x.device, q, scales)
+    qr, qc = (cols, rows) if transpose else (rows, cols)
+    _check_dtype(q, torch.float8_e4m3fn, "q")
+    _check_shape(q, (qr, qc), "q")
+    lds = _check_scales(scales, (-(-qc // 128), -(-qr // 128) if BLOCK[block] else qr), "scales")
+    px, ldx, code = _row_array(x, (rows, cols), "x")
+    st = gemm_fp8_quantize(rows, cols, px, ldx, code, BLOCK[block], int(bool(transpose)),
+                           q.data_ptr(), _row_major_ld(q, "q"), scales.data_ptr(), lds,
+                           _stream_handle(stream, x.device))
+    if st != 0:
+        raise GemmError(st, "gemm_fp8_quantize")
+    return q
+
+
+def _fp8_operands(torch, A, a_scales, B, b_scales, D):
+    _check_dtype(A, torch.float8_e4m3fn, "A")
+    _check_dtype(B, torch.float8_e4m3fn, "B")
+    if A.dim() != 2:
+        raise ValueError("A must be 2-D")
+    M, K = A.shape
+    N = B.shape[-2]
+    if B.shape[-1] != K:
+        raise ValueError("shape mismatch: A %s, B %s" % (tuple(A.shape), tuple(B.shape)))
+    kb = -(-K // 128)
+    ld_as = _check_scales(a_scales, (kb, M), "a_scales")
+    _check_dtype(b_scales, torch.float32, "b_scales")
+    if b_scales.dim() != B.dim():
+        raise ValueError("b_scales must have as many dimensions as B")
+    block = BLOCK["rows"] if b_scales.shape[-1] == N else BLOCK["tiles"]
+    _check_shape(b_scales, (*B.shape[:-2], kb, N if block == BLOCK["rows"] else -(-N // 128)),
+                 "b_scales")
+    return M, N, K, max(ld_as, M), block
+
+
+def _batched(t, name):
+    """(leading dimension, stride) of a batch of row-major matrices."""
+    G, rows, cols = t.shape
+    if cols > 1 and t.stride(2) != 1:
+        raise ValueError("%s must be row-major (unit column stride)" % name)
+    ld = t.stride(1) if rows > 1 else max(cols, 1)
+    return ld, t.stride(0) if G > 1 else rows * ld
+
+
+def _check_offsets(offsets, G):
+    import torch
+    _check_dtype(offsets, torch.int32, "offsets")
+    if tuple(offsets.shape) != (G + 1,) or not offsets.is_contiguous():
+        raise ValueError("offsets must be %d contiguous int32 values" % (G + 1))
+    return offsets.data_ptr()
+
+
+def fp8gemm(A, a_scales, B, b_scales, D, alpha=1.0, beta=0.0, stream=None):
+    """D <- alpha*(A @ B^T) + beta*D in place: A (M, K) and B (N, K) float8_e4m3fn, D float32 or
+    bfloat16; a_scales (ceil(K / 128), M); b_scales (ceil(K / 128), N), or ceil(N / 128) in place
+    of N for 128 x 128 blocks (see fp8_quantize)."""
+    import torch
+    if B.dim() != 2:
+        raise ValueError("B must be 2-D")
+    _same_device(D.device, A, a_scales, B, b_scales)
+    M, N, K, ld_as, block = _fp8_operands(torch, A, a_scales, B, b_scales, D)
+    pd, ldd, code = _row_array(D, (M, N), "D")
+    st = gemm_fp8gemm(M, N, K, alpha, A.data_ptr(), _row_major_ld(A, "A"), a_scales.data_ptr(),
+                      ld_as, B.data_ptr(), _row_major_ld(B, "B"), b_scales.data_ptr(),
+                      _row_major_ld(b_scales, "b_scales"), block, beta, pd, ldd, code,
+                      _stream_handle(stream, D.device))
+    if st != 0:
+        raise GemmError(st, "gemm_fp8gemm")
+    return D
+
+
+def fp8gemm_grouped(A, a_scales, B, b_scales, offsets, D, alpha=1.0, beta=0.0, stream=None):
+    """fp8gemm for the rows offsets[g] .. offsets[g + 1] - 1 of A and D with B[g] (G, N, K) and
+    b_scales[g]; offsets (G + 1,) int32, on the device."""
+    import torch
+    if B.dim() != 3:
+        raise ValueError("B must be 3-D")
+    _same_device(D.device, A, a_scales, B, b_scales, offsets)
+    M, N, K, ld_as, block = _fp8_operands(torch, A, a_scales, B, b_scales, D)
+    G = B.shape[0]
+    ldb, stride_b = _batched(B, "B")
+    ld_bs, stride_bs = _batched(b_scales, "b_scales")
+    pd, ldd, code = _row_array(D, (M, N), "D")
+    st = gemm_fp8gemm_grouped(G, _check_offsets(offsets, G), M, N, K, alpha, A.data_ptr(),
+                              _row_major_ld(A, "A"), a_scales.data_ptr(), ld_as, B.data_ptr(), ldb,
+                              stride_b, b_scales.data_ptr(), ld_bs, stride_bs, block, beta, pd, ldd,
+                              code, _stream_handle(stream, D.device))
+    if st != 0:
+        raise GemmError(st, "gemm_fp8gemm_grouped")
+    return D
+
+
+def bf16gemm_grouped(A, B, offsets, D, alpha=1.0, beta=0.0, transpose_b=False, stream=None):
+    """D[t] <- alpha*(A[t] @ B[g]) + beta*D[t] in place for the rows t = offsets[g] ..
+    offsets[g + 1] - 1 of each group; A (rows, K) and B (G, K, N) bfloat16 -- with transpose_b
+    (G, N, K), and D = A @ B[g]^T --, D float32 or bfloat16, offsets (G + 1,) int32 on the device."""
+    import torch
+    _check_dtype(A, torch.bfloat16, "A")
+    _check_dtype(B, torch.bfloat16, "B")
+    if A.dim() != 2 or B.dim() != 3:
+        raise ValueError("A must be 2-D and B 3-D")
+    _same_device(D.device, A, B, offsets)
+    rows, K = A.shape
+    G = B.shape[0]
+    N = B.shape[1 if transpose_b else 2]
+    _check_shape(B, (G, N, K) if transpose_b else (G, K, N), "B")
+    ldb, stride_b = _batched(B, "B")
+    pd, ldd, code = _row_array(D, (rows, N), "D")
+    st = gemm_bf16gemm_grouped(G, _check_offsets(offsets, G), rows, N, K, alpha, A.data_ptr(),
+                               _row_major_ld(A, "A"), B.data_ptr(), ldb, stride_b,
+                               int(bool(transpose_b)), beta, pd, ldd, code,
+                               _stream_handle(stream, D.device))
+    if st != 0:
+        raise GemmError(st, "gemm_bf16gemm_grouped")
+    return D
+
+
+def bf16gemm_grouped_wgrad(A, dD, offsets, dB, alpha=1.0, beta=0.0, stream=None):
+    """dB[g] <- alpha*(A_g^T @ dD_g) + beta*dB[g] in place: A (rows, K) and dD (rows, N) bfloat16,
+    dB (G, K, N) float32 or bfloat16; a group without rows gets beta*dB[g]."""
+    import torch
+    _check_dtype(A, torch.bfloat16, "A")
+    _check_dtype(dD, torch.bfloat16, "dD")
+    if A.dim() != 2 or dD.dim() != 2 or dB.dim() != 3:
+        raise ValueError("A and dD must be 2-D and dB 3-D")
+    _same_device(dB.device, A, dD, offsets)
+    rows, K = A.shape
+    N, G = dD.shape[1], dB.shape[0]
+    _check_shape(dD, (rows, N), "dD")
+    _check_shape(dB, (G, K, N), "dB")
+    code = _float_code(dB, "dB")
+    ldb, stride_b = _batched(dB, "dB")
+    st = gemm_bf16gemm_grouped_wgrad(G, _check_offsets(offsets, G), rows, N, K, alpha, A.data_ptr(),
+                                     _row_major_ld(A, "A"), dD.data_ptr(), _row_major_ld(dD, "dD"),
+                                     beta, dB.data_ptr(), ldb, stride_b, code,
+                                     _stream_handle(stream, dB.device))
+    if st != 0:
+        raise GemmError(st, "gemm_bf16gemm_grouped_wgrad")
+    return dB

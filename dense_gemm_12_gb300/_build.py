@@ -19,8 +19,9 @@ LIB_NAME = "libgemm12.so"
 LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
-SOURCES = ["api.cu", "sgemm_simt.cu", "bf16_tc.cu", "bf16_decode.cu", "decode_noalloc.cu"]
-HEADERS = ["ptx.cuh", "internal.h", "epilogue.cuh", "dispatch_table.inc"]
+SOURCES = ["api.cu", "sgemm_simt.cu", "bf16_tc.cu", "bf16_decode.cu", "decode_noalloc.cu",
+           "norm.cu", "fp8_quantize.cu", "fp8_tc.cu", "grouped_tc.cu"]
+HEADERS = ["ptx.cuh", "internal.h", "epilogue.cuh", "dispatch_table.inc", "ops.cuh", "groups.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",

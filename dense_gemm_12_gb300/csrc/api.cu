@@ -12,6 +12,7 @@
 
 #include "../../include/gemm12.h"
 #include "internal.h"
+#include "ops.cuh"
 
 namespace g12 {
 
@@ -575,6 +576,48 @@ gemm_status_t abi_device(int* num_sms, uint32_t** err_word) {
   *num_sms = st->num_sms;
   *err_word = st->err_word;
   return GEMM_OK;
+}
+
+gemm_status_t abi_from_cuda(cudaError_t e) { return from_cuda(e); }
+
+// Buffers of the stream's scratch area for entry points in other translation
+// units; the lock is held until the caller has queued the kernels that use
+// them.
+gemm_status_t abi_scratch(cudaStream_t stream, int64_t floats, std::unique_lock<std::mutex>& lock,
+                          float** ws) {
+  gemm_status_t s;
+  DeviceState* st = device_state(&s);
+  if (st == nullptr) return s;
+  lock = std::unique_lock<std::mutex>(st->ws_mutex);
+  Scratch* sc = nullptr;
+  s = ensure_scratch(*st, stream, floats, 0, &sc);
+  if (s == GEMM_OK) *ws = sc->ws;
+  return s;
+}
+
+gemm_status_t abi_stage(cudaStream_t stream, int64_t bytes, std::unique_lock<std::mutex>& lock,
+                        uint8_t** buf) {
+  gemm_status_t s;
+  DeviceState* st = device_state(&s);
+  if (st == nullptr) return s;
+  lock = std::unique_lock<std::mutex>(st->ws_mutex);
+  return ensure_stage(*st, stream, bytes, buf);
+}
+
+bool abi_encode_tiled(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base,
+                      const int64_t* dims, const int64_t* strides, const uint32_t* box) {
+  EncodeTiledFn enc = encode_fn();
+  if (enc == nullptr || rank < 2 || rank > 3) return false;
+  cuuint64_t d[3], t[2];
+  cuuint32_t b[3], e[3] = {1, 1, 1};
+  for (int i = 0; i < rank; ++i) {
+    d[i] = static_cast<cuuint64_t>(dims[i]);
+    b[i] = box[i];
+    if (i > 0) t[i - 1] = static_cast<cuuint64_t>(strides[i - 1]);
+  }
+  return enc(map, type, static_cast<cuuint32_t>(rank), const_cast<void*>(base), d, t, b, e,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace g12

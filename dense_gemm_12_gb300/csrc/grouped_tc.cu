@@ -1,0 +1,573 @@
+// grouped_tc.cu -- bf16 products grouped by expert with ragged row counts, on
+// the 5th-generation tensor cores.  Group g has rows offsets[g] ..
+// offsets[g + 1] - 1 of A, and a K x N matrix B[g]:
+//
+//     forward           D[t] = alpha A[t] B[g] + beta D[t]
+//     input gradient    the same with B[g]^T (B[g] is then N x K)
+//     weight gradient   dB[g] = alpha sum_{t in g} A[t]^T dD[t] + beta dB[g]
+//
+// The kernel is the dense one's (bf16_tc.cu): a TMA producer, one MMA issuer
+// (M = 128, N = 256, K = 16), two accumulators in TMEM, four warps writing
+// finished tiles; persistent CTAs walk the tiles of all groups in one order
+// (groups.cuh).  What is different:
+//   * a group's last row tile reads rows of the next group.  They only reach
+//     accumulator rows that are not written.
+//   * in the weight gradient the ragged direction is the one summed over, so
+//     rows past the group's end must not reach the sum, whatever they hold
+//     (NaN included): the issuing warp zeroes them in shared memory, in both
+//     operands, before the MMAs of a group's last block.
+//   * a weight gradient's group without rows is written as beta dB[g].
+#include "groups.cuh"
+#include "ops.cuh"
+
+namespace g12 {
+namespace {
+
+constexpr int BM = 128, BN = 256, BK = 64;
+constexpr int STAGES = 4;
+constexpr int kStageBytesA = BM * BK * 2;
+constexpr int kStageBytesB = BK * BN * 2;
+constexpr int kBoxBytes = BK * 64 * 2;  // one MN-major box: 64 of M or N, 64 of k
+constexpr int kStageBytes = kStageBytesA + kStageBytesB;
+constexpr int kThreads = 192;
+constexpr int kOutThreads = 128;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kOutBarAny = 1;
+constexpr int kOutWarpBytes = 32 * 32 * 4;
+
+// Layouts: which operands are contiguous along k ("K-major").
+enum Mode : int { kForward = 0, kTransB = 1, kWeightGrad = 2 };
+
+struct GroupedArgs {
+  int rows;             // of A (and dD)
+  int M, N, K;          // kWeightGrad: M x N is one dB[g] and K unused; else N columns, K summed
+  int groups;
+  const int32_t* offsets;
+  float alpha, beta;
+  void* D;
+  int64_t ldd, stride_d;
+  int d_type, d_vec;
+  int tile_rows;        // rows of A per tile (not kWeightGrad)
+  int band;
+  int product;          // 0: alpha == 0 or K == 0, operands are not read
+  uint32_t* err;
+};
+
+struct __align__(8) Tail {
+  uint64_t full[STAGES];
+  uint64_t empty[STAGES];
+  uint64_t tmem_full[2];
+  uint64_t tmem_empty[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort_flag;
+  GroupTable groups;
+};
+
+constexpr size_t kSmemBytes = 1024 + STAGES * kStageBytes + 4 * kOutWarpBytes + sizeof(Tail);
+static_assert(kSmemBytes <= 227 * 1024, "grouped kernel shared memory");
+
+// One work item: its k-blocks, where its rows (or, for the weight gradient,
+// its M) start, and its output rows.
+struct Item {
+  int group, tn;
+  int row0;      // first row of A read (forward) / first row of the group (weight gradient)
+  int m0;        // weight gradient: first row of dB
+  int rows;      // output rows
+  int num_kb;
+  int last;      // weight gradient: rows of the last k-block
+};
+
+template <int MODE>
+__device__ __forceinline__ Item item_of(const GroupedArgs& p, const GroupTable& tab, int t,
+                                        int tiles_n, int num_kb, int& g) {
+  Item w;
+  if (MODE != kWeightGrad) {
+    const GroupTile f = group_tile(tab, t, tiles_n, p.band, p.tile_rows, g);
+    w.group = f.group;
+    w.tn = f.tn;
+    w.row0 = f.row0;
+    w.m0 = 0;
+    w.rows = f.rows;
+    w.num_kb = num_kb;
+    w.last = BK;
+    return w;
+  }
+  const int tiles_m = (p.M + BM - 1) / BM;
+  const int per = tiles_m * tiles_n;
+  w.group = t / per;
+  const int local = t - w.group * per;
+  const int per_band = p.band * tiles_n;
+  const int b = local / per_band;
+  const int high = min(tiles_m - b * p.band, p.band);
+  const int in_band = local - b * per_band;
+  w.tn = in_band / high;
+  w.m0 = (b * p.band + in_band % high) * BM;
+  w.row0 = tab.row[w.group];
+  w.rows = min(BM, p.M - w.m0);
+  const int n = p.product ? tab.row[w.group + 1] - w.row0 : 0;
+  w.num_kb = (n + BK - 1) / BK;
+  w.last = n - (w.num_kb - 1) * BK;
+  return w;
+}
+
+// 32 accumulator rows x 32 columns of this warp: turned around in its 4 KB of
+// shared memory (16-byte pieces XOR-swizzled by row), then 8 lanes cover a
+// row's 32 columns.
+__device__ __forceinline__ void write_chunk(const GroupedArgs& p, float4* stg, const uint32_t (&r)[32],
+                                            float alpha, void* D, int64_t row_base, int rows,
+                                            int col0) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    stg[lane * 8 + (q ^ (lane & 7))] =
+        make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
+                    __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]));
+  __syncwarp();
+  const int ch = lane & 7;
+  const int col = col0 + 4 * ch;
+  const bool whole = col + 4 <= p.N && p.d_vec;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int rr = i * 4 + (lane >> 3);
+    if (rr >= rows || col >= p.N) continue;
+    const float4 s = stg[rr * 8 + (ch ^ (rr & 7))];
+    float v[4] = {alpha * s.x, alpha * s.y, alpha * s.z, alpha * s.w};
+    const int64_t at = (row_base + rr) * p.ldd + col;
+    if (p.beta != 0.0f) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (col + k < p.N) v[k] = fmaf(p.beta, load1(D, p.d_type, at + k), v[k]);
+    }
+    if (whole) {
+      if (p.d_type == GEMM_OUT_F32)
+        *reinterpret_cast<float4*>(static_cast<float*>(D) + at) = make_float4(v[0], v[1], v[2], v[3]);
+      else
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(D) + at) =
+            make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (col + k < p.N) store1(D, p.d_type, at + k, v[k]);
+    }
+  }
+  __syncwarp();
+}
+
+template <int MODE>
+__global__ void __launch_bounds__(kThreads, 1)
+    grouped_kernel(const __grid_constant__ GroupedArgs p, const __grid_constant__ CUtensorMap tmA,
+                   const __grid_constant__ CUtensorMap tmB) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = align_smem<1024>(smem_raw);
+  uint8_t* out_stage = smem + STAGES * kStageBytes;
+  Tail* tail = reinterpret_cast<Tail*>(out_stage + 4 * kOutWarpBytes);
+  volatile int* abort_flag = &tail->abort_flag;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  constexpr bool kGrad = MODE == kWeightGrad;
+  constexpr uint32_t kIdesc =
+      idesc_bf16_f32(BM, BN, /*A MN-major*/ kGrad ? 1 : 0, /*B MN-major*/ MODE == kTransB ? 0 : 1);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&tail->full[s], 1);
+      mbar_init(&tail->empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tail->tmem_full[b], 1);
+      mbar_init(&tail->tmem_empty[b], kOutThreads);
+    }
+    mbar_init(&tail->drain, 1);
+    tail->abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&tail->tmem_base, kTmemCols);
+    tmem_relinquish_alloc_permit();
+  }
+  // Everything above touches no global memory and may overlap the previous
+  // kernel's last CTAs; every global access below follows its completion.
+  grid_dependency_wait();
+  if (threadIdx.x == 0) grid_launch_dependents();
+  if (warp == 2) build_groups(tail->groups, p.offsets, p.groups, p.rows, kGrad ? 1 : p.tile_rows);
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem_base = tail->tmem_base;
+  const GroupTable& tab = tail->groups;
+  const int tiles_n = (p.N + BN - 1) / BN;
+  const int tiles = kGrad ? p.groups * ((p.M + BM - 1) / BM) * tiles_n
+                          : tab.tile[p.groups] * tiles_n;
+  const int num_kb = p.product ? (p.K + BK - 1) / BK : 0;
+
+  if (warp == 0) {
+    // -------------------------------------------------------- TMA producer
+    if (lane == 0) {
+      uint32_t it = 0;
+      int g = 0;
+      bool ok = true;
+      const uint32_t bytes =
+          static_cast<uint32_t>((kGrad ? kStageBytesA : p.tile_rows * BK * 2) + kStageBytesB);
+      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+        const Item w = item_of<MODE>(p, tab, t, tiles_n, num_kb, g);
+        for (int kb = 0; kb < w.num_kb; ++kb, ++it) {
+          const uint32_t s = it % STAGES, round = it / STAGES;
+          if (!mbar_wait(&tail->empty[s], (round & 1u) ^ 1u, abort_flag, p.err)) {
+            ok = false;
+            break;
+          }
+          uint8_t* sa = smem + s * kStageBytes;
+          uint8_t* sb = sa + kStageBytesA;
+          uint64_t* bar = &tail->full[s];
+          mbar_arrive_expect_tx(bar, bytes);
+          if (kGrad) {
+            const int k = w.row0 + kb * BK;
+#pragma unroll
+            for (int j = 0; j < BM / 64; ++j)
+              tma_load_2d(sa + j * kBoxBytes, &tmA, w.m0 + j * 64, k, bar);
+#pragma unroll
+            for (int j = 0; j < BN / 64; ++j)
+              tma_load_2d(sb + j * kBoxBytes, &tmB, w.tn * BN + j * 64, k, bar);
+          } else {
+            tma_load_2d(sa, &tmA, kb * BK, w.row0, bar);
+            if (MODE == kTransB) {
+              tma_load_3d(sb, &tmB, kb * BK, w.tn * BN, w.group, bar);
+            } else {
+#pragma unroll
+              for (int j = 0; j < BN / 64; ++j)
+                tma_load_3d(sb + j * kBoxBytes, &tmB, w.tn * BN + j * 64, kb * BK, w.group, bar);
+            }
+          }
+        }
+      }
+      if (!ok) {
+        for (uint32_t j = it > STAGES ? it - STAGES : 0u; j < it; ++j)
+          mbar_drain_wait(&tail->full[j % STAGES], (j / STAGES) & 1u);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // -------------------------------------- MMA issuer (lane 0 of the warp)
+    uint32_t it = 0, j = 0;
+    int g = 0;
+    bool ok = true, issued = false;
+    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+      const Item w = item_of<MODE>(p, tab, t, tiles_n, num_kb, g);
+      if (w.num_kb == 0) continue;
+      const uint32_t ab = j & 1u, ar = j >> 1;
+      ++j;
+      bool got = mbar_wait(&tail->tmem_empty[ab], (ar & 1u) ^ 1u, abort_flag, p.err);
+      if (__any_sync(0xffffffffu, !got)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after_sync();
+      const uint32_t d_tmem = tmem_base + ab * BN;
+      for (int kb = 0; kb < w.num_kb; ++kb, ++it) {
+        const uint32_t s = it % STAGES, round = it / STAGES;
+        got = mbar_wait(&tail->full[s], round & 1u, abort_flag, p.err);
+        if (__any_sync(0xffffffffu, !got)) {
+          ok = false;
+          break;
+        }
+        uint8_t* stage = smem + s * kStageBytes;
+        if (kGrad && kb == w.num_kb - 1 && w.last < BK) {
+          // Rows of the next group: row k of a box is its bytes 128 k ..
+          // 128 k + 127, whatever the swizzle does inside them.
+          const int pieces = (BK - w.last) * 8;
+#pragma unroll 1
+          for (int box = 0; box < (BM + BN) / 64; ++box) {
+            uint4* z = reinterpret_cast<uint4*>(stage + box * kBoxBytes + w.last * 128);
+            for (int i = lane; i < pieces; i += 32) z[i] = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (lane == 0) {
+          tc_fence_after_sync();
+          const uint32_t sa = smem_u32(stage);
+          const uint32_t sb = sa + kStageBytesA;
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; ++kk) {
+            // K-major: 8-row groups 1024 B apart, a K step of 16 is 32 B.
+            // MN-major: 64-wide boxes 8 KB apart (LBO), 8-row k groups 1024 B
+            // apart (SBO), a K step of 16 rows is 2048 B.
+            const uint64_t adesc = kGrad ? smem_desc_sw128(sa + kk * 2048, kBoxBytes, 1024)
+                                         : smem_desc_sw128(sa + kk * 32, 16, 1024);
+            const uint64_t bdesc = MODE == kTransB ? smem_desc_sw128(sb + kk * 32, 16, 1024)
+                                                   : smem_desc_sw128(sb + kk * 2048, kBoxBytes, 1024);
+            tc_mma_f16(d_tmem, adesc, bdesc, kIdesc, (kb != 0 || kk != 0) ? 1u : 0u);
+          }
+          tc_commit(&tail->empty[s]);
+        }
+        issued = true;
+        __syncwarp();
+      }
+      if (!ok) break;
+      if (lane == 0) tc_commit(&tail->tmem_full[ab]);
+      __syncwarp();
+    }
+    if (!ok && issued && lane == 0) {
+      // Let every MMA this thread issued finish before TMEM is released.
+      tc_commit(&tail->drain);
+      mbar_drain_wait(&tail->drain, 0);
+    }
+    __syncwarp();
+  } else {
+    // -------------------------------------------------------------- output
+    const int quarter = warp & 3;  // TMEM lanes this warp may access
+    float4* stg = reinterpret_cast<float4*>(out_stage + quarter * kOutWarpBytes);
+    uint32_t j = 0;
+    int g = 0;
+    for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+      const Item w = item_of<MODE>(p, tab, t, tiles_n, num_kb, g);
+      const int rows = min(w.rows - quarter * 32, 32);
+      const int64_t row_base =
+          (kGrad ? w.m0 : w.row0) + quarter * 32;
+      void* D = p.D;
+      if (kGrad) {
+        const int64_t at = w.group * p.stride_d;
+        D = p.d_type == GEMM_OUT_F32 ? static_cast<void*>(static_cast<float*>(D) + at)
+                                     : static_cast<void*>(static_cast<__nv_bfloat16*>(D) + at);
+      }
+      const int chunks = min(BN / 32, (p.N - w.tn * BN + 31) / 32);
+      if (w.num_kb == 0) {
+        uint32_t zero[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) zero[i] = 0u;
+        if (rows > 0) {
+#pragma unroll 1
+          for (int c = 0; c < chunks; ++c)
+            write_chunk(p, stg, zero, 0.0f, D, row_base, rows, w.tn * BN + c * 32);
+        }
+        continue;
+      }
+      const uint32_t ab = j & 1u, ar = j >> 1;
+      ++j;
+      const bool ok = mbar_wait(&tail->tmem_full[ab], ar & 1u, abort_flag, p.err);
+      // Leave together if a wait ran out anywhere (see named_bar_any).
+      if (named_bar_any(kOutBarAny, kOutThreads, !ok)) break;
+      tc_fence_after_sync();
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + ab * BN;
+      if (rows > 0) {
+#pragma unroll 1
+        for (int c = 0; c < chunks; ++c) {
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(taddr + c * 32, r);
+          tmem_wait_ld(r);
+          write_chunk(p, stg, r, p.alpha, D, row_base, rows, w.tn * BN + c * 32);
+        }
+      }
+      tc_fence_before_sync();
+      mbar_arrive(&tail->tmem_empty[ab]);
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  if (warp == 1) tmem_dealloc(tmem_base, kTmemCols);
+}
+
+struct Operand {
+  const void* p;
+  int64_t rows, cols, ld;
+  int64_t count, stride;
+};
+
+bool tma_describes(const Operand& o) {
+  return !ops_misaligned(o.p, 16) && o.ld % 8 == 0 && (o.count == 1 || o.stride % 8 == 0);
+}
+
+int64_t staged_bytes(const Operand& o) {
+  return (o.count * o.rows * ((o.cols + 7) / 8 * 8) * 2 + 255) / 256 * 256;
+}
+
+// A copy that TMA can describe: rows padded to 16 bytes, matrices dense.
+__global__ void stage_bf16_kernel(const uint16_t* src, int64_t ld, int64_t stride, uint16_t* dst,
+                                  int64_t ld2, int64_t rows, int64_t cols, int64_t count) {
+  grid_dependency_wait();
+  const int64_t pieces = ld2 / 8;
+  const int64_t total = count * rows * pieces;
+  for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    const int64_t line = i / pieces, c = (i - line * pieces) * 8;
+    const int64_t m = line / rows, r = line - m * rows;
+    const uint16_t* s = src + m * stride + r * ld + c;
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c + j < cols) w[j >> 1] |= static_cast<uint32_t>(s[j]) << (16 * (j & 1));
+    *reinterpret_cast<uint4*>(dst + line * ld2 + c) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+cudaError_t stage(Operand& o, uint8_t* to, int num_sms, cudaStream_t s) {
+  const int64_t ld2 = (o.cols + 7) / 8 * 8;
+  const int64_t total = o.count * o.rows * (ld2 / 8);
+  const int64_t want = (total + 255) / 256, fit = static_cast<int64_t>(num_sms) * 8;
+  const uint16_t* src = static_cast<const uint16_t*>(o.p);
+  uint16_t* dst = reinterpret_cast<uint16_t*>(to);
+  const int64_t ld = o.ld, stride = o.stride, rows = o.rows, cols = o.cols, count = o.count;
+  const cudaError_t e =
+      ops_launch<stage_bf16_kernel>(dim3(static_cast<unsigned>(want < fit ? want : fit)), 256, 0, 1,
+                                    s, src, ld, stride, dst, ld2, rows, cols, count);
+  o.p = dst;
+  o.ld = ld2;
+  o.stride = o.rows * ld2;
+  return e;
+}
+
+bool bad_dim(int64_t v) { return v < 0 || v > kOpsMaxDim; }
+
+// Stages the operands that TMA cannot describe and encodes the maps (of B with
+// rank_b dimensions); box_a and box_b: elements along the innermost and the
+// next dimension.
+gemm_status_t operands(Operand a, Operand b, int rank_b, const uint32_t (&box_a)[2], const uint32_t (&box_b)[2],
+                       int num_sms, cudaStream_t s, std::unique_lock<std::mutex>& lock,
+                       CUtensorMap* tmA, CUtensorMap* tmB) {
+  const int64_t need_a = tma_describes(a) ? 0 : staged_bytes(a);
+  const int64_t need_b = tma_describes(b) ? 0 : staged_bytes(b);
+  if (need_a + need_b > 0) {
+    uint8_t* buf = nullptr;
+    const gemm_status_t st = abi_stage(s, need_a + need_b, lock, &buf);
+    if (st != GEMM_OK) return st;
+    cudaError_t e = need_a > 0 ? stage(a, buf, num_sms, s) : cudaSuccess;
+    if (e == cudaSuccess && need_b > 0) e = stage(b, buf + need_a, num_sms, s);
+    if (e != cudaSuccess) return abi_from_cuda(e);
+  }
+  const int64_t da[2] = {a.cols, a.rows}, ta[1] = {a.ld * 2};
+  const int64_t db[3] = {b.cols, b.rows, b.count};
+  const int64_t tb[2] = {b.ld * 2, (b.count > 1 ? b.stride : b.ld * b.rows) * 2};
+  const uint32_t bb[3] = {box_b[0], box_b[1], 1};
+  if (!abi_encode_tiled(tmA, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.p, da, ta, box_a) ||
+      !abi_encode_tiled(tmB, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank_b, b.p, db, tb, bb))
+    return GEMM_ERR_LAUNCH;
+  return GEMM_OK;
+}
+
+}  // namespace
+}  // namespace g12
+
+using namespace g12;
+
+extern "C" {
+
+gemm_status_t gemm_bf16gemm_grouped(int64_t G, const int32_t* offsets, int64_t rows, int64_t N,
+                                    int64_t K, float alpha, const void* A, int64_t lda,
+                                    const void* B, int64_t ldb, int64_t stride_b, int transpose_b,
+                                    float beta, void* D, int64_t ldd, int d_type, void* stream) {
+  const int d_bytes = float_type_bytes(d_type);
+  if (bad_dim(G) || bad_dim(rows) || bad_dim(N) || bad_dim(K) || d_bytes == 0)
+    return GEMM_ERR_INVALID_VALUE;
+  if (G == 0 || rows == 0 || N == 0) return GEMM_OK;
+  const bool product = K > 0 && alpha != 0.0f;
+  if (offsets == nullptr || ops_misaligned(offsets, 4) || D == nullptr || ldd < N || bad_dim(ldd) ||
+      ops_misaligned(D, d_bytes))
+    return GEMM_ERR_INVALID_VALUE;
+  const int64_t brows = transpose_b ? N : K, bcols = transpose_b ? K : N;
+  if (product) {
+    if (A == nullptr || B == nullptr || lda < K || bad_dim(lda) || ldb < bcols || bad_dim(ldb) ||
+        (G > 1 && stride_b < (brows - 1) * ldb + bcols))
+      return GEMM_ERR_INVALID_VALUE;
+    if (ops_misaligned(A, 2) || ops_misaligned(B, 2)) return GEMM_ERR_MISALIGNED;
+  }
+  if (G > kMaxGroups) return GEMM_ERR_UNSUPPORTED;
+  int sms = 0;
+  uint32_t* err = nullptr;
+  gemm_status_t st = abi_device(&sms, &err);
+  if (st != GEMM_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  GroupedArgs a{};
+  a.rows = static_cast<int>(rows);
+  a.N = static_cast<int>(N);
+  a.K = static_cast<int>(K);
+  a.groups = static_cast<int>(G);
+  a.offsets = offsets;
+  a.alpha = alpha;
+  a.beta = beta;
+  a.D = D;
+  a.ldd = ldd;
+  a.d_type = d_type;
+  a.d_vec = !ops_misaligned(D, 16) && ldd % (16 / d_bytes) == 0;
+  a.tile_rows = rows > 64 ? 128 : (rows > 32 ? 64 : (rows > 16 ? 32 : 16));
+  a.band = 8;
+  a.product = product ? 1 : 0;
+  a.err = err;
+  std::unique_lock<std::mutex> lock;
+  CUtensorMap tmA{}, tmB{};
+  if (product) {
+    const uint32_t box_a[2] = {BK, static_cast<uint32_t>(a.tile_rows)};
+    const uint32_t box_b[2] = {BK, static_cast<uint32_t>(transpose_b ? BN : BK)};
+    st = operands(Operand{A, rows, K, lda, 1, 0}, Operand{B, brows, bcols, ldb, G, stride_b}, 3,
+                  box_a, box_b, sms, s, lock, &tmA, &tmB);
+    if (st != GEMM_OK) return st;
+  }
+  const int64_t row_tiles = (rows + a.tile_rows - 1) / a.tile_rows + (G < rows ? G : rows);
+  const int64_t tiles = row_tiles * ((N + BN - 1) / BN);
+  if (tiles + sms > kOpsMaxDim) return GEMM_ERR_UNSUPPORTED;
+  const dim3 grid(static_cast<unsigned>(tiles < sms ? tiles : sms));
+  return abi_from_cuda(
+      transpose_b ? ops_launch<grouped_kernel<kTransB>>(grid, kThreads, kSmemBytes, 1, s, a, tmA, tmB)
+                  : ops_launch<grouped_kernel<kForward>>(grid, kThreads, kSmemBytes, 1, s, a, tmA, tmB));
+}
+
+gemm_status_t gemm_bf16gemm_grouped_wgrad(int64_t G, const int32_t* offsets, int64_t rows,
+                                          int64_t N, int64_t K, float alpha, const void* A,
+                                          int64_t lda, const void* dD, int64_t lddd, float beta,
+                                          void* dB, int64_t ldb, int64_t stride_b, int d_type,
+                                          void* stream) {
+  const int d_bytes = float_type_bytes(d_type);
+  if (bad_dim(G) || bad_dim(rows) || bad_dim(N) || bad_dim(K) || d_bytes == 0)
+    return GEMM_ERR_INVALID_VALUE;
+  if (G == 0 || N == 0 || K == 0) return GEMM_OK;
+  const bool product = rows > 0 && alpha != 0.0f;
+  if (offsets == nullptr || ops_misaligned(offsets, 4) || dB == nullptr || ldb < N ||
+      bad_dim(ldb) || ops_misaligned(dB, d_bytes) || (G > 1 && stride_b < (K - 1) * ldb + N))
+    return GEMM_ERR_INVALID_VALUE;
+  if (product) {
+    if (A == nullptr || dD == nullptr || lda < K || bad_dim(lda) || lddd < N || bad_dim(lddd))
+      return GEMM_ERR_INVALID_VALUE;
+    if (ops_misaligned(A, 2) || ops_misaligned(dD, 2)) return GEMM_ERR_MISALIGNED;
+  }
+  const int64_t per = ((K + BM - 1) / BM) * ((N + BN - 1) / BN);
+  if (G > kMaxGroups || G * per > kOpsMaxDim / 2) return GEMM_ERR_UNSUPPORTED;
+  int sms = 0;
+  uint32_t* err = nullptr;
+  gemm_status_t st = abi_device(&sms, &err);
+  if (st != GEMM_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  GroupedArgs a{};
+  a.rows = static_cast<int>(rows);
+  a.M = static_cast<int>(K);
+  a.N = static_cast<int>(N);
+  a.K = 0;
+  a.groups = static_cast<int>(G);
+  a.offsets = offsets;
+  a.alpha = alpha;
+  a.beta = beta;
+  a.D = dB;
+  a.ldd = ldb;
+  a.stride_d = stride_b;
+  a.d_type = d_type;
+  a.d_vec = !ops_misaligned(dB, 16) && ldb % (16 / d_bytes) == 0 &&
+            (G == 1 || stride_b % (16 / d_bytes) == 0);
+  a.tile_rows = BM;
+  a.band = 8;
+  a.product = product ? 1 : 0;
+  a.err = err;
+  std::unique_lock<std::mutex> lock;
+  CUtensorMap tmA{}, tmB{};
+  if (product) {
+    const uint32_t box[2] = {64, BK};
+    st = operands(Operand{A, rows, K, lda, 1, 0}, Operand{dD, rows, N, lddd, 1, 0}, 2, box, box, sms,
+                  s, lock, &tmA, &tmB);
+    if (st != GEMM_OK) return st;
+  }
+  const int64_t tiles = G * per;
+  const dim3 grid(static_cast<unsigned>(tiles < sms ? tiles : sms));
+  return abi_from_cuda(
+      ops_launch<grouped_kernel<kWeightGrad>>(grid, kThreads, kSmemBytes, 1, s, a, tmA, tmB));
+}
+
+}  // extern "C"

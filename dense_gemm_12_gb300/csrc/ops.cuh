@@ -1,0 +1,269 @@
+// ops.cuh -- what the operators around the GEMMs share (normalisation, fp8
+// quantisation, block-scaled fp8 products, products grouped by expert):
+// pieces of the C ABI they borrow from api.cu, element types, fp8 block
+// scales, and the PTX wrappers that the plain GEMM kernels do not need.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cfloat>
+#include <cstdint>
+#include <mutex>
+
+#include "../../include/gemm12.h"
+#include "ptx.cuh"
+
+namespace g12 {
+
+// ------------------------------------------------------------ host pieces
+// (defined in api.cu)
+gemm_status_t abi_device(int* num_sms, uint32_t** err_word);
+// `lock` is taken (on the device's scratch mutex) and must be held until the
+// kernels that use the buffer are queued.  GEMM_ERR_NO_MEMORY inside a stream
+// capture when the stream's buffer is too small.
+gemm_status_t abi_scratch(cudaStream_t stream, int64_t floats, std::unique_lock<std::mutex>& lock,
+                          float** ws);
+gemm_status_t abi_stage(cudaStream_t stream, int64_t bytes, std::unique_lock<std::mutex>& lock,
+                        uint8_t** buf);
+// Tensor map of `rank` (2 or 3) dimensions, innermost first; strides in bytes
+// of dimensions 1 .. rank - 1; 128-byte swizzle; zeros outside.
+bool abi_encode_tiled(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base,
+                      const int64_t* dims, const int64_t* strides, const uint32_t* box);
+gemm_status_t abi_from_cuda(cudaError_t e);
+
+constexpr int64_t kOpsMaxDim = (int64_t{1} << 31) - 1;
+
+inline bool ops_misaligned(const void* p, uintptr_t bytes) {
+  return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0;
+}
+// A row-major array of `type` (gemm_out_t): element bytes, 0 for a type that
+// the operator does not take.
+inline int float_type_bytes(int type) {
+  return type == GEMM_OUT_F32 ? 4 : (type == GEMM_OUT_BF16 ? 2 : 0);
+}
+
+// Sets a kernel's dynamic shared memory limit, once per device.
+template <auto Kernel>
+cudaError_t ops_allow_smem(size_t bytes) {
+  static std::atomic<uint64_t> done{0};  // one bit per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+  if ((done.load(std::memory_order_relaxed) & bit) != 0) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(bytes));
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
+// Launches with programmatic stream serialization, as the GEMM kernels are:
+// every kernel here waits in grid_dependency_wait() before its first global
+// access.  cluster > 1: in clusters of that many CTAs along x.
+template <auto Kernel, typename... Args>
+cudaError_t ops_launch(dim3 grid, int threads, size_t smem, int cluster, cudaStream_t stream,
+                       const Args&... args) {
+  if (smem > 48 * 1024) {
+    const cudaError_t e = ops_allow_smem<Kernel>(smem);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster > 1 ? cluster : 1);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, Kernel, args...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// ------------------------------------------------------- fp8 block scales
+constexpr float kFp8Max = 448.0f;             // largest finite E4M3 value
+constexpr float kFp8ScaleMin = FLT_MIN;       // 2^-126: blocks of zeros keep a usable scale
+constexpr int kFp8Block = 128;
+
+// |v| if finite, else 0: infinities and NaN do not set a block's scale.
+__device__ __forceinline__ float finite_abs(float v) {
+  const float a = fabsf(v);
+  return a <= FLT_MAX ? a : 0.0f;
+}
+
+// Scale of a block whose largest finite magnitude is amax, and the factor
+// that its values are multiplied by before rounding.  The factor is one
+// correctly rounded quotient, so a value's product with it has the same two
+// roundings as its quotient by the scale.
+__device__ __forceinline__ float fp8_scale(float amax) {
+  return fmaxf(__fdiv_rn(amax, kFp8Max), kFp8ScaleMin);
+}
+__device__ __forceinline__ float fp8_factor(float amax) {
+  return fminf(__fdiv_rn(kFp8Max, amax), 1.0f / kFp8ScaleMin);
+}
+
+// Four values -> four E4M3 bytes (nearest even, saturating, NaN stays NaN).
+__device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+
+// ------------------------------------------------ eight elements of a row
+// Vector forms: 16-byte aligned pieces.  Strided forms: elements c, c + 16,
+// ..., c + 112 of a 128-column block, so that the 16 lanes of a block read
+// consecutive elements; those at or past `n` read as zero and are not
+// written.  Loads are marked as read once (evict first).
+__device__ __forceinline__ void load8_vec(const void* p, int type, int64_t at, float (&v)[8]) {
+  if (type == GEMM_OUT_BF16) {
+    const uint4 u = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + at));
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  } else {
+    const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+    const float4 a = __ldcs(f), b = __ldcs(f + 1);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+}
+
+__device__ __forceinline__ float load1(const void* p, int type, int64_t at) {
+  return type == GEMM_OUT_BF16 ? __bfloat162float(__ldcs(static_cast<const __nv_bfloat16*>(p) + at))
+                               : __ldcs(static_cast<const float*>(p) + at);
+}
+
+__device__ __forceinline__ void store1(void* p, int type, int64_t at, float v) {
+  if (type == GEMM_OUT_BF16)
+    static_cast<__nv_bfloat16*>(p)[at] = __float2bfloat16_rn(v);
+  else
+    static_cast<float*>(p)[at] = v;
+}
+
+__device__ __forceinline__ void load8_strided(const void* p, int type, int64_t row_at, int c, int n,
+                                              float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = c + 16 * i < n ? load1(p, type, row_at + c + 16 * i) : 0.0f;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ void store8_vec(void* p, int type, int64_t at, const float (&v)[8]) {
+  if (type == GEMM_OUT_BF16) {
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p) + at) =
+        make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                   pack_bf16(v[6], v[7]));
+  } else {
+    float4* f = reinterpret_cast<float4*>(static_cast<float*>(p) + at);
+    f[0] = make_float4(v[0], v[1], v[2], v[3]);
+    f[1] = make_float4(v[4], v[5], v[6], v[7]);
+  }
+}
+
+__device__ __forceinline__ void store8_strided(void* p, int type, int64_t row_at, int c, int n,
+                                               const float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (c + 16 * i < n) store1(p, type, row_at + c + 16 * i, v[i]);
+}
+
+// --------------------------------------------------------- PTX additions
+// 3-D tiled copy global -> shared; x is the innermost coordinate.
+__device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, int32_t x,
+                                            int32_t y, int32_t z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// D[tmem] (+)= A[smem] x B[smem] with 8-bit floating operands, single CTA.
+__device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Instruction descriptor of tcgen05.mma kind::f8f6f4 with E4M3 A and B (format
+// 0), both K-major, and an fp32 accumulator: fields as in idesc_bf16_f32.
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N) {
+  return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+// Waits for this thread's TMEM loads; r is tied to the wait so that no use of
+// the loaded registers is scheduled before it.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+
+// Two fp32 values in one register pair, and the packed operations on them.
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 f32x2_parts(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ uint64_t f32x2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t f32x2_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Registers per thread of the calling warpgroup after launch.  The shares of
+// a block's warpgroups add up to at most what it was launched with.
+template <int N>
+__device__ __forceinline__ void regs_give_back() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_take() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+}  // namespace g12

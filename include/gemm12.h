@@ -515,6 +515,197 @@ gemm_status_t gemm_quantization(int64_t M, int64_t N, int64_t BM, int64_t BN,
                                 int64_t num_sms, int64_t ctas_per_sm,
                                 gemm_quantization_t *out);
 
+/*
+ * Operators around the GEMMs of a transformer's layers: a root-mean-square
+ * norm whose output is ready for an 8-bit product, fp8 quantisation by
+ * blocks, products of such matrices, and products grouped by expert.  They
+ * share the conventions at the top of this file (device pointers, row-major,
+ * asynchronous on `stream`, no alignment needed beyond the element size), and
+ * these:
+ *
+ *  fp8        E4M3 (see GEMM_OUT_F8E4M3), one byte per value.
+ *  Scales     fp32.  A matrix whose rows are contiguous along k has a scale
+ *             per block of 128 values of k and either one row
+ *             (GEMM_BLOCK_ROWS) or 128 rows (GEMM_BLOCK_TILES); the last
+ *             blocks may be partial.  Scale (b, r) of k-block b and row (or
+ *             block of rows) r is at scales[b * ld_scales + r].  A value is
+ *             its byte's E4M3 value times its block's scale.
+ *  Types      x_type, y_type, d_type, ... are GEMM_OUT_F32 or GEMM_OUT_BF16.
+ *  Memory     gemm_rmsnorm_backward keeps partial sums of the weight's
+ *             gradient in the stream's scratch; operands of the products
+ *             that TMA cannot describe (base not 16-byte aligned, or a row
+ *             pitch or matrix stride that is not a multiple of 16 bytes) are
+ *             always copied into the stream's staging buffer.  Where that
+ *             memory cannot be had (inside a stream capture on a stream
+ *             whose buffer is too small, or out of memory) the call returns
+ *             GEMM_ERR_NO_MEMORY and queues nothing.
+ *  Order      Sums are always added in the same order: the same call gives
+ *             the same bits.
+ */
+typedef enum {
+    GEMM_BLOCK_ROWS = 0,   /* 1 x 128 blocks                                     */
+    GEMM_BLOCK_TILES = 1   /* 128 x 128 blocks                                   */
+} gemm_block_t;
+
+/*
+ * gemm_rmsnorm -- for each of `rows` rows of `dim` values (dim <= 2^30):
+ *
+ *     h = x + residual          (h = x without a residual)
+ *     rstd = 1 / sqrt(mean(h^2) + eps)
+ *     y = h * rstd * weight
+ *
+ * in fp32, each output rounded once from there.  Every output is optional:
+ * h (the sum, for the next residual), y, q with scales (y in fp8 with
+ * GEMM_BLOCK_ROWS scales, as gemm_fp8_quantize would give from the unrounded
+ * y), and rstd (for the backward pass).  x may be fp32 or bf16, and so may the
+ * residual and the outputs.  An output may take the place of an input of the
+ * same type and leading dimension (h that of the residual, y that of x);
+ * apart from that nothing may overlap.  A row whose sum of squares exceeds
+ * the fp32 range gives rstd = 0.
+ * Errors: GEMM_ERR_INVALID_VALUE for NULL x or weight, q without scales or
+ * scales without q, an unknown type, a leading dimension below dim (rows for
+ * the scales), or a pointer not aligned to its element.
+ */
+typedef struct {
+    const void *x;          /* rows x dim                                        */
+    int64_t ldx;
+    int x_type;
+    const void *residual;   /* rows x dim, or NULL                               */
+    int64_t ldr;
+    int residual_type;
+    void *h;                /* rows x dim, or NULL                               */
+    int64_t ldh;
+    int h_type;
+    const float *weight;    /* dim                                               */
+    float eps;
+    void *y;                /* rows x dim, or NULL                               */
+    int64_t ldy;
+    int y_type;
+    void *q;                /* rows x dim fp8, or NULL                           */
+    int64_t ldq;
+    float *scales;          /* ceil(dim / 128) x rows, with q                    */
+    int64_t ld_scales;
+    float *rstd;            /* rows, or NULL                                     */
+} gemm_rmsnorm_t;
+
+gemm_status_t gemm_rmsnorm(int64_t rows, int64_t dim, const gemm_rmsnorm_t *args, void *stream);
+
+/*
+ * gemm_rmsnorm_backward -- the gradients of gemm_rmsnorm's y with respect to h
+ * (and so to x and to the residual) and to the weight, in fp32:
+ *
+ *     g = dy * weight       xh = h * rstd
+ *     dh = rstd * (g - xh * mean(g * xh)) + residual_grad
+ *     dweight = sum over rows of dy * xh
+ *
+ * h and rstd are the forward pass's; residual_grad is the gradient that
+ * reaches h along the skip connection, or NULL.  dweight (dim fp32 values,
+ * overwritten; zeros for rows == 0) may be NULL.  dh may take the place of dy,
+ * h or residual_grad of the same type and leading dimension for dim <= 16384,
+ * and for any dim without dweight.
+ */
+typedef struct {
+    const void *dy;             /* rows x dim                                    */
+    int64_t lddy;
+    int dy_type;
+    const void *h;              /* rows x dim                                    */
+    int64_t ldh;
+    int h_type;
+    const float *weight;        /* dim                                           */
+    const float *rstd;          /* rows                                          */
+    const void *residual_grad;  /* rows x dim, or NULL                           */
+    int64_t ldrg;
+    int residual_grad_type;
+    void *dh;                   /* rows x dim                                    */
+    int64_t lddh;
+    int dh_type;
+    float *dweight;             /* dim, or NULL                                  */
+} gemm_rmsnorm_grad_t;
+
+gemm_status_t gemm_rmsnorm_backward(int64_t rows, int64_t dim, const gemm_rmsnorm_grad_t *args,
+                                    void *stream);
+
+/*
+ * gemm_fp8_quantize -- the rows x cols matrix x, or its transpose, in fp8 with
+ * block scales:
+ *
+ *     a = largest finite |x| of the block
+ *     scale = max(a / 448, 2^-126)      q = e4m3(x / scale)
+ *
+ * rounded to nearest even; infinities saturate to +-448 and NaN stays NaN.
+ * The quotient is formed as x * (448 / a) in fp32.  q (ldq) is rows x cols, or
+ * cols x rows with `transpose`, and `block` (a gemm_block_t) is the shape of
+ * its blocks; scales (ld_scales) as above, for q's rows and columns.
+ */
+gemm_status_t gemm_fp8_quantize(int64_t rows, int64_t cols, const void *x, int64_t ldx, int x_type,
+                                int block, int transpose, void *q, int64_t ldq, float *scales,
+                                int64_t ld_scales, void *stream);
+
+/*
+ * gemm_fp8gemm -- D <- alpha * A x B^T + beta * D for fp8 A (M x K,
+ * GEMM_BLOCK_ROWS scales) and B (N x K, `b_block` scales), both contiguous
+ * along k:
+ *
+ *     D[i][j] = alpha * sum over k-blocks b of
+ *               a_scale(b, i) * b_scale(b, j) * sum_{k in b} A[i][k] * B[j][k]
+ *               + beta * D[i][j]
+ *
+ * GEMM_BLOCK_TILES is the usual choice for weights (activations x weights,
+ * or gradients x weights quantised the other way round), GEMM_BLOCK_ROWS for
+ * weight gradients.  A block's products are summed by the tensor cores in
+ * fp32, the scaled block sums in fp32 registers.  D (ldd) is fp32 or bf16 and
+ * is not read when beta == 0.  K == 0 or alpha == 0: A, B and the scales are
+ * not read.  D must not overlap the operands.
+ */
+gemm_status_t gemm_fp8gemm(int64_t M, int64_t N, int64_t K, float alpha, const void *A,
+                           int64_t lda, const float *a_scales, int64_t ld_as, const void *B,
+                           int64_t ldb, const float *b_scales, int64_t ld_bs, int b_block,
+                           float beta, void *D, int64_t ldd, int d_type, void *stream);
+
+/*
+ * Products grouped by expert.  Group g (0 <= g < G <= 1024) has the rows
+ * offsets[g] .. offsets[g + 1] - 1 of A (rows x K) and a matrix B[g] at
+ * B + g * stride_b (elements).  `offsets` are G + 1 non-decreasing int32
+ * values from 0 to `rows` in device memory; the host never reads them, so no
+ * call waits for the router that writes them, and a captured call takes the
+ * values that they have at each replay.  (Offsets out of order or out of range
+ * are clamped: groups are then wrong, accesses are not.)  Groups may be empty.
+ * Rows before offsets[0] or from offsets[G] on belong to no group: the rows of
+ * D there are not written.
+ *
+ * gemm_bf16gemm_grouped -- D[t] <- alpha * A[t] x B[g] + beta * D[t] for the
+ * rows t of each group; bf16 A (lda) and B, fp32 or bf16 D (ldd).  B[g] is
+ * K x N (ldb >= N), or with transpose_b N x K (ldb >= K) and D = A x B[g]^T:
+ * the gradient with respect to A is this call with dD in A's place, the same
+ * B, and N and K exchanged.
+ *
+ * gemm_bf16gemm_grouped_wgrad -- the gradient with respect to B:
+ * dB[g] <- alpha * A_g^T x dD_g + beta * dB[g], with A rows x K, dD rows x N
+ * (both bf16) and dB[g] K x N (ldb, stride_b; fp32 or bf16).  A group without
+ * rows has dB[g] <- beta * dB[g].
+ *
+ * gemm_fp8gemm_grouped -- gemm_fp8gemm for the rows of each group: A with its
+ * scales for all rows, B[g] N x K, its scales at b_scales + g * stride_bs.
+ *
+ * Error bounds per element are those of the dense calls for the group's
+ * product.  G > 1024: GEMM_ERR_UNSUPPORTED.
+ */
+gemm_status_t gemm_bf16gemm_grouped(int64_t G, const int32_t *offsets, int64_t rows, int64_t N,
+                                    int64_t K, float alpha, const void *A, int64_t lda,
+                                    const void *B, int64_t ldb, int64_t stride_b, int transpose_b,
+                                    float beta, void *D, int64_t ldd, int d_type, void *stream);
+gemm_status_t gemm_bf16gemm_grouped_wgrad(int64_t G, const int32_t *offsets, int64_t rows,
+                                          int64_t N, int64_t K, float alpha, const void *A,
+                                          int64_t lda, const void *dD, int64_t lddd, float beta,
+                                          void *dB, int64_t ldb, int64_t stride_b, int d_type,
+                                          void *stream);
+gemm_status_t gemm_fp8gemm_grouped(int64_t G, const int32_t *offsets, int64_t rows, int64_t N,
+                                   int64_t K, float alpha, const void *A, int64_t lda,
+                                   const float *a_scales, int64_t ld_as, const void *B,
+                                   int64_t ldb, int64_t stride_b, const float *b_scales,
+                                   int64_t ld_bs, int64_t stride_bs, int b_block, float beta,
+                                   void *D, int64_t ldd, int d_type, void *stream);
+
 /* Library version, major * 10000 + minor * 100 + patch. */
 int gemm_version(void);
 
