@@ -119,6 +119,8 @@ def library_path() -> str:
 def load_library(build_if_missing: bool = False):
     """Load libgemm12.so (optionally compiling it first) and declare signatures."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -524,58 +526,63 @@ def bf16gemm_fused(A, B, D, C=None, alpha=1.0, beta=0.0, bias=None, act="none", 
 
 
 # ------------------------------------------- operators around the GEMMs
-_FLOAT_CODES = None
+# A call of a small operator takes a few microseconds on the GPU, so these
+# helpers look at each tensor once: the device number (-1 on the host), dtype,
+# shape and strides.
+_TORCH = None       # torch, its current-stream getter and the dtypes used below
+_FLOAT_CODES = {}   # dtype -> gemm_out_t
 
 
-def _float_code(t, name):
-    """gemm_out_t of a float32 or bfloat16 CUDA tensor."""
-    global _FLOAT_CODES
-    if _FLOAT_CODES is None:
+def _torch_once():
+    global _TORCH
+    if _TORCH is None:
         import torch
-        _FLOAT_CODES = {torch.float32: OUT["f32"], torch.bfloat16: OUT["bf16"]}
+        _FLOAT_CODES.update({torch.float32: OUT["f32"], torch.bfloat16: OUT["bf16"]})
+        getter = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if getter is None:
+            def getter(index):
+                return torch.cuda.current_stream(index).cuda_stream
+        _TORCH = (getter, torch.float8_e4m3fn, torch.float32, torch.bfloat16, torch.int32)
+    return _TORCH
+
+
+def _stream_of(dev, stream):
+    if dev < 0:
+        raise TypeError("all tensors must be CUDA tensors")
+    return _TORCH[0](dev) if stream is None else stream.cuda_stream
+
+
+def _array(t, shape, dtype, dev, name):
+    """(address, leading dimension) of a row-major matrix (or of each of a batch), checked."""
+    if t.dtype != dtype or t.get_device() != dev:
+        raise TypeError("%s must be a %s tensor on the other operands' device" % (name, dtype))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, not %s" % (name, tuple(shape), tuple(t.shape)))
+    strides = t.stride()
+    if strides[-1] != 1 and shape[-1] > 1:
+        raise ValueError("%s must be row-major (unit column stride)" % name)
+    return t.data_ptr(), strides[-2] if shape[-2] > 1 else max(shape[-1], 1)
+
+
+def _float_array(t, shape, dev, name):
+    """(address, leading dimension, type) of a float32 or bfloat16 matrix."""
     code = _FLOAT_CODES.get(t.dtype)
-    if code is None or not t.is_cuda:
-        raise TypeError("%s must be a float32 or bfloat16 CUDA tensor" % name)
-    return code
+    if code is None:
+        raise TypeError("%s must be a float32 or bfloat16 tensor" % name)
+    return (*_array(t, shape, t.dtype, dev, name), code)
 
 
-def _check_dtype(t, dtype, name):
-    if t.dtype != dtype or not t.is_cuda:
-        raise TypeError("%s must be a %s CUDA tensor" % (name, dtype))
-
-
-def _check_shape(t, shape, name):
-    if tuple(t.shape) != shape:
-        raise ValueError("%s must have shape %s, not %s" % (name, shape, tuple(t.shape)))
-
-
-def _check_vector(t, n, name):
-    import torch
-    _check_dtype(t, torch.float32, name)
+def _vector(t, n, dtype, dev, name):
+    """Address of a contiguous vector of n values."""
+    if t.dtype != dtype or t.get_device() != dev:
+        raise TypeError("%s must be a %s tensor on the other operands' device" % (name, dtype))
     if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
         raise ValueError("%s must be a contiguous vector of %d values" % (name, n))
     return t.data_ptr()
 
 
-def _check_scales(t, shape, name):
-    """Pitch of a matrix of scales: k-blocks x rows (or blocks of rows)."""
-    import torch
-    _check_dtype(t, torch.float32, name)
-    _check_shape(t, shape, name)
-    return _row_major_ld(t, name)
-
-
-def _row_array(t, shape, name):
-    """(address, leading dimension, type) of a row-major float array."""
-    code = _float_code(t, name)
-    _check_shape(t, shape, name)
-    return t.data_ptr(), _row_major_ld(t, name), code
-
-
-def _same_device(device, *tensors):
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError("all tensors must be on %s" % (device,))
+def _batch_stride(t, ld):
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * ld
 
 
 def rmsnorm(x, weight, eps=1e-6, residual=None, h=None, y=None, q=None, scales=None, rstd=None,
@@ -584,31 +591,29 @@ def rmsnorm(x, weight, eps=1e-6, residual=None, h=None, y=None, q=None, scales=N
     (rows, dim), into the given outputs: h, y (float32 or bfloat16), q with scales (y in
     float8_e4m3fn, scales (ceil(dim / 128), rows) float32) and rstd (rows,).  weight is float32.
     h may be the residual itself and y may be x itself."""
-    import torch
+    _, f8, f32, _, _ = _torch_once()
     if x.dim() != 2:
         raise ValueError("x must be 2-D")
-    rows, dim = x.shape
-    _same_device(x.device, weight, residual, h, y, q, scales, rstd)
+    shape, dev = x.shape, x.get_device()
+    rows, dim = shape
+    handle = _stream_of(dev, stream)
     a = RmsnormArgs()
-    a.x, a.ldx, a.x_type = _row_array(x, (rows, dim), "x")
-    a.weight, a.eps = _check_vector(weight, dim, "weight"), eps
+    a.x, a.ldx, a.x_type = _float_array(x, shape, dev, "x")
+    a.weight, a.eps = _vector(weight, dim, f32, dev, "weight"), eps
     if residual is not None:
-        a.residual, a.ldr, a.residual_type = _row_array(residual, (rows, dim), "residual")
+        a.residual, a.ldr, a.residual_type = _float_array(residual, shape, dev, "residual")
     if h is not None:
-        a.h, a.ldh, a.h_type = _row_array(h, (rows, dim), "h")
+        a.h, a.ldh, a.h_type = _float_array(h, shape, dev, "h")
     if y is not None:
-        a.y, a.ldy, a.y_type = _row_array(y, (rows, dim), "y")
+        a.y, a.ldy, a.y_type = _float_array(y, shape, dev, "y")
     if (q is None) != (scales is None):
         raise ValueError("q and scales come together")
     if q is not None:
-        _check_dtype(q, torch.float8_e4m3fn, "q")
-        _check_shape(q, (rows, dim), "q")
-        a.q, a.ldq = q.data_ptr(), _row_major_ld(q, "q")
-        a.ld_scales = max(_check_scales(scales, (-(-dim // 128), rows), "scales"), rows)
-        a.scales = scales.data_ptr()
+        a.q, a.ldq = _array(q, shape, f8, dev, "q")
+        a.scales, a.ld_scales = _array(scales, (-(-dim // 128), rows), f32, dev, "scales")
     if rstd is not None:
-        a.rstd = _check_vector(rstd, rows, "rstd")
-    st = load_library().gemm_rmsnorm(rows, dim, ctypes.byref(a), _stream_handle(stream, x.device))
+        a.rstd = _vector(rstd, rows, f32, dev, "rstd")
+    st = load_library().gemm_rmsnorm(rows, dim, ctypes.byref(a), handle)
     if st != 0:
         raise GemmError(st, "gemm_rmsnorm")
 
@@ -616,22 +621,24 @@ def rmsnorm(x, weight, eps=1e-6, residual=None, h=None, y=None, q=None, scales=N
 def rmsnorm_backward(dy, h, weight, rstd, dh, dweight=None, residual_grad=None, stream=None):
     """Gradients of rmsnorm's y: dh <- the gradient with respect to h (and so x and the
     residual) plus residual_grad, dweight (dim,) <- the one with respect to the weight."""
+    f32 = _torch_once()[2]
     if dy.dim() != 2:
         raise ValueError("dy must be 2-D")
-    rows, dim = dy.shape
-    _same_device(dy.device, h, weight, rstd, dh, dweight, residual_grad)
+    shape, dev = dy.shape, dy.get_device()
+    rows, dim = shape
+    handle = _stream_of(dev, stream)
     a = RmsnormGradArgs()
-    a.dy, a.lddy, a.dy_type = _row_array(dy, (rows, dim), "dy")
-    a.h, a.ldh, a.h_type = _row_array(h, (rows, dim), "h")
-    a.dh, a.lddh, a.dh_type = _row_array(dh, (rows, dim), "dh")
-    a.weight, a.rstd = _check_vector(weight, dim, "weight"), _check_vector(rstd, rows, "rstd")
+    a.dy, a.lddy, a.dy_type = _float_array(dy, shape, dev, "dy")
+    a.h, a.ldh, a.h_type = _float_array(h, shape, dev, "h")
+    a.dh, a.lddh, a.dh_type = _float_array(dh, shape, dev, "dh")
+    a.weight = _vector(weight, dim, f32, dev, "weight")
+    a.rstd = _vector(rstd, rows, f32, dev, "rstd")
     if residual_grad is not None:
-        a.residual_grad, a.ldrg, a.residual_grad_type = _row_array(residual_grad, (rows, dim),
-                                                                   "residual_grad")
+        a.residual_grad, a.ldrg, a.residual_grad_type = _float_array(residual_grad, shape, dev,
+                                                                     "residual_grad")
     if dweight is not None:
-        a.dweight = _check_vector(dweight, dim, "dweight")
-    st = load_library().gemm_rmsnorm_backward(rows, dim, ctypes.byref(a),
-                                              _stream_handle(stream, dy.device))
+        a.dweight = _vector(dweight, dim, f32, dev, "dweight")
+    st = load_library().gemm_rmsnorm_backward(rows, dim, ctypes.byref(a), handle)
     if st != 0:
         raise GemmError(st, "gemm_rmsnorm_backward")
     return dh
@@ -641,75 +648,51 @@ def fp8_quantize(x, q, scales, block="rows", transpose=False, stream=None):
     """x (rows, cols), float32 or bfloat16, or its transpose, into q (float8_e4m3fn) with one
     float32 scale per 1 x 128 ("rows") or 128 x 128 ("tiles") block of q: scales[b, r] is that
     of columns 128 b .. 128 b + 127 and row (or block of rows) r."""
-    import torch
+    _, f8, f32, _, _ = _torch_once()
     if x.dim() != 2:
         raise ValueError("x must be 2-D")
     rows, cols = x.shape
-    _same_device(x.device, q, scales)
+    dev = x.get_device()
+    handle = _stream_of(dev, stream)
+    code = BLOCK[block]
     qr, qc = (cols, rows) if transpose else (rows, cols)
-    _check_dtype(q, torch.float8_e4m3fn, "q")
-    _check_shape(q, (qr, qc), "q")
-    lds = _check_scales(scales, (-(-qc // 128), -(-qr // 128) if BLOCK[block] else qr), "scales")
-    px, ldx, code = _row_array(x, (rows, cols), "x")
-    st = gemm_fp8_quantize(rows, cols, px, ldx, code, BLOCK[block], int(bool(transpose)),
-                           q.data_ptr(), _row_major_ld(q, "q"), scales.data_ptr(), lds,
-                           _stream_handle(stream, x.device))
+    px, ldx, x_type = _float_array(x, x.shape, dev, "x")
+    pq, ldq = _array(q, (qr, qc), f8, dev, "q")
+    ps, lds = _array(scales, (-(-qc // 128), -(-qr // 128) if code else qr), f32, dev, "scales")
+    st = load_library().gemm_fp8_quantize(rows, cols, px, ldx, x_type, code, 1 if transpose else 0,
+                                          pq, ldq, ps, lds, handle)
     if st != 0:
         raise GemmError(st, "gemm_fp8_quantize")
     return q
 
 
-def _fp8_operands(torch, A, a_scales, B, b_scales, D):
-    _check_dtype(A, torch.float8_e4m3fn, "A")
-    _check_dtype(B, torch.float8_e4m3fn, "B")
-    if A.dim() != 2:
-        raise ValueError("A must be 2-D")
-    M, K = A.shape
-    N = B.shape[-2]
-    if B.shape[-1] != K:
-        raise ValueError("shape mismatch: A %s, B %s" % (tuple(A.shape), tuple(B.shape)))
-    kb = -(-K // 128)
-    ld_as = _check_scales(a_scales, (kb, M), "a_scales")
-    _check_dtype(b_scales, torch.float32, "b_scales")
-    if b_scales.dim() != B.dim():
-        raise ValueError("b_scales must have as many dimensions as B")
-    block = BLOCK["rows"] if b_scales.shape[-1] == N else BLOCK["tiles"]
-    _check_shape(b_scales, (*B.shape[:-2], kb, N if block == BLOCK["rows"] else -(-N // 128)),
-                 "b_scales")
-    return M, N, K, max(ld_as, M), block
-
-
-def _batched(t, name):
-    """(leading dimension, stride) of a batch of row-major matrices."""
-    G, rows, cols = t.shape
-    if cols > 1 and t.stride(2) != 1:
-        raise ValueError("%s must be row-major (unit column stride)" % name)
-    ld = t.stride(1) if rows > 1 else max(cols, 1)
-    return ld, t.stride(0) if G > 1 else rows * ld
-
-
-def _check_offsets(offsets, G):
-    import torch
-    _check_dtype(offsets, torch.int32, "offsets")
-    if tuple(offsets.shape) != (G + 1,) or not offsets.is_contiguous():
-        raise ValueError("offsets must be %d contiguous int32 values" % (G + 1))
-    return offsets.data_ptr()
+def _b_scales(b_scales, lead, kb, N, dev):
+    """(address, leading dimension, block) of B's scales: one per row, or per 128 rows."""
+    last = b_scales.shape[-1] if b_scales.dim() else -1
+    block = 0 if last == N else 1
+    return (*_array(b_scales, (*lead, kb, N if block == 0 else -(-N // 128)), _TORCH[2], dev,
+                    "b_scales"), block)
 
 
 def fp8gemm(A, a_scales, B, b_scales, D, alpha=1.0, beta=0.0, stream=None):
     """D <- alpha*(A @ B^T) + beta*D in place: A (M, K) and B (N, K) float8_e4m3fn, D float32 or
     bfloat16; a_scales (ceil(K / 128), M); b_scales (ceil(K / 128), N), or ceil(N / 128) in place
     of N for 128 x 128 blocks (see fp8_quantize)."""
-    import torch
-    if B.dim() != 2:
-        raise ValueError("B must be 2-D")
-    _same_device(D.device, A, a_scales, B, b_scales)
-    M, N, K, ld_as, block = _fp8_operands(torch, A, a_scales, B, b_scales, D)
-    pd, ldd, code = _row_array(D, (M, N), "D")
-    st = gemm_fp8gemm(M, N, K, alpha, A.data_ptr(), _row_major_ld(A, "A"), a_scales.data_ptr(),
-                      ld_as, B.data_ptr(), _row_major_ld(B, "B"), b_scales.data_ptr(),
-                      _row_major_ld(b_scales, "b_scales"), block, beta, pd, ldd, code,
-                      _stream_handle(stream, D.device))
+    _, f8, f32, _, _ = _torch_once()
+    if A.dim() != 2 or B.dim() != 2:
+        raise ValueError("A and B must be 2-D")
+    M, K = A.shape
+    N = B.shape[0]
+    dev = D.get_device()
+    handle = _stream_of(dev, stream)
+    kb = -(-K // 128)
+    pa, lda = _array(A, (M, K), f8, dev, "A")
+    pb, ldb = _array(B, (N, K), f8, dev, "B")
+    psa, ld_as = _array(a_scales, (kb, M), f32, dev, "a_scales")
+    psb, ld_bs, block = _b_scales(b_scales, (), kb, N, dev)
+    pd, ldd, code = _float_array(D, (M, N), dev, "D")
+    st = load_library().gemm_fp8gemm(M, N, K, alpha, pa, lda, psa, ld_as, pb, ldb, psb, ld_bs,
+                                     block, beta, pd, ldd, code, handle)
     if st != 0:
         raise GemmError(st, "gemm_fp8gemm")
     return D
@@ -718,19 +701,23 @@ def fp8gemm(A, a_scales, B, b_scales, D, alpha=1.0, beta=0.0, stream=None):
 def fp8gemm_grouped(A, a_scales, B, b_scales, offsets, D, alpha=1.0, beta=0.0, stream=None):
     """fp8gemm for the rows offsets[g] .. offsets[g + 1] - 1 of A and D with B[g] (G, N, K) and
     b_scales[g]; offsets (G + 1,) int32, on the device."""
-    import torch
-    if B.dim() != 3:
-        raise ValueError("B must be 3-D")
-    _same_device(D.device, A, a_scales, B, b_scales, offsets)
-    M, N, K, ld_as, block = _fp8_operands(torch, A, a_scales, B, b_scales, D)
-    G = B.shape[0]
-    ldb, stride_b = _batched(B, "B")
-    ld_bs, stride_bs = _batched(b_scales, "b_scales")
-    pd, ldd, code = _row_array(D, (M, N), "D")
-    st = gemm_fp8gemm_grouped(G, _check_offsets(offsets, G), M, N, K, alpha, A.data_ptr(),
-                              _row_major_ld(A, "A"), a_scales.data_ptr(), ld_as, B.data_ptr(), ldb,
-                              stride_b, b_scales.data_ptr(), ld_bs, stride_bs, block, beta, pd, ldd,
-                              code, _stream_handle(stream, D.device))
+    _, f8, f32, _, i32 = _torch_once()
+    if A.dim() != 2 or B.dim() != 3:
+        raise ValueError("A must be 2-D and B 3-D")
+    M, K = A.shape
+    G, N = B.shape[0], B.shape[1]
+    dev = D.get_device()
+    handle = _stream_of(dev, stream)
+    kb = -(-K // 128)
+    pa, lda = _array(A, (M, K), f8, dev, "A")
+    pb, ldb = _array(B, (G, N, K), f8, dev, "B")
+    psa, ld_as = _array(a_scales, (kb, M), f32, dev, "a_scales")
+    psb, ld_bs, block = _b_scales(b_scales, (G,), kb, N, dev)
+    pd, ldd, code = _float_array(D, (M, N), dev, "D")
+    st = load_library().gemm_fp8gemm_grouped(
+        G, _vector(offsets, G + 1, i32, dev, "offsets"), M, N, K, alpha, pa, lda, psa, ld_as, pb,
+        ldb, _batch_stride(B, ldb), psb, ld_bs, _batch_stride(b_scales, ld_bs), block, beta, pd,
+        ldd, code, handle)
     if st != 0:
         raise GemmError(st, "gemm_fp8gemm_grouped")
     return D
@@ -740,22 +727,20 @@ def bf16gemm_grouped(A, B, offsets, D, alpha=1.0, beta=0.0, transpose_b=False, s
     """D[t] <- alpha*(A[t] @ B[g]) + beta*D[t] in place for the rows t = offsets[g] ..
     offsets[g + 1] - 1 of each group; A (rows, K) and B (G, K, N) bfloat16 -- with transpose_b
     (G, N, K), and D = A @ B[g]^T --, D float32 or bfloat16, offsets (G + 1,) int32 on the device."""
-    import torch
-    _check_dtype(A, torch.bfloat16, "A")
-    _check_dtype(B, torch.bfloat16, "B")
+    _, _, _, b16, i32 = _torch_once()
     if A.dim() != 2 or B.dim() != 3:
         raise ValueError("A must be 2-D and B 3-D")
-    _same_device(D.device, A, B, offsets)
     rows, K = A.shape
     G = B.shape[0]
     N = B.shape[1 if transpose_b else 2]
-    _check_shape(B, (G, N, K) if transpose_b else (G, K, N), "B")
-    ldb, stride_b = _batched(B, "B")
-    pd, ldd, code = _row_array(D, (rows, N), "D")
-    st = gemm_bf16gemm_grouped(G, _check_offsets(offsets, G), rows, N, K, alpha, A.data_ptr(),
-                               _row_major_ld(A, "A"), B.data_ptr(), ldb, stride_b,
-                               int(bool(transpose_b)), beta, pd, ldd, code,
-                               _stream_handle(stream, D.device))
+    dev = D.get_device()
+    handle = _stream_of(dev, stream)
+    pa, lda = _array(A, (rows, K), b16, dev, "A")
+    pb, ldb = _array(B, (G, N, K) if transpose_b else (G, K, N), b16, dev, "B")
+    pd, ldd, code = _float_array(D, (rows, N), dev, "D")
+    st = load_library().gemm_bf16gemm_grouped(
+        G, _vector(offsets, G + 1, i32, dev, "offsets"), rows, N, K, alpha, pa, lda, pb, ldb,
+        _batch_stride(B, ldb), 1 if transpose_b else 0, beta, pd, ldd, code, handle)
     if st != 0:
         raise GemmError(st, "gemm_bf16gemm_grouped")
     return D
@@ -764,22 +749,19 @@ def bf16gemm_grouped(A, B, offsets, D, alpha=1.0, beta=0.0, transpose_b=False, s
 def bf16gemm_grouped_wgrad(A, dD, offsets, dB, alpha=1.0, beta=0.0, stream=None):
     """dB[g] <- alpha*(A_g^T @ dD_g) + beta*dB[g] in place: A (rows, K) and dD (rows, N) bfloat16,
     dB (G, K, N) float32 or bfloat16; a group without rows gets beta*dB[g]."""
-    import torch
-    _check_dtype(A, torch.bfloat16, "A")
-    _check_dtype(dD, torch.bfloat16, "dD")
+    _, _, _, b16, i32 = _torch_once()
     if A.dim() != 2 or dD.dim() != 2 or dB.dim() != 3:
         raise ValueError("A and dD must be 2-D and dB 3-D")
-    _same_device(dB.device, A, dD, offsets)
     rows, K = A.shape
     N, G = dD.shape[1], dB.shape[0]
-    _check_shape(dD, (rows, N), "dD")
-    _check_shape(dB, (G, K, N), "dB")
-    code = _float_code(dB, "dB")
-    ldb, stride_b = _batched(dB, "dB")
-    st = gemm_bf16gemm_grouped_wgrad(G, _check_offsets(offsets, G), rows, N, K, alpha, A.data_ptr(),
-                                     _row_major_ld(A, "A"), dD.data_ptr(), _row_major_ld(dD, "dD"),
-                                     beta, dB.data_ptr(), ldb, stride_b, code,
-                                     _stream_handle(stream, dB.device))
+    dev = dB.get_device()
+    handle = _stream_of(dev, stream)
+    pa, lda = _array(A, (rows, K), b16, dev, "A")
+    pd, lddd = _array(dD, (rows, N), b16, dev, "dD")
+    pb, ldb, code = _float_array(dB, (G, K, N), dev, "dB")
+    st = load_library().gemm_bf16gemm_grouped_wgrad(
+        G, _vector(offsets, G + 1, i32, dev, "offsets"), rows, N, K, alpha, pa, lda, pd, lddd, beta,
+        pb, ldb, _batch_stride(dB, ldb), code, handle)
     if st != 0:
         raise GemmError(st, "gemm_bf16gemm_grouped_wgrad")
     return dB
