@@ -597,22 +597,18 @@ def rmsnorm(x, weight, eps=1e-6, residual=None, h=None, y=None, q=None, scales=N
     shape, dev = x.shape, x.get_device()
     rows, dim = shape
     handle = _stream_of(dev, stream)
-    a = RmsnormArgs()
-    a.x, a.ldx, a.x_type = _float_array(x, shape, dev, "x")
-    a.weight, a.eps = _vector(weight, dim, f32, dev, "weight"), eps
-    if residual is not None:
-        a.residual, a.ldr, a.residual_type = _float_array(residual, shape, dev, "residual")
-    if h is not None:
-        a.h, a.ldh, a.h_type = _float_array(h, shape, dev, "h")
-    if y is not None:
-        a.y, a.ldy, a.y_type = _float_array(y, shape, dev, "y")
     if (q is None) != (scales is None):
         raise ValueError("q and scales come together")
-    if q is not None:
-        a.q, a.ldq = _array(q, shape, f8, dev, "q")
-        a.scales, a.ld_scales = _array(scales, (-(-dim // 128), rows), f32, dev, "scales")
-    if rstd is not None:
-        a.rstd = _vector(rstd, rows, f32, dev, "rstd")
+    none = (None, 0, 0)
+    a = RmsnormArgs(
+        *_float_array(x, shape, dev, "x"),
+        *(none if residual is None else _float_array(residual, shape, dev, "residual")),
+        *(none if h is None else _float_array(h, shape, dev, "h")),
+        _vector(weight, dim, f32, dev, "weight"), eps,
+        *(none if y is None else _float_array(y, shape, dev, "y")),
+        *((None, 0) if q is None else _array(q, shape, f8, dev, "q")),
+        *((None, 0) if q is None else _array(scales, (-(-dim // 128), rows), f32, dev, "scales")),
+        None if rstd is None else _vector(rstd, rows, f32, dev, "rstd"))
     st = load_library().gemm_rmsnorm(rows, dim, ctypes.byref(a), handle)
     if st != 0:
         raise GemmError(st, "gemm_rmsnorm")
@@ -627,17 +623,13 @@ def rmsnorm_backward(dy, h, weight, rstd, dh, dweight=None, residual_grad=None, 
     shape, dev = dy.shape, dy.get_device()
     rows, dim = shape
     handle = _stream_of(dev, stream)
-    a = RmsnormGradArgs()
-    a.dy, a.lddy, a.dy_type = _float_array(dy, shape, dev, "dy")
-    a.h, a.ldh, a.h_type = _float_array(h, shape, dev, "h")
-    a.dh, a.lddh, a.dh_type = _float_array(dh, shape, dev, "dh")
-    a.weight = _vector(weight, dim, f32, dev, "weight")
-    a.rstd = _vector(rstd, rows, f32, dev, "rstd")
-    if residual_grad is not None:
-        a.residual_grad, a.ldrg, a.residual_grad_type = _float_array(residual_grad, shape, dev,
-                                                                     "residual_grad")
-    if dweight is not None:
-        a.dweight = _vector(dweight, dim, f32, dev, "dweight")
+    a = RmsnormGradArgs(
+        *_float_array(dy, shape, dev, "dy"), *_float_array(h, shape, dev, "h"),
+        _vector(weight, dim, f32, dev, "weight"), _vector(rstd, rows, f32, dev, "rstd"),
+        *((None, 0, 0) if residual_grad is None else
+          _float_array(residual_grad, shape, dev, "residual_grad")),
+        *_float_array(dh, shape, dev, "dh"),
+        None if dweight is None else _vector(dweight, dim, f32, dev, "dweight"))
     st = load_library().gemm_rmsnorm_backward(rows, dim, ctypes.byref(a), handle)
     if st != 0:
         raise GemmError(st, "gemm_rmsnorm_backward")

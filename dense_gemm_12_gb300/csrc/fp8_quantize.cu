@@ -23,24 +23,13 @@ struct QuantArgs {
   int q_vec;  // rows of q can be written in 16-byte pieces
 };
 
-// Eight elements of row r from column c on (c a multiple of 8); zero outside.
-__device__ __forceinline__ void load8_edge(const QuantArgs& a, int64_t r, int64_t c, float (&v)[8]) {
-  if (r < a.rows && a.x_vec && c + 8 <= a.cols) {
-    load8_vec(a.x, a.x_type, r * a.ldx + c, v);
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    v[i] = r < a.rows && c + i < a.cols ? load1(a.x, a.x_type, r * a.ldx + c + i) : 0.0f;
-}
-
 // 1 x 128 blocks along the rows of x: 16 lanes take one block; the thread's
 // kRowUnits units are loaded before the first is reduced.  Rows that cannot
 // be moved in vectors are read and written by elements 16 apart, which keeps
 // consecutive lanes on consecutive elements.
 constexpr int kRowUnits = 4;
 
-template <bool VEC>
+template <bool VEC, int T>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const __grid_constant__ QuantArgs a) {
   grid_dependency_wait();
   grid_launch_dependents();
@@ -51,7 +40,7 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const __grid_constan
   // every lane of a warp takes the same number of turns: the shuffles below
   for (int64_t base = static_cast<int64_t>(blockIdx.x) * 16; base < units;
        base += stride * kRowUnits) {
-    float v[kRowUnits][8];
+    Raw8<T> raw[kRowUnits];
     int64_t row[kRowUnits], blk[kRowUnits];
     bool in[kRowUnits];
 #pragma unroll
@@ -61,23 +50,15 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const __grid_constan
       row[u] = in[u] ? unit / kb : 0;
       blk[u] = in[u] ? unit - row[u] * kb : 0;
       const int64_t c0 = blk[u] * kFp8Block;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[u][i] = 0.0f;
-      if (!in[u]) continue;
-      if (VEC) {
-        if (c0 + l * 8 < a.cols) load8_vec(a.x, a.x_type, row[u] * a.ldx + c0 + l * 8, v[u]);
-      } else {
-        const int n = static_cast<int>(min(a.cols - c0, static_cast<int64_t>(kFp8Block)));
-        load8_strided(a.x, a.x_type, row[u] * a.ldx + c0, l, n, v[u]);
-      }
+      const int n = static_cast<int>(min(a.cols - c0, static_cast<int64_t>(kFp8Block)));
+      const int c = VEC ? l * 8 : l;
+      raw[u] = load8<VEC, T>(a.x, a.x_type, row[u] * a.ldx + c0, c, n, in[u] && c < n);
     }
 #pragma unroll
     for (int u = 0; u < kRowUnits; ++u) {
-      float amax = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, finite_abs(v[u][i]));
-#pragma unroll
-      for (int s = 8; s > 0; s >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, s));
+      float v[8];
+      widen8<VEC, T>(raw[u], a.x_type, v);
+      const float amax = block_amax(v);
       if (!in[u]) continue;
       const float f = fp8_factor(amax);
       const int64_t c0 = blk[u] * kFp8Block;
@@ -85,14 +66,14 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const __grid_constan
       if (VEC) {
         if (c0 + l * 8 < a.cols)
           *reinterpret_cast<uint2*>(q + l * 8) =
-              make_uint2(pack_e4m3(v[u][0] * f, v[u][1] * f, v[u][2] * f, v[u][3] * f),
-                         pack_e4m3(v[u][4] * f, v[u][5] * f, v[u][6] * f, v[u][7] * f));
+              make_uint2(pack_e4m3(v[0] * f, v[1] * f, v[2] * f, v[3] * f),
+                         pack_e4m3(v[4] * f, v[5] * f, v[6] * f, v[7] * f));
       } else {
         const int n = static_cast<int>(min(a.cols - c0, static_cast<int64_t>(kFp8Block)));
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           if (l + 16 * i < n)
-            q[l + 16 * i] = __nv_cvt_float_to_fp8(v[u][i] * f, __NV_SATFINITE, __NV_E4M3);
+            q[l + 16 * i] = __nv_cvt_float_to_fp8(v[i] * f, __NV_SATFINITE, __NV_E4M3);
       }
       if (l == 0) a.scales[blk[u] * a.ld_scales + row[u]] = fp8_scale(amax);
     }
@@ -104,7 +85,7 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const __grid_constan
 // output goes through shared memory: eight values down a column make one
 // 8-byte piece of an output row; a row's 16 pieces are XOR-swizzled by its
 // 8-column group, so that the 16 lanes of a write fall in distinct banks.
-template <bool TILES, bool TRANSPOSE>
+template <bool TILES, bool TRANSPOSE, int T>
 __global__ void __launch_bounds__(256) quantize_tile_kernel(const __grid_constant__ QuantArgs a) {
   __shared__ __align__(16) uint8_t turned[TRANSPOSE ? 128 * 128 : 16];
   __shared__ float colmax[TILES ? 1 : 8][TILES ? 1 : 128];
@@ -118,8 +99,21 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const __grid_constan
     const int64_t tr = tile / tiles_c, tc = tile - tr * tiles_c;
     const int64_t r0 = tr * 128 + rg * 8, c0 = tc * 128 + cg * 8;
     float v[8][8];  // [row][column]
+    if (a.x_vec && c0 + 8 <= a.cols) {
+      Raw8<T> raw[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) load8_edge(a, r0 + i, c0, v[i]);
+      for (int i = 0; i < 8; ++i)
+        raw[i] = load8<true, T>(a.x, a.x_type, (r0 + i) * a.ldx + c0, 0, 8, r0 + i < a.rows);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) widen8<true, T>(raw[i], a.x_type, v[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          v[i][j] = r0 + i < a.rows && c0 + j < a.cols
+                        ? load1(a.x, T, (r0 + i) * a.ldx + c0 + j) : 0.0f;
+    }
     float f[8];  // factor of each column
     if (TILES) {
       float amax = 0.0f;
@@ -215,6 +209,14 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const __grid_constan
   }
 }
 
+template <int T>
+cudaError_t launch_tiles(const QuantArgs& a, int block, bool transpose, dim3 grid, cudaStream_t s) {
+  if (block == GEMM_BLOCK_ROWS)
+    return ops_launch<quantize_tile_kernel<false, true, T>>(grid, 256, 0, 1, s, a);
+  if (transpose) return ops_launch<quantize_tile_kernel<true, true, T>>(grid, 256, 0, 1, s, a);
+  return ops_launch<quantize_tile_kernel<true, false, T>>(grid, 256, 0, 1, s, a);
+}
+
 }  // namespace
 }  // namespace g12
 
@@ -260,18 +262,19 @@ extern "C" gemm_status_t gemm_fp8_quantize(int64_t rows, int64_t cols, const voi
     if (ctas > fit) ctas = (ctas + kRowUnits - 1) / kRowUnits > fit ? fit : (ctas + kRowUnits - 1) / kRowUnits;
     const dim3 grid(static_cast<unsigned>(ctas));
     const bool vec = a.x_vec && cols % 8 == 0 && !ops_misaligned(q, 8) && ldq % 8 == 0;
-    return abi_from_cuda(vec ? ops_launch<quantize_rows_kernel<true>>(grid, 256, 0, 1, s, a)
-                             : ops_launch<quantize_rows_kernel<false>>(grid, 256, 0, 1, s, a));
+    cudaError_t e;
+    if (!vec)
+      e = ops_launch<quantize_rows_kernel<false, kAnyType>>(grid, 256, 0, 1, s, a);
+    else if (x_type == GEMM_OUT_BF16)
+      e = ops_launch<quantize_rows_kernel<true, GEMM_OUT_BF16>>(grid, 256, 0, 1, s, a);
+    else
+      e = ops_launch<quantize_rows_kernel<true, GEMM_OUT_F32>>(grid, 256, 0, 1, s, a);
+    return abi_from_cuda(e);
   }
   const int64_t tiles = ((rows + 127) / 128) * ((cols + 127) / 128);
   const int64_t fit = static_cast<int64_t>(sms) * 2;
   const dim3 grid(static_cast<unsigned>(tiles < fit ? tiles : fit));
-  cudaError_t e;
-  if (block == GEMM_BLOCK_ROWS)
-    e = ops_launch<quantize_tile_kernel<false, true>>(grid, 256, 0, 1, s, a);
-  else if (transpose)
-    e = ops_launch<quantize_tile_kernel<true, true>>(grid, 256, 0, 1, s, a);
-  else
-    e = ops_launch<quantize_tile_kernel<true, false>>(grid, 256, 0, 1, s, a);
-  return abi_from_cuda(e);
+  return abi_from_cuda(x_type == GEMM_OUT_BF16
+                           ? launch_tiles<GEMM_OUT_BF16>(a, block, transpose != 0, grid, s)
+                           : launch_tiles<GEMM_OUT_F32>(a, block, transpose != 0, grid, s));
 }

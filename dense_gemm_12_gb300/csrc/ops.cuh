@@ -46,18 +46,22 @@ inline int float_type_bytes(int type) {
   return type == GEMM_OUT_F32 ? 4 : (type == GEMM_OUT_BF16 ? 2 : 0);
 }
 
-// Sets a kernel's dynamic shared memory limit, once per device.
+// Raises a kernel's dynamic shared memory limit to at least `bytes` (once per
+// device and size; the limit only ever grows).
 template <auto Kernel>
 cudaError_t ops_allow_smem(size_t bytes) {
-  static std::atomic<uint64_t> done{0};  // one bit per device
+  static std::mutex mutex;
+  static std::atomic<size_t> limit[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
-  if ((done.load(std::memory_order_relaxed) & bit) != 0) return cudaSuccess;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (limit[dev].load(std::memory_order_acquire) >= bytes) return cudaSuccess;
+  std::lock_guard<std::mutex> lock(mutex);
+  if (limit[dev].load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
   e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(bytes));
-  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  if (e == cudaSuccess) limit[dev].store(bytes, std::memory_order_release);
   return e;
 }
 
@@ -100,6 +104,23 @@ __device__ __forceinline__ float finite_abs(float v) {
   return a <= FLT_MAX ? a : 0.0f;
 }
 
+// Largest finite magnitude of eight values over the 16 lanes of a block; all
+// 32 lanes call it together.  fmaxf passes over NaN; infinities are rare, and
+// only when one shows up are the values looked at one by one.
+__device__ __forceinline__ float block_amax(const float (&v)[8]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+  if (__any_sync(0xffffffffu, m > FLT_MAX)) {
+    m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, finite_abs(v[i]));
+  }
+#pragma unroll
+  for (int s = 8; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+  return m;
+}
+
 // Scale of a block whose largest finite magnitude is amax, and the factor
 // that its values are multiplied by before rounding.  The factor is one
 // correctly rounded quotient, so a value's product with it has the same two
@@ -119,26 +140,21 @@ __device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d
 }
 
 // ------------------------------------------------ eight elements of a row
-// Vector forms: 16-byte aligned pieces.  Strided forms: elements c, c + 16,
-// ..., c + 112 of a 128-column block, so that the 16 lanes of a block read
-// consecutive elements; those at or past `n` read as zero and are not
-// written.  Loads are marked as read once (evict first).
-__device__ __forceinline__ void load8_vec(const void* p, int type, int64_t at, float (&v)[8]) {
-  if (type == GEMM_OUT_BF16) {
-    const uint4 u = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + at));
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  } else {
-    const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
-    const float4 a = __ldcs(f), b = __ldcs(f + 1);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  }
-}
+// A thread moves eight elements of a row at a time.  Vector form: they are
+// consecutive, 16-byte aligned.  Strided form (rows that cannot be moved in
+// vectors): elements c, c + 16, ..., c + 112 of a 128-column block, so that
+// the 16 lanes of a block read consecutive elements; those at or past `n` read
+// as zero and are not written.  Loading (Raw8) and widening are apart, so that
+// a thread's loads are all on their way before the first is used, and are
+// marked as read once (evict first).
+//
+// T: GEMM_OUT_F32, GEMM_OUT_BF16, or kAnyType for a type known at run time.
+constexpr int kAnyType = 2;
+
+template <int T>
+struct Raw8 {
+  uint32_t w[T == GEMM_OUT_BF16 ? 4 : 8];
+};
 
 __device__ __forceinline__ float load1(const void* p, int type, int64_t at) {
   return type == GEMM_OUT_BF16 ? __bfloat162float(__ldcs(static_cast<const __nv_bfloat16*>(p) + at))
@@ -152,10 +168,51 @@ __device__ __forceinline__ void store1(void* p, int type, int64_t at, float v) {
     static_cast<float*>(p)[at] = v;
 }
 
-__device__ __forceinline__ void load8_strided(const void* p, int type, int64_t row_at, int c, int n,
-                                              float (&v)[8]) {
+template <int T>
+__device__ __forceinline__ Raw8<T> load8_vec(const void* p, int type, int64_t at) {
+  Raw8<T> r;
+  const bool half = T == GEMM_OUT_BF16 || (T == kAnyType && type == GEMM_OUT_BF16);
+  const uint4* src = half ? reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + at)
+                          : reinterpret_cast<const uint4*>(static_cast<const float*>(p) + at);
+  const uint4 a = __ldcs(src);
+  r.w[0] = a.x; r.w[1] = a.y; r.w[2] = a.z; r.w[3] = a.w;
+  if constexpr (T != GEMM_OUT_BF16) {
+    uint4 b = make_uint4(0u, 0u, 0u, 0u);
+    if (!half) b = __ldcs(src + 1);
+    r.w[4] = b.x; r.w[5] = b.y; r.w[6] = b.z; r.w[7] = b.w;
+  }
+  return r;
+}
+
+template <int T>
+__device__ __forceinline__ void widen_vec(const Raw8<T>& r, int type, float (&v)[8]) {
+  if (T == GEMM_OUT_BF16 || (T == kAnyType && type == GEMM_OUT_BF16)) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = c + 16 * i < n ? load1(p, type, row_at + c + 16 * i) : 0.0f;
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(r.w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(r.w[i] & 0xffff0000u);
+    }
+  } else if constexpr (T != GEMM_OUT_BF16) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r.w[i]);
+  }
+}
+
+// Strided forms (types at run time): the raw words are already fp32.
+__device__ __forceinline__ Raw8<kAnyType> load8_strided(const void* p, int type, int64_t row_at,
+                                                        int c, int n) {
+  Raw8<kAnyType> r;
+  if (type == GEMM_OUT_BF16) {
+    const unsigned short* src = static_cast<const unsigned short*>(p) + row_at;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      r.w[i] = c + 16 * i < n ? static_cast<uint32_t>(__ldcs(src + c + 16 * i)) << 16 : 0u;
+  } else {
+    const uint32_t* src = static_cast<const uint32_t*>(p) + row_at;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.w[i] = c + 16 * i < n ? __ldcs(src + c + 16 * i) : 0u;
+  }
+  return r;
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
@@ -182,6 +239,53 @@ __device__ __forceinline__ void store8_strided(void* p, int type, int64_t row_at
     if (c + 16 * i < n) store1(p, type, row_at + c + 16 * i, v[i]);
 }
 
+// Eight consecutive elements from shared memory (16-byte aligned).
+template <int T>
+__device__ __forceinline__ Raw8<T> load8_smem(const uint8_t* row, int c) {
+  static_assert(T != kAnyType, "the type is known");
+  Raw8<T> r;
+  const uint4* src = reinterpret_cast<const uint4*>(row + c * (T == GEMM_OUT_BF16 ? 2 : 4));
+  const uint4 a = src[0];
+  r.w[0] = a.x; r.w[1] = a.y; r.w[2] = a.z; r.w[3] = a.w;
+  if constexpr (T != GEMM_OUT_BF16) {
+    const uint4 b = src[1];
+    r.w[4] = b.x; r.w[5] = b.y; r.w[6] = b.z; r.w[7] = b.w;
+  }
+  return r;
+}
+
+// Either form, zero where `in` is false.
+template <bool VEC, int T>
+__device__ __forceinline__ Raw8<T> load8(const void* p, int type, int64_t row_at, int c, int n,
+                                         bool in) {
+  Raw8<T> r{};
+  if constexpr (VEC) {
+    if (in) r = load8_vec<T>(p, type, row_at + c);
+  } else {
+    if (in) r = load8_strided(p, type, row_at, c, n);
+  }
+  return r;
+}
+
+template <bool VEC, int T>
+__device__ __forceinline__ void widen8(const Raw8<T>& r, int type, float (&v)[8]) {
+  if constexpr (VEC) {
+    widen_vec<T>(r, type, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r.w[i]);
+  }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store8(void* p, int type, int64_t row_at, int c, int n,
+                                       const float (&v)[8]) {
+  if (VEC)
+    store8_vec(p, type, row_at + c, v);
+  else
+    store8_strided(p, type, row_at, c, n, v);
+}
+
 // --------------------------------------------------------- PTX additions
 // 3-D tiled copy global -> shared; x is the innermost coordinate.
 __device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, int32_t x,
@@ -190,6 +294,17 @@ __device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* m
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(smem_dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// Contiguous copy global -> shared; both addresses 16-byte aligned, `bytes` a
+// multiple of 16, counted on `bar`.
+__device__ __forceinline__ void bulk_load(void* smem_dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(smem_dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
       : "memory");
 }
 

@@ -601,8 +601,7 @@ gemm_status_t gemm_rmsnorm(int64_t rows, int64_t dim, const gemm_rmsnorm_t *args
  * h and rstd are the forward pass's; residual_grad is the gradient that
  * reaches h along the skip connection, or NULL.  dweight (dim fp32 values,
  * overwritten; zeros for rows == 0) may be NULL.  dh may take the place of dy,
- * h or residual_grad of the same type and leading dimension for dim <= 16384,
- * and for any dim without dweight.
+ * h or residual_grad of the same type and leading dimension.
  */
 typedef struct {
     const void *dy;             /* rows x dim                                    */

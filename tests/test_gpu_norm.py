@@ -180,7 +180,21 @@ def test_backward_against_differences(dim):
         assert abs(num - float((dw.double() * f).sum())) <= ((dim / 32 + 128) * U32 + 1e-9) * size
 
 
-def test_backward_in_place_without_weight_gradient_and_without_rows():
+@pytest.mark.parametrize("dim", [768, 10000, 20000])
+def test_backward_in_place(dim):
+    x, dy, c = randn(40, dim, seed=16), randn(40, dim, seed=17), randn(40, dim, seed=18)
+    w, rstd = 1.0 + randn(dim, seed=19, scale=0.2), torch.empty(40, device="cuda")
+    g.rmsnorm(x, w, eps=EPS, rstd=rstd)
+    dh, dw = torch.empty_like(x), torch.empty(dim, device="cuda")
+    g.rmsnorm_backward(dy, x, w, rstd, dh, dw, residual_grad=c)
+    for which in range(3):  # over dy, h, residual_grad
+        args = [dy.clone(), x.clone(), c.clone()]
+        dw2 = torch.empty_like(dw)
+        g.rmsnorm_backward(args[0], args[1], w, rstd, args[which], dw2, residual_grad=args[2])
+        assert torch.equal(args[which], dh) and torch.equal(dw2, dw)
+
+
+def test_backward_without_weight_gradient_and_without_rows():
     x, dy, c = randn(40, 768, seed=16), randn(40, 768, seed=17), randn(40, 768, seed=18)
     w, rstd = 1.0 + randn(768, seed=19, scale=0.2), torch.empty(40, device="cuda")
     g.rmsnorm(x, w, eps=EPS, rstd=rstd)
@@ -188,9 +202,6 @@ def test_backward_in_place_without_weight_gradient_and_without_rows():
     g.rmsnorm_backward(dy, x, w, rstd, dh, dw, residual_grad=c)
     over = c.clone()
     g.rmsnorm_backward(dy, x, w, rstd, over, residual_grad=over)
-    assert torch.equal(over, dh)
-    over = dy.clone()
-    g.rmsnorm_backward(over, x, w, rstd, over, residual_grad=c)
     assert torch.equal(over, dh)
     none = torch.empty(0, 768, device="cuda")
     g.rmsnorm_backward(none, none, w, torch.empty(0, device="cuda"), none, dw)
