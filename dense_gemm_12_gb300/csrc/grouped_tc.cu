@@ -111,12 +111,57 @@ __device__ __forceinline__ Item item_of(const GroupedArgs& p, const GroupTable& 
   return w;
 }
 
-// 32 accumulator rows x 32 columns of this warp: turned around in its 4 KB of
-// shared memory (16-byte pieces XOR-swizzled by row), then 8 lanes cover a
-// row's 32 columns.
-__device__ __forceinline__ void write_chunk(const GroupedArgs& p, float4* stg, const uint32_t (&r)[32],
-                                            float alpha, void* D, int64_t row_base, int rows,
-                                            int col0) {
+// 32 accumulator rows x 64 columns of this warp (r, s: 32 columns each) as
+// bf16: packed in registers, turned around in the warp's 4 KB of shared memory
+// (128-byte rows, 16-byte pieces XOR-swizzled by row) and written with 8 lanes
+// to a row.  All pieces are read back before the first is stored: a load after
+// a store to a possibly aliasing address could not be issued early.
+__device__ __forceinline__ void write_bf16(const GroupedArgs& p, uint4* stg, const uint32_t (&r)[32],
+                                           const uint32_t (&s)[32], float alpha, __nv_bfloat16* D,
+                                           int64_t row_base, int rows, int col0) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int k = (q & 3) * 8 + 2 * i;
+      w[i] = q < 4 ? pack_bf16(alpha * __uint_as_float(r[k]), alpha * __uint_as_float(r[k + 1]))
+                   : pack_bf16(alpha * __uint_as_float(s[k]), alpha * __uint_as_float(s[k + 1]));
+    }
+    stg[lane * 8 + (q ^ (lane & 7))] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __syncwarp();
+  const int piece = lane & 7, rl = lane >> 3;
+  const int col = col0 + 8 * piece;
+  uint4 v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = stg[(i * 4 + rl) * 8 + (piece ^ ((i * 4 + rl) & 7))];
+  __nv_bfloat16* d = D + (row_base + rl) * p.ldd + col;
+  if (col + 8 <= p.N && p.d_vec) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i * 4 + rl < rows) *reinterpret_cast<uint4*>(d + i * 4 * p.ldd) = v[i];
+  } else {
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+      if (i * 4 + rl >= rows) break;
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (col + k < p.N)
+          reinterpret_cast<uint16_t*>(d + i * 4 * p.ldd)[k] =
+              static_cast<uint16_t>(w[k >> 1] >> (16 * (k & 1)));
+    }
+  }
+  __syncwarp();
+}
+
+// 32 accumulator rows x 32 columns of this warp in fp32 through the same 4 KB,
+// where D is fp32 or read as well (beta != 0): 4 columns per lane.  The old
+// values of D are read before the first store.
+__device__ __forceinline__ void write_any(const GroupedArgs& p, float4* stg, const uint32_t (&r)[32],
+                                          float alpha, void* D, int64_t row_base, int rows, int col0) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int q = 0; q < 8; ++q)
@@ -124,35 +169,95 @@ __device__ __forceinline__ void write_chunk(const GroupedArgs& p, float4* stg, c
         make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
                     __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]));
   __syncwarp();
-  const int ch = lane & 7;
+  const int ch = lane & 7, rl = lane >> 3;
   const int col = col0 + 4 * ch;
   const bool whole = col + 4 <= p.N && p.d_vec;
+  float4 v[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int rr = i * 4 + (lane >> 3);
-    if (rr >= rows || col >= p.N) continue;
-    const float4 s = stg[rr * 8 + (ch ^ (rr & 7))];
-    float v[4] = {alpha * s.x, alpha * s.y, alpha * s.z, alpha * s.w};
-    const int64_t at = (row_base + rr) * p.ldd + col;
-    if (p.beta != 0.0f) {
+    const int rr = i * 4 + rl;
+    const float4 a = stg[rr * 8 + (ch ^ (rr & 7))];
+    v[i] = make_float4(alpha * a.x, alpha * a.y, alpha * a.z, alpha * a.w);
+  }
+  const int64_t at0 = (row_base + rl) * p.ldd + col, step = 4 * p.ldd;
+  if (p.beta != 0.0f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i * 4 + rl >= rows) continue;
+      float o[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        if (col + k < p.N) v[k] = fmaf(p.beta, load1(D, p.d_type, at + k), v[k]);
+        o[k] = col + k < p.N ? load1(D, p.d_type, at0 + i * step + k) : 0.0f;
+      v[i] = make_float4(fmaf(p.beta, o[0], v[i].x), fmaf(p.beta, o[1], v[i].y),
+                         fmaf(p.beta, o[2], v[i].z), fmaf(p.beta, o[3], v[i].w));
     }
-    if (whole) {
-      if (p.d_type == GEMM_OUT_F32)
-        *reinterpret_cast<float4*>(static_cast<float*>(D) + at) = make_float4(v[0], v[1], v[2], v[3]);
-      else
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(D) + at) =
-            make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-    } else {
+  }
+  if (whole && p.d_type == GEMM_OUT_F32) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i * 4 + rl < rows)
+        *reinterpret_cast<float4*>(static_cast<float*>(D) + at0 + i * step) = v[i];
+  } else if (whole) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i * 4 + rl < rows)
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(D) + at0 + i * step) =
+            make_uint2(pack_bf16(v[i].x, v[i].y), pack_bf16(v[i].z, v[i].w));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i * 4 + rl >= rows) continue;
+      const float w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        if (col + k < p.N) store1(D, p.d_type, at + k, v[k]);
+        if (col + k < p.N) store1(D, p.d_type, at0 + i * step + k, w[k]);
     }
   }
   __syncwarp();
 }
+
+// The 32 rows x 256 columns of this warp (fewer at the edges).  load(c, r):
+// columns 32 c .. 32 c + 31 of its rows.
+template <typename Load>
+__device__ __forceinline__ void write_tile(const GroupedArgs& p, uint8_t* stg, float alpha, void* D,
+                                           int64_t row_base, int rows, int col0, Load load) {
+  const int chunks = min(BN / 32, (p.N - col0 + 31) / 32);
+  if (p.d_type == GEMM_OUT_BF16 && p.beta == 0.0f) {
+#pragma unroll 1
+    for (int c = 0; c < chunks; c += 2) {
+      uint32_t r[32], s[32];
+      load(c, r);
+      load(c + 1, s);  // past the last chunk: columns that are not written
+      load.wait();
+      write_bf16(p, reinterpret_cast<uint4*>(stg), r, s, alpha, static_cast<__nv_bfloat16*>(D),
+                 row_base, rows, col0 + c * 32);
+    }
+    return;
+  }
+#pragma unroll 1
+  for (int c = 0; c < chunks; ++c) {
+    uint32_t r[32];
+    load(c, r);
+    load.wait();
+    write_any(p, reinterpret_cast<float4*>(stg), r, alpha, D, row_base, rows, col0 + c * 32);
+  }
+}
+
+struct FromTmem {
+  uint32_t taddr;
+  __device__ __forceinline__ void operator()(int c, uint32_t (&r)[32]) const {
+    tmem_ld_32x32b_x32(taddr + c * 32, r);
+  }
+  __device__ __forceinline__ void wait() const { tc_wait_ld(); }
+};
+
+struct Zeros {
+  __device__ __forceinline__ void operator()(int, uint32_t (&r)[32]) const {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) r[i] = 0u;
+  }
+  __device__ __forceinline__ void wait() const {}
+};
 
 template <int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -248,7 +353,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    // -------------------------------------- MMA issuer (lane 0 of the warp)
+    // -------------------------------------------------------- MMA issuer
+    // K-major: 8-row groups 1024 B apart, a K step of 16 is 32 B.  MN-major:
+    // 64-wide boxes 8 KB apart (LBO), 8-row k groups 1024 B apart (SBO), a K
+    // step of 16 rows is 2048 B.
+    const uint32_t sa0 = smem_u32(smem), sb0 = sa0 + kStageBytesA;
+    const uint64_t da0 = kGrad ? smem_desc_sw128(sa0, kBoxBytes, 1024) : smem_desc_sw128(sa0, 16, 1024);
+    const uint64_t db0 = MODE == kTransB ? smem_desc_sw128(sb0, 16, 1024)
+                                         : smem_desc_sw128(sb0, kBoxBytes, 1024);
+    constexpr uint32_t kStepA = (kGrad ? 2048 : 32) >> 4, kStepB = (MODE == kTransB ? 32 : 2048) >> 4;
     uint32_t it = 0, j = 0;
     int g = 0;
     bool ok = true, issued = false;
@@ -284,40 +397,33 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
         }
-        if (lane == 0) {
-          tc_fence_after_sync();
-          const uint32_t sa = smem_u32(stage);
-          const uint32_t sb = sa + kStageBytesA;
+        tc_fence_after_sync();
+        const uint64_t at = static_cast<uint64_t>(s * (kStageBytes >> 4));
+        if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk) {
-            // K-major: 8-row groups 1024 B apart, a K step of 16 is 32 B.
-            // MN-major: 64-wide boxes 8 KB apart (LBO), 8-row k groups 1024 B
-            // apart (SBO), a K step of 16 rows is 2048 B.
-            const uint64_t adesc = kGrad ? smem_desc_sw128(sa + kk * 2048, kBoxBytes, 1024)
-                                         : smem_desc_sw128(sa + kk * 32, 16, 1024);
-            const uint64_t bdesc = MODE == kTransB ? smem_desc_sw128(sb + kk * 32, 16, 1024)
-                                                   : smem_desc_sw128(sb + kk * 2048, kBoxBytes, 1024);
-            tc_mma_f16(d_tmem, adesc, bdesc, kIdesc, (kb != 0 || kk != 0) ? 1u : 0u);
-          }
+          for (int kk = 0; kk < BK / 16; ++kk)
+            tc_mma_f16(d_tmem, da0 + at + kk * kStepA, db0 + at + kk * kStepB, kIdesc,
+                       (kb != 0 || kk != 0) ? 1u : 0u);
           tc_commit(&tail->empty[s]);
         }
         issued = true;
         __syncwarp();
       }
       if (!ok) break;
-      if (lane == 0) tc_commit(&tail->tmem_full[ab]);
+      if (elect_one()) tc_commit(&tail->tmem_full[ab]);
       __syncwarp();
     }
-    if (!ok && issued && lane == 0) {
-      // Let every MMA this thread issued finish before TMEM is released.
-      tc_commit(&tail->drain);
+    if (!ok && issued) {
+      // Let every MMA this warp issued finish before TMEM is released.
+      if (elect_one()) tc_commit(&tail->drain);
+      __syncwarp();
       mbar_drain_wait(&tail->drain, 0);
     }
     __syncwarp();
   } else {
     // -------------------------------------------------------------- output
     const int quarter = warp & 3;  // TMEM lanes this warp may access
-    float4* stg = reinterpret_cast<float4*>(out_stage + quarter * kOutWarpBytes);
+    uint8_t* stg = out_stage + quarter * kOutWarpBytes;
     uint32_t j = 0;
     int g = 0;
     for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
@@ -331,16 +437,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         D = p.d_type == GEMM_OUT_F32 ? static_cast<void*>(static_cast<float*>(D) + at)
                                      : static_cast<void*>(static_cast<__nv_bfloat16*>(D) + at);
       }
-      const int chunks = min(BN / 32, (p.N - w.tn * BN + 31) / 32);
       if (w.num_kb == 0) {
-        uint32_t zero[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) zero[i] = 0u;
-        if (rows > 0) {
-#pragma unroll 1
-          for (int c = 0; c < chunks; ++c)
-            write_chunk(p, stg, zero, 0.0f, D, row_base, rows, w.tn * BN + c * 32);
-        }
+        if (rows > 0) write_tile(p, stg, 0.0f, D, row_base, rows, w.tn * BN, Zeros{});
         continue;
       }
       const uint32_t ab = j & 1u, ar = j >> 1;
@@ -350,15 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (named_bar_any(kOutBarAny, kOutThreads, !ok)) break;
       tc_fence_after_sync();
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + ab * BN;
-      if (rows > 0) {
-#pragma unroll 1
-        for (int c = 0; c < chunks; ++c) {
-          uint32_t r[32];
-          tmem_ld_32x32b_x32(taddr + c * 32, r);
-          tmem_wait_ld(r);
-          write_chunk(p, stg, r, p.alpha, D, row_base, rows, w.tn * BN + c * 32);
-        }
-      }
+      if (rows > 0) write_tile(p, stg, p.alpha, D, row_base, rows, w.tn * BN, FromTmem{taddr});
       tc_fence_before_sync();
       mbar_arrive(&tail->tmem_empty[ab]);
     }
