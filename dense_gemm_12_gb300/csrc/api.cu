@@ -605,7 +605,8 @@ gemm_status_t abi_stage(cudaStream_t stream, int64_t bytes, std::unique_lock<std
 }
 
 bool abi_encode_tiled(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base,
-                      const int64_t* dims, const int64_t* strides, const uint32_t* box) {
+                      const int64_t* dims, const int64_t* strides, const uint32_t* box,
+                      CUtensorMapSwizzle swizzle) {
   EncodeTiledFn enc = encode_fn();
   if (enc == nullptr || rank < 2 || rank > 3) return false;
   cuuint64_t d[3], t[2];
@@ -616,7 +617,7 @@ bool abi_encode_tiled(CUtensorMap* map, CUtensorMapDataType type, int rank, cons
     if (i > 0) t[i - 1] = static_cast<cuuint64_t>(strides[i - 1]);
   }
   return enc(map, type, static_cast<cuuint32_t>(rank), const_cast<void*>(base), d, t, b, e,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

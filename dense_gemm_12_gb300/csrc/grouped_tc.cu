@@ -24,11 +24,14 @@ namespace g12 {
 namespace {
 
 constexpr int BM = 128, BN = 256, BK = 64;
-constexpr int STAGES = 4;
+constexpr int kRingBytes = 192 * 1024;
 constexpr int kStageBytesA = BM * BK * 2;
-constexpr int kStageBytesB = BK * BN * 2;
 constexpr int kBoxBytes = BK * 64 * 2;  // one MN-major box: 64 of M or N, 64 of k
-constexpr int kStageBytes = kStageBytesA + kStageBytesB;
+// A pair's CTAs hold half of the tile's B each.
+constexpr int b_cols(bool pair) { return pair ? BN / 2 : BN; }
+constexpr int stage_bytes(bool pair) { return kStageBytesA + BK * b_cols(pair) * 2; }  // 48 or 32 KB
+constexpr int ring_stages(bool pair) { return kRingBytes / stage_bytes(pair); }        // 4 or 6
+constexpr int kMaxStages = 6;
 constexpr int kThreads = 192;
 constexpr int kOutThreads = 128;
 constexpr uint32_t kTmemCols = 512;
@@ -49,13 +52,14 @@ struct GroupedArgs {
   int d_type, d_vec;
   int tile_rows;        // rows of A per tile (not kWeightGrad)
   int band;
+  int d_tma;            // beta == 0 and TMA can describe D: whole pieces leave by TMA
   int product;          // 0: alpha == 0 or K == 0, operands are not read
   uint32_t* err;
 };
 
 struct __align__(8) Tail {
-  uint64_t full[STAGES];
-  uint64_t empty[STAGES];
+  uint64_t full[kMaxStages];
+  uint64_t empty[kMaxStages];
   uint64_t tmem_full[2];
   uint64_t tmem_empty[2];
   uint64_t drain;
@@ -64,7 +68,7 @@ struct __align__(8) Tail {
   GroupTable groups;
 };
 
-constexpr size_t kSmemBytes = 1024 + STAGES * kStageBytes + 4 * kOutWarpBytes + sizeof(Tail);
+constexpr size_t kSmemBytes = 1024 + kRingBytes + 4 * kOutWarpBytes + sizeof(Tail);
 static_assert(kSmemBytes <= 227 * 1024, "grouped kernel shared memory");
 
 // One work item: its k-blocks, where its rows (or, for the weight gradient,
@@ -78,17 +82,18 @@ struct Item {
   int last;      // weight gradient: rows of the last k-block
 };
 
-template <int MODE>
+template <int MODE, bool PAIR>
 __device__ __forceinline__ Item item_of(const GroupedArgs& p, const GroupTable& tab, int t,
-                                        int tiles_n, int num_kb, int& g) {
+                                        int tiles_n, int num_kb, int rank, int& g) {
   Item w;
   if (MODE != kWeightGrad) {
     const GroupTile f = group_tile(tab, t, tiles_n, p.band, p.tile_rows, g);
     w.group = f.group;
     w.tn = f.tn;
-    w.row0 = f.row0;
+    // of a pair's 256 rows the CTA takes 128, perhaps none
+    w.row0 = f.row0 + (PAIR ? rank * BM : 0);
     w.m0 = 0;
-    w.rows = f.rows;
+    w.rows = PAIR ? min(f.rows - rank * BM, BM) : f.rows;
     w.num_kb = num_kb;
     w.last = BK;
     return w;
@@ -216,6 +221,61 @@ __device__ __forceinline__ void write_any(const GroupedArgs& p, float4* stg, con
   __syncwarp();
 }
 
+// The same where TMA can describe D and beta is 0: pieces of 32 rows x 64
+// bytes (32 columns of bf16, or 16 of fp32) are scaled and packed in registers,
+// written to one of the warp's two 2 KB buffers (16-byte pieces XOR-swizzled as
+// the tensor map's 64-byte swizzle has them) and stored by one TMA copy, which
+// the map clips at D's edges.  The next 32 accumulator columns are read
+// meanwhile.  seq: pieces so far; a buffer is rewritten once the copy two
+// pieces back has read it.  row, z: coordinates of the first row.
+__device__ __forceinline__ void stage_piece(const CUtensorMap* tmD, uint32_t stg, uint32_t& seq,
+                                            const uint32_t (&w)[16], int col, int row, int z) {
+  const uint32_t lane = threadIdx.x & 31;
+  if (lane == 0) bulk_wait_group_read<1>();
+  __syncwarp();
+  const uint32_t buf = stg + (seq & 1u) * 2048u;
+  ++seq;
+#pragma unroll
+  for (uint32_t q = 0; q < 4; ++q)
+    st_shared_u4(buf + lane * 64u + ((q ^ ((lane >> 1) & 3u)) << 4), w[4 * q], w[4 * q + 1],
+                 w[4 * q + 2], w[4 * q + 3]);
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_3d(tmD, buf, col, row, z);
+    bulk_commit_group();
+  }
+}
+
+__device__ __forceinline__ void write_tma(const GroupedArgs& p, const CUtensorMap* tmD, uint32_t taddr,
+                                          uint32_t stg, uint32_t& seq, int row, int z, int col0) {
+  const int chunks = min(BN / 32, (p.N - col0 + 31) / 32);
+  uint32_t r[32], next[32];
+  tmem_ld_32x32b_x32(taddr, next);
+#pragma unroll 1
+  for (int c = 0; c < chunks; ++c) {
+    tmem_wait_ld(next);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) r[i] = next[i];
+    if (c + 1 < chunks) tmem_ld_32x32b_x32(taddr + (c + 1) * 32, next);
+    uint32_t w[16];
+    if (p.d_type == GEMM_OUT_BF16) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        w[i] = pack_bf16(p.alpha * __uint_as_float(r[2 * i]), p.alpha * __uint_as_float(r[2 * i + 1]));
+      stage_piece(tmD, stg, seq, w, col0 + c * 32, row, z);
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          w[i] = __float_as_uint(p.alpha * __uint_as_float(r[16 * h + i]));
+        if (col0 + c * 32 + h * 16 < p.N) stage_piece(tmD, stg, seq, w, col0 + c * 32 + h * 16, row, z);
+      }
+    }
+  }
+}
+
 // The 32 rows x 256 columns of this warp (fewer at the edges).  load(c, r):
 // columns 32 c .. 32 c + 31 of its rows.
 template <typename Load>
@@ -259,20 +319,31 @@ struct Zeros {
   __device__ __forceinline__ void wait() const {}
 };
 
-template <int MODE>
+// PAIR (not for the weight gradient): two CTAs share a 256 x 256 tile and one
+// stream of M = 256 MMAs, barriers as in the dense pair kernel (bf16_tc.cu).
+// Each SM's shared memory then takes 32 KB of operands per k-block and gives
+// the tensor core as much, instead of 48 KB each way: with one CTA per tile
+// that traffic (768 cycles at 128 B per cycle) outlasts the MMAs (512).
+template <int MODE, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_kernel(const __grid_constant__ GroupedArgs p, const __grid_constant__ CUtensorMap tmA,
-                   const __grid_constant__ CUtensorMap tmB) {
+                   const __grid_constant__ CUtensorMap tmB,
+                   const __grid_constant__ CUtensorMap tmD) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = align_smem<1024>(smem_raw);
-  uint8_t* out_stage = smem + STAGES * kStageBytes;
+  uint8_t* out_stage = smem + kRingBytes;
   Tail* tail = reinterpret_cast<Tail*>(out_stage + 4 * kOutWarpBytes);
-  volatile int* abort_flag = &tail->abort_flag;
+  int* abort_flag = &tail->abort_flag;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   constexpr bool kGrad = MODE == kWeightGrad;
+  static_assert(!(kGrad && PAIR), "the weight gradient runs on single CTAs");
+  constexpr int STAGES = ring_stages(PAIR), kStageBytes = stage_bytes(PAIR);
+  const int rank = PAIR ? static_cast<int>(cluster_cta_rank() & 1u) : 0;
+  const int first = static_cast<int>(blockIdx.x) / (PAIR ? 2 : 1);
+  const int stride = static_cast<int>(gridDim.x) / (PAIR ? 2 : 1);
   constexpr uint32_t kIdesc =
-      idesc_bf16_f32(BM, BN, /*A MN-major*/ kGrad ? 1 : 0, /*B MN-major*/ MODE == kTransB ? 0 : 1);
+      idesc_bf16_f32(PAIR ? 2 * BM : BM, BN, /*A MN-major*/ kGrad ? 1 : 0, /*B MN-major*/ MODE == kTransB ? 0 : 1);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -281,15 +352,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tail->tmem_full[b], 1);
-      mbar_init(&tail->tmem_empty[b], kOutThreads);
+      mbar_init(&tail->tmem_empty[b], (PAIR ? 2 : 1) * (kOutThreads / 32));
     }
     mbar_init(&tail->drain, 1);
     tail->abort_flag = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
-    tmem_alloc(&tail->tmem_base, kTmemCols);
-    tmem_relinquish_alloc_permit();
+    if (PAIR) {
+      tmem_alloc_pair(&tail->tmem_base, kTmemCols);
+      tmem_relinquish_alloc_permit_pair();
+    } else {
+      tmem_alloc(&tail->tmem_base, kTmemCols);
+      tmem_relinquish_alloc_permit();
+    }
   }
   // Everything above touches no global memory and may overlap the previous
   // kernel's last CTAs; every global access below follows its completion.
@@ -298,6 +374,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 2) build_groups(tail->groups, p.offsets, p.groups, p.rows, kGrad ? 1 : p.tile_rows);
   tc_fence_before_sync();
   __syncthreads();
+  // Both CTAs of a pair signal barriers of the even one: all must be
+  // initialised first.
+  if (PAIR) cluster_sync();
   tc_fence_after_sync();
   const uint32_t tmem_base = tail->tmem_base;
   const GroupTable& tab = tail->groups;
@@ -312,21 +391,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t it = 0;
       int g = 0;
       bool ok = true;
-      const uint32_t bytes =
-          static_cast<uint32_t>((kGrad ? kStageBytesA : p.tile_rows * BK * 2) + kStageBytesB);
-      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-        const Item w = item_of<MODE>(p, tab, t, tiles_n, num_kb, g);
+      const uint32_t bytes = PAIR ? 2u * kStageBytes
+                                  : static_cast<uint32_t>(((kGrad ? BM : p.tile_rows) + BN) * BK * 2);
+      const uint32_t full0 = PAIR ? mapa_shared(smem_u32(&tail->full[0]), 0) : 0u;
+      for (int t = first; t < tiles && ok; t += stride) {
+        const Item w = item_of<MODE, PAIR>(p, tab, t, tiles_n, num_kb, rank, g);
         for (int kb = 0; kb < w.num_kb; ++kb, ++it) {
           const uint32_t s = it % STAGES, round = it / STAGES;
-          if (!mbar_wait(&tail->empty[s], (round & 1u) ^ 1u, abort_flag, p.err)) {
+          if (!mbar_wait_late(&tail->empty[s], (round & 1u) ^ 1u, abort_flag, p.err)) {
             ok = false;
             break;
           }
           uint8_t* sa = smem + s * kStageBytes;
           uint8_t* sb = sa + kStageBytesA;
           uint64_t* bar = &tail->full[s];
-          mbar_arrive_expect_tx(bar, bytes);
-          if (kGrad) {
+          if (rank == 0) mbar_arrive_expect_tx(bar, bytes);
+          if (PAIR) {
+            const uint32_t full = full0 + s * static_cast<uint32_t>(sizeof(uint64_t));
+            const int n0 = w.tn * BN + rank * (BN / 2);
+            tma_load_2d_pair(sa, &tmA, kb * BK, w.row0, full);
+            if (MODE == kTransB) {
+              tma_load_3d_pair(sb, &tmB, kb * BK, n0, w.group, full);
+            } else {
+#pragma unroll
+              for (int j = 0; j < BN / 128; ++j)
+                tma_load_3d_pair(sb + j * kBoxBytes, &tmB, n0 + j * 64, kb * BK, w.group, full);
+            }
+          } else if (kGrad) {
             const int k = w.row0 + kb * BK;
 #pragma unroll
             for (int j = 0; j < BM / 64; ++j)
@@ -346,12 +437,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (!ok) {
+      if (PAIR) {
+        // Leave only after the MMAs have read every stage this CTA filled:
+        // then all of its copies have landed and every commit aimed at its
+        // barriers has arrived.
+        const uint64_t t0 = globaltimer_ns();
+        for (uint32_t j = it > STAGES ? it - STAGES : 0u; j < it; ++j)
+          while (!mbar_try_wait(&tail->empty[j % STAGES], (j / STAGES) & 1u))
+            if (globaltimer_ns() - t0 > kWaitLimitNs) break;
+      } else if (!ok) {
         for (uint32_t j = it > STAGES ? it - STAGES : 0u; j < it; ++j)
           mbar_drain_wait(&tail->full[j % STAGES], (j / STAGES) & 1u);
       }
     }
     __syncwarp();
+  } else if (warp == 1 && rank != 0) {
+    // the even CTA issues for both
   } else if (warp == 1) {
     // -------------------------------------------------------- MMA issuer
     // K-major: 8-row groups 1024 B apart, a K step of 16 is 32 B.  MN-major:
@@ -365,12 +466,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t it = 0, j = 0;
     int g = 0;
     bool ok = true, issued = false;
-    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-      const Item w = item_of<MODE>(p, tab, t, tiles_n, num_kb, g);
+    for (int t = first; t < tiles && ok; t += stride) {
+      const Item w = item_of<MODE, PAIR>(p, tab, t, tiles_n, num_kb, rank, g);
       if (w.num_kb == 0) continue;
       const uint32_t ab = j & 1u, ar = j >> 1;
       ++j;
-      bool got = mbar_wait(&tail->tmem_empty[ab], (ar & 1u) ^ 1u, abort_flag, p.err);
+      bool got = mbar_wait_late(&tail->tmem_empty[ab], (ar & 1u) ^ 1u, abort_flag, p.err);
       if (__any_sync(0xffffffffu, !got)) {
         ok = false;
         break;
@@ -379,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t d_tmem = tmem_base + ab * BN;
       for (int kb = 0; kb < w.num_kb; ++kb, ++it) {
         const uint32_t s = it % STAGES, round = it / STAGES;
-        got = mbar_wait(&tail->full[s], round & 1u, abort_flag, p.err);
+        got = mbar_wait_late(&tail->full[s], round & 1u, abort_flag, p.err);
         if (__any_sync(0xffffffffu, !got)) {
           ok = false;
           break;
@@ -401,21 +502,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t at = static_cast<uint64_t>(s * (kStageBytes >> 4));
         if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk)
-            tc_mma_f16(d_tmem, da0 + at + kk * kStepA, db0 + at + kk * kStepB, kIdesc,
-                       (kb != 0 || kk != 0) ? 1u : 0u);
-          tc_commit(&tail->empty[s]);
+          for (int kk = 0; kk < BK / 16; ++kk) {
+            if (PAIR)
+              tc_mma_f16_pair(d_tmem, da0 + at + kk * kStepA, db0 + at + kk * kStepB, kIdesc,
+                              (kb != 0 || kk != 0) ? 1u : 0u);
+            else
+              tc_mma_f16(d_tmem, da0 + at + kk * kStepA, db0 + at + kk * kStepB, kIdesc,
+                         (kb != 0 || kk != 0) ? 1u : 0u);
+          }
+          if (PAIR)
+            tc_commit_pair_multicast(&tail->empty[s], 0x3);
+          else
+            tc_commit(&tail->empty[s]);
         }
         issued = true;
         __syncwarp();
       }
       if (!ok) break;
-      if (elect_one()) tc_commit(&tail->tmem_full[ab]);
+      if (elect_one()) {
+        if (PAIR)
+          tc_commit_pair_multicast(&tail->tmem_full[ab], 0x3);
+        else
+          tc_commit(&tail->tmem_full[ab]);
+      }
       __syncwarp();
     }
-    if (!ok && issued) {
+    if (ok && PAIR) {
+      // no arrival of the odd CTA is still on its way at exit
+      for (uint32_t jj = j > 2 ? j - 2 : 0u; jj < j; ++jj)
+        if (!mbar_wait_late(&tail->tmem_empty[jj & 1u], (jj >> 1) & 1u, abort_flag, p.err)) break;
+    } else if (!ok && issued) {
       // Let every MMA this warp issued finish before TMEM is released.
-      if (elect_one()) tc_commit(&tail->drain);
+      if (elect_one()) {
+        if (PAIR)
+          tc_commit_pair(&tail->drain);
+        else
+          tc_commit(&tail->drain);
+      }
       __syncwarp();
       mbar_drain_wait(&tail->drain, 0);
     }
@@ -424,10 +547,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // -------------------------------------------------------------- output
     const int quarter = warp & 3;  // TMEM lanes this warp may access
     uint8_t* stg = out_stage + quarter * kOutWarpBytes;
-    uint32_t j = 0;
+    uint32_t j = 0, seq = 0;
     int g = 0;
-    for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-      const Item w = item_of<MODE>(p, tab, t, tiles_n, num_kb, g);
+    for (int t = first; t < tiles; t += stride) {
+      const Item w = item_of<MODE, PAIR>(p, tab, t, tiles_n, num_kb, rank, g);
       const int rows = min(w.rows - quarter * 32, 32);
       const int64_t row_base =
           (kGrad ? w.m0 : w.row0) + quarter * 32;
@@ -438,25 +561,83 @@ __global__ void __launch_bounds__(kThreads, 1)
                                      : static_cast<void*>(static_cast<__nv_bfloat16*>(D) + at);
       }
       if (w.num_kb == 0) {
+        if (p.d_tma) {
+          if (lane == 0) bulk_wait_group_read<0>();
+          __syncwarp();
+        }
         if (rows > 0) write_tile(p, stg, 0.0f, D, row_base, rows, w.tn * BN, Zeros{});
         continue;
       }
       const uint32_t ab = j & 1u, ar = j >> 1;
       ++j;
-      const bool ok = mbar_wait(&tail->tmem_full[ab], ar & 1u, abort_flag, p.err);
+      const bool ok = mbar_wait_late(&tail->tmem_full[ab], ar & 1u, abort_flag, p.err);
       // Leave together if a wait ran out anywhere (see named_bar_any).
       if (named_bar_any(kOutBarAny, kOutThreads, !ok)) break;
       tc_fence_after_sync();
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + ab * BN;
-      if (rows > 0) write_tile(p, stg, p.alpha, D, row_base, rows, w.tn * BN, FromTmem{taddr});
+      // a piece with rows of another group in it (not the weight gradient's:
+      // its matrices end where the map clips) is written row by row
+      if (p.d_tma && rows > 0 && (kGrad || rows == 32)) {
+        write_tma(p, &tmD, taddr, smem_u32(stg), seq, static_cast<int>(row_base),
+                  kGrad ? w.group : 0, w.tn * BN);
+      } else if (rows > 0) {
+        if (p.d_tma) {  // the copies from the staging area have read it
+          if (lane == 0) bulk_wait_group_read<0>();
+          __syncwarp();
+        }
+        write_tile(p, stg, p.alpha, D, row_base, rows, w.tn * BN, FromTmem{taddr});
+      }
       tc_fence_before_sync();
-      mbar_arrive(&tail->tmem_empty[ab]);
+      __syncwarp();
+      if (lane == 0) {
+        if (PAIR)
+          mbar_arrive_remote(mapa_shared(smem_u32(&tail->tmem_empty[ab]), 0));
+        else
+          mbar_arrive(&tail->tmem_empty[ab]);
+      }
     }
   }
+  if (warp >= 2 && p.d_tma && lane == 0) bulk_wait_group_all();  // the stores are complete
+  __syncwarp();
   tc_fence_before_sync();
   __syncthreads();
+  // Neither CTA of a pair releases TMEM or exits while the pair's MMAs or
+  // copies can still touch it.
+  if (PAIR) cluster_sync();
   tc_fence_after_sync();
-  if (warp == 1) tmem_dealloc(tmem_base, kTmemCols);
+  if (warp == 1) {
+    if (PAIR)
+      tmem_dealloc_pair(tmem_base, kTmemCols);
+    else
+      tmem_dealloc(tmem_base, kTmemCols);
+  }
+}
+
+// CTA pairs that can be resident at once on the current device; 0 if unknown.
+int max_pairs() {
+  static std::atomic<int> cache[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  const int known = cache[dev].load(std::memory_order_relaxed);
+  if (known != 0) return known;
+  int n = 0;
+  if (ops_allow_smem<grouped_kernel<kForward, true>>(kSmemBytes) == cudaSuccess) {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, grouped_kernel<kForward, true>, &cfg) != cudaSuccess) n = 0;
+  }
+  cudaGetLastError();
+  if (n > 0) cache[dev].store(n, std::memory_order_relaxed);
+  return n;
 }
 
 struct Operand {
@@ -506,6 +687,20 @@ cudaError_t stage(Operand& o, uint8_t* to, int num_sms, cudaStream_t s) {
   o.ld = ld2;
   o.stride = o.rows * ld2;
   return e;
+}
+
+// The map of D for write_tma: matrices of rows x cols.
+bool encode_output(CUtensorMap* tm, void* D, int d_type, int64_t rows, int64_t cols, int64_t ld,
+                   int64_t count, int64_t stride) {
+  const int bytes = float_type_bytes(d_type);
+  if (ops_misaligned(D, 16) || ld * bytes % 16 != 0 || (count > 1 && stride * bytes % 16 != 0))
+    return false;
+  const int64_t dims[3] = {cols, rows, count};
+  const int64_t strides[2] = {ld * bytes, (count > 1 ? stride : ld * rows) * bytes};
+  const uint32_t box[3] = {static_cast<uint32_t>(64 / bytes), 32, 1};
+  return abi_encode_tiled(tm, d_type == GEMM_OUT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                      : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                          3, D, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 bool bad_dim(int64_t v) { return v < 0 || v > kOpsMaxDim; }
@@ -580,26 +775,47 @@ gemm_status_t gemm_bf16gemm_grouped(int64_t G, const int32_t* offsets, int64_t r
   a.ldd = ldd;
   a.d_type = d_type;
   a.d_vec = !ops_misaligned(D, 16) && ldd % (16 / d_bytes) == 0;
-  a.tile_rows = rows > 64 ? 128 : (rows > 32 ? 64 : (rows > 16 ? 32 : 16));
+  // CTA pairs where their rounds of tiles take less time: a k-block takes a
+  // pair 512 cycles (its MMAs) and a single CTA 768 (operands through shared
+  // memory), and each group's last row tile is half full on average.
+  const int64_t tiles_n = (N + BN - 1) / BN;
+  const int64_t tiles_1 = (rows / BM + (G + 1) / 2) * tiles_n;
+  const int64_t tiles_2 = (rows / (2 * BM) + (G + 1) / 2) * tiles_n;
+  const int pairs = max_pairs();
+  const bool pair = pairs > 0 && 2 * ((tiles_2 + pairs - 1) / pairs) < 3 * ((tiles_1 + sms - 1) / sms);
+  a.tile_rows = pair ? 2 * BM : rows > 64 ? 128 : (rows > 32 ? 64 : (rows > 16 ? 32 : 16));
   a.band = 8;
   a.product = product ? 1 : 0;
   a.err = err;
   std::unique_lock<std::mutex> lock;
-  CUtensorMap tmA{}, tmB{};
+  CUtensorMap tmA{}, tmB{}, tmD{};
+  a.d_tma = product && beta == 0.0f && encode_output(&tmD, D, d_type, rows, N, ldd, 1, 0);
   if (product) {
-    const uint32_t box_a[2] = {BK, static_cast<uint32_t>(a.tile_rows)};
-    const uint32_t box_b[2] = {BK, static_cast<uint32_t>(transpose_b ? BN : BK)};
+    const uint32_t box_a[2] = {BK, static_cast<uint32_t>(pair ? BM : a.tile_rows)};
+    const uint32_t box_b[2] = {BK, static_cast<uint32_t>(transpose_b ? b_cols(pair) : BK)};
     st = operands(Operand{A, rows, K, lda, 1, 0}, Operand{B, brows, bcols, ldb, G, stride_b}, 3,
                   box_a, box_b, sms, s, lock, &tmA, &tmB);
     if (st != GEMM_OK) return st;
   }
   const int64_t row_tiles = (rows + a.tile_rows - 1) / a.tile_rows + (G < rows ? G : rows);
-  const int64_t tiles = row_tiles * ((N + BN - 1) / BN);
+  const int64_t tiles = row_tiles * tiles_n;
   if (tiles + sms > kOpsMaxDim) return GEMM_ERR_UNSUPPORTED;
+  if (pair) {
+    const dim3 grid(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs)));
+    return abi_from_cuda(
+        transpose_b
+            ? ops_launch<grouped_kernel<kTransB, true>>(grid, kThreads, kSmemBytes, 2, s, a, tmA, tmB,
+                                                           tmD)
+            : ops_launch<grouped_kernel<kForward, true>>(grid, kThreads, kSmemBytes, 2, s, a, tmA, tmB,
+                                                           tmD));
+  }
   const dim3 grid(static_cast<unsigned>(tiles < sms ? tiles : sms));
   return abi_from_cuda(
-      transpose_b ? ops_launch<grouped_kernel<kTransB>>(grid, kThreads, kSmemBytes, 1, s, a, tmA, tmB)
-                  : ops_launch<grouped_kernel<kForward>>(grid, kThreads, kSmemBytes, 1, s, a, tmA, tmB));
+      transpose_b
+          ? ops_launch<grouped_kernel<kTransB, false>>(grid, kThreads, kSmemBytes, 1, s, a, tmA, tmB,
+                                                           tmD)
+          : ops_launch<grouped_kernel<kForward, false>>(grid, kThreads, kSmemBytes, 1, s, a, tmA, tmB,
+                                                           tmD));
 }
 
 gemm_status_t gemm_bf16gemm_grouped_wgrad(int64_t G, const int32_t* offsets, int64_t rows,
@@ -647,7 +863,8 @@ gemm_status_t gemm_bf16gemm_grouped_wgrad(int64_t G, const int32_t* offsets, int
   a.product = product ? 1 : 0;
   a.err = err;
   std::unique_lock<std::mutex> lock;
-  CUtensorMap tmA{}, tmB{};
+  CUtensorMap tmA{}, tmB{}, tmD{};
+  a.d_tma = product && beta == 0.0f && encode_output(&tmD, dB, d_type, K, N, ldb, G, stride_b);
   if (product) {
     const uint32_t box[2] = {64, BK};
     st = operands(Operand{A, rows, K, lda, 1, 0}, Operand{dD, rows, N, lddd, 1, 0}, 2, box, box, sms,
@@ -657,7 +874,8 @@ gemm_status_t gemm_bf16gemm_grouped_wgrad(int64_t G, const int32_t* offsets, int
   const int64_t tiles = G * per;
   const dim3 grid(static_cast<unsigned>(tiles < sms ? tiles : sms));
   return abi_from_cuda(
-      ops_launch<grouped_kernel<kWeightGrad>>(grid, kThreads, kSmemBytes, 1, s, a, tmA, tmB));
+      ops_launch<grouped_kernel<kWeightGrad, false>>(grid, kThreads, kSmemBytes, 1, s, a, tmA, tmB,
+                                                           tmD));
 }
 
 }  // extern "C"

@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_kernel(const __grid_const
         const int c = chunk_col<VEC>(chunk);
         in[k] = chunk < chunks && c < a.dim;
         if constexpr (RING) {
-          if (k == 0) mbar_wait(&ring.full[slot], parity, &ring.abort_flag, a.ring.err);
+          if (k == 0) mbar_wait_late(&ring.full[slot], parity, &ring.abort_flag, a.ring.err);
           raw[k].from_ring(a, stages + slot * stage_bytes, c, in[k]);
         } else {
           raw[k].load(a, row, c, in[k]);
@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_grad_kernel(const __grid_
       Raw8<TD> dy[C];
       Raw8<TH> rh[C];
       const uint8_t* from = stages + slot * stage_bytes;
-      if (RING) mbar_wait(&ring.full[slot], parity, &ring.abort_flag, a.ring.err);
+      if (RING) mbar_wait_late(&ring.full[slot], parity, &ring.abort_flag, a.ring.err);
       auto get = [&](int k, int c, bool in) {
         if constexpr (RING) {
           dy[k] = {};

@@ -30,9 +30,10 @@ gemm_status_t abi_scratch(cudaStream_t stream, int64_t floats, std::unique_lock<
 gemm_status_t abi_stage(cudaStream_t stream, int64_t bytes, std::unique_lock<std::mutex>& lock,
                         uint8_t** buf);
 // Tensor map of `rank` (2 or 3) dimensions, innermost first; strides in bytes
-// of dimensions 1 .. rank - 1; 128-byte swizzle; zeros outside.
+// of dimensions 1 .. rank - 1; zeros outside.
 bool abi_encode_tiled(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base,
-                      const int64_t* dims, const int64_t* strides, const uint32_t* box);
+                      const int64_t* dims, const int64_t* strides, const uint32_t* box,
+                      CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
 gemm_status_t abi_from_cuda(cudaError_t e);
 
 constexpr int64_t kOpsMaxDim = (int64_t{1} << 31) - 1;
@@ -349,8 +350,7 @@ __device__ __forceinline__ bool mbar_wait_at(uint32_t bar, uint32_t parity, uint
   const uint64_t t0 = globaltimer_ns();
   while (true) {
 #pragma unroll 1
-    for (int i = 0; i < 32; ++i)
-      if (mbar_try_wait_at(bar, parity)) return true;
+    for (int i = 0; i < 32; ++i) { if (mbar_try_wait_at(bar, parity)) return true; }
     if (ld_shared_volatile(abort_flag)) return false;
     if (globaltimer_ns() - t0 > kWaitLimitNs) {
       asm volatile("st.volatile.shared.s32 [%0], %1;" ::"r"(abort_flag), "r"(1) : "memory");
@@ -358,6 +358,11 @@ __device__ __forceinline__ bool mbar_wait_at(uint32_t bar, uint32_t parity, uint
       return false;
     }
   }
+}
+
+__device__ __forceinline__ bool mbar_wait_late(uint64_t* bar, uint32_t parity, int* abort_flag,
+                                               uint32_t* err_word) {
+  return mbar_wait_at(smem_u32(bar), parity, smem_u32(abort_flag), err_word);
 }
 
 __device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
@@ -368,6 +373,13 @@ __device__ __forceinline__ void cp_async_4_at(uint32_t smem_dst, const void* gme
                                               uint32_t src_bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_dst), "l"(gmem_src),
                "r"(src_bytes)
+               : "memory");
+}
+
+__device__ __forceinline__ void st_shared_u4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                             uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+               "r"(d)
                : "memory");
 }
 
@@ -393,6 +405,17 @@ __device__ __forceinline__ float4 ld_shared_v4(uint32_t addr) {
 // 1000 cycles and more.
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// 3-D tiled copy shared -> global of one box, in the issuing thread's bulk
+// group; elements outside the tensor are not written.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t smem_src, int32_t x,
+                                             int32_t y, int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(smem_src), "r"(x), "r"(y), "r"(z)
+      : "memory");
 }
 
 // Contiguous copy global -> shared; both addresses 16-byte aligned, `bytes` a
