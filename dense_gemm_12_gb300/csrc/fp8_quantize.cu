@@ -6,6 +6,8 @@
 //
 // Bound by memory: every value is read once, held in registers over its
 // block's maximum, and written once.
+#include <type_traits>
+
 #include "ops.cuh"
 
 namespace g12 {
@@ -19,57 +21,79 @@ struct QuantArgs {
   int64_t ldq;
   float* scales;
   int64_t ld_scales;
-  int x_vec;  // rows of x can be read in 16-byte pieces
-  int q_vec;  // rows of q can be written in 16-byte pieces
+  int q_vec;   // rows of q can be written in 16-byte pieces
+  int stages;  // tile kernel: tiles in the ring (0: x cannot be read by TMA)
+  uint32_t* err;
 };
 
-// 1 x 128 blocks along the rows of x: 16 lanes take one block; the thread's
-// kRowUnits units are loaded before the first is reduced.  Rows that cannot
-// be moved in vectors are read and written by elements 16 apart, which keeps
-// consecutive lanes on consecutive elements.
-constexpr int kRowUnits = 4;
+// 1 x 128 blocks along the rows of x.  A thread's kRowUnits units are loaded
+// before the first is reduced.  Three forms: 16 consecutive elements a thread
+// and 8 lanes a block (two quotients and the maximum's shuffles per block are
+// what the instructions go to: with 8 elements a thread 8192 x 8192 in bf16
+// took 52 us); 8 consecutive elements; and, for rows that cannot be moved in
+// vectors, 8 elements 16 apart, which keeps consecutive lanes on consecutive
+// elements.
+enum RowForm : int { kStrided8 = 0, kVec8 = 1, kVec16 = 2 };
+constexpr int kRowUnits = 2;
 
-template <bool VEC, int T>
+template <int FORM, int T>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const __grid_constant__ QuantArgs a) {
+  constexpr bool VEC = FORM != kStrided8;
+  constexpr int E = FORM == kVec16 ? 16 : 8, LANES = kFp8Block / E, PER_CTA = 256 / LANES;
   grid_dependency_wait();
   grid_launch_dependents();
-  const int l = threadIdx.x & 15;
+  const int l = threadIdx.x % LANES;
   const int64_t kb = (a.cols + kFp8Block - 1) / kFp8Block;
   const int64_t units = a.rows * kb;
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * 16;
+  const bool small = units < (int64_t{1} << 31);  // 32-bit quotients
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * PER_CTA;
   // every lane of a warp takes the same number of turns: the shuffles below
-  for (int64_t base = static_cast<int64_t>(blockIdx.x) * 16; base < units;
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * PER_CTA; base < units;
        base += stride * kRowUnits) {
-    Raw8<T> raw[kRowUnits];
+    Raw8<T> raw[kRowUnits][E / 8];
     int64_t row[kRowUnits], blk[kRowUnits];
     bool in[kRowUnits];
 #pragma unroll
     for (int u = 0; u < kRowUnits; ++u) {
-      const int64_t unit = base + u * stride + (threadIdx.x >> 4);
+      const int64_t unit = base + u * stride + threadIdx.x / LANES;
       in[u] = unit < units;
-      row[u] = in[u] ? unit / kb : 0;
+      row[u] = !in[u] ? 0 : small ? static_cast<uint32_t>(unit) / static_cast<uint32_t>(kb) : unit / kb;
       blk[u] = in[u] ? unit - row[u] * kb : 0;
       const int64_t c0 = blk[u] * kFp8Block;
       const int n = static_cast<int>(min(a.cols - c0, static_cast<int64_t>(kFp8Block)));
-      const int c = VEC ? l * 8 : l;
-      raw[u] = load8<VEC, T>(a.x, a.x_type, row[u] * a.ldx + c0, c, n, in[u] && c < n);
+      const int c = VEC ? l * E : l;
+#pragma unroll
+      for (int h = 0; h < E / 8; ++h)
+        raw[u][h] = load8<VEC, T>(a.x, a.x_type, row[u] * a.ldx + c0, c + 8 * h, n, in[u] && c < n);
     }
 #pragma unroll
     for (int u = 0; u < kRowUnits; ++u) {
-      float v[8];
-      widen8<VEC, T>(raw[u], a.x_type, v);
-      const float amax = block_amax(v);
+      float v[E];
+#pragma unroll
+      for (int h = 0; h < E / 8; ++h) {
+        float w[8];
+        widen8<VEC, T>(raw[u][h], a.x_type, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[8 * h + i] = w[i];
+      }
+      const float amax = block_amax<LANES>(v);
       if (!in[u]) continue;
       const float f = fp8_factor(amax);
       const int64_t c0 = blk[u] * kFp8Block;
       uint8_t* q = a.q + row[u] * a.ldq + c0;
-      if (VEC) {
-        if (c0 + l * 8 < a.cols)
-          *reinterpret_cast<uint2*>(q + l * 8) =
-              make_uint2(pack_e4m3(v[0] * f, v[1] * f, v[2] * f, v[3] * f),
-                         pack_e4m3(v[4] * f, v[5] * f, v[6] * f, v[7] * f));
+      const int n = static_cast<int>(min(a.cols - c0, static_cast<int64_t>(kFp8Block)));
+      if constexpr (VEC) {
+        uint32_t w[E / 4];
+#pragma unroll
+        for (int i = 0; i < E / 4; ++i)
+          w[i] = pack_e4m3(v[4 * i] * f, v[4 * i + 1] * f, v[4 * i + 2] * f, v[4 * i + 3] * f);
+        if (l * E < n) {
+          if constexpr (E == 16)
+            *reinterpret_cast<uint4*>(q + l * E) = make_uint4(w[0], w[1], w[2], w[3]);
+          else
+            *reinterpret_cast<uint2*>(q + l * E) = make_uint2(w[0], w[1]);
+        }
       } else {
-        const int n = static_cast<int>(min(a.cols - c0, static_cast<int64_t>(kFp8Block)));
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           if (l + 16 * i < n)
@@ -80,39 +104,107 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const __grid_constan
   }
 }
 
-// One 128 x 128 tile of x per CTA turn.  Thread (rg, cg) = (t / 16, t % 16)
-// holds rows 8 rg .. 8 rg + 7 of columns 8 cg .. 8 cg + 7.  The transposed
-// output goes through shared memory: eight values down a column make one
-// 8-byte piece of an output row; a row's 16 pieces are XOR-swizzled by its
-// 8-column group, so that the 16 lanes of a write fall in distinct banks.
+template <int FORM, int T>
+cudaError_t launch_rows(const QuantArgs& a, int num_sms, cudaStream_t s) {
+  constexpr int per_cta = 256 / (kFp8Block / (FORM == kVec16 ? 16 : 8));
+  const int64_t units = a.rows * ((a.cols + kFp8Block - 1) / kFp8Block);
+  // few units: one per group of lanes; many: kRowUnits each, up to eight CTAs per SM
+  int64_t ctas = (units + per_cta - 1) / per_cta;
+  const int64_t fit = static_cast<int64_t>(num_sms) * 8;
+  if (ctas > fit) {
+    const int64_t fewer = (ctas + kRowUnits - 1) / kRowUnits;
+    ctas = fewer > fit ? fit : fewer;
+  }
+  return ops_launch<quantize_rows_kernel<FORM, T>>(dim3(static_cast<unsigned>(ctas)), 256, 0, 1, s, a);
+}
+
+// One 128 x 128 tile of x per CTA turn, through shared memory.  Where TMA can
+// describe x, one thread keeps `stages` tiles on their way (zeros outside x);
+// a thread waiting for its own 16-byte loads instead left too few in flight
+// (8192 x 8192 in bf16: 49 us).  Otherwise each warp reads a row's elements
+// with consecutive lanes.  Thread (rg, cg) = (t / 16, t % 16) then holds rows
+// 8 rg .. 8 rg + 7 of columns 8 cg .. 8 cg + 7.  The transposed output goes
+// through shared memory again: eight values down a column make one 8-byte
+// piece of an output row; a row's 16 pieces are XOR-swizzled by its 8-column
+// group, so that the 16 lanes of a write fall in distinct banks.
+constexpr int kTile = 128;
+constexpr int kMaxTileStages = 4;
+
 template <bool TILES, bool TRANSPOSE, int T>
-__global__ void __launch_bounds__(256) quantize_tile_kernel(const __grid_constant__ QuantArgs a) {
+__global__ void __launch_bounds__(256) quantize_tile_kernel(const __grid_constant__ QuantArgs a,
+                                                            const __grid_constant__ CUtensorMap tmX) {
   __shared__ __align__(16) uint8_t turned[TRANSPOSE ? 128 * 128 : 16];
   __shared__ float colmax[TILES ? 1 : 8][TILES ? 1 : 128];
+  __shared__ __align__(16) float factor[TILES ? 4 : 128];
   __shared__ float tilemax[8];
-  grid_dependency_wait();
-  grid_launch_dependents();
+  __shared__ uint64_t full[kMaxTileStages];
+  __shared__ int abort_flag;
+  extern __shared__ __align__(128) uint8_t dyn_smem[];
+  uint8_t* const ring = align_smem<128>(dyn_smem);
+  constexpr int kElem = T == GEMM_OUT_BF16 ? 2 : 4;
+  constexpr int kTileBytes = kTile * kTile * kElem;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int cg = t & 15, rg = t >> 4;
   const int64_t tiles_c = (a.cols + 127) / 128, tiles_r = (a.rows + 127) / 128;
-  for (int64_t tile = blockIdx.x; tile < tiles_r * tiles_c; tile += gridDim.x) {
+  const int64_t tiles = tiles_r * tiles_c;
+  auto fetch = [&](int64_t tile, int s) {
+    const int64_t tr = tile / tiles_c, tc = tile - tr * tiles_c;
+    mbar_arrive_expect_tx(&full[s], kTileBytes);
+    tma_load_2d(ring + s * kTileBytes, &tmX, static_cast<int>(tc * kTile),
+                static_cast<int>(tr * kTile), &full[s]);
+  };
+  if (a.stages > 0) {
+    if (t == 0) {
+      for (int s = 0; s < a.stages; ++s) mbar_init(&full[s], 1);
+      abort_flag = 0;
+      fence_barrier_init();
+    }
+    __syncthreads();
+  }
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (a.stages > 0 && t == 0)
+    for (int s = 0; s < a.stages; ++s) {
+      const int64_t tile = blockIdx.x + static_cast<int64_t>(s) * gridDim.x;
+      if (tile < tiles) fetch(tile, s);
+    }
+  int slot = 0;
+  uint32_t parity = 0;
+  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
     const int64_t tr = tile / tiles_c, tc = tile - tr * tiles_c;
     const int64_t r0 = tr * 128 + rg * 8, c0 = tc * 128 + cg * 8;
-    float v[8][8];  // [row][column]
-    if (a.x_vec && c0 + 8 <= a.cols) {
-      Raw8<T> raw[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        raw[i] = load8<true, T>(a.x, a.x_type, (r0 + i) * a.ldx + c0, 0, 8, r0 + i < a.rows);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) widen8<true, T>(raw[i], a.x_type, v[i]);
+    if (a.stages > 0) {
+      mbar_wait_late(&full[slot], parity, &abort_flag, a.err);
     } else {
+      // rows warp, warp + 8, ...; lane l takes columns l, l + 32, l + 64, l + 96
+      using E = std::conditional_t<T == GEMM_OUT_BF16, uint16_t, uint32_t>;
+      E* to = reinterpret_cast<E*>(ring);
+      const E* from = static_cast<const E*>(a.x) + tc * kTile;
+      const int n = static_cast<int>(min(a.cols - tc * kTile, static_cast<int64_t>(kTile)));
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        E v[8][4];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int64_t r = tr * kTile + half * 64 + i * 8 + warp;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            v[i][j] = r < a.rows && lane + 32 * j < n ? __ldcs(from + r * a.ldx + lane + 32 * j) : E(0);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            to[(half * 64 + i * 8 + warp) * kTile + lane + 32 * j] = v[i][j];
+      }
+      __syncthreads();
+    }
+    float v[8][8];  // [row][column]
+    {
+      const uint8_t* from = ring + slot * kTileBytes + rg * 8 * (kTile * kElem);
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          v[i][j] = r0 + i < a.rows && c0 + j < a.cols
-                        ? load1(a.x, T, (r0 + i) * a.ldx + c0 + j) : 0.0f;
+        widen_vec<T>(load8_smem<T>(from + i * (kTile * kElem), cg * 8), T, v[i]);
     }
     float f[8];  // factor of each column
     if (TILES) {
@@ -148,13 +240,25 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const __grid_constan
         for (int j = 0; j < 8; ++j) colmax[warp][cg * 8 + j] = f[j];
       }
       __syncthreads();
+      if (t < 128) {  // one thread per column: the quotients are long
+        float m = colmax[0][TILES ? 0 : t];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        float m = colmax[0][cg * 8 + j];
+        for (int w = 1; w < 8; ++w) m = fmaxf(m, colmax[TILES ? 0 : w][TILES ? 0 : t]);
+        const int64_t c = tc * 128 + t;
+        if (c < a.cols) a.scales[tr * a.ld_scales + c] = fp8_scale(m);
+        factor[TILES ? 0 : t] = fp8_factor(m);
+      }
+      __syncthreads();
 #pragma unroll
-        for (int w = 1; w < 8; ++w) m = fmaxf(m, colmax[w][cg * 8 + j]);
-        if (rg == 0 && c0 + j < a.cols) a.scales[tr * a.ld_scales + c0 + j] = fp8_scale(m);
-        f[j] = fp8_factor(m);
+      for (int j = 0; j < 8; ++j) f[j] = factor[TILES ? 0 : cg * 8 + j];
+    }
+    // every thread has read the tile (the barrier among the maxima above)
+    if (a.stages > 0) {
+      const int64_t next = tile + static_cast<int64_t>(a.stages) * gridDim.x;
+      if (t == 0 && next < tiles && !*const_cast<volatile int*>(&abort_flag)) fetch(next, slot);
+      if (++slot == a.stages) {
+        slot = 0;
+        parity ^= 1u;
       }
     }
     if constexpr (!TRANSPOSE) {
@@ -207,14 +311,30 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const __grid_constan
     }
     __syncthreads();  // `turned` and the maxima are rewritten by the next tile
   }
+  if (a.stages > 0 && t == 0 && abort_flag) {
+    // after a wait ran out: the copies in flight land before the CTA leaves
+    for (int i = 0; i < a.stages; ++i) {
+      mbar_drain_wait(&full[slot], parity);
+      if (++slot == a.stages) {
+        slot = 0;
+        parity ^= 1u;
+      }
+    }
+  }
 }
 
 template <int T>
-cudaError_t launch_tiles(const QuantArgs& a, int block, bool transpose, dim3 grid, cudaStream_t s) {
+cudaError_t launch_tiles(const QuantArgs& a, const CUtensorMap& tmX, int block, bool transpose,
+                         int num_sms, cudaStream_t s) {
+  const int64_t tiles = ((a.rows + 127) / 128) * ((a.cols + 127) / 128);
+  const int64_t fit = static_cast<int64_t>(num_sms) * 2;  // the kernel's registers
+  const dim3 grid(static_cast<unsigned>(tiles < fit ? tiles : fit));
+  const size_t smem =
+      128 + static_cast<size_t>(a.stages > 0 ? a.stages : 1) * kTile * kTile * (T == GEMM_OUT_BF16 ? 2 : 4);
   if (block == GEMM_BLOCK_ROWS)
-    return ops_launch<quantize_tile_kernel<false, true, T>>(grid, 256, 0, 1, s, a);
-  if (transpose) return ops_launch<quantize_tile_kernel<true, true, T>>(grid, 256, 0, 1, s, a);
-  return ops_launch<quantize_tile_kernel<true, false, T>>(grid, 256, 0, 1, s, a);
+    return ops_launch<quantize_tile_kernel<false, true, T>>(grid, 256, smem, 1, s, a, tmX);
+  if (transpose) return ops_launch<quantize_tile_kernel<true, true, T>>(grid, 256, smem, 1, s, a, tmX);
+  return ops_launch<quantize_tile_kernel<true, false, T>>(grid, 256, smem, 1, s, a, tmX);
 }
 
 }  // namespace
@@ -251,30 +371,31 @@ extern "C" gemm_status_t gemm_fp8_quantize(int64_t rows, int64_t cols, const voi
   a.ldq = ldq;
   a.scales = scales;
   a.ld_scales = ld_scales;
-  a.x_vec = !ops_misaligned(x, 16) && ldx % (16 / bytes) == 0;
+  const bool x_vec = !ops_misaligned(x, 16) && ldx % (16 / bytes) == 0;
+  a.err = err;
   a.q_vec = !ops_misaligned(q, 16) && ldq % 16 == 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (block == GEMM_BLOCK_ROWS && !transpose) {
-    const int64_t units = rows * ((cols + 127) / 128);
-    // few units: one per half-warp; many: kRowUnits each, eight CTAs per SM
-    int64_t ctas = (units + 15) / 16;
-    const int64_t fit = static_cast<int64_t>(sms) * 8;
-    if (ctas > fit) ctas = (ctas + kRowUnits - 1) / kRowUnits > fit ? fit : (ctas + kRowUnits - 1) / kRowUnits;
-    const dim3 grid(static_cast<unsigned>(ctas));
-    const bool vec = a.x_vec && cols % 8 == 0 && !ops_misaligned(q, 8) && ldq % 8 == 0;
+    const bool q16 = !ops_misaligned(q, 16) && ldq % 16 == 0;
+    const bool q8 = !ops_misaligned(q, 8) && ldq % 8 == 0;
+    const bool half = x_type == GEMM_OUT_BF16;
     cudaError_t e;
-    if (!vec)
-      e = ops_launch<quantize_rows_kernel<false, kAnyType>>(grid, 256, 0, 1, s, a);
-    else if (x_type == GEMM_OUT_BF16)
-      e = ops_launch<quantize_rows_kernel<true, GEMM_OUT_BF16>>(grid, 256, 0, 1, s, a);
+    if (x_vec && q16 && cols % 16 == 0)
+      e = half ? launch_rows<kVec16, GEMM_OUT_BF16>(a, sms, s) : launch_rows<kVec16, GEMM_OUT_F32>(a, sms, s);
+    else if (x_vec && q8 && cols % 8 == 0)
+      e = half ? launch_rows<kVec8, GEMM_OUT_BF16>(a, sms, s) : launch_rows<kVec8, GEMM_OUT_F32>(a, sms, s);
     else
-      e = ops_launch<quantize_rows_kernel<true, GEMM_OUT_F32>>(grid, 256, 0, 1, s, a);
+      e = launch_rows<kStrided8, kAnyType>(a, sms, s);
     return abi_from_cuda(e);
   }
-  const int64_t tiles = ((rows + 127) / 128) * ((cols + 127) / 128);
-  const int64_t fit = static_cast<int64_t>(sms) * 2;
-  const dim3 grid(static_cast<unsigned>(tiles < fit ? tiles : fit));
+  CUtensorMap tmX{};
+  const int64_t dims[2] = {cols, rows}, pitch[1] = {ldx * bytes};
+  const uint32_t box[2] = {kTile, kTile};
+  if (x_vec && abi_encode_tiled(&tmX, bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                                2, x, dims, pitch, box, CU_TENSOR_MAP_SWIZZLE_NONE))
+    a.stages = bytes == 2 ? 2 : 1;
   return abi_from_cuda(x_type == GEMM_OUT_BF16
-                           ? launch_tiles<GEMM_OUT_BF16>(a, block, transpose != 0, grid, s)
-                           : launch_tiles<GEMM_OUT_F32>(a, block, transpose != 0, grid, s));
+                           ? launch_tiles<GEMM_OUT_BF16>(a, tmX, block, transpose != 0, sms, s)
+                           : launch_tiles<GEMM_OUT_F32>(a, tmX, block, transpose != 0, sms, s));
 }

@@ -123,7 +123,7 @@ __device__ __forceinline__ void write_y(const NormArgs& a, int64_t row, int c, b
     if (a.p.y != nullptr) store8<VEC>(a.p.y, a.p.y_type, row * a.p.ldy, c, a.dim, y);
   }
   if (a.p.q == nullptr) return;
-  const float amax = block_amax(y);
+  const float amax = block_amax<16>(y);
   if (!in) return;
   const float f = fp8_factor(amax);
   uint8_t* q = static_cast<uint8_t*>(a.p.q) + row * a.p.ldq;

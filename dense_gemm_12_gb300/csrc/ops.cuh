@@ -72,7 +72,7 @@ cudaError_t ops_allow_smem(size_t bytes) {
 template <auto Kernel, typename... Args>
 cudaError_t ops_launch(dim3 grid, int threads, size_t smem, int cluster, cudaStream_t stream,
                        const Args&... args) {
-  if (smem > 48 * 1024) {
+  if (smem > 16 * 1024) {  // with what the kernel has statically, perhaps over the default
     const cudaError_t e = ops_allow_smem<Kernel>(smem);
     if (e != cudaSuccess) return e;
   }
@@ -105,20 +105,21 @@ __device__ __forceinline__ float finite_abs(float v) {
   return a <= FLT_MAX ? a : 0.0f;
 }
 
-// Largest finite magnitude of eight values over the 16 lanes of a block; all
-// 32 lanes call it together.  fmaxf passes over NaN; infinities are rare, and
-// only when one shows up are the values looked at one by one.
-__device__ __forceinline__ float block_amax(const float (&v)[8]) {
+// Largest finite magnitude of a thread's values over the LANES lanes of a block
+// (16 or 8); all 32 lanes call it together.  fmaxf passes over NaN; infinities
+// are rare, and only when one shows up are the values looked at one by one.
+template <int LANES, int E>
+__device__ __forceinline__ float block_amax(const float (&v)[E]) {
   float m = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+  for (int i = 0; i < E; ++i) m = fmaxf(m, fabsf(v[i]));
   if (__any_sync(0xffffffffu, m > FLT_MAX)) {
     m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, finite_abs(v[i]));
+    for (int i = 0; i < E; ++i) m = fmaxf(m, finite_abs(v[i]));
   }
 #pragma unroll
-  for (int s = 8; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+  for (int s = LANES / 2; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
   return m;
 }
 
