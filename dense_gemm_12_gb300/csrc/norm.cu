@@ -172,7 +172,7 @@ struct Inputs {
 // time mostly from L2).  Nothing of a row is written before its last read, so
 // outputs may take the place of inputs element by element.
 template <int C, bool VEC, int TX, int TR, bool RING = false>
-__global__ void __launch_bounds__(kMaxThreads, 1) norm_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(kMaxThreads, RING ? 2 : 1) norm_kernel(const __grid_constant__ NormArgs a) {
   __shared__ float red[2][16];
   __shared__ Ring ring;
   extern __shared__ uint4 dyn_smem[];
@@ -336,9 +336,12 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_grad_kernel(const __grid_
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[k][i] = 0.0f;
   uint32_t turn = 0;
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * per_cta + sub; row < a.rows;
-       row += static_cast<int64_t>(gridDim.x) * per_cta) {
-    const float rstd = a.p.rstd[row];
+  const int64_t row_step = static_cast<int64_t>(gridDim.x) * per_cta;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * per_cta + sub;
+  float next_rstd = row < a.rows ? a.p.rstd[row] : 0.0f;  // loaded a row ahead
+  for (; row < a.rows; row += row_step) {
+    const float rstd = next_rstd;
+    if (row + row_step < a.rows) next_rstd = a.p.rstd[row + row_step];
     float dot = 0.0f;
     if constexpr (C > 0) {
       // RING: both halves read the stage, which keeps registers free for more
@@ -503,10 +506,11 @@ __global__ void __launch_bounds__(256) dweight_kernel(const __grid_constant__ Gr
 }
 
 // dw[col] = sum of the `parts` partial sums, always in the same order: a
-// warp's lanes take 32 columns, the block's 8 warps every 8th part.
-__global__ void __launch_bounds__(256) add_parts_kernel(const float* part, int parts, int dim,
-                                                        float* dw) {
-  __shared__ float sums[8][32];
+// warp's lanes take 32 columns, the block's 32 warps every 32nd part (few
+// loads one after the other: the time of this kernel is their latency).
+__global__ void __launch_bounds__(1024) add_parts_kernel(const float* part, int parts, int dim,
+                                                         float* dw) {
+  __shared__ float sums[32][33];
   grid_dependency_wait();
   grid_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -514,14 +518,16 @@ __global__ void __launch_bounds__(256) add_parts_kernel(const float* part, int p
   float s = 0.0f;
   if (col < dim) {
 #pragma unroll 8
-    for (int p = warp; p < parts; p += 8) s += __ldcg(part + static_cast<int64_t>(p) * dim + col);
+    for (int p = warp; p < parts; p += 32) s += __ldcg(part + static_cast<int64_t>(p) * dim + col);
   }
   sums[warp][lane] = s;
   __syncthreads();
-  if (warp == 0 && col < dim) {
-    for (int r = 1; r < 8; ++r) s += sums[r][lane];
-    dw[col] = s;
-  }
+  // warp w adds column w's 32 sums
+  s = sums[lane][warp];
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+  const int64_t out = static_cast<int64_t>(blockIdx.x) * 32 + warp;
+  if (lane == 0 && out < dim) dw[out] = s;
 }
 
 struct RowPlan {
@@ -697,7 +703,7 @@ gemm_status_t gemm_rmsnorm(int64_t rows, int64_t dim, const gemm_rmsnorm_t* args
     const int64_t bytes = dim * (type_bytes(p.x_type) +
                                  (p.residual == nullptr ? 0 : type_bytes(p.residual_type)));
     const RowPlan pr = plan_rows(rows, chunks, sms, 2, 2);
-    const int ring_grid = plan_ring(pr, rows, bytes, sms, pr.chunks_per_thread == 1 ? 1152 : 896, a.ring);
+    const int ring_grid = plan_ring(pr, rows, bytes, sms, 1024, a.ring);
     if (ring_grid > 0) {
       grid = ring_grid;
       pl = pr;
@@ -750,7 +756,7 @@ gemm_status_t gemm_rmsnorm_backward(int64_t rows, int64_t dim, const gemm_rmsnor
         dim * (type_bytes(p.dy_type) + type_bytes(p.h_type) +
                (p.residual_grad == nullptr ? 0 : type_bytes(p.residual_grad_type)));
     const int ring_grid =
-        plan_ring(pl, rows, bytes, sms, pl.chunks_per_thread == 1 ? 1024 : 768, a.ring);
+        plan_ring(pl, rows, bytes, sms, pl.chunks_per_thread == 1 ? 768 : 640, a.ring);
     if (ring_grid > 0) grid = ring_grid;
   }
   const bool by_column = pl.chunks_per_thread == 0;
@@ -771,7 +777,7 @@ gemm_status_t gemm_rmsnorm_backward(int64_t rows, int64_t dim, const gemm_rmsnor
   const dim3 g(static_cast<unsigned>((dim + 31) / 32));
   const float* part = a.part;
   return abi_from_cuda(
-      ops_launch<add_parts_kernel>(g, 256, 0, 1, s, part, parts, a.dim, p.dweight));
+      ops_launch<add_parts_kernel>(g, 1024, 0, 1, s, part, parts, a.dim, p.dweight));
 }
 
 }  // extern "C"
