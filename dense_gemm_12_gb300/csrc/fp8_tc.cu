@@ -58,6 +58,8 @@ constexpr int few_regs(bool rows) { return rows ? 40 : 72; }
 constexpr int many_regs(bool rows) { return rows ? 232 : 208; }
 static_assert(few_regs(true) + 2 * many_regs(true) <= 504, "registers at launch");
 static_assert(few_regs(false) + 2 * many_regs(false) <= 504, "registers at launch");
+// k-blocks of B that a CTA of a split tile asks L2 for early.
+constexpr int kEarlyBlocks = 4;
 // A warp's output staging: 32 rows x 64 bytes.
 constexpr int kOutBytes = 32 * 64;
 
@@ -154,11 +156,11 @@ __device__ __forceinline__ uint64_t add_pair(uint64_t sum, uint32_t lo, uint32_t
 // Adds C columns of one block's accumulator (r) to the sums.
 template <bool ROWS, int C>
 __device__ __forceinline__ void add_scaled(uint64_t* acc, const uint32_t (&r)[C], uint64_t s,
-                                           uint32_t sb) {
+                                           const float* sb) {
 #pragma unroll
   for (int i = 0; i < C / 2; i += 2) {
     if (ROWS) {
-      const float4 c = ld_shared_v4(sb + 8 * i);
+      const float4 c = *reinterpret_cast<const float4*>(sb + 2 * i);
       acc[i] = add_pair(acc[i], r[2 * i], r[2 * i + 1], s, c.x, c.y);
       acc[i + 1] = add_pair(acc[i + 1], r[2 * i + 2], r[2 * i + 3], s, c.z, c.w);
     } else {
@@ -317,7 +319,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_relinquish_alloc_permit();
     }
   }
-  // Everything above touches no global memory and may overlap the previous
+  if (CLUSTER && warp == 0 && lane == 0) {
+    // One tile per cluster, so the CTA's part of B is known: its first blocks
+    // may come to L2 while the previous kernel ends (nothing is read from
+    // them before the wait below).
+    const int parts = p.cluster, part = static_cast<int>(cluster_cta_rank());
+    const int tn = (static_cast<int>(blockIdx.x) / parts) / ((p.M + p.tile_rows - 1) / p.tile_rows);
+    const int kb = part * p.num_kb / parts, end = (part + 1) * p.num_kb / parts;
+    for (int i = 0; i < kEarlyBlocks && kb + i < end; ++i)
+      tma_prefetch_l2_3d(&tmB, (kb + i) * BK, tn * BN, 0);
+  }
+  // Everything above reads no global memory and may overlap the previous
   // kernel's last CTAs; every global access below follows its completion.
   grid_dependency_wait();
   if (threadIdx.x == 0) grid_launch_dependents();
@@ -518,9 +530,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after_sync();
         if (live) {
           const uint32_t sc = scales_at + s * (kScaleFloats * 4);
-          const uint32_t sb = sc + 4 * (BM + (ROWS ? half * kWarpCols : half));
           float f1 = ld_shared_f32(sc + 4 * row);
-          if (!ROWS) f1 *= ld_shared_f32(sb);
+          if (!ROWS) f1 *= ld_shared_f32(sc + 4 * (BM + half));
+          // the columns' scales (ROWS)
+          const float* sb = tail->scales[s] + BM + half * kWarpCols;
           const uint64_t f = f32x2(f1, f1);
           const uint32_t taddr = lane_base + b * BN;
           uint32_t ra[32], rb[16];
@@ -529,17 +542,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_wait_ld();
           add_scaled<ROWS>(acc, ra, f, sb);
           tmem_ld_32x32b_x32(taddr + 48, ra);
-          add_scaled<ROWS>(acc + 16, rb, f, sb + 128);
+          add_scaled<ROWS>(acc + 16, rb, f, sb + 32);
           tmem_ld_32x32b_x16(taddr + 80, rb);
           tc_wait_ld();
-          add_scaled<ROWS>(acc + 24, ra, f, sb + 192);
+          add_scaled<ROWS>(acc + 24, ra, f, sb + 48);
           tmem_ld_32x32b_x32(taddr + 96, ra);
-          add_scaled<ROWS>(acc + 40, rb, f, sb + 320);
+          add_scaled<ROWS>(acc + 40, rb, f, sb + 80);
           tc_wait_ld();
           tc_fence_before_sync();
           __syncwarp();
           if (lane == 0) release<PAIR>(tmem_empty_at + 8 * b);
-          add_scaled<ROWS>(acc + 48, ra, f, sb + 384);
+          add_scaled<ROWS>(acc + 48, ra, f, sb + 96);
           __syncwarp();
           if (lane == 0) mbar_arrive_at(sempty_at + 8 * s);
         } else {
