@@ -14,13 +14,24 @@
 //                  into a 4-stage ring (one 128-byte swizzle atom of fp8 wide)
 //   * warp 1       TMEM and MMAs (M = 128, N = 256, K = 32; four per block),
 //                  into two TMEM accumulators of 256 columns in turn
-//   * warp 2       the block's scales into a small ring (cp.async: any address)
+//   * warp 2       the block's scales into a ring of their own (cp.async: any
+//                  address), on the operands' barrier
 //   * warps 4..11  sums: 32 rows x 128 columns per warp, one row per thread,
 //                  128 fp32 sums in registers, updated with packed FMAs
-// The MMAs of a block take at least 512 cycles; reading its accumulator
-// (64 KB per warpgroup) and the 256 FMA cycles per SM fit beside them, so the
-// tensor core stays the bound where the ring keeps up.  Registers move from
-// the first warpgroup to the other two (setmaxnreg) to hold the sums.
+// Registers move from the first warpgroup to the other two (setmaxnreg) to
+// hold the sums.
+//
+// What bounds it.  A block's MMAs take 512 cycles at the tensor core's rate,
+// its operands 768 through shared memory (48 KB written, 48 KB read, 128 B per
+// cycle), and a sum warp about 900: three TMEM loads, 64 packed FMAs, and its
+// visits to barriers and scales in shared memory, which is busy with operands
+// and answers late.  So the visits are few: one barrier for operands and
+// scales, one commit per block that both frees the stage and announces the
+// accumulator, no copies of loaded registers.  Measured 409-429 us at 8192^3
+// (2.6 PFLOP/s), 64 us at 4096^3 (2.1), against 499 and 75 us before those
+// three.  CTA pairs, which halve the operands' traffic, came to the same (436
+// us): each block's accumulator then travels through two CTAs' barriers.  Scales
+// for each row of B cost a second product per element: 97 us at 4096^3.
 //
 // Few tiles: the CTAs of a cluster split a tile's k-blocks and add their sums
 // through distributed shared memory, in k order.  Rows of A beyond a group's
@@ -34,30 +45,24 @@ namespace g12 {
 namespace {
 
 constexpr int BM = 128, BN = 256, BK = kFp8Block;
-// What one CTA does: a tile by itself, a share of a tile's k-blocks in a
-// cluster, or half of a 256 x 256 tile with its peer (a CTA pair).
-enum Form : int { kSingle = 0, kSplit = 1, kPair = 2 };
-constexpr int kRingBytes = 192 * 1024;
+constexpr int STAGES = 4;
 constexpr int kStageBytesA = BM * BK;
-// B rows of a stage: a pair's CTAs hold half of the tile's each
-constexpr int b_rows(int form) { return form == kPair ? BN / 2 : BN; }
-constexpr int stage_bytes(int form) { return kStageBytesA + b_rows(form) * BK; }  // 48 or 32 KB
-constexpr int ring_stages(int form) { return kRingBytes / stage_bytes(form); }    // 4 or 6
-constexpr int kMaxStages = 6;
-constexpr int SSTAGES = 4;
+constexpr int kStageBytes = kStageBytesA + BN * BK;  // 48 KB
+constexpr int kRingBytes = STAGES * kStageBytes;
+// Slots of the scales' ring.  A block's scales are loaded with its operands
+// (one barrier for both), that is once the MMAs of the block STAGES before it
+// are done; those followed the release of the accumulator two further back, by
+// which time every sum warp had read that block's scales.
+constexpr int SSLOTS = STAGES + 2;
 constexpr int kScaleFloats = BM + BN;
 constexpr int kThreads = 384;
 constexpr int kSumThreads = 256;
 constexpr int kSumWarps = kSumThreads / 32;
 constexpr int kWarpCols = BN / 2;  // columns of one sum warp
 constexpr uint32_t kTmemCols = 512;
-// Registers after the split: 384 threads launch with 168 each, so the three
-// warpgroups' shares add up to at most 504.  The instance with a scale per row
-// of B needs more for its sums.
-constexpr int few_regs(bool rows) { return rows ? 40 : 72; }
-constexpr int many_regs(bool rows) { return rows ? 232 : 208; }
-static_assert(few_regs(true) + 2 * many_regs(true) <= 504, "registers at launch");
-static_assert(few_regs(false) + 2 * many_regs(false) <= 504, "registers at launch");
+constexpr uint32_t kIdesc = idesc_e4m3_f32(BM, BN);
+// 384 threads launch with 168 registers each; 40 + 2 x 232 = 3 x 168.
+constexpr int kFewRegs = 40, kManyRegs = 232;
 // k-blocks of B that a CTA of a split tile asks L2 for early.
 constexpr int kEarlyBlocks = 4;
 // A warp's output staging: 32 rows x 64 bytes.
@@ -77,18 +82,16 @@ struct Fp8Args {
   int64_t ldd;
   int d_type;
   int d_vec;            // rows of D can be written in 16-byte pieces
-  int tile_rows;        // rows of A per tile: 16, 32, 64 or 128 (pairs: 256)
+  int tile_rows;        // rows of A per tile: 16, 32, 64 or 128
   int band;             // row tiles per band of the schedule
   int cluster;          // > 1: CTAs that split one tile's k-blocks
   uint32_t* err;
 };
 
 struct __align__(16) Tail {
-  float scales[SSTAGES][kScaleFloats];
-  uint64_t full[kMaxStages];
-  uint64_t done[kMaxStages];
-  uint64_t sfull[SSTAGES];
-  uint64_t sempty[SSTAGES];
+  float scales[SSLOTS][kScaleFloats];
+  uint64_t full[STAGES];
+  uint64_t done[STAGES];
   uint64_t tmem_empty[2];
   uint64_t drain;
   uint32_t tmem_base;
@@ -99,25 +102,6 @@ struct __align__(16) Tail {
 constexpr size_t kSmemBytes = 1024 + kRingBytes + kSumWarps * kOutBytes + sizeof(Tail);
 static_assert(kSmemBytes <= 227 * 1024, "fp8 kernel shared memory");
 static_assert(BM * BN * 4 <= kRingBytes, "a cluster's sums fit in the ring");
-
-// The rows of a pair's tile that CTA `rank` of it takes (perhaps none).
-template <bool PAIR>
-__device__ __forceinline__ GroupTile cta_tile(GroupTile w, int rank) {
-  if (PAIR) {
-    w.row0 += rank * BM;
-    w.rows = min(w.rows - rank * BM, BM);
-  }
-  return w;
-}
-
-// Arrives on an accumulator's release barrier: the even CTA's in a pair.
-template <bool PAIR>
-__device__ __forceinline__ void release(uint32_t bar) {
-  if (PAIR)
-    mbar_arrive_remote(mapa_shared(bar, 0));
-  else
-    mbar_arrive_at(bar);
-}
 
 // Rows of a tile that sum warp (quarter, half) writes; 0 where it has no columns.
 __device__ __forceinline__ int live_rows(const GroupTile& w, int quarter, int half, int N) {
@@ -156,11 +140,11 @@ __device__ __forceinline__ uint64_t add_pair(uint64_t sum, uint32_t lo, uint32_t
 // Adds C columns of one block's accumulator (r) to the sums.
 template <bool ROWS, int C>
 __device__ __forceinline__ void add_scaled(uint64_t* acc, const uint32_t (&r)[C], uint64_t s,
-                                           const float* sb) {
+                                           uint32_t sb) {
 #pragma unroll
   for (int i = 0; i < C / 2; i += 2) {
     if (ROWS) {
-      const float4 c = *reinterpret_cast<const float4*>(sb + 2 * i);
+      const float4 c = ld_shared_v4(sb + 8 * i);
       acc[i] = add_pair(acc[i], r[2 * i], r[2 * i + 1], s, c.x, c.y);
       acc[i + 1] = add_pair(acc[i + 1], r[2 * i + 2], r[2 * i + 3], s, c.z, c.w);
     } else {
@@ -264,14 +248,10 @@ __device__ __forceinline__ void write_sums(const Fp8Args& p, uint8_t* stage, con
   }
 }
 
-// ROWS: sb has a scale per row of B (else per 128 rows).
-// kSplit: one tile per cluster of p.cluster CTAs, its k-blocks split among
-// them.  kPair: the even CTA's issuer runs one stream of M = 256 MMAs for both
-// CTAs; barriers as in the dense pair kernel (bf16_tc.cu): full and tmem_empty
-// count in the even CTA for both, empty and tmem_full are signalled in both.
-// Every thread of a CTA reaches the cluster barriers, also after a bounded
-// wait ran out.
-template <bool ROWS, int FORM>
+// ROWS: sb has a scale per row of B (else per 128 rows).  CLUSTER: one tile
+// per cluster of p.cluster CTAs, its k-blocks split among them.  Every thread
+// of a CTA reaches the cluster barriers, also after a bounded wait ran out.
+template <bool ROWS, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_kernel(const __grid_constant__ Fp8Args p, const __grid_constant__ CUtensorMap tmA,
                const __grid_constant__ CUtensorMap tmB) {
@@ -283,41 +263,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tail_at = smem_u32(tail);
   const uint32_t abort_flag = tail_at + offsetof(Tail, abort_flag);
   const uint32_t full_at = tail_at + offsetof(Tail, full), done_at = tail_at + offsetof(Tail, done);
-  const uint32_t sfull_at = tail_at + offsetof(Tail, sfull);
-  const uint32_t sempty_at = tail_at + offsetof(Tail, sempty);
   const uint32_t tmem_empty_at = tail_at + offsetof(Tail, tmem_empty);
   const uint32_t scales_at = tail_at + offsetof(Tail, scales);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  constexpr bool CLUSTER = FORM == kSplit, PAIR = FORM == kPair;
-  constexpr int STAGES = ring_stages(FORM), kStageBytes = stage_bytes(FORM);
-  constexpr uint32_t kIdesc = idesc_e4m3_f32(PAIR ? 2 * BM : BM, BN);
-  const int rank = PAIR ? static_cast<int>(cluster_cta_rank() & 1u) : 0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&tail->full[s], 1);
+      mbar_init(&tail->full[s], 1 + 32);  // the producer, and the scale warp's lanes
       mbar_init(&tail->done[s], 1);
     }
-    for (int s = 0; s < SSTAGES; ++s) {
-      mbar_init(&tail->sfull[s], 32);
-      mbar_init(&tail->sempty[s], kSumWarps);
-    }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(&tail->tmem_empty[b], PAIR ? 2 * kSumWarps : kSumWarps);
-    }
+    for (int b = 0; b < 2; ++b) mbar_init(&tail->tmem_empty[b], kSumWarps);
     mbar_init(&tail->drain, 1);
     tail->abort_flag = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
-    if (PAIR) {
-      tmem_alloc_pair(&tail->tmem_base, kTmemCols);
-      tmem_relinquish_alloc_permit_pair();
-    } else {
-      tmem_alloc(&tail->tmem_base, kTmemCols);
-      tmem_relinquish_alloc_permit();
-    }
+    tmem_alloc(&tail->tmem_base, kTmemCols);
+    tmem_relinquish_alloc_permit();
   }
   if (CLUSTER && warp == 0 && lane == 0) {
     // One tile per cluster, so the CTA's part of B is known: its first blocks
@@ -336,32 +299,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 3) build_groups(tail->groups, p.offsets, p.groups, p.M, p.tile_rows);
   tc_fence_before_sync();
   __syncthreads();
-  // Both CTAs of a pair signal barriers of the even one: all must be
-  // initialised first.
-  if (PAIR) cluster_sync();
   tc_fence_after_sync();
   const uint32_t tmem_base = tail->tmem_base;
   const GroupTable& groups = tail->groups;
   const int tiles_n = (p.N + BN - 1) / BN;
   const int tiles = groups.tile[p.groups] * tiles_n;
-  const int split = CLUSTER ? p.cluster : (PAIR ? 2 : 1);  // CTAs per tile
+  const int split = CLUSTER ? p.cluster : 1;  // CTAs per tile
   const int part = CLUSTER ? static_cast<int>(cluster_cta_rank()) : 0;
   const int first = static_cast<int>(blockIdx.x) / split;
-  const int stride = CLUSTER ? tiles : static_cast<int>(gridDim.x) / split;  // CLUSTER: one tile
+  const int stride = CLUSTER ? tiles : static_cast<int>(gridDim.x);  // CLUSTER: one tile
   const int kb0 = CLUSTER ? part * p.num_kb / split : 0;  // num_kb <= 2^24, part <= 8
   const int kb1 = CLUSTER ? (part + 1) * p.num_kb / split : p.num_kb;
 
   if (warp < 4) {
-    regs_give_back<few_regs(ROWS)>();
+    regs_give_back<kFewRegs>();
     if (warp == 0) {
       // ------------------------------------------------------ TMA producer
       if (lane == 0) {
         uint32_t it = 0;
         int g = 0;
         bool ok = true;
-        const uint32_t bytes = PAIR ? 2u * kStageBytes
-                                    : static_cast<uint32_t>((p.tile_rows + BN) * BK);
-        const uint32_t full0 = PAIR ? mapa_shared(smem_u32(&tail->full[0]), 0) : 0u;
+        const uint32_t bytes = static_cast<uint32_t>((p.tile_rows + BN) * BK);
         for (int t = first; t < tiles && ok; t += stride) {
           const GroupTile w = group_tile(groups, t, tiles_n, p.band, p.tile_rows, g);
           for (int kb = kb0; kb < kb1; ++kb, ++it) {
@@ -371,28 +329,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               break;
             }
             uint8_t* sa = smem + s * kStageBytes;
-            if (PAIR) {
-              const uint32_t full = full0 + s * static_cast<uint32_t>(sizeof(uint64_t));
-              if (rank == 0) mbar_arrive_expect_tx(&tail->full[s], bytes);
-              tma_load_2d_pair(sa, &tmA, kb * BK, w.row0 + rank * BM, full);
-              tma_load_3d_pair(sa + kStageBytesA, &tmB, kb * BK, w.tn * BN + rank * (BN / 2),
-                               w.group, full);
-            } else {
-              mbar_arrive_expect_tx(&tail->full[s], bytes);
-              tma_load_2d(sa, &tmA, kb * BK, w.row0, &tail->full[s]);
-              tma_load_3d(sa + kStageBytesA, &tmB, kb * BK, w.tn * BN, w.group, &tail->full[s]);
-            }
+            mbar_arrive_expect_tx(&tail->full[s], bytes);
+            tma_load_2d(sa, &tmA, kb * BK, w.row0, &tail->full[s]);
+            tma_load_3d(sa + kStageBytesA, &tmB, kb * BK, w.tn * BN, w.group, &tail->full[s]);
           }
         }
-        if (PAIR) {
-          // Leave only after the MMAs have read every stage this CTA filled:
-          // then all of its copies have landed and every commit aimed at its
-          // barriers has arrived.
-          const uint64_t t0 = globaltimer_ns();
-          for (uint32_t j = it > STAGES ? it - STAGES : 0u; j < it; ++j)
-            while (!mbar_try_wait(&tail->done[j % STAGES], (j / STAGES) & 1u))
-              if (globaltimer_ns() - t0 > kWaitLimitNs) break;
-        } else
         if (!ok) {
           for (uint32_t j = it > STAGES ? it - STAGES : 0u; j < it; ++j)
             mbar_drain_wait(&tail->full[j % STAGES], (j / STAGES) & 1u);
@@ -401,62 +342,39 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     } else if (warp == 1) {
       // -------------------------------------------------------- MMA issuer
-      if (rank == 0) {
-        uint32_t it = 0, s = 0, parity = 0;
-        bool ok = true, issued = false;
-        // K-major: 8-row groups 1024 B apart.  A stage, and 32 B for each step
-        // of 32 of k, only move the address field: the descriptors are sums.
-        const uint64_t da0 = smem_desc_sw128(smem_u32(smem), 16, 1024);
-        const uint64_t db0 = smem_desc_sw128(smem_u32(smem) + kStageBytesA, 16, 1024);
-        for (int t = first; t < tiles && ok; t += stride) {
-          for (int kb = kb0; kb < kb1; ++kb, ++it) {
-            const uint32_t b = it & 1u;
-            const bool got =
-                mbar_wait_at(full_at + 8 * s, parity, abort_flag, p.err) &&
-                mbar_wait_at(tmem_empty_at + 8 * b, ((it >> 1) & 1u) ^ 1u, abort_flag, p.err);
-            if (__any_sync(0xffffffffu, !got)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after_sync();
-            const uint64_t step = static_cast<uint64_t>(s * (kStageBytes >> 4));
-            if (elect_one()) {
-#pragma unroll
-              for (int kk = 0; kk < BK / 32; ++kk) {
-                if (PAIR)
-                  tc_mma_f8_pair(tmem_base + b * BN, da0 + step + kk * 2, db0 + step + kk * 2,
-                                 kIdesc, kk != 0 ? 1u : 0u);
-                else
-                  tc_mma_f8(tmem_base + b * BN, da0 + step + kk * 2, db0 + step + kk * 2, kIdesc,
-                            kk != 0 ? 1u : 0u);
-              }
-              if (PAIR)
-                tc_commit_pair_multicast(&tail->done[s], 0x3);
-              else
-                tc_commit(&tail->done[s]);
-            }
-            __syncwarp();
-            issued = true;
-            if (++s == STAGES) {
-              s = 0;
-              parity ^= 1u;
-            }
+      uint32_t it = 0;
+      bool ok = true, issued = false;
+      // K-major: 8-row groups 1024 B apart.  A stage, and 32 B for each step of
+      // 32 of k, only move the address field: the descriptors are sums.
+      const uint64_t da0 = smem_desc_sw128(smem_u32(smem), 16, 1024);
+      const uint64_t db0 = smem_desc_sw128(smem_u32(smem) + kStageBytesA, 16, 1024);
+      for (int t = first; t < tiles && ok; t += stride) {
+        for (int kb = kb0; kb < kb1; ++kb, ++it) {
+          const uint32_t s = it % STAGES, b = it & 1u;
+          const bool got =
+              mbar_wait_at(full_at + 8 * s, (it / STAGES) & 1u, abort_flag, p.err) &&
+              mbar_wait_at(tmem_empty_at + 8 * b, ((it >> 1) & 1u) ^ 1u, abort_flag, p.err);
+          if (__any_sync(0xffffffffu, !got)) {
+            ok = false;
+            break;
           }
-        }
-        if (ok && PAIR) {
-          // no arrival of the odd CTA is still on its way at exit
-          for (uint32_t j = it > 2 ? it - 2 : 0u; j < it; ++j)
-            if (!mbar_wait_at(tmem_empty_at + 8 * (j & 1u), (j >> 1) & 1u, abort_flag, p.err)) break;
-        } else if (!ok && issued) {
+          tc_fence_after_sync();
+          const uint64_t step = static_cast<uint64_t>(s * (kStageBytes >> 4));
           if (elect_one()) {
-            if (PAIR)
-              tc_commit_pair(&tail->drain);
-            else
-              tc_commit(&tail->drain);
+#pragma unroll
+            for (int kk = 0; kk < BK / 32; ++kk)
+              tc_mma_f8(tmem_base + b * BN, da0 + step + kk * 2, db0 + step + kk * 2, kIdesc,
+                        kk != 0 ? 1u : 0u);
+            tc_commit(&tail->done[s]);
           }
           __syncwarp();
-          mbar_drain_wait(&tail->drain, 0);
+          issued = true;
         }
+      }
+      if (!ok && issued) {
+        if (elect_one()) tc_commit(&tail->drain);
+        __syncwarp();
+        mbar_drain_wait(&tail->drain, 0);
       }
       __syncwarp();
     } else if (warp == 2) {
@@ -466,26 +384,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       const int nb = (p.N + kFp8Block - 1) / kFp8Block;
       for (int t = first; t < tiles && ok; t += stride) {
-        const GroupTile w = cta_tile<PAIR>(group_tile(groups, t, tiles_n, p.band, p.tile_rows, g), rank);
+        const GroupTile w = group_tile(groups, t, tiles_n, p.band, p.tile_rows, g);
         const int col0 = ROWS ? w.tn * BN : w.tn * 2;        // first scale of B,
         const int cols = min(ROWS ? BN : 2, (ROWS ? p.N : nb) - col0);  // and how many
         const float* sa = p.sa + kb0 * p.ld_sa + w.row0;
         const float* sb = p.sb + w.group * p.stride_sb + kb0 * p.ld_sb + col0;
         for (int kb = kb0; kb < kb1; ++kb, ++it, sa += p.ld_sa, sb += p.ld_sb) {
-          const uint32_t s = it % SSTAGES, round = it / SSTAGES;
-          const bool got = mbar_wait_at(sempty_at + 8 * s, (round & 1u) ^ 1u, abort_flag, p.err);
+          const uint32_t s = it % STAGES;
+          const bool got =
+              mbar_wait_at(done_at + 8 * s, ((it / STAGES) & 1u) ^ 1u, abort_flag, p.err);
           if (__any_sync(0xffffffffu, !got)) {
             ok = false;
             break;
           }
-          const uint32_t dst = scales_at + s * (kScaleFloats * 4);
+          const uint32_t dst = scales_at + it % SSLOTS * (kScaleFloats * 4);
 #pragma unroll 1
           for (int i = lane; i < BM; i += 32)
             cp_async_4_at(dst + 4 * i, i < w.rows ? sa + i : p.sa, i < w.rows ? 4u : 0u);
 #pragma unroll 1
           for (int i = lane; i < (ROWS ? BN : 2); i += 32)
             cp_async_4_at(dst + 4 * (BM + i), i < cols ? sb + i : p.sb, i < cols ? 4u : 0u);
-          cp_async_mbar_arrive_noinc(&tail->sfull[s]);
+          cp_async_mbar_arrive_noinc(&tail->full[s]);
         }
       }
       cp_async_wait_all();
@@ -497,76 +416,71 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ---------------------------------------------------------------- sums
-    regs_take<many_regs(ROWS)>();
+    regs_take<kManyRegs>();
     const int quarter = warp & 3;         // TMEM lanes this warp may access
     const int half = (warp - 4) >> 2;     // which 128 columns
     const int row = quarter * 32 + lane;
     uint8_t* stage = out_stage + (warp - 4) * kOutBytes;
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
                                static_cast<uint32_t>(half * kWarpCols);
-    uint32_t it = 0, ds = 0, dparity = 0;  // ds, dparity: the block's stage of the ring
+    uint32_t it = 0, slot = 0;  // slot: it % SSLOTS
     int g = 0;
     bool ok = true;
     for (int t = first; t < tiles && ok; t += stride) {
       // a warp without rows or columns only keeps the rings moving
-      const bool live =
-          live_rows(cta_tile<PAIR>(group_tile(groups, t, tiles_n, p.band, p.tile_rows, g), rank),
-                    quarter, half, p.N) > 0;
+      const bool live = live_rows(group_tile(groups, t, tiles_n, p.band, p.tile_rows, g), quarter,
+                                  half, p.N) > 0;
       uint64_t acc[kWarpCols / 2];
 #pragma unroll
       for (int i = 0; i < kWarpCols / 2; ++i) acc[i] = 0ull;
       for (int kb = kb0; kb < kb1; ++kb, ++it) {
-        const uint32_t s = it % SSTAGES, b = it & 1u;
-        const bool got = mbar_wait_at(sfull_at + 8 * s, (it / SSTAGES) & 1u, abort_flag, p.err) &&
-                         mbar_wait_at(done_at + 8 * ds, dparity, abort_flag, p.err);
-        if (__any_sync(0xffffffffu, !got)) {
-          ok = false;
-          break;
-        }
-        if (++ds == STAGES) {
-          ds = 0;
-          dparity ^= 1u;
-        }
+        const uint32_t b = it & 1u;
+        // All lanes ask the same barrier in the same instruction and get the
+        // same answer.
+        ok = mbar_wait_at(done_at + 8 * (it % STAGES), (it / STAGES) & 1u, abort_flag, p.err);
+        if (!ok) break;
+        const uint32_t sc = scales_at + slot * (kScaleFloats * 4);
+        if (++slot == SSLOTS) slot = 0;
         tc_fence_after_sync();
         if (live) {
-          const uint32_t sc = scales_at + s * (kScaleFloats * 4);
-          float f1 = ld_shared_f32(sc + 4 * row);
-          if (!ROWS) f1 *= ld_shared_f32(sc + 4 * (BM + half));
-          // the columns' scales (ROWS)
-          const float* sb = tail->scales[s] + BM + half * kWarpCols;
-          const uint64_t f = f32x2(f1, f1);
           const uint32_t taddr = lane_base + b * BN;
+          // 32 and 16 columns in turn, two loads on their way at a time: 128
+          // sums and 48 values fit the registers, and what the accumulator's
+          // release waits for is three loads' latency.
           uint32_t ra[32], rb[16];
           tmem_ld_32x32b_x32(taddr, ra);
           tmem_ld_32x32b_x16(taddr + 32, rb);
+          // this thread's row's scale, and (ROWS: those of) the columns
+          float f1 = ld_shared_f32(sc + 4 * row);
+          if (!ROWS) f1 *= ld_shared_f32(sc + 4 * (BM + half));
+          const uint32_t sb = sc + 4 * (BM + half * kWarpCols);
+          const uint64_t f = f32x2(f1, f1);
           tc_wait_ld();
           add_scaled<ROWS>(acc, ra, f, sb);
           tmem_ld_32x32b_x32(taddr + 48, ra);
-          add_scaled<ROWS>(acc + 16, rb, f, sb + 32);
+          add_scaled<ROWS>(acc + 16, rb, f, sb + 128);
           tmem_ld_32x32b_x16(taddr + 80, rb);
           tc_wait_ld();
-          add_scaled<ROWS>(acc + 24, ra, f, sb + 48);
+          add_scaled<ROWS>(acc + 24, ra, f, sb + 192);
           tmem_ld_32x32b_x32(taddr + 96, ra);
-          add_scaled<ROWS>(acc + 40, rb, f, sb + 80);
+          add_scaled<ROWS>(acc + 40, rb, f, sb + 320);
           tc_wait_ld();
+          // The accumulator has been read, and by rows the scales are used up:
+          // the MMAs of the block after next may overwrite it while its last
+          // columns are added.
+          if (ROWS) add_scaled<ROWS>(acc + 48, ra, f, sb + 384);
           tc_fence_before_sync();
           __syncwarp();
-          if (lane == 0) release<PAIR>(tmem_empty_at + 8 * b);
-          add_scaled<ROWS>(acc + 48, ra, f, sb + 96);
-          __syncwarp();
-          if (lane == 0) mbar_arrive_at(sempty_at + 8 * s);
+          if (lane == 0) mbar_arrive_at(tmem_empty_at + 8 * b);
+          if (!ROWS) add_scaled<ROWS>(acc + 48, ra, f, sb + 384);
         } else {
           tc_fence_before_sync();
           __syncwarp();
-          if (lane == 0) {
-            release<PAIR>(tmem_empty_at + 8 * b);
-            mbar_arrive_at(sempty_at + 8 * s);
-          }
+          if (lane == 0) mbar_arrive_at(tmem_empty_at + 8 * b);
         }
       }
       // found again rather than kept: the loop above needs the registers
-      const GroupTile w =
-          cta_tile<PAIR>(group_tile(groups, t, tiles_n, p.band, p.tile_rows, g), rank);
+      const GroupTile w = group_tile(groups, t, tiles_n, p.band, p.tile_rows, g);
       if (CLUSTER) {
         // This CTA's k-blocks are done, and with them every use of the ring:
         // its sums go there, 1 KB per row, 16-byte pieces swizzled by row.
@@ -617,21 +531,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before_sync();
   __syncthreads();
-  // Neither CTA of a pair releases TMEM or exits while the pair's MMAs or
-  // copies can still touch it.
-  if (PAIR) cluster_sync();
   tc_fence_after_sync();
-  if (warp == 1) {
-    if (PAIR)
-      tmem_dealloc_pair(tmem_base, kTmemCols);
-    else
-      tmem_dealloc(tmem_base, kTmemCols);
-  }
+  if (warp == 1) tmem_dealloc(tmem_base, kTmemCols);
 }
 
-// Clusters of S CTAs (pairs for S == 2 of kPair) that can be resident at once on
-// the current device; 0 if unknown.
-template <int FORM>
+// Clusters of S CTAs that can be resident at once on the current device; 0 if
+// unknown.
 int max_clusters(int S) {
   static std::atomic<int> cache[64][9];
   int dev = 0;
@@ -639,7 +544,7 @@ int max_clusters(int S) {
   const int known = cache[dev][S].load(std::memory_order_relaxed);
   if (known != 0) return known;
   int n = 0;
-  if (ops_allow_smem<fp8_kernel<false, FORM>>(kSmemBytes) == cudaSuccess) {
+  if (ops_allow_smem<fp8_kernel<false, true>>(kSmemBytes) == cudaSuccess) {
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -651,7 +556,7 @@ int max_clusters(int S) {
     cfg.dynamicSmemBytes = kSmemBytes;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, fp8_kernel<false, FORM>, &cfg) != cudaSuccess) n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, fp8_kernel<false, true>, &cfg) != cudaSuccess) n = 0;
   }
   cudaGetLastError();
   if (n > 0) cache[dev][S].store(n, std::memory_order_relaxed);
@@ -665,7 +570,7 @@ int choose_split(int64_t tiles, int num_kb, int num_sms) {
   int best = 1;
   double cost = num_kb;
   for (int s = 2; s <= 8 && s <= num_kb; ++s) {
-    if (tiles * s > num_sms || tiles > max_clusters<kSplit>(s)) continue;
+    if (tiles * s > num_sms || tiles > max_clusters(s)) continue;
     const double c = (num_kb + s - 1) / s + 5.0;
     if (c < cost) {
       cost = c;
@@ -723,13 +628,13 @@ int64_t staged_bytes(const Operand& o) {
   return (o.count * o.rows * ((o.cols + 15) / 16 * 16) + 255) / 256 * 256;
 }
 
-template <int FORM>
+template <bool CLUSTER>
 gemm_status_t launch(bool by_rows, int64_t ctas, int cluster, const Fp8Args& a,
                      const CUtensorMap& tmA, const CUtensorMap& tmB, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>(ctas));
   return abi_from_cuda(
-      by_rows ? ops_launch<fp8_kernel<true, FORM>>(grid, kThreads, kSmemBytes, cluster, s, a, tmA, tmB)
-              : ops_launch<fp8_kernel<false, FORM>>(grid, kThreads, kSmemBytes, cluster, s, a, tmA,
+      by_rows ? ops_launch<fp8_kernel<true, CLUSTER>>(grid, kThreads, kSmemBytes, cluster, s, a, tmA, tmB)
+              : ops_launch<fp8_kernel<false, CLUSTER>>(grid, kThreads, kSmemBytes, cluster, s, a, tmA,
                                                     tmB));
 }
 
@@ -784,13 +689,7 @@ gemm_status_t run(int64_t G, const int32_t* offsets, int64_t M, int64_t N, int64
   a.d_vec = !ops_misaligned(D, 16) && ldd % (16 / d_bytes) == 0;
   a.err = err;
   a.band = 8;
-  // CTA pairs (half the operand bytes written to and read from each SM's
-  // shared memory per product) for long k loops over several rounds of tiles:
-  // 468 against 488 us at 8192^3, but 60 against 58 us at 3000 x 5000 x 1999
-  // and 182 against 172 us for 16384 rows over 32 experts (4096 x 2048).
-  const int64_t pair_tiles = ((M + 2 * BM - 1) / (2 * BM)) * ((N + BN - 1) / BN);
-  const bool pair = !grouped && K >= 4096 && pair_tiles >= 2 * sms;
-  a.tile_rows = pair ? 2 * BM : M >= BM ? BM : (M > 32 ? (M > 64 ? BM : 64) : (M > 16 ? 32 : 16));
+  a.tile_rows = M >= BM ? BM : (M > 32 ? (M > 64 ? BM : 64) : (M > 16 ? 32 : 16));
 
   std::unique_lock<std::mutex> lock;
   CUtensorMap tmA{}, tmB{};
@@ -807,10 +706,10 @@ gemm_status_t run(int64_t G, const int32_t* offsets, int64_t M, int64_t N, int64
       if (e != cudaSuccess) return abi_from_cuda(e);
     }
     const int64_t da[2] = {K, M}, ta[1] = {oa.ld};
-    const uint32_t ba[2] = {BK, static_cast<uint32_t>(pair ? BM : a.tile_rows)};
+    const uint32_t ba[2] = {BK, static_cast<uint32_t>(a.tile_rows)};
     // one matrix: any stride describes it
     const int64_t db[3] = {K, N, G}, tb[2] = {ob.ld, G > 1 ? ob.stride : ob.ld * N};
-    const uint32_t bb[3] = {BK, static_cast<uint32_t>(b_rows(pair ? kPair : kSingle)), 1};
+    const uint32_t bb[3] = {BK, BN, 1};
     if (!abi_encode_tiled(&tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, oa.p, da, ta, ba) ||
         !abi_encode_tiled(&tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, ob.p, db, tb, bb))
       return GEMM_ERR_LAUNCH;
@@ -821,14 +720,9 @@ gemm_status_t run(int64_t G, const int32_t* offsets, int64_t M, int64_t N, int64
   const int64_t tiles = row_tiles * tiles_n;
   if (tiles + sms > kOpsMaxDim) return GEMM_ERR_UNSUPPORTED;
   const bool by_rows = b_block == GEMM_BLOCK_ROWS;
-  if (pair) {
-    const int64_t fit = max_clusters<kPair>(2) > 0 ? max_clusters<kPair>(2) : sms / 2;
-    const int64_t ctas = 2 * (tiles < fit ? tiles : fit);
-    return launch<kPair>(by_rows, ctas, 2, a, tmA, tmB, s);
-  }
   a.cluster = grouped ? 1 : choose_split(tiles, a.num_kb, sms);
-  if (a.cluster > 1) return launch<kSplit>(by_rows, tiles * a.cluster, a.cluster, a, tmA, tmB, s);
-  return launch<kSingle>(by_rows, tiles < sms ? tiles : sms, 1, a, tmA, tmB, s);
+  if (a.cluster > 1) return launch<true>(by_rows, tiles * a.cluster, a.cluster, a, tmA, tmB, s);
+  return launch<false>(by_rows, tiles < sms ? tiles : sms, 1, a, tmA, tmB, s);
 }
 
 }  // namespace
