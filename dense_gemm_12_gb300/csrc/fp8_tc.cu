@@ -31,7 +31,10 @@
 // (2.6 PFLOP/s), 64 us at 4096^3 (2.1), against 499 and 75 us before those
 // three.  CTA pairs, which halve the operands' traffic, came to the same (436
 // us): each block's accumulator then travels through two CTAs' barriers.  Scales
-// for each row of B cost a second product per element: 97 us at 4096^3.
+// for each row of B cost a second product per element and all scales in all
+// threads: 98 us at 4096^3.  Reading the accumulator with four threads to a row,
+// each with a quarter of the scales, took 102 us, and the two halves of the
+// columns half a block apart 100 us.
 //
 // Few tiles: the CTAs of a cluster split a tile's k-blocks and add their sums
 // through distributed shared memory, in k order.  Rows of A beyond a group's

@@ -14,8 +14,12 @@
 //     accumulator rows that are not written.
 //   * in the weight gradient the ragged direction is the one summed over, so
 //     rows past the group's end must not reach the sum, whatever they hold
-//     (NaN included): the issuing warp zeroes them in shared memory, in both
-//     operands, before the MMAs of a group's last block.
+//     (NaN included): of a group's last block the issuing warp runs only the
+//     steps of 16 rows that the group reaches, and zeroes the rest of the last
+//     one in shared memory, in both operands (8001 rows of 24 groups, 1024 x
+//     2048: 44.4 us against 45.6 with the whole block zeroed and summed).
+//     Groups are taken as they come: by falling size it took 49.0 us, since the
+//     small ones then write their matrices at once, with nothing to compute.
 //   * a weight gradient's group without rows is written as beta dB[g].
 #include "groups.cuh"
 #include "ops.cuh"
@@ -486,11 +490,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         uint8_t* stage = smem + s * kStageBytes;
-        if (kGrad && kb == w.num_kb - 1 && w.last < BK) {
-          // Rows of the next group: row k of a box is its bytes 128 k ..
-          // 128 k + 127, whatever the swizzle does inside them.
-          const int pieces = (BK - w.last) * 8;
-#pragma unroll 1
+        // The last block of a weight gradient: only the steps of 16 rows that
+        // the group reaches, its last step's other rows (of the next group)
+        // zeroed.  Row k of a box is its bytes 128 k .. 128 k + 127, whatever
+        // the swizzle does inside them.
+        const int steps = kGrad && kb == w.num_kb - 1 ? (w.last + 15) / 16 : BK / 16;
+        if (kGrad && kb == w.num_kb - 1 && (w.last & 15) != 0) {
+          const int pieces = (steps * 16 - w.last) * 8;
+#pragma unroll
           for (int box = 0; box < (BM + BN) / 64; ++box) {
             uint4* z = reinterpret_cast<uint4*>(stage + box * kBoxBytes + w.last * 128);
             for (int i = lane; i < pieces; i += 32) z[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -503,6 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < BK / 16; ++kk) {
+            if (kGrad && kk >= steps) break;
             if (PAIR)
               tc_mma_f16_pair(d_tmem, da0 + at + kk * kStepA, db0 + at + kk * kStepB, kIdesc,
                               (kb != 0 || kk != 0) ? 1u : 0u);
