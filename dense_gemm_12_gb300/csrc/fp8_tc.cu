@@ -510,21 +510,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         const GroupTile w = group_tile(groups, first, tiles_n, p.band, p.tile_rows, g);
         const int c0 = part * (BN / 4) / split, c1 = (part + 1) * (BN / 4) / split;
         const int width = c1 - c0;
-        const uint32_t base = smem_u32(smem);
-        for (int i = threadIdx.x - 128; i < w.rows * width; i += kSumThreads) {
-          const int r = i / width, c = c0 + i - r * width;
-          const int col = w.tn * BN + c * 4;
-          if (col >= p.N) continue;
-          const uint32_t at = base + static_cast<uint32_t>((r * (BN / 4) + (c ^ (r & 7))) * 16);
-          float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          for (int src = 0; src < split; ++src) {
-            const float4 v = ld_shared_cluster_v4(mapa_shared(at, static_cast<uint32_t>(src)));
-            s.x += v.x;
-            s.y += v.y;
-            s.z += v.z;
-            s.w += v.w;
+        // 8, 16 or 32 threads to a row's pieces of this CTA; the rows of a thread
+        // are a multiple of 8 apart, so their swizzle is the same.
+        const int lanes = width <= 8 ? 8 : (width <= 16 ? 16 : 32);
+        const int tid = static_cast<int>(threadIdx.x) - 128;
+        const int c = c0 + (tid & (lanes - 1)), step = kSumThreads / lanes;
+        const int r0 = tid / lanes, col = w.tn * BN + c * 4;
+        const uint32_t at = smem_u32(smem) + static_cast<uint32_t>((c ^ (r0 & 7)) * 16);
+        if (c < c1 && col < p.N) {
+          // (Four rows at a time took longer: 9.9 us against 8.5 for four CTAs'
+          // parts of 128 x 4096 x 1024.)
+          for (int r = r0; r < w.rows; r += step) {
+            float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int src = 0; src < split; ++src) {
+              const float4 v =
+                  ld_shared_cluster_v4(mapa_shared(at + r * (BN * 4), static_cast<uint32_t>(src)));
+              sum.x += v.x;
+              sum.y += v.y;
+              sum.z += v.z;
+              sum.w += v.w;
+            }
+            store4(p, w.row0 + r, col, sum);
           }
-          store4(p, w.row0 + r, col, s);
         }
       }
       __syncwarp();
@@ -568,13 +575,16 @@ int max_clusters(int S) {
 
 // CTAs that split each tile's k-blocks, when all tiles fit in one round: the
 // S whose longest share of k-blocks plus the cost of adding S sums is least.
-// In k-block times (~0.27 us); exchanging and adding the sums costs about 5.
-int choose_split(int64_t tiles, int num_kb, int num_sms) {
+// In k-block times (0.4 us, 0.75 with a scale per row of B); exchanging and
+// adding the sums costs 6 or 4 of them (128 x 4096 x 1024 in four parts 8.5 us
+// against 8.0 whole, 512 x 2048 x 2048 10.3 against 11.1; with a scale per row
+// 1000^3 10.3 against 13.2).
+int choose_split(int64_t tiles, int num_kb, int num_sms, bool by_rows) {
   int best = 1;
   double cost = num_kb;
   for (int s = 2; s <= 8 && s <= num_kb; ++s) {
     if (tiles * s > num_sms || tiles > max_clusters(s)) continue;
-    const double c = (num_kb + s - 1) / s + 5.0;
+    const double c = (num_kb + s - 1) / s + (by_rows ? 4.0 : 6.0);
     if (c < cost) {
       cost = c;
       best = s;
@@ -723,7 +733,7 @@ gemm_status_t run(int64_t G, const int32_t* offsets, int64_t M, int64_t N, int64
   const int64_t tiles = row_tiles * tiles_n;
   if (tiles + sms > kOpsMaxDim) return GEMM_ERR_UNSUPPORTED;
   const bool by_rows = b_block == GEMM_BLOCK_ROWS;
-  a.cluster = grouped ? 1 : choose_split(tiles, a.num_kb, sms);
+  a.cluster = grouped ? 1 : choose_split(tiles, a.num_kb, sms, by_rows);
   if (a.cluster > 1) return launch<true>(by_rows, tiles * a.cluster, a.cluster, a, tmA, tmB, s);
   return launch<false>(by_rows, tiles < sms ? tiles : sms, 1, a, tmA, tmB, s);
 }
