@@ -14,10 +14,11 @@
 //     accumulator rows that are not written.
 //   * in the weight gradient the ragged direction is the one summed over, so
 //     rows past the group's end must not reach the sum, whatever they hold
-//     (NaN included): of a group's last block the issuing warp runs only the
-//     steps of 16 rows that the group reaches, and zeroes the rest of the last
-//     one in shared memory, in both operands (8001 rows of 24 groups, 1024 x
-//     2048: 44.4 us against 45.6 with the whole block zeroed and summed).
+//     (NaN included): of a group's last block only the steps of 16 rows that
+//     the group reaches run, and the rest of the last one is zeroed in shared
+//     memory, in both operands (8001 rows of 24 groups, 1024 x 2048: 44.4 us
+//     against 45.6 with the whole block zeroed and summed) -- by the issuing
+//     warp, or in a pair by a warp of each CTA's own.
 //     Groups are taken as they come: by falling size it took 49.0 us, since the
 //     small ones then write their matrices at once, with nothing to compute.
 //   * a weight gradient's group without rows is written as beta dB[g].
@@ -37,6 +38,8 @@ constexpr int stage_bytes(bool pair) { return kStageBytesA + BK * b_cols(pair) *
 constexpr int ring_stages(bool pair) { return kRingBytes / stage_bytes(pair); }        // 4 or 6
 constexpr int kMaxStages = 6;
 constexpr int kThreads = 192;
+constexpr int kRaggedThreads = 224;  // a pair's weight gradient: a warp for ragged ends
+constexpr int kRaggedWarp = 6;
 constexpr int kOutThreads = 128;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOutBarAny = 1;
@@ -66,6 +69,8 @@ struct __align__(8) Tail {
   uint64_t empty[kMaxStages];
   uint64_t tmem_full[2];
   uint64_t tmem_empty[2];
+  uint64_t landed[kMaxStages];  // a pair's weight gradient, a group's ragged last
+  uint64_t ragged[kMaxStages];  // block: it is here / its end is zeroed in both CTAs
   uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
@@ -102,7 +107,8 @@ __device__ __forceinline__ Item item_of(const GroupedArgs& p, const GroupTable& 
     w.last = BK;
     return w;
   }
-  const int tiles_m = (p.M + BM - 1) / BM;
+  constexpr int kTileM = PAIR ? 2 * BM : BM;
+  const int tiles_m = (p.M + kTileM - 1) / kTileM;
   const int per = tiles_m * tiles_n;
   w.group = t / per;
   const int local = t - w.group * per;
@@ -111,13 +117,32 @@ __device__ __forceinline__ Item item_of(const GroupedArgs& p, const GroupTable& 
   const int high = min(tiles_m - b * p.band, p.band);
   const int in_band = local - b * per_band;
   w.tn = in_band / high;
-  w.m0 = (b * p.band + in_band % high) * BM;
+  w.m0 = (b * p.band + in_band % high) * kTileM + (PAIR ? rank * BM : 0);
   w.row0 = tab.row[w.group];
   w.rows = min(BM, p.M - w.m0);
   const int n = p.product ? tab.row[w.group + 1] - w.row0 : 0;
   w.num_kb = (n + BK - 1) / BK;
   w.last = n - (w.num_kb - 1) * BK;
   return w;
+}
+
+// Whether block kb of a weight gradient holds rows of the next group in its
+// last step.
+__device__ __forceinline__ bool is_ragged(const Item& w, int kb) {
+  return kb == w.num_kb - 1 && (w.last & 15) != 0;
+}
+
+// Zeroes those rows in a stage of `boxes` boxes; all lanes of a warp.  Row k of
+// a box is its bytes 128 k .. 128 k + 127, whatever the swizzle does inside them.
+__device__ __forceinline__ void zero_ragged(uint8_t* stage, const Item& w, int boxes) {
+  const int pieces = (16 - (w.last & 15)) * 8;
+#pragma unroll
+  for (int box = 0; box < boxes; ++box) {
+    uint4* z = reinterpret_cast<uint4*>(stage + box * kBoxBytes + w.last * 128);
+    for (int i = threadIdx.x & 31; i < pieces; i += 32) z[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
 }
 
 // 32 accumulator rows x 64 columns of this warp (r, s: 32 columns each) as
@@ -323,13 +348,13 @@ struct Zeros {
   __device__ __forceinline__ void wait() const {}
 };
 
-// PAIR (not for the weight gradient): two CTAs share a 256 x 256 tile and one
-// stream of M = 256 MMAs, barriers as in the dense pair kernel (bf16_tc.cu).
+// PAIR: two CTAs share a 256 x 256 tile and one stream of M = 256 MMAs,
+// barriers as in the dense pair kernel (bf16_tc.cu).
 // Each SM's shared memory then takes 32 KB of operands per k-block and gives
 // the tensor core as much, instead of 48 KB each way: with one CTA per tile
 // that traffic (768 cycles at 128 B per cycle) outlasts the MMAs (512).
 template <int MODE, bool PAIR>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(MODE == kWeightGrad && PAIR ? kRaggedThreads : kThreads, 1)
     grouped_kernel(const __grid_constant__ GroupedArgs p, const __grid_constant__ CUtensorMap tmA,
                    const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmD) {
@@ -341,7 +366,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   constexpr bool kGrad = MODE == kWeightGrad;
-  static_assert(!(kGrad && PAIR), "the weight gradient runs on single CTAs");
   constexpr int STAGES = ring_stages(PAIR), kStageBytes = stage_bytes(PAIR);
   const int rank = PAIR ? static_cast<int>(cluster_cta_rank() & 1u) : 0;
   const int first = static_cast<int>(blockIdx.x) / (PAIR ? 2 : 1);
@@ -353,6 +377,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&tail->full[s], 1);
       mbar_init(&tail->empty[s], 1);
+      if (kGrad && PAIR) {
+        mbar_init(&tail->landed[s], 1);
+        mbar_init(&tail->ragged[s], 2);
+      }
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tail->tmem_full[b], 1);
@@ -385,7 +413,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem_base = tail->tmem_base;
   const GroupTable& tab = tail->groups;
   const int tiles_n = (p.N + BN - 1) / BN;
-  const int tiles = kGrad ? p.groups * ((p.M + BM - 1) / BM) * tiles_n
+  constexpr int kTileM = PAIR ? 2 * BM : BM;  // of the weight gradient
+  const int tiles = kGrad ? p.groups * ((p.M + kTileM - 1) / kTileM) * tiles_n
                           : tab.tile[p.groups] * tiles_n;
   const int num_kb = p.product ? (p.K + BK - 1) / BK : 0;
 
@@ -409,8 +438,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint8_t* sa = smem + s * kStageBytes;
           uint8_t* sb = sa + kStageBytesA;
           uint64_t* bar = &tail->full[s];
+          if (kGrad && PAIR && is_ragged(w, kb)) {
+            // to this CTA's own warp for ragged ends, which passes it on
+            if (rank == 0) mbar_arrive(bar);
+            bar = &tail->landed[s];
+            mbar_arrive_expect_tx(bar, kStageBytes);
+            const int k = w.row0 + kb * BK;
+#pragma unroll
+            for (int j = 0; j < BM / 64; ++j)
+              tma_load_2d(sa + j * kBoxBytes, &tmA, w.m0 + j * 64, k, bar);
+#pragma unroll
+            for (int j = 0; j < BN / 128; ++j)
+              tma_load_2d(sb + j * kBoxBytes, &tmB, w.tn * BN + rank * (BN / 2) + j * 64, k, bar);
+            continue;
+          }
           if (rank == 0) mbar_arrive_expect_tx(bar, bytes);
-          if (PAIR) {
+          if (PAIR && kGrad) {
+            const uint32_t full = full0 + s * static_cast<uint32_t>(sizeof(uint64_t));
+            const int k = w.row0 + kb * BK;
+#pragma unroll
+            for (int j = 0; j < BM / 64; ++j)
+              tma_load_2d_pair(sa + j * kBoxBytes, &tmA, w.m0 + j * 64, k, full);
+#pragma unroll
+            for (int j = 0; j < BN / 128; ++j)
+              tma_load_2d_pair(sb + j * kBoxBytes, &tmB, w.tn * BN + rank * (BN / 2) + j * 64, k, full);
+          } else if (PAIR) {
             const uint32_t full = full0 + s * static_cast<uint32_t>(sizeof(uint64_t));
             const int n0 = w.tn * BN + rank * (BN / 2);
             tma_load_2d_pair(sa, &tmA, kb * BK, w.row0, full);
@@ -467,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t db0 = MODE == kTransB ? smem_desc_sw128(sb0, 16, 1024)
                                          : smem_desc_sw128(sb0, kBoxBytes, 1024);
     constexpr uint32_t kStepA = (kGrad ? 2048 : 32) >> 4, kStepB = (MODE == kTransB ? 32 : 2048) >> 4;
-    uint32_t it = 0, j = 0;
+    uint32_t it = 0, j = 0, ragged_parity = 0;
     int g = 0;
     bool ok = true, issued = false;
     for (int t = first; t < tiles && ok; t += stride) {
@@ -489,21 +541,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = false;
           break;
         }
-        uint8_t* stage = smem + s * kStageBytes;
-        // The last block of a weight gradient: only the steps of 16 rows that
-        // the group reaches, its last step's other rows (of the next group)
-        // zeroed.  Row k of a box is its bytes 128 k .. 128 k + 127, whatever
-        // the swizzle does inside them.
+        // of a weight gradient's last block only the steps of 16 rows that the
+        // group reaches
         const int steps = kGrad && kb == w.num_kb - 1 ? (w.last + 15) / 16 : BK / 16;
-        if (kGrad && kb == w.num_kb - 1 && (w.last & 15) != 0) {
-          const int pieces = (steps * 16 - w.last) * 8;
-#pragma unroll
-          for (int box = 0; box < (BM + BN) / 64; ++box) {
-            uint4* z = reinterpret_cast<uint4*>(stage + box * kBoxBytes + w.last * 128);
-            for (int i = lane; i < pieces; i += 32) z[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (kGrad && PAIR && is_ragged(w, kb)) {
+          got = mbar_wait_late(&tail->ragged[s], ragged_parity >> s & 1u, abort_flag, p.err);
+          ragged_parity ^= 1u << s;
+          if (__any_sync(0xffffffffu, !got)) {
+            ok = false;
+            break;
           }
-          fence_proxy_async_smem();
-          __syncwarp();
+          fence_acq_rel_cluster();
+        } else if (kGrad && is_ragged(w, kb)) {
+          zero_ragged(smem + s * kStageBytes, w, (BM + BN) / 64);
         }
         tc_fence_after_sync();
         const uint64_t at = static_cast<uint64_t>(s * (kStageBytes >> 4));
@@ -551,6 +601,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_drain_wait(&tail->drain, 0);
     }
     __syncwarp();
+  } else if (kGrad && PAIR && warp == kRaggedWarp) {
+    // ---------------------------------------------------------- ragged ends
+    // Zeroed in each CTA as soon as the block has landed there, well before its
+    // MMAs; the even CTA's issuer hears of both.
+    uint32_t it = 0, parity = 0;  // bits by stage
+    int g = 0;
+    const uint32_t ragged0 = mapa_shared(smem_u32(&tail->ragged[0]), 0);
+    for (int t = first; t < tiles; t += stride) {
+      const Item w = item_of<MODE, PAIR>(p, tab, t, tiles_n, num_kb, rank, g);
+      it += static_cast<uint32_t>(w.num_kb);
+      if (w.num_kb == 0 || !is_ragged(w, w.num_kb - 1)) continue;
+      const uint32_t s = (it - 1) % STAGES;
+      const bool got = mbar_wait_late(&tail->landed[s], parity >> s & 1u, abort_flag, p.err);
+      parity ^= 1u << s;
+      if (__any_sync(0xffffffffu, !got)) break;
+      zero_ragged(smem + s * kStageBytes, w, (BM + BN / 2) / 64);
+      if (lane == 0) mbar_arrive_cluster(ragged0 + s * static_cast<uint32_t>(sizeof(uint64_t)));
+    }
   } else {
     // -------------------------------------------------------------- output
     const int quarter = warp & 3;  // TMEM lanes this warp may access
@@ -844,8 +912,10 @@ gemm_status_t gemm_bf16gemm_grouped_wgrad(int64_t G, const int32_t* offsets, int
       return GEMM_ERR_INVALID_VALUE;
     if (ops_misaligned(A, 2) || ops_misaligned(dD, 2)) return GEMM_ERR_MISALIGNED;
   }
-  const int64_t per = ((K + BM - 1) / BM) * ((N + BN - 1) / BN);
-  if (G > kMaxGroups || G * per > kOpsMaxDim / 2) return GEMM_ERR_UNSUPPORTED;
+  const int64_t tiles_n = (N + BN - 1) / BN;
+  const int64_t tiles_1 = G * ((K + BM - 1) / BM) * tiles_n;
+  const int64_t tiles_2 = G * ((K + 2 * BM - 1) / (2 * BM)) * tiles_n;
+  if (G > kMaxGroups || tiles_1 > kOpsMaxDim / 2) return GEMM_ERR_UNSUPPORTED;
   int sms = 0;
   uint32_t* err = nullptr;
   gemm_status_t st = abi_device(&sms, &err);
@@ -879,11 +949,20 @@ gemm_status_t gemm_bf16gemm_grouped_wgrad(int64_t G, const int32_t* offsets, int
                   s, lock, &tmA, &tmB);
     if (st != GEMM_OK) return st;
   }
-  const int64_t tiles = G * per;
-  const dim3 grid(static_cast<unsigned>(tiles < sms ? tiles : sms));
-  return abi_from_cuda(
-      ops_launch<grouped_kernel<kWeightGrad, false>>(grid, kThreads, kSmemBytes, 1, s, a, tmA, tmB,
-                                                           tmD));
+  // CTA pairs as for the forward product, but from 512 rows a group on: before
+  // that writing the matrices is most of the time, and a pair's tile of 256 rows
+  // of them leaves in one piece (8192 rows, 1024 x 2048: 16 groups 33.0 us
+  // against 36.2, 64 groups of 78 rows, 512 x 1024, 32.2 against 28.4).
+  const int pairs = max_pairs();
+  if (pairs > 0 && rows >= 512 * G &&
+      2 * ((tiles_2 + pairs - 1) / pairs) < 3 * ((tiles_1 + sms - 1) / sms)) {
+    const dim3 grid(static_cast<unsigned>(2 * (tiles_2 < pairs ? tiles_2 : pairs)));
+    return abi_from_cuda(ops_launch<grouped_kernel<kWeightGrad, true>>(
+        grid, kRaggedThreads, kSmemBytes, 2, s, a, tmA, tmB, tmD));
+  }
+  const dim3 grid(static_cast<unsigned>(tiles_1 < sms ? tiles_1 : sms));
+  return abi_from_cuda(ops_launch<grouped_kernel<kWeightGrad, false>>(
+      grid, kThreads, kSmemBytes, 1, s, a, tmA, tmB, tmD));
 }
 
 }  // extern "C"

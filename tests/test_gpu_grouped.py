@@ -251,3 +251,28 @@ def test_most_groups_and_a_graph():
         graph.replay()
         stream.synchronize()
     assert torch.equal(D, first[0]) and torch.equal(dB, first[1])
+
+
+@pytest.mark.parametrize("counts,start,tail", [([600], 0, 0), ([513, 1, 1537, 0, 1000], 3, 4),
+                                               ([1025, 999], 0, 1), ([16, 2000, 15, 47], 1, 0),
+                                               ([0, 0, 3000], 7, 9)])
+@pytest.mark.parametrize("N,K", [(300, 200), (520, 1024), (256, 129), (2048, 700), (9, 385)])
+def test_weight_gradient_of_long_groups(counts, start, tail, N, K):
+    G, rows = len(counts), start + sum(counts) + tail
+    A = Guarded((rows, K), torch.bfloat16, -K % 8).set(randn(rows, K, seed=6)).t
+    dD = Guarded((rows, N), torch.bfloat16, -N % 8).set(randn(rows, N, seed=7)).t
+    off, ends = offsets_of(counts, start), [start + sum(counts[:i]) for i in range(G + 1)]
+    for out, alpha, beta in (("bf16", 1.0, 0.0), ("f32", 2.0, -0.5)):
+        for keep in (0, 1):  # every other group holds NaN, and the rows of none: neither reaches the rest
+            a, d = A.clone(), dD.clone()
+            a[:start], d[ends[-1]:] = float("nan"), float("nan")
+            for i in range(G):
+                if i % 2 != keep:
+                    a[ends[i]:ends[i + 1]], d[ends[i]:ends[i + 1]] = float("nan"), float("nan")
+            B0 = randn(G, K, N, seed=8, dtype=DTYPE[out])
+            dB = Guarded((G, K, N), DTYPE[out], 8).set(B0 if beta else torch.full_like(B0, float("nan")))
+            g.bf16gemm_grouped_wgrad(a, d, off, dB.t, alpha=alpha, beta=beta)
+            check_device_error()
+            assert dB.clean_outside()
+            for i in range(keep, G, 2):
+                check(dB.t[i], a[ends[i]:ends[i + 1]].t(), d[ends[i]:ends[i + 1]], alpha, beta, B0[i], out)
