@@ -292,7 +292,8 @@ struct GradArgs {
 // the rows that its CTA takes, and the CTA writes them as one row of `part`.
 // C == 0: two passes over the row; dw is left to dweight_kernel.
 template <int C, bool VEC, int TD, int TH, bool RING = false>
-__global__ void __launch_bounds__(kMaxThreads, 1) norm_grad_kernel(const __grid_constant__ GradArgs a) {
+__global__ void __launch_bounds__(RING && C == 1 ? 1024 : kMaxThreads, 1)
+    norm_grad_kernel(const __grid_constant__ GradArgs a) {
   __shared__ float red[2][16];
   __shared__ Ring ring;
   extern __shared__ uint4 dyn_smem[];  // the ring, or several rows' dw sums
@@ -751,9 +752,13 @@ gemm_status_t gemm_rmsnorm_backward(int64_t rows, int64_t dim, const gemm_rmsnor
   const int64_t chunks = vec ? dim / 8 : (dim + kFp8Block - 1) / kFp8Block * 16;
   // the registers hold four chunks of dw and of both inputs only in bf16
   const bool both_bf16 = vec && p.dy_type == GEMM_OUT_BF16 && p.h_type == GEMM_OUT_BF16;
-  // Rows that are not moved in vectors: one chunk a thread (bf16, 4000 x
-  // 3001: 36 us against 54 with two; 16000 x 515: 26 us against 32).
-  const RowPlan pl = plan_rows(rows, chunks, sms, vec ? 2 : 1, both_bf16 ? 4 : 2);
+  // Two chunks a thread where one would leave threads over or not reach: short
+  // rows of few threads, long ones.  Otherwise one, for more threads an SM (bf16
+  // with the skip connection's gradient, 8192 x 4096 54 us against 57, 16384 x
+  // 1024 33 against 37; but 16384 x 512 22 with two, 24 with one) and always
+  // where rows are not moved in vectors (4000 x 3001 36 us against 54).
+  const bool two = vec && (chunks <= 64 || chunks > kMaxThreads);
+  const RowPlan pl = plan_rows(rows, chunks, sms, two ? 2 : 1, both_bf16 ? 4 : 2);
   a.tpr = pl.tpr;
   a.ring.err = err;
   int grid = row_grid(rows, pl, sms, pl.chunks_per_thread == 1 ? 768 : 512);
@@ -762,7 +767,7 @@ gemm_status_t gemm_rmsnorm_backward(int64_t rows, int64_t dim, const gemm_rmsnor
         dim * (type_bytes(p.dy_type) + type_bytes(p.h_type) +
                (p.residual_grad == nullptr ? 0 : type_bytes(p.residual_grad_type)));
     const int ring_grid =
-        plan_ring(pl, rows, bytes, sms, pl.chunks_per_thread == 1 ? 768 : 640, a.ring);
+        plan_ring(pl, rows, bytes, sms, pl.chunks_per_thread == 1 ? 1024 : 640, a.ring);
     if (ring_grid > 0) grid = ring_grid;
   }
   const bool by_column = pl.chunks_per_thread == 0;
