@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kMaxThreads, RING ? 2 : 1) norm_kernel(const _
   __shared__ Ring ring;
   extern __shared__ uint4 dyn_smem[];
   uint8_t* const stages = reinterpret_cast<uint8_t*>(dyn_smem);
-  const int stage_bytes = a.dim * (type_bytes(TX) + (TR < 0 ? 0 : type_bytes(TR)));
+  const int stage_bytes = RING ? a.dim * (type_bytes(TX) + (TR < 0 ? 0 : type_bytes(TR))) : 0;
   // thread 0: copies `row` into stage s
   auto fetch = [&](int64_t row, int s) {
     uint8_t* to = stages + s * stage_bytes;
@@ -298,8 +298,9 @@ __global__ void __launch_bounds__(RING && C == 1 ? 1024 : kMaxThreads, 1)
   __shared__ Ring ring;
   extern __shared__ uint4 dyn_smem[];  // the ring, or several rows' dw sums
   uint8_t* const stages = reinterpret_cast<uint8_t*>(dyn_smem);
-  const int bytes_d = a.dim * type_bytes(TD), bytes_h = a.dim * type_bytes(TH);
-  const int bytes_r = a.p.residual_grad == nullptr ? 0 : a.dim * type_bytes(a.p.residual_grad_type);
+  const int ring_dim = RING ? a.dim : 0;
+  const int bytes_d = ring_dim * type_bytes(TD), bytes_h = ring_dim * type_bytes(TH);
+  const int bytes_r = a.p.residual_grad == nullptr ? 0 : ring_dim * type_bytes(a.p.residual_grad_type);
   const int stage_bytes = bytes_d + bytes_h + bytes_r;
   auto fetch = [&](int64_t row, int s) {
     uint8_t* to = stages + s * stage_bytes;
@@ -772,7 +773,10 @@ gemm_status_t gemm_rmsnorm_backward(int64_t rows, int64_t dim, const gemm_rmsnor
   }
   const bool by_column = pl.chunks_per_thread == 0;
   int parts = grid;
-  if (by_column) parts = static_cast<int>(rows < 64 ? rows : 64);
+  if (by_column) {  // up to 64, of 256 MB together
+    parts = static_cast<int>(rows < 64 ? rows : 64);
+    while (parts > 1 && parts * dim > (int64_t{1} << 26)) parts /= 2;
+  }
   std::unique_lock<std::mutex> lock;
   if (p.dweight != nullptr) {
     st = abi_scratch(s, static_cast<int64_t>(parts) * dim, lock, &a.part);
