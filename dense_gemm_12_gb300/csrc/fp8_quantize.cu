@@ -29,10 +29,10 @@ struct QuantArgs {
 // 1 x 128 blocks along the rows of x.  A thread's kRowUnits units are loaded
 // before the first is reduced.  Three forms: 16 consecutive elements a thread
 // and 8 lanes a block (two quotients and the maximum's shuffles per block are
-// what the instructions go to: with 8 elements a thread 8192 x 8192 in bf16
-// took 52 us); 8 consecutive elements; and, for rows that cannot be moved in
-// vectors, 8 elements 16 apart, which keeps consecutive lanes on consecutive
-// elements.
+// what the instructions go to: 8192 x 8192 in bf16 takes 38 us, 5.3 TB/s, and
+// took 52 us with 8 elements a thread); 8 consecutive elements; and, for rows
+// that cannot be moved in vectors, 8 elements 16 apart, which keeps consecutive
+// lanes on consecutive elements.
 enum RowForm : int { kStrided8 = 0, kVec8 = 1, kVec16 = 2 };
 constexpr int kRowUnits = 2;
 
@@ -121,8 +121,10 @@ cudaError_t launch_rows(const QuantArgs& a, int num_sms, cudaStream_t s) {
 // One 128 x 128 tile of x per CTA turn, through shared memory.  Where TMA can
 // describe x, one thread keeps `stages` tiles on their way (zeros outside x);
 // a thread waiting for its own 16-byte loads instead left too few in flight
-// (8192 x 8192 in bf16: 49 us).  Otherwise each warp reads a row's elements
-// with consecutive lanes.  Thread (rg, cg) = (t / 16, t % 16) then holds rows
+// (8192 x 8192 in bf16: 49 us, against 33 with the ring).  Otherwise each warp
+// reads 16 rows' elements with consecutive lanes, all before the first is used,
+// and through L1, since neighbouring loads share sectors (3000 x 1999: 8.5 us;
+// 9.5 in two halves and streaming).  Thread (rg, cg) = (t / 16, t % 16) then holds rows
 // 8 rg .. 8 rg + 7 of columns 8 cg .. 8 cg + 7.  The transposed output goes
 // through shared memory again: eight values down a column make one 8-byte
 // piece of an output row; a row's 16 pieces are XOR-swizzled by its 8-column
@@ -181,22 +183,18 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const __grid_constan
       E* to = reinterpret_cast<E*>(ring);
       const E* from = static_cast<const E*>(a.x) + tc * kTile;
       const int n = static_cast<int>(min(a.cols - tc * kTile, static_cast<int64_t>(kTile)));
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        E v[8][4];
+      E v[16][4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int64_t r = tr * kTile + half * 64 + i * 8 + warp;
+      for (int i = 0; i < 16; ++i) {
+        const int64_t r = tr * kTile + i * 8 + warp;
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            v[i][j] = r < a.rows && lane + 32 * j < n ? __ldcs(from + r * a.ldx + lane + 32 * j) : E(0);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            to[(half * 64 + i * 8 + warp) * kTile + lane + 32 * j] = v[i][j];
+        for (int j = 0; j < 4; ++j)
+          v[i][j] = r < a.rows && lane + 32 * j < n ? __ldg(from + r * a.ldx + lane + 32 * j) : E(0);
       }
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) to[(i * 8 + warp) * kTile + lane + 32 * j] = v[i][j];
       __syncthreads();
     }
     float v[8][8];  // [row][column]
