@@ -106,11 +106,6 @@ constexpr size_t kSmemBytes = 1024 + kRingBytes + kSumWarps * kOutBytes + sizeof
 static_assert(kSmemBytes <= 227 * 1024, "fp8 kernel shared memory");
 static_assert(BM * BN * 4 <= kRingBytes, "a cluster's sums fit in the ring");
 
-// Rows of a tile that sum warp (quarter, half) writes; 0 where it has no columns.
-__device__ __forceinline__ int live_rows(const GroupTile& w, int quarter, int half, int N) {
-  return w.tn * BN + half * kWarpCols < N ? min(w.rows - quarter * 32, 32) : 0;
-}
-
 // Sums of two columns plus their accumulator values, scaled.  Volatile, and
 // taking the values as they were loaded: so nothing of it moves above the
 // (volatile) wait for the loads, and no register is copied to tie the loads to
@@ -184,6 +179,47 @@ __device__ __forceinline__ void store4(const Fp8Args& p, int64_t row, int col, f
     if (col + i < p.N) store1(p.D, p.d_type, at + i, v[i]);
 }
 
+// write_sums where nothing is clipped and D is only written: 64 bytes of each
+// row at a time, addresses advanced by constants.
+template <bool BF16>
+__device__ __forceinline__ void write_whole(const Fp8Args& p, uint8_t* stage, const uint64_t* acc,
+                                            int64_t row_base, int col_base) {
+  constexpr int kElem = BF16 ? 2 : 4, kPairs = BF16 ? 16 : 8;
+  const int lane = threadIdx.x & 31;
+  const int swz = (lane >> 1) & 3;
+  uint4* mine = reinterpret_cast<uint4*>(stage + lane * 64);
+  const int rl = lane >> 2, pc = lane & 3;
+  const float a = p.num_kb > 0 ? p.alpha : 0.0f;
+  uint8_t* d = static_cast<uint8_t*>(p.D) + ((row_base + rl) * p.ldd + col_base) * kElem + pc * 16;
+  const int64_t step = 8 * p.ldd * kElem;
+  const uint4* theirs = reinterpret_cast<const uint4*>(stage + rl * 64) + (pc ^ ((rl >> 1) & 3));
+#pragma unroll
+  for (int c = 0; c < kWarpCols * kElem / 64; ++c) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < kPairs / 4; ++i) {
+        const float2 f = f32x2_parts(acc[c * kPairs + q * (kPairs / 4) + i]);
+        if (BF16) {
+          w[i] = pack_bf16(a * f.x, a * f.y);
+        } else {
+          w[2 * i] = __float_as_uint(a * f.x);
+          w[2 * i + 1] = __float_as_uint(a * f.y);
+        }
+      }
+      mine[q ^ swz] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __syncwarp();
+    uint4 w[4];  // rows rl, rl + 8, ...: 8 rows on, the swizzle is the same
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = theirs[i * 8 * 4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(d + i * step + c * 64) = w[i];
+    __syncwarp();
+  }
+}
+
 // This warp's 32 rows x 128 columns of sums to D.  A thread holds one row, so
 // its values are turned around in the warp's 2 KB of shared memory -- 64-byte
 // rows whose 16-byte pieces are XOR-swizzled, so that neither side conflicts
@@ -191,6 +227,13 @@ __device__ __forceinline__ void store4(const Fp8Args& p, int64_t row, int col, f
 // time, or 16 sums in fp32 where D is fp32 or read as well (beta != 0).
 __device__ __forceinline__ void write_sums(const Fp8Args& p, uint8_t* stage, const uint64_t* acc,
                                            int64_t row_base, int rows, int col_base) {
+  if (rows == 32 && col_base + kWarpCols <= p.N && p.d_vec && p.beta == 0.0f) {
+    if (p.d_type == GEMM_OUT_BF16)
+      write_whole<true>(p, stage, acc, row_base, col_base);
+    else
+      write_whole<false>(p, stage, acc, row_base, col_base);
+    return;
+  }
   const int lane = threadIdx.x & 31;
   const int swz = (lane >> 1) & 3;
   uint4* mine = reinterpret_cast<uint4*>(stage + lane * 64);
@@ -430,9 +473,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     int g = 0;
     bool ok = true;
     for (int t = first; t < tiles && ok; t += stride) {
-      // a warp without rows or columns only keeps the rings moving
-      const bool live = live_rows(group_tile(groups, t, tiles_n, p.band, p.tile_rows, g), quarter,
-                                  half, p.N) > 0;
+      // where the sums go; kept in the warp's staging area, since the loop below
+      // needs the registers
+      bool live;
+      {
+        const GroupTile w = group_tile(groups, t, tiles_n, p.band, p.tile_rows, g);
+        const int rows = min(w.rows - quarter * 32, 32), col_base = w.tn * BN + half * kWarpCols;
+        live = rows > 0 && col_base < p.N;
+        if (!CLUSTER && lane == 0)
+          *reinterpret_cast<int4*>(stage) = make_int4(w.row0 + quarter * 32, rows, col_base, 0);
+        __syncwarp();
+      }
       uint64_t acc[kWarpCols / 2];
 #pragma unroll
       for (int i = 0; i < kWarpCols / 2; ++i) acc[i] = 0ull;
@@ -445,45 +496,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t sc = scales_at + slot * (kScaleFloats * 4);
         if (++slot == SSLOTS) slot = 0;
         tc_fence_after_sync();
-        if (live) {
-          const uint32_t taddr = lane_base + b * BN;
-          // 32 and 16 columns in turn, two loads on their way at a time: 128
-          // sums and 48 values fit the registers, and what the accumulator's
-          // release waits for is three loads' latency.
-          uint32_t ra[32], rb[16];
-          tmem_ld_32x32b_x32(taddr, ra);
-          tmem_ld_32x32b_x16(taddr + 32, rb);
-          // this thread's row's scale, and (ROWS: those of) the columns
-          float f1 = ld_shared_f32(sc + 4 * row);
-          if (!ROWS) f1 *= ld_shared_f32(sc + 4 * (BM + half));
-          const uint32_t sb = sc + 4 * (BM + half * kWarpCols);
-          const uint64_t f = f32x2(f1, f1);
-          tc_wait_ld();
-          add_scaled<ROWS>(acc, ra, f, sb);
-          tmem_ld_32x32b_x32(taddr + 48, ra);
-          add_scaled<ROWS>(acc + 16, rb, f, sb + 128);
-          tmem_ld_32x32b_x16(taddr + 80, rb);
-          tc_wait_ld();
-          add_scaled<ROWS>(acc + 24, ra, f, sb + 192);
-          tmem_ld_32x32b_x32(taddr + 96, ra);
-          add_scaled<ROWS>(acc + 40, rb, f, sb + 320);
-          tc_wait_ld();
-          // The accumulator has been read, and by rows the scales are used up:
-          // the MMAs of the block after next may overwrite it while its last
-          // columns are added.
-          if (ROWS) add_scaled<ROWS>(acc + 48, ra, f, sb + 384);
-          tc_fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_at(tmem_empty_at + 8 * b);
-          if (!ROWS) add_scaled<ROWS>(acc + 48, ra, f, sb + 384);
-        } else {
-          tc_fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_at(tmem_empty_at + 8 * b);
-        }
+        // Warps without rows or columns of the tile add too: a branch around this
+        // costs more (3000 x 5000 x 1999, a scale per row of B: 56 us against 54).
+        const uint32_t taddr = lane_base + b * BN;
+        // 32 and 16 columns in turn, two loads on their way at a time: 128
+        // sums and 48 values fit the registers, and what the accumulator's
+        // release waits for is three loads' latency.
+        uint32_t ra[32], rb[16];
+        tmem_ld_32x32b_x32(taddr, ra);
+        tmem_ld_32x32b_x16(taddr + 32, rb);
+        // this thread's row's scale, and (ROWS: those of) the columns
+        float f1 = ld_shared_f32(sc + 4 * row);
+        if (!ROWS) f1 *= ld_shared_f32(sc + 4 * (BM + half));
+        const uint32_t sb = sc + 4 * (BM + half * kWarpCols);
+        const uint64_t f = f32x2(f1, f1);
+        tc_wait_ld();
+        add_scaled<ROWS>(acc, ra, f, sb);
+        tmem_ld_32x32b_x32(taddr + 48, ra);
+        add_scaled<ROWS>(acc + 16, rb, f, sb + 128);
+        tmem_ld_32x32b_x16(taddr + 80, rb);
+        tc_wait_ld();
+        add_scaled<ROWS>(acc + 24, ra, f, sb + 192);
+        tmem_ld_32x32b_x32(taddr + 96, ra);
+        add_scaled<ROWS>(acc + 40, rb, f, sb + 320);
+        tc_wait_ld();
+        // The accumulator has been read, and by rows the scales are used up:
+        // the MMAs of the block after next may overwrite it while its last
+        // columns are added.
+        if (ROWS) add_scaled<ROWS>(acc + 48, ra, f, sb + 384);
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_at(tmem_empty_at + 8 * b);
+        if (!ROWS) add_scaled<ROWS>(acc + 48, ra, f, sb + 384);
       }
-      // found again rather than kept: the loop above needs the registers
-      const GroupTile w = group_tile(groups, t, tiles_n, p.band, p.tile_rows, g);
       if (CLUSTER) {
         // This CTA's k-blocks are done, and with them every use of the ring:
         // its sums go there, 1 KB per row, 16-byte pieces swizzled by row.
@@ -497,9 +542,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         break;
       }
-      if (live && ok)
-        write_sums(p, stage, acc, w.row0 + quarter * 32, live_rows(w, quarter, half, p.N),
-                   w.tn * BN + half * kWarpCols);
+      const int4 w = ld_shared_i4(smem_u32(stage));
+      __syncwarp();
+      if (ok && live) write_sums(p, stage, acc, w.x, w.y, w.z);
     }
     if (CLUSTER) {
       __syncwarp();

@@ -92,10 +92,10 @@ __device__ __forceinline__ GroupTile group_tile(const GroupTable& tab, int t, in
   const int b = local / per_band;
   const int high = min(tiles_m - b * band, band);
   const int in_band = local - b * per_band;
-  const int tm = b * band + in_band % high;
   GroupTile r;
   r.group = g;
-  r.tn = in_band / high;
+  r.tn = high == 8 ? in_band >> 3 : in_band / high;  // whole bands are 8 high
+  const int tm = b * band + in_band - r.tn * high;
   r.row0 = tab.row[g] + tm * tile_rows;
   r.rows = min(tile_rows, tab.row[g + 1] - r.row0);
   return r;
