@@ -9,6 +9,8 @@
 #include <cstring>
 #include <map>
 #include <mutex>
+#include <new>
+#include <vector>
 
 #include "../../include/gemm12.h"
 #include "internal.h"
@@ -25,14 +27,24 @@ namespace {
 constexpr int kMaxDevices = 64;
 constexpr int64_t kMaxDim = (int64_t{1} << 31) - 1;
 
+struct Buffer {
+  void* p = nullptr;
+  int64_t bytes = 0;
+  bool in_graph = false;  // handed out during a capture: a graph holds its address
+};
+
+// What a stream's buffers hold: partial sums, arrival counters, and aligned
+// copies of operands the TMA engine cannot describe (stage_operands).
+enum BufferKind : int { kWs = 0, kCounters = 1, kStage = 2, kBufferKinds = 3 };
+
 struct Scratch {
-  float* ws = nullptr;
-  int64_t ws_floats = 0;
-  uint32_t* counters = nullptr;
-  int64_t counter_count = 0;
-  // Aligned copies of operands the TMA engine cannot describe (stage_operands).
-  uint8_t* stage = nullptr;
-  int64_t stage_bytes = 0;
+  Buffer buf[kBufferKinds];
+  // Outgrown buffers that captured graphs still use, kept as long as the
+  // stream's own.
+  std::vector<Buffer> kept[kBufferKinds];
+
+  float* ws() const { return static_cast<float*>(buf[kWs].p); }
+  uint32_t* counters() const { return static_cast<uint32_t*>(buf[kCounters].p); }
 };
 
 struct DeviceState {
@@ -43,8 +55,9 @@ struct DeviceState {
   uint32_t* err_word = nullptr;
   // Split-K scratch (partial sums + arrival counters) and operand staging
   // copies, one set per stream: calls on one stream are ordered by it, calls
-  // on different streams never share a buffer.  Grown on demand, freed by
-  // gemm_shutdown.
+  // on different streams never share a buffer.  Grown on demand (a
+  // buffer that a captured graph uses is kept), freed by gemm_release_stream
+  // and gemm_shutdown.
   std::mutex ws_mutex;
   std::map<void*, Scratch> scratch;
 };
@@ -177,24 +190,47 @@ bool capturing(cudaStream_t stream) {
   return cs != cudaStreamCaptureStatusNone;
 }
 
-// Replaces *buf (of *have bytes) by a stream-ordered allocation of `bytes`
-// on `stream`: the old buffer is released after the work already queued on
-// the stream (its only user), the new one is ready for the work queued after
-// this call.  Nothing waits on the host.
-gemm_status_t regrow(void** buf, int64_t* have, int64_t bytes, cudaStream_t stream) {
-  if (*buf != nullptr && cudaFreeAsync(*buf, stream) != cudaSuccess) {
+// Replaces a buffer of `sc` by a stream-ordered allocation of `bytes` on
+// `stream`: the old one is released after the work already queued on the
+// stream (its only user), the new one is ready for the work queued after
+// this call.  Nothing waits on the host.  A buffer that a captured graph uses
+// is kept instead of released: replays write to it at any later time.
+gemm_status_t regrow(Scratch& sc, BufferKind kind, int64_t bytes, cudaStream_t stream) {
+  Buffer& b = sc.buf[kind];
+  if (b.in_graph) {
+    try {
+      sc.kept[kind].push_back(b);
+    } catch (const std::bad_alloc&) {
+      return GEMM_ERR_NO_MEMORY;
+    }
+  } else if (b.p != nullptr && cudaFreeAsync(b.p, stream) != cudaSuccess) {
     cudaGetLastError();
     return GEMM_ERR_LAUNCH;
   }
-  *buf = nullptr;
-  *have = 0;
-  if (cudaMallocAsync(buf, static_cast<size_t>(bytes), stream) != cudaSuccess) {
+  b = Buffer{};
+  if (cudaMallocAsync(&b.p, static_cast<size_t>(bytes), stream) != cudaSuccess) {
     cudaGetLastError();
-    *buf = nullptr;
+    b.p = nullptr;
     return GEMM_ERR_NO_MEMORY;
   }
-  *have = bytes;
+  b.bytes = bytes;
   return GEMM_OK;
+}
+
+// Queues the release of all buffers of `sc` on `stream`.
+gemm_status_t release(Scratch& sc, cudaStream_t stream) {
+  gemm_status_t result = GEMM_OK;
+  auto drop = [&](const Buffer& b) {
+    if (b.p != nullptr && cudaFreeAsync(b.p, stream) != cudaSuccess) {
+      cudaGetLastError();
+      result = GEMM_ERR_LAUNCH;
+    }
+  };
+  for (int k = 0; k < kBufferKinds; ++k) {
+    drop(sc.buf[k]);
+    for (const Buffer& b : sc.kept[k]) drop(b);
+  }
+  return result;
 }
 
 // The scratch area of `stream` on this device, grown to at least the given
@@ -206,25 +242,22 @@ gemm_status_t ensure_scratch(DeviceState& st, cudaStream_t stream, int64_t float
                              int64_t counters, Scratch** out) {
   Scratch& sc = st.scratch[static_cast<void*>(stream)];
   *out = &sc;
-  if (sc.ws_floats >= floats && sc.counter_count >= counters) return GEMM_OK;
-  if (capturing(stream)) return GEMM_ERR_NO_MEMORY;
-  if (sc.ws_floats < floats) {
-    int64_t bytes = 0;
-    const gemm_status_t s = regrow(reinterpret_cast<void**>(&sc.ws), &bytes,
-                                   floats * static_cast<int64_t>(sizeof(float)), stream);
-    sc.ws_floats = bytes / static_cast<int64_t>(sizeof(float));
-    if (s != GEMM_OK) return s;
-  }
-  if (sc.counter_count < counters) {
-    int64_t bytes = 0;
-    const gemm_status_t s = regrow(reinterpret_cast<void**>(&sc.counters), &bytes,
-                                   counters * static_cast<int64_t>(sizeof(uint32_t)), stream);
-    sc.counter_count = bytes / static_cast<int64_t>(sizeof(uint32_t));
-    if (s != GEMM_OK) return s;
-    if (cudaMemsetAsync(sc.counters, 0, static_cast<size_t>(bytes), stream) != cudaSuccess) {
-      cudaGetLastError();
-      return GEMM_ERR_LAUNCH;
+  const bool in_graph = capturing(stream);
+  const int64_t need[2] = {floats * static_cast<int64_t>(sizeof(float)),
+                           counters * static_cast<int64_t>(sizeof(uint32_t))};
+  if (in_graph && (sc.buf[kWs].bytes < need[kWs] || sc.buf[kCounters].bytes < need[kCounters]))
+    return GEMM_ERR_NO_MEMORY;
+  for (BufferKind k : {kWs, kCounters}) {
+    if (sc.buf[k].bytes < need[k]) {
+      const gemm_status_t s = regrow(sc, k, need[k], stream);
+      if (s != GEMM_OK) return s;
+      if (k == kCounters &&
+          cudaMemsetAsync(sc.buf[k].p, 0, static_cast<size_t>(need[k]), stream) != cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_LAUNCH;
+      }
     }
+    if (in_graph && need[k] > 0) sc.buf[k].in_graph = true;
   }
   return GEMM_OK;
 }
@@ -234,13 +267,14 @@ gemm_status_t ensure_scratch(DeviceState& st, cudaStream_t stream, int64_t float
 // stream capture).  Caller holds st.ws_mutex.
 gemm_status_t ensure_stage(DeviceState& st, cudaStream_t stream, int64_t bytes, uint8_t** out) {
   Scratch& sc = st.scratch[static_cast<void*>(stream)];
-  if (sc.stage_bytes < bytes) {
-    if (capturing(stream)) return GEMM_ERR_NO_MEMORY;
-    const gemm_status_t s = regrow(reinterpret_cast<void**>(&sc.stage), &sc.stage_bytes, bytes,
-                                   stream);
+  const bool in_graph = capturing(stream);
+  if (sc.buf[kStage].bytes < bytes) {
+    if (in_graph) return GEMM_ERR_NO_MEMORY;
+    const gemm_status_t s = regrow(sc, kStage, bytes, stream);
     if (s != GEMM_OK) return s;
   }
-  *out = sc.stage;
+  if (in_graph) sc.buf[kStage].in_graph = true;
+  *out = static_cast<uint8_t*>(sc.buf[kStage].p);
   return GEMM_OK;
 }
 
@@ -408,8 +442,8 @@ gemm_status_t plan_simt(DeviceState* st, cudaStream_t cs, SimtArgs& a, SimtPlan&
     Scratch* sc = nullptr;
     const gemm_status_t s = ensure_scratch(*st, cs, pl.ws_floats, pl.counters, &sc);
     if (s == GEMM_OK) {
-      a.ws = sc->ws;
-      a.counters = sc->counters;
+      a.ws = sc->ws();
+      a.counters = sc->counters();
     } else if (s == GEMM_ERR_NO_MEMORY) {
       pl = simt_plan_whole(pl, a.M, a.N, st->num_sms);
     } else {
@@ -591,7 +625,7 @@ gemm_status_t abi_scratch(cudaStream_t stream, int64_t floats, std::unique_lock<
   lock = std::unique_lock<std::mutex>(st->ws_mutex);
   Scratch* sc = nullptr;
   s = ensure_scratch(*st, stream, floats, 0, &sc);
-  if (s == GEMM_OK) *ws = sc->ws;
+  if (s == GEMM_OK) *ws = sc->ws();
   return s;
 }
 
@@ -865,8 +899,8 @@ static gemm_status_t run_bf16_tensor_core(DeviceState* st, gemm_path_t path, int
       Scratch* sc = nullptr;
       const gemm_status_t s = ensure_scratch(*st, cs, pl.ws_floats, pl.counters, &sc);
       if (s == GEMM_OK) {
-        a.ws = sc->ws;
-        a.counters = sc->counters;
+        a.ws = sc->ws();
+        a.counters = sc->counters();
       } else if (s == GEMM_ERR_NO_MEMORY) {
         const TileConfig whole{pl.pair ? GEMM_KERNEL_CTA_PAIR : GEMM_KERNEL_SINGLE_CTA, 1,
                                pl.group_m};
@@ -922,8 +956,8 @@ static gemm_status_t run_bf16_tensor_core(DeviceState* st, gemm_path_t path, int
                                 lock);
   }
   if (s != GEMM_OK) return s;
-  a.workspace = sc->ws;
-  a.counters = sc->counters;
+  a.workspace = sc->ws();
+  a.counters = sc->counters();
   return from_cuda(launch_tc_decode(a, &tmA, &tmB, grid, cs));
 }
 
@@ -1153,9 +1187,13 @@ gemm_status_t gemm_check_device_error(void* stream) {
   {
     std::lock_guard<std::mutex> lock(st->ws_mutex);
     cudaDeviceSynchronize();
-    for (auto& kv : st->scratch)
-      if (kv.second.counters)
-        cudaMemset(kv.second.counters, 0, kv.second.counter_count * sizeof(uint32_t));
+    auto reset = [](const Buffer& b) {
+      if (b.p != nullptr) cudaMemset(b.p, 0, static_cast<size_t>(b.bytes));
+    };
+    for (auto& kv : st->scratch) {
+      reset(kv.second.buf[kCounters]);
+      for (const Buffer& b : kv.second.kept[kCounters]) reset(b);
+    }
     cudaDeviceSynchronize();
   }
   cudaGetLastError();
@@ -1182,11 +1220,7 @@ gemm_status_t gemm_shutdown(void) {
     }
     // Stream-ordered allocations, released on the legacy stream once the
     // device is idle (the streams they were made on may no longer exist).
-    for (auto& kv : st.scratch) {
-      if (kv.second.ws) cudaFreeAsync(kv.second.ws, 0);
-      if (kv.second.counters) cudaFreeAsync(kv.second.counters, 0);
-      if (kv.second.stage) cudaFreeAsync(kv.second.stage, 0);
-    }
+    for (auto& kv : st.scratch) release(kv.second, 0);
     st.scratch.clear();
     if (cudaDeviceSynchronize() != cudaSuccess) {
       cudaGetLastError();
@@ -1206,14 +1240,7 @@ gemm_status_t gemm_release_stream(void* stream) {
   auto it = st->scratch.find(stream);
   if (it == st->scratch.end()) return GEMM_OK;
   if (capturing(cs)) return GEMM_ERR_INVALID_VALUE;
-  Scratch& sc = it->second;
-  gemm_status_t result = GEMM_OK;
-  for (void* p : {static_cast<void*>(sc.ws), static_cast<void*>(sc.counters),
-                  static_cast<void*>(sc.stage)})
-    if (p != nullptr && cudaFreeAsync(p, cs) != cudaSuccess) {
-      cudaGetLastError();
-      result = GEMM_ERR_LAUNCH;
-    }
+  const gemm_status_t result = release(it->second, cs);
   st->scratch.erase(it);
   return result;
 }

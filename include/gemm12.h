@@ -68,7 +68,14 @@
  *             (cudaMallocAsync / cudaFreeAsync on `stream`, from the
  *             device's default memory pool): growing never blocks the host,
  *             the old buffer is released after the work already queued on
- *             the stream.
+ *             the stream.  A graph captured from calls on a stream holds the
+ *             addresses of the stream's buffers: one that has been used
+ *             inside a capture is never released by growth, only by
+ *             gemm_release_stream or gemm_shutdown, after which such graphs
+ *             must not be replayed.  As the graph's replays and the stream's
+ *             other calls (and other graphs captured on it) share these
+ *             buffers, they must be ordered one after the other: replay on
+ *             that stream, or wait for it with events.
  *             Without the scratch it needs -- out of memory, or inside a
  *             stream capture (CUDA graph), where the library allocates
  *             nothing -- a call still runs: split tiles run whole instead
@@ -294,7 +301,8 @@ gemm_status_t gemm_bf16gemm_decode_static(int64_t M, int64_t N, int64_t K, float
  * keeps for `stream` on the current device (see Memory above), stream-ordered
  * after the work already queued on that stream; a later call on the stream
  * allocates them again.  Call it before destroying a stream that has run
- * GEMMs, so that the buffers do not outlive it.  Returns GEMM_OK (also when
+ * GEMMs, so that the buffers do not outlive it, and after the last replay of
+ * the graphs captured on it.  Returns GEMM_OK (also when
  * the stream has none), GEMM_ERR_INVALID_VALUE while the stream is being
  * captured, GEMM_ERR_LAUNCH if a free could not be queued.
  */
@@ -317,7 +325,8 @@ const char *gemm_status_string(gemm_status_t status);
 gemm_status_t gemm_check_device_error(void *stream);
 
 /* Free the scratch and staging buffers of every stream on every device
- * (see Memory above).  Call with no GEMM in flight. */
+ * (see Memory above).  Call with no GEMM in flight, and replay no graph
+ * captured before it afterwards. */
 gemm_status_t gemm_shutdown(void);
 
 /* Kernel paths a call can take (reported by gemm_select_path). */
