@@ -704,7 +704,7 @@ gemm_status_t run(int64_t G, const int32_t* offsets, int64_t M, int64_t N, int64
                   int b_block, float beta, void* D, int64_t ldd, int d_type, bool grouped,
                   void* stream) {
   const int d_bytes = float_type_bytes(d_type);
-  if (M < 0 || N < 0 || K < 0 || M > kOpsMaxDim || N > kOpsMaxDim || K > kOpsMaxDim ||
+  if (M < 0 || N < 0 || K < 0 || M > kOpsMaxTiled || N > kOpsMaxTiled || K > kOpsMaxDim ||
       d_bytes == 0 || (b_block != GEMM_BLOCK_ROWS && b_block != GEMM_BLOCK_TILES))
     return GEMM_ERR_INVALID_VALUE;
   if (G < 0) return GEMM_ERR_INVALID_VALUE;

@@ -780,6 +780,7 @@ bool encode_output(CUtensorMap* tm, void* D, int d_type, int64_t rows, int64_t c
 }
 
 bool bad_dim(int64_t v) { return v < 0 || v > kOpsMaxDim; }
+bool bad_tiled(int64_t v) { return v < 0 || v > kOpsMaxTiled; }
 
 // Stages the operands that TMA cannot describe and encodes the maps (of B with
 // rank_b dimensions); box_a and box_b: elements along the innermost and the
@@ -819,7 +820,7 @@ gemm_status_t gemm_bf16gemm_grouped(int64_t G, const int32_t* offsets, int64_t r
                                     const void* B, int64_t ldb, int64_t stride_b, int transpose_b,
                                     float beta, void* D, int64_t ldd, int d_type, void* stream) {
   const int d_bytes = float_type_bytes(d_type);
-  if (bad_dim(G) || bad_dim(rows) || bad_dim(N) || bad_dim(K) || d_bytes == 0)
+  if (bad_dim(G) || bad_tiled(rows) || bad_tiled(N) || bad_tiled(K) || d_bytes == 0)
     return GEMM_ERR_INVALID_VALUE;
   if (G == 0 || rows == 0 || N == 0) return GEMM_OK;
   const bool product = K > 0 && alpha != 0.0f;
@@ -900,7 +901,7 @@ gemm_status_t gemm_bf16gemm_grouped_wgrad(int64_t G, const int32_t* offsets, int
                                           void* dB, int64_t ldb, int64_t stride_b, int d_type,
                                           void* stream) {
   const int d_bytes = float_type_bytes(d_type);
-  if (bad_dim(G) || bad_dim(rows) || bad_dim(N) || bad_dim(K) || d_bytes == 0)
+  if (bad_dim(G) || bad_tiled(rows) || bad_tiled(N) || bad_tiled(K) || d_bytes == 0)
     return GEMM_ERR_INVALID_VALUE;
   if (G == 0 || N == 0 || K == 0) return GEMM_OK;
   const bool product = rows > 0 && alpha != 0.0f;

@@ -37,6 +37,10 @@ bool abi_encode_tiled(CUtensorMap* map, CUtensorMapDataType type, int rank, cons
 gemm_status_t abi_from_cuda(cudaError_t e);
 
 constexpr int64_t kOpsMaxDim = (int64_t{1} << 31) - 1;
+// Largest extent that a product cuts into tiles: its kernels keep rows, columns
+// and tile counts in 32 bits, and go up to 255 past a position when they round
+// up to a tile or step to a tile's end.
+constexpr int64_t kOpsMaxTiled = kOpsMaxDim - 255;
 
 inline bool ops_misaligned(const void* p, uintptr_t bytes) {
   return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0;

@@ -540,6 +540,9 @@ gemm_status_t gemm_quantization(int64_t M, int64_t N, int64_t BM, int64_t BN,
  *             block of rows) r is at scales[b * ld_scales + r].  A value is
  *             its byte's E4M3 value times its block's scale.
  *  Types      x_type, y_type, d_type, ... are GEMM_OUT_F32 or GEMM_OUT_BF16.
+ *  Sizes      Below 2^31, as at the top; what a product cuts into tiles (M or
+ *             rows, N, and K of the bf16 products) at most 2^31 - 256, and
+ *             the norm's dim at most 2^30.  More is GEMM_ERR_INVALID_VALUE.
  *  Memory     gemm_rmsnorm_backward keeps partial sums of the weight's
  *             gradient in the stream's scratch; operands of the products
  *             that TMA cannot describe (base not 16-byte aligned, or a row
