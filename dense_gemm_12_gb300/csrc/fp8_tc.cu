@@ -491,9 +491,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < kWarpCols / 2; ++i) acc[i] = 0ull;
       for (int kb = kb0; kb < kb1; ++kb, ++it) {
         const uint32_t b = it & 1u;
-        // All lanes ask the same barrier in the same instruction and get the
-        // same answer.
-        ok = mbar_wait_at(done_at + 8 * (it % STAGES), (it / STAGES) & 1u, abort_flag, p.err);
+        // Lanes that had to poll may have left the wait apart, and where it runs
+        // out with different answers: the vote brings the warp together for the
+        // loads below, or out of the loop.
+        ok = __all_sync(0xffffffffu, mbar_wait_at(done_at + 8 * (it % STAGES), (it / STAGES) & 1u,
+                                                  abort_flag, p.err));
         if (!ok) break;
         const uint32_t sc = scales_at + slot * (kScaleFloats * 4);
         if (++slot == SSLOTS) slot = 0;
