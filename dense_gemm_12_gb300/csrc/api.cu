@@ -876,8 +876,11 @@ static gemm_status_t run_bf16_tensor_core(DeviceState* st, gemm_path_t path, int
     a.err = st->err_word;
     const TileConfig tc = resolve_config(true, M, N, K, st->num_sms, cfg, nullptr);
     // The plain output stage with beta == 0 writes whole tiles by TMA when
-    // D's base and row pitch allow a tensor map.
-    const bool tma_out = !tc_fused(epi) && epi.beta == 0.0f && tma_ok(epi.D, epi.ldd, 4);
+    // D's base and row pitch allow a tensor map, and its rows end with a 16-byte
+    // piece: a TMA store writes the piece that a row ends in to its end, over
+    // what follows the row.
+    const bool tma_out =
+        !tc_fused(epi) && epi.beta == 0.0f && tma_ok(epi.D, epi.ldd, 4) && N % 4 == 0;
     TcPlan pl = tc_plan(a.M, a.N, a.K, st->num_sms, &tc, tma_out);
     // Tiles that all fit in one round add their k-parts through distributed
     // shared memory (single-CTA kernel).

@@ -257,6 +257,11 @@ __device__ __forceinline__ void write_any(const GroupedArgs& p, float4* stg, con
 // the map clips at D's edges.  The next 32 accumulator columns are read
 // meanwhile.  seq: pieces so far; a buffer is rewritten once the copy two
 // pieces back has read it.  row, z: coordinates of the first row.
+//
+// Along a row the copy is clipped to whole 16-byte pieces only: a last piece
+// that D's row ends in would be written to its end, over what follows the row.
+// Where rows end so, the chunk that holds the end is left to the caller.
+// Returns the number of chunks written.
 __device__ __forceinline__ void stage_piece(const CUtensorMap* tmD, uint32_t stg, uint32_t& seq,
                                             const uint32_t (&w)[16], int col, int row, int z) {
   const uint32_t lane = threadIdx.x & 31;
@@ -276,9 +281,11 @@ __device__ __forceinline__ void stage_piece(const CUtensorMap* tmD, uint32_t stg
   }
 }
 
-__device__ __forceinline__ void write_tma(const GroupedArgs& p, const CUtensorMap* tmD, uint32_t taddr,
-                                          uint32_t stg, uint32_t& seq, int row, int z, int col0) {
-  const int chunks = min(BN / 32, (p.N - col0 + 31) / 32);
+__device__ __forceinline__ int write_tma(const GroupedArgs& p, const CUtensorMap* tmD, uint32_t taddr,
+                                         uint32_t stg, uint32_t& seq, int row, int z, int col0) {
+  const bool whole = (p.N & (p.d_type == GEMM_OUT_BF16 ? 7 : 3)) == 0;
+  const int chunks = min(BN / 32, (p.N - col0 + (whole ? 31 : 0)) / 32);
+  if (chunks == 0) return 0;
   uint32_t r[32], next[32];
   tmem_ld_32x32b_x32(taddr, next);
 #pragma unroll 1
@@ -303,20 +310,22 @@ __device__ __forceinline__ void write_tma(const GroupedArgs& p, const CUtensorMa
       }
     }
   }
+  return chunks;
 }
 
-// The 32 rows x 256 columns of this warp (fewer at the edges).  load(c, r):
-// columns 32 c .. 32 c + 31 of its rows.
+// The 32 rows x 256 columns of this warp (fewer at the edges), from chunk
+// `first` on.  load(c, r): columns 32 c .. 32 c + 31 of its rows.
 template <typename Load>
 __device__ __forceinline__ void write_tile(const GroupedArgs& p, uint8_t* stg, float alpha, void* D,
-                                           int64_t row_base, int rows, int col0, Load load) {
+                                           int64_t row_base, int rows, int col0, Load load,
+                                           int first = 0) {
   const int chunks = min(BN / 32, (p.N - col0 + 31) / 32);
   if (p.d_type == GEMM_OUT_BF16 && p.beta == 0.0f) {
 #pragma unroll 1
-    for (int c = 0; c < chunks; c += 2) {
+    for (int c = first; c < chunks; c += 2) {
       uint32_t r[32], s[32];
       load(c, r);
-      load(c + 1, s);  // past the last chunk: columns that are not written
+      load(min(c + 1, BN / 32 - 1), s);  // past the last chunk: columns that are not written
       load.wait();
       write_bf16(p, reinterpret_cast<uint4*>(stg), r, s, alpha, static_cast<__nv_bfloat16*>(D),
                  row_base, rows, col0 + c * 32);
@@ -324,7 +333,7 @@ __device__ __forceinline__ void write_tile(const GroupedArgs& p, uint8_t* stg, f
     return;
   }
 #pragma unroll 1
-  for (int c = 0; c < chunks; ++c) {
+  for (int c = first; c < chunks; ++c) {
     uint32_t r[32];
     load(c, r);
     load.wait();
@@ -653,15 +662,16 @@ __global__ void __launch_bounds__(MODE == kWeightGrad && PAIR ? kRaggedThreads :
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + ab * BN;
       // a piece with rows of another group in it (not the weight gradient's:
       // its matrices end where the map clips) is written row by row
-      if (p.d_tma && rows > 0 && (kGrad || rows == 32)) {
-        write_tma(p, &tmD, taddr, smem_u32(stg), seq, static_cast<int>(row_base),
-                  kGrad ? w.group : 0, w.tn * BN);
-      } else if (rows > 0) {
+      int written = 0;
+      if (p.d_tma && rows > 0 && (kGrad || rows == 32))
+        written = write_tma(p, &tmD, taddr, smem_u32(stg), seq, static_cast<int>(row_base),
+                            kGrad ? w.group : 0, w.tn * BN);
+      if (rows > 0 && written < BN / 32 && w.tn * BN + written * 32 < p.N) {
         if (p.d_tma) {  // the copies from the staging area have read it
           if (lane == 0) bulk_wait_group_read<0>();
           __syncwarp();
         }
-        write_tile(p, stg, p.alpha, D, row_base, rows, w.tn * BN, FromTmem{taddr});
+        write_tile(p, stg, p.alpha, D, row_base, rows, w.tn * BN, FromTmem{taddr}, written);
       }
       tc_fence_before_sync();
       __syncwarp();

@@ -145,7 +145,7 @@ struct TcArgs {
   int cluster;
   // 1: the plain output stage (fp32 D = alpha * acc, beta == 0) writes whole
   // units through TMA stores described by the kernel's D tensor map (fp32,
-  // dims {N, M}, row pitch ldd, box 32 x 32, 128-byte swizzle).
+  // dims {N, M}, row pitch ldd, box 32 x 32, 128-byte swizzle); N % 4 == 0.
   int d_tma;
 };
 
