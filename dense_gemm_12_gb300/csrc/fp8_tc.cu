@@ -648,8 +648,12 @@ struct Operand {
   int64_t count, stride;    // matrices
 };
 
+// Row pitch in a tensor map.  A single row has none of its own: any will do.
+int64_t map_pitch(const Operand& o) { return o.rows == 1 ? (o.cols + 15) / 16 * 16 : o.ld; }
+
 bool tma_describes(const Operand& o) {
-  return !ops_misaligned(o.p, 16) && o.ld % 16 == 0 && (o.count == 1 || o.stride % 16 == 0);
+  return !ops_misaligned(o.p, 16) && map_pitch(o) % 16 == 0 &&
+         (o.count == 1 || o.stride % 16 == 0);
 }
 
 // Bytes of the copies that TMA can describe (rows padded to 16 bytes).
@@ -748,7 +752,7 @@ gemm_status_t run(int64_t G, const int32_t* offsets, int64_t M, int64_t N, int64
   a.D = D;
   a.ldd = ldd;
   a.d_type = d_type;
-  a.d_vec = !ops_misaligned(D, 16) && ldd % (16 / d_bytes) == 0;
+  a.d_vec = !ops_misaligned(D, 16) && (M == 1 || ldd % (16 / d_bytes) == 0);
   a.err = err;
   a.band = 8;
   a.tile_rows = M >= BM ? BM : (M > 32 ? (M > 64 ? BM : 64) : (M > 16 ? 32 : 16));
@@ -767,10 +771,11 @@ gemm_status_t run(int64_t G, const int32_t* offsets, int64_t M, int64_t N, int64
       if (e == cudaSuccess && need_b > 0) e = stage(ob, buf + need_a, sms, s);
       if (e != cudaSuccess) return abi_from_cuda(e);
     }
-    const int64_t da[2] = {K, M}, ta[1] = {oa.ld};
+    const int64_t da[2] = {K, M}, ta[1] = {map_pitch(oa)};
     const uint32_t ba[2] = {BK, static_cast<uint32_t>(a.tile_rows)};
     // one matrix: any stride describes it
-    const int64_t db[3] = {K, N, G}, tb[2] = {ob.ld, G > 1 ? ob.stride : ob.ld * N};
+    const int64_t db[3] = {K, N, G}, tb[2] = {map_pitch(ob),
+                                              G > 1 ? ob.stride : map_pitch(ob) * N};
     const uint32_t bb[3] = {BK, BN, 1};
     if (!abi_encode_tiled(&tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, oa.p, da, ta, ba) ||
         !abi_encode_tiled(&tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, ob.p, db, tb, bb))

@@ -732,8 +732,12 @@ struct Operand {
   int64_t count, stride;
 };
 
+// Row pitch in a tensor map.  A single row has none of its own: any will do.
+int64_t map_pitch(const Operand& o) { return o.rows == 1 ? (o.cols + 7) / 8 * 8 : o.ld; }
+
 bool tma_describes(const Operand& o) {
-  return !ops_misaligned(o.p, 16) && o.ld % 8 == 0 && (o.count == 1 || o.stride % 8 == 0);
+  return !ops_misaligned(o.p, 16) && map_pitch(o) % 8 == 0 &&
+         (o.count == 1 || o.stride % 8 == 0);
 }
 
 int64_t staged_bytes(const Operand& o) {
@@ -779,6 +783,8 @@ cudaError_t stage(Operand& o, uint8_t* to, int num_sms, cudaStream_t s) {
 bool encode_output(CUtensorMap* tm, void* D, int d_type, int64_t rows, int64_t cols, int64_t ld,
                    int64_t count, int64_t stride) {
   const int bytes = float_type_bytes(d_type);
+  const int64_t piece = 16 / bytes;
+  if (rows == 1) ld = (cols + piece - 1) / piece * piece;  // a single row's pitch is never used
   if (ops_misaligned(D, 16) || ld * bytes % 16 != 0 || (count > 1 && stride * bytes % 16 != 0))
     return false;
   const int64_t dims[3] = {cols, rows, count};
@@ -808,9 +814,10 @@ gemm_status_t operands(Operand a, Operand b, int rank_b, const uint32_t (&box_a)
     if (e == cudaSuccess && need_b > 0) e = stage(b, buf + need_a, num_sms, s);
     if (e != cudaSuccess) return abi_from_cuda(e);
   }
-  const int64_t da[2] = {a.cols, a.rows}, ta[1] = {a.ld * 2};
+  const int64_t da[2] = {a.cols, a.rows}, ta[1] = {map_pitch(a) * 2};
   const int64_t db[3] = {b.cols, b.rows, b.count};
-  const int64_t tb[2] = {b.ld * 2, (b.count > 1 ? b.stride : b.ld * b.rows) * 2};
+  const int64_t tb[2] = {map_pitch(b) * 2,
+                         (b.count > 1 ? b.stride : map_pitch(b) * b.rows) * 2};
   const uint32_t bb[3] = {box_b[0], box_b[1], 1};
   if (!abi_encode_tiled(tmA, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.p, da, ta, box_a) ||
       !abi_encode_tiled(tmB, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank_b, b.p, db, tb, bb))
@@ -861,7 +868,7 @@ gemm_status_t gemm_bf16gemm_grouped(int64_t G, const int32_t* offsets, int64_t r
   a.D = D;
   a.ldd = ldd;
   a.d_type = d_type;
-  a.d_vec = !ops_misaligned(D, 16) && ldd % (16 / d_bytes) == 0;
+  a.d_vec = !ops_misaligned(D, 16) && (rows == 1 || ldd % (16 / d_bytes) == 0);
   // CTA pairs where their rounds of tiles take less time: a k-block takes a
   // pair 512 cycles (its MMAs) and a single CTA 768 (operands through shared
   // memory), and each group's last row tile is half full on average.
@@ -945,7 +952,7 @@ gemm_status_t gemm_bf16gemm_grouped_wgrad(int64_t G, const int32_t* offsets, int
   a.ldd = ldb;
   a.stride_d = stride_b;
   a.d_type = d_type;
-  a.d_vec = !ops_misaligned(dB, 16) && ldb % (16 / d_bytes) == 0 &&
+  a.d_vec = !ops_misaligned(dB, 16) && (K == 1 || ldb % (16 / d_bytes) == 0) &&
             (G == 1 || stride_b % (16 / d_bytes) == 0);
   a.tile_rows = BM;
   a.band = 8;

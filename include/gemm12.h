@@ -545,8 +545,9 @@ gemm_status_t gemm_quantization(int64_t M, int64_t N, int64_t BM, int64_t BN,
  *             the norm's dim at most 2^30.  More is GEMM_ERR_INVALID_VALUE.
  *  Memory     gemm_rmsnorm_backward keeps partial sums of the weight's
  *             gradient in the stream's scratch; operands of the products
- *             that TMA cannot describe (base not 16-byte aligned, or a row
- *             pitch or matrix stride that is not a multiple of 16 bytes) are
+ *             that TMA cannot describe (base not 16-byte aligned, or a matrix
+ *             stride, or the row pitch of more than one row, that is not a
+ *             multiple of 16 bytes) are
  *             always copied into the stream's staging buffer.  Where that
  *             memory cannot be had (inside a stream capture on a stream
  *             whose buffer is too small, or out of memory) the call returns
