@@ -579,13 +579,10 @@ cudaError_t launch_norm(const NormArgs& a, const RowPlan& p, int grid, cudaStrea
   const dim3 g(static_cast<unsigned>(grid));
   const int threads = p.tpr * p.per_cta;
   if constexpr (VEC) {
-    if (a.ring.stages > 0) {
+    if (a.ring.stages > 0) {  // more than one warp a row: two chunks a thread (plan_rows)
       const size_t smem = static_cast<size_t>(a.ring.stages) * a.dim *
                           (type_bytes(TX) + (TR < 0 ? 0 : type_bytes(TR)));
-      switch (p.chunks_per_thread) {
-        case 1: return ops_launch<norm_kernel<1, VEC, TX, TR, true>>(g, threads, smem, 1, s, a);
-        default: return ops_launch<norm_kernel<2, VEC, TX, TR, true>>(g, threads, smem, 1, s, a);
-      }
+      return ops_launch<norm_kernel<2, VEC, TX, TR, true>>(g, threads, smem, 1, s, a);
     }
   }
   switch (p.chunks_per_thread) {
