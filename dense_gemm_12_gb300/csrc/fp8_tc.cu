@@ -21,22 +21,28 @@
 // Registers move from the first warpgroup to the other two (setmaxnreg) to
 // hold the sums.
 //
-// What bounds it.  A block's MMAs take 512 cycles at the tensor core's rate,
-// its operands 768 through shared memory (48 KB written, 48 KB read, 128 B per
-// cycle); measured, a block takes 730 to 750.  A sum warp needs about 560 of
-// them: three TMEM loads, 64 packed FMAs, and its visits to barriers and scales
-// in shared memory, which is busy with operands and answers late.  So the visits
-// are few: one barrier for operands and scales, one commit per block that both
-// frees the stage and announces the accumulator, no copies of loaded registers.
+// What bounds it.  The sum warps.  A block's MMAs take 512 cycles at the tensor
+// core's rate, and a block takes 730 to 750.  By clock readings in the roles'
+// loops (which add 100 cycles to a block), the issuer finds its operands there
+// and waits 200 to 300 cycles for an accumulator, while the sum warps find every
+// block done when they come to it: of their 840 cycles then, 190 go to the
+// barrier's answer, 380 to 400 to three TMEM loads and the additions up to the
+// accumulator's release, 250 to the last additions and the way round the loop.
+// Scales and barriers lie in shared memory, which is busy with operands (48 KB
+// written and 48 KB read per block) and answers late.  So the visits are few:
+// one barrier for operands and scales, one commit per block that both frees the
+// stage and announces the accumulator, no copies of loaded registers.
 // A tile's end costs 3400 cycles more (64 KB of bf16 leave in 2850, 128 KB of
 // fp32 in 5900), in which the MMAs run two blocks ahead at most.  Measured
-// 395-430 us at 8192^3 (2.6-2.8 PFLOP/s, the clock at the power limit), 62 us at
-// 4096^3 (2.2; 69 us into fp32).  CTA pairs, which halve the operands' traffic,
-// came to the same: each block's accumulator then travels through two CTAs'
-// barriers.  Scales for each row of B cost a second product per element and all
-// scales in all threads, 1330 cycles a block, 98 us at 4096^3.  Reading the
-// accumulator with four threads to a row, each with a quarter of the scales,
-// took 102 us, and the two halves of the columns half a block apart 100 us.
+// 394-423 us at 8192^3 (2.6-2.8 PFLOP/s, the clock at the power limit), 61 us at
+// 4096^3 (2.2; 68 us into fp32).  CTA pairs, which halve the operands' traffic,
+// came to the same: it is not the operands that are waited for, and each block's
+// accumulator then travels through two CTAs' barriers.  Scales for each row of B
+// cost a second product per element and all scales in all threads: 980 cycles to
+// the release instead of 400, 1330 a block, 92 us at 4096^3 (98 when the next
+// two were tried).  Reading the accumulator with four threads to a row, each
+// with a quarter of the scales, took 102 us, and the two halves of the columns
+// half a block apart 100 us.
 //
 // Few tiles: the CTAs of a cluster split a tile's k-blocks and add their sums
 // through distributed shared memory, in k order.  Rows of A beyond a group's
