@@ -109,8 +109,11 @@ __device__ __forceinline__ void mbar_drain_wait(uint64_t* bar, uint32_t parity) 
 // Named barrier `id` over `nthreads` threads that also ORs a predicate: every
 // participant gets true if any of them passed true.  Used to leave a loop
 // together when a bounded wait ran out in some of the threads, so that no
-// thread is left waiting at a later barrier for threads that have gone.
+// thread is left waiting at a later barrier for threads that have gone.  The
+// barrier is a warp-wide instruction, and lanes may have left such a wait
+// apart: they come together first.  Whole warps only.
 __device__ __forceinline__ bool named_bar_any(uint32_t id, uint32_t nthreads, bool v) {
+  __syncwarp();
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred pin, pout;\n\t"

@@ -28,3 +28,12 @@ def test_a_warp_agrees_on_the_outcome_of_a_wait(name, count):
         voted = "_sync(0xffffffffu" in statement
         asked = re.search(r"(__any_sync\(0xffffffffu, !%s\)|named_bar_any\(\w+, \w+, !%s\))" % (var, var), after)
         assert voted or asked, statement
+
+
+def test_a_warp_is_together_at_the_barrier_after_a_wait():
+    # the barrier that collects the answers of several warps is itself warp-wide
+    with open(os.path.join(CSRC, "ptx.cuh")) as f:
+        text = f.read()
+    body = text[text.index("bool named_bar_any("):]
+    body = body[:body.index("\n}\n")]
+    assert "bar.red" in body and body.index("__syncwarp()") < body.index("asm volatile")
