@@ -31,6 +31,9 @@ __all__ = [
     "gemm_fp8_quantize", "gemm_fp8gemm", "gemm_fp8gemm_grouped", "gemm_bf16gemm_grouped",
     "gemm_bf16gemm_grouped_wgrad", "rmsnorm", "rmsnorm_backward", "fp8_quantize", "fp8gemm",
     "fp8gemm_grouped", "bf16gemm_grouped", "bf16gemm_grouped_wgrad",
+    "gemm_expert_route", "gemm_expert_route_backward", "gemm_expert_sort", "gemm_expert_dispatch",
+    "gemm_expert_combine", "gemm_expert_combine_backward", "expert_route", "expert_route_backward",
+    "expert_sort", "expert_dispatch", "expert_combine", "expert_combine_backward",
 ]
 
 STATUS = {
@@ -190,6 +193,22 @@ def load_library(build_if_missing: bool = False):
         lib.gemm_bf16gemm_grouped_wgrad.argtypes = [i64, vp, i64, i64, i64, f32, vp, i64, vp, i64,
                                                     f32, vp, i64, i64, cint, vp]
         lib.gemm_bf16gemm_grouped_wgrad.restype = cint
+        lib.gemm_expert_route.argtypes = [i64, i64, i64, vp, i64, cint, cint, vp, vp, vp]
+        lib.gemm_expert_route.restype = cint
+        lib.gemm_expert_route_backward.argtypes = [i64, i64, i64, vp, i64, cint, cint, vp, vp, vp, i64,
+                                                   cint, vp]
+        lib.gemm_expert_route_backward.restype = cint
+        lib.gemm_expert_sort.argtypes = [i64, i64, vp, vp, vp, vp, vp]
+        lib.gemm_expert_sort.restype = cint
+        lib.gemm_expert_dispatch.argtypes = [i64, i64, i64, i64, cint, vp, i64, vp, vp, i64, vp, i64, vp,
+                                             i64, vp]
+        lib.gemm_expert_dispatch.restype = cint
+        lib.gemm_expert_combine.argtypes = [i64, i64, i64, i64, vp, i64, cint, vp, vp, vp, i64, cint, vp,
+                                            i64, cint, vp]
+        lib.gemm_expert_combine.restype = cint
+        lib.gemm_expert_combine_backward.argtypes = [i64, i64, i64, i64, vp, i64, cint, vp, i64, cint, vp,
+                                                     vp, vp, i64, cint, vp, vp]
+        lib.gemm_expert_combine_backward.restype = cint
         lib.gemm_version.argtypes = []
         lib.gemm_version.restype = cint
         _lib = lib
@@ -383,6 +402,46 @@ def gemm_bf16gemm_grouped_wgrad(G, offsets, rows, N, K, alpha, A, lda, dD, lddd,
                                                       lddd, beta, dB, ldb, stride_b, d_type, stream)
 
 
+def gemm_expert_route(rows, G, top, logits, ld, logits_type, normalize, expert, weight, stream=0) -> int:
+    """Each row's `top` largest logits and their weights. Returns the status."""
+    return load_library().gemm_expert_route(rows, G, top, logits, ld, logits_type, normalize, expert,
+                                            weight, stream)
+
+
+def gemm_expert_route_backward(rows, G, top, logits, ld, logits_type, normalize, expert, dweight,
+                               dlogits, ldd, dlogits_type, stream=0) -> int:
+    """The logits' gradient. Returns the status."""
+    return load_library().gemm_expert_route_backward(rows, G, top, logits, ld, logits_type, normalize,
+                                                     expert, dweight, dlogits, ldd, dlogits_type, stream)
+
+
+def gemm_expert_sort(n, G, expert, slot, offsets, source, stream=0) -> int:
+    """Pairs sorted by expert. Returns the status."""
+    return load_library().gemm_expert_sort(n, G, expert, slot, offsets, source, stream)
+
+
+def gemm_expert_dispatch(rows, top, n, dim, elem_bytes, x, ldx, slot, a, lda, x_scales, ld_xs, a_scales,
+                         ld_as, stream=0) -> int:
+    """The tokens' rows to their experts' places. Returns the status."""
+    return load_library().gemm_expert_dispatch(rows, top, n, dim, elem_bytes, x, ldx, slot, a, lda,
+                                               x_scales, ld_xs, a_scales, ld_as, stream)
+
+
+def gemm_expert_combine(rows, top, n, dim, a, lda, a_type, slot, weight, residual, ldr, residual_type,
+                        out, ldo, out_type, stream=0) -> int:
+    """The experts' rows back to the tokens, weighted. Returns the status."""
+    return load_library().gemm_expert_combine(rows, top, n, dim, a, lda, a_type, slot, weight, residual,
+                                              ldr, residual_type, out, ldo, out_type, stream)
+
+
+def gemm_expert_combine_backward(rows, top, n, dim, dout, lddo, dout_type, a, lda, a_type, slot, weight,
+                                 da, ldda, da_type, dweight, stream=0) -> int:
+    """Its gradients. Returns the status."""
+    return load_library().gemm_expert_combine_backward(rows, top, n, dim, dout, lddo, dout_type, a, lda,
+                                                       a_type, slot, weight, da, ldda, da_type, dweight,
+                                                       stream)
+
+
 # ------------------------------------------------------------ tensor helpers
 def _row_major_ld(t, name):
     if t.dim() != 2:
@@ -531,6 +590,7 @@ def bf16gemm_fused(A, B, D, C=None, alpha=1.0, beta=0.0, bias=None, act="none", 
 # shape and strides.
 _TORCH = None       # torch, its current-stream getter and the dtypes used below
 _FLOAT_CODES = {}   # dtype -> gemm_out_t
+_ROW_BYTES = {}     # dtype -> bytes, of rows that are only moved
 
 
 def _torch_once():
@@ -538,6 +598,7 @@ def _torch_once():
     if _TORCH is None:
         import torch
         _FLOAT_CODES.update({torch.float32: OUT["f32"], torch.bfloat16: OUT["bf16"]})
+        _ROW_BYTES.update({torch.float32: 4, torch.bfloat16: 2, torch.float8_e4m3fn: 1, torch.int8: 1})
         getter = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         if getter is None:
             def getter(index):
@@ -757,3 +818,142 @@ def bf16gemm_grouped_wgrad(A, dD, offsets, dB, alpha=1.0, beta=0.0, stream=None)
     if st != 0:
         raise GemmError(st, "gemm_bf16gemm_grouped_wgrad")
     return dB
+
+
+def _dense(t, shape, dtype, dev, name):
+    """Address of a contiguous array of this shape."""
+    if t.dtype != dtype or t.get_device() != dev:
+        raise TypeError("%s must be a %s tensor on the other operands' device" % (name, dtype))
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError("%s must be contiguous, of shape %s" % (name, tuple(shape)))
+    return t.data_ptr()
+
+
+def _pairs(t, name):
+    if t.dim() != 2:
+        raise ValueError("%s must be 2-D (rows, top)" % name)
+    return t.shape
+
+
+def expert_route(logits, expert, weight, normalize=False, stream=None):
+    """The top largest of each row of logits (rows, G), float32 or bfloat16, into expert (rows, top)
+    int32, the largest first, and their shares of the row's softmax -- with normalize, of the chosen
+    ones' -- into weight (rows, top) float32.  Logits of -inf are never chosen: expert -1, weight 0."""
+    _, _, f32, _, i32 = _torch_once()
+    shape = _pairs(expert, "expert")
+    if logits.dim() != 2 or logits.shape[0] != shape[0]:
+        raise ValueError("logits must be 2-D with expert's rows")
+    dev = logits.get_device()
+    handle = _stream_of(dev, stream)
+    st = load_library().gemm_expert_route(
+        shape[0], logits.shape[1], shape[1], *_float_array(logits, logits.shape, dev, "logits"),
+        1 if normalize else 0, _dense(expert, shape, i32, dev, "expert"),
+        _dense(weight, shape, f32, dev, "weight"), handle)
+    if st != 0:
+        raise GemmError(st, "gemm_expert_route")
+
+
+def expert_route_backward(logits, expert, dweight, dlogits, normalize=False, stream=None):
+    """dlogits <- the gradient of expert_route's weights with respect to the logits."""
+    _, _, f32, _, i32 = _torch_once()
+    shape = _pairs(expert, "expert")
+    if logits.dim() != 2 or logits.shape[0] != shape[0]:
+        raise ValueError("logits must be 2-D with expert's rows")
+    dev = logits.get_device()
+    handle = _stream_of(dev, stream)
+    st = load_library().gemm_expert_route_backward(
+        shape[0], logits.shape[1], shape[1], *_float_array(logits, logits.shape, dev, "logits"),
+        1 if normalize else 0, _dense(expert, shape, i32, dev, "expert"),
+        _dense(dweight, shape, f32, dev, "dweight"),
+        *_float_array(dlogits, logits.shape, dev, "dlogits"), handle)
+    if st != 0:
+        raise GemmError(st, "gemm_expert_route_backward")
+    return dlogits
+
+
+def expert_sort(expert, slot, offsets, source=None, stream=None):
+    """The pairs (token, choice) of expert (rows, top) int32 sorted by expert, each expert's in their
+    order: offsets (G + 1,) int32 for the grouped products, slot (rows, top) int32 the pairs' rows (-1
+    where the id is outside 0 .. G - 1), source (rows * top,) int32 the rows' pairs (-1 behind the
+    last)."""
+    i32 = _torch_once()[4]
+    shape = _pairs(expert, "expert")
+    if offsets.dim() != 1 or offsets.shape[0] < 1:
+        raise ValueError("offsets must be a vector of G + 1 values")
+    n, dev = shape[0] * shape[1], expert.get_device()
+    handle = _stream_of(dev, stream)
+    st = load_library().gemm_expert_sort(
+        n, offsets.shape[0] - 1, _dense(expert, shape, i32, dev, "expert"),
+        _dense(slot, shape, i32, dev, "slot"), _vector(offsets, offsets.shape[0], i32, dev, "offsets"),
+        None if source is None else _vector(source, n, i32, dev, "source"), handle)
+    if st != 0:
+        raise GemmError(st, "gemm_expert_sort")
+
+
+def expert_dispatch(x, slot, a, x_scales=None, a_scales=None, stream=None):
+    """a[slot[r, j]] <- x[r] for each token r and choice j: x (rows, dim), slot (rows, top) int32 from
+    expert_sort, a (n, dim) of x's dtype (float32, bfloat16, float8_e4m3fn or int8).  With scales: x's
+    fp8 scales (ceil(dim / 128), rows) to a's (ceil(dim / 128), n).  Other rows of a stay."""
+    f32, i32 = _torch_once()[2], _torch_once()[4]
+    shape = _pairs(slot, "slot")
+    if x.dim() != 2 or a.dim() != 2 or x.shape[0] != shape[0]:
+        raise ValueError("x and a must be 2-D, x with slot's rows")
+    if x.dtype not in _ROW_BYTES:
+        raise TypeError("x must be a float32, bfloat16, float8_e4m3fn or int8 tensor")
+    if (x_scales is None) != (a_scales is None):
+        raise ValueError("x_scales and a_scales come together")
+    rows, dim = x.shape
+    n, dev = a.shape[0], x.get_device()
+    handle = _stream_of(dev, stream)
+    kb = -(-dim // 128)
+    none = (None, 0)
+    st = load_library().gemm_expert_dispatch(
+        rows, shape[1], n, dim, _ROW_BYTES[x.dtype], *_array(x, (rows, dim), x.dtype, dev, "x"),
+        _dense(slot, shape, i32, dev, "slot"), *_array(a, (n, dim), x.dtype, dev, "a"),
+        *(none if x_scales is None else _array(x_scales, (kb, rows), f32, dev, "x_scales")),
+        *(none if x_scales is None else _array(a_scales, (kb, n), f32, dev, "a_scales")), handle)
+    if st != 0:
+        raise GemmError(st, "gemm_expert_dispatch")
+    return a
+
+
+def expert_combine(a, slot, out, weight=None, residual=None, stream=None):
+    """out[r] <- residual[r] + sum over j of weight[r, j] * a[slot[r, j]]: a (n, dim), residual and out
+    (rows, dim) float32 or bfloat16, weight (rows, top) float32 (None: 1, which is expert_dispatch's
+    gradient).  out may be the residual itself."""
+    _, _, f32, _, i32 = _torch_once()
+    shape = _pairs(slot, "slot")
+    if a.dim() != 2 or out.dim() != 2:
+        raise ValueError("a and out must be 2-D")
+    n, dim = a.shape
+    rows, dev = shape[0], out.get_device()
+    handle = _stream_of(dev, stream)
+    st = load_library().gemm_expert_combine(
+        rows, shape[1], n, dim, *_float_array(a, (n, dim), dev, "a"),
+        _dense(slot, shape, i32, dev, "slot"),
+        None if weight is None else _dense(weight, shape, f32, dev, "weight"),
+        *((None, 0, 0) if residual is None else _float_array(residual, (rows, dim), dev, "residual")),
+        *_float_array(out, (rows, dim), dev, "out"), handle)
+    if st != 0:
+        raise GemmError(st, "gemm_expert_combine")
+    return out
+
+
+def expert_combine_backward(dout, a, slot, weight, da=None, dweight=None, stream=None):
+    """Gradients of expert_combine: da[slot[r, j]] <- weight[r, j] * dout[r] (n, dim), dweight[r, j] <-
+    the product of dout[r] and a[slot[r, j]] (0 without a row).  da may be a itself."""
+    _, _, f32, _, i32 = _torch_once()
+    shape = _pairs(slot, "slot")
+    if a.dim() != 2 or dout.dim() != 2:
+        raise ValueError("a and dout must be 2-D")
+    n, dim = a.shape
+    rows, dev = shape[0], dout.get_device()
+    handle = _stream_of(dev, stream)
+    st = load_library().gemm_expert_combine_backward(
+        rows, shape[1], n, dim, *_float_array(dout, (rows, dim), dev, "dout"),
+        *_float_array(a, (n, dim), dev, "a"), _dense(slot, shape, i32, dev, "slot"),
+        _dense(weight, shape, f32, dev, "weight"),
+        *((None, 0, 0) if da is None else _float_array(da, (n, dim), dev, "da")),
+        None if dweight is None else _dense(dweight, shape, f32, dev, "dweight"), handle)
+    if st != 0:
+        raise GemmError(st, "gemm_expert_combine_backward")

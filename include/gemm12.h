@@ -544,7 +544,8 @@ gemm_status_t gemm_quantization(int64_t M, int64_t N, int64_t BM, int64_t BN,
  *             rows, N, and K of the bf16 products) at most 2^31 - 256, and
  *             the norm's dim at most 2^30.  More is GEMM_ERR_INVALID_VALUE.
  *  Memory     gemm_rmsnorm_backward keeps partial sums of the weight's
- *             gradient in the stream's scratch; operands of the products
+ *             gradient in the stream's scratch, gemm_expert_sort counters;
+ *             operands of the products
  *             that TMA cannot describe (base not 16-byte aligned, or a matrix
  *             stride, or the row pitch of more than one row, that is not a
  *             multiple of 16 bytes) are
@@ -717,6 +718,92 @@ gemm_status_t gemm_fp8gemm_grouped(int64_t G, const int32_t *offsets, int64_t ro
                                    int64_t ldb, int64_t stride_b, const float *b_scales,
                                    int64_t ld_bs, int64_t stride_bs, int b_block, float beta,
                                    void *D, int64_t ldd, int d_type, void *stream);
+
+/*
+ * The rows around products grouped by expert.  A router gives each of `rows`
+ * tokens `top` experts (0 <= top <= 32, top <= G <= 1024; more is
+ * GEMM_ERR_UNSUPPORTED) with weights; the rows x top pairs (token, choice) are
+ * numbered token after token.  Their ids, places and weights are contiguous
+ * rows x top arrays in device memory, and rows * top is below 2^31.
+ *
+ * gemm_expert_route -- the `top` largest of each row's G logits (ld, fp32 or
+ * bf16), the largest first and of equal ones the lowest index first, and their
+ * weights in fp32:
+ *
+ *     p = softmax(logits)     weight_j = p[expert_j]
+ *     or, with `normalize`,   weight_j = p[expert_j] / sum over j of p[expert_j]
+ *
+ * A logit of -infinity masks its expert out, and neither that nor NaN is ever
+ * chosen: choices that cannot be made are expert -1 with weight 0 (all of a row
+ * whose logits are all masked).  A NaN or +infinity among a row's logits makes
+ * the weights that it enters NaN.
+ *
+ * gemm_expert_route_backward -- the logits' gradient, given dweight:
+ *
+ *     dlogits_i = p_i * (g_i - sum_j dweight_j p[expert_j]),
+ *     g_i = sum of dweight_j over the j with expert_j = i
+ *
+ * or, with `normalize`, dlogits_i = the sum over those j of
+ * weight_j * (dweight_j - sum_j dweight_j weight_j).  Ids outside 0 .. G - 1
+ * are no choice.  dlogits may take the place of the logits (same type and ld).
+ */
+gemm_status_t gemm_expert_route(int64_t rows, int64_t G, int64_t top, const void *logits, int64_t ld,
+                                int logits_type, int normalize, int32_t *expert, float *weight,
+                                void *stream);
+gemm_status_t gemm_expert_route_backward(int64_t rows, int64_t G, int64_t top, const void *logits,
+                                         int64_t ld, int logits_type, int normalize,
+                                         const int32_t *expert, const float *dweight, void *dlogits,
+                                         int64_t ldd, int dlogits_type, void *stream);
+
+/*
+ * gemm_expert_sort -- n pairs sorted by expert, those of one expert in their
+ * order: offsets (G + 1 values, for the grouped products) are the experts'
+ * first rows, slot[i] is pair i's row, and source (NULL, or n values) the other
+ * way round: source[slot[i]] = i.  Pairs whose id is outside 0 .. G - 1 have no
+ * row: slot -1; source is -1 from row offsets[G] on.  More than 8192 pairs
+ * need counters in the stream's scratch (see Memory).
+ */
+gemm_status_t gemm_expert_sort(int64_t n, int64_t G, const int32_t *expert, int32_t *slot,
+                               int32_t *offsets, int32_t *source, void *stream);
+
+/*
+ * gemm_expert_dispatch -- a[slot[r][j]] = x[r]: each token's row (of `dim`
+ * elements of elem_bytes = 1, 2 or 4) to its places among the n rows of `a`.
+ * x_scales and a_scales, both or neither: the rows' fp8 scales, ceil(dim / 128)
+ * x rows and x n, moved likewise.  Here and below a slot outside 0 .. n - 1 is
+ * no row, and rows of `a` that no slot names are not written.  A slot that
+ * names a row twice leaves one of the two there.
+ *
+ * gemm_expert_combine -- back again:
+ *
+ *     out[r] = residual[r] + sum over j of weight[r][j] * a[slot[r][j]]
+ *
+ * in fp32, in the order of j, rounded once; weight NULL: 1 (which is the
+ * gradient of gemm_expert_dispatch); residual NULL: 0.  a, residual and out are
+ * fp32 or bf16 each; out may take the place of the residual (same type and ld).
+ *
+ * gemm_expert_combine_backward -- with dout the gradient of out,
+ *
+ *     da[slot[r][j]] = weight[r][j] * dout[r]
+ *     dweight[r][j] = sum over the row of dout[r] * a[slot[r][j]]
+ *
+ * (0 for a pair without a row).  Either may be NULL; `a` is read for dweight
+ * only, and da may take its place (same type and ld).  The residual's gradient
+ * is dout itself.
+ */
+gemm_status_t gemm_expert_dispatch(int64_t rows, int64_t top, int64_t n, int64_t dim, int elem_bytes,
+                                   const void *x, int64_t ldx, const int32_t *slot, void *a, int64_t lda,
+                                   const float *x_scales, int64_t ld_xs, float *a_scales, int64_t ld_as,
+                                   void *stream);
+gemm_status_t gemm_expert_combine(int64_t rows, int64_t top, int64_t n, int64_t dim, const void *a,
+                                  int64_t lda, int a_type, const int32_t *slot, const float *weight,
+                                  const void *residual, int64_t ldr, int residual_type, void *out,
+                                  int64_t ldo, int out_type, void *stream);
+gemm_status_t gemm_expert_combine_backward(int64_t rows, int64_t top, int64_t n, int64_t dim,
+                                           const void *dout, int64_t lddo, int dout_type, const void *a,
+                                           int64_t lda, int a_type, const int32_t *slot,
+                                           const float *weight, void *da, int64_t ldda, int da_type,
+                                           float *dweight, void *stream);
 
 /* Library version, major * 10000 + minor * 100 + patch. */
 int gemm_version(void);
