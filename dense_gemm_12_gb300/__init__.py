@@ -34,6 +34,8 @@ __all__ = [
     "gemm_expert_route", "gemm_expert_route_backward", "gemm_expert_sort", "gemm_expert_dispatch",
     "gemm_expert_combine", "gemm_expert_combine_backward", "expert_route", "expert_route_backward",
     "expert_sort", "expert_dispatch", "expert_combine", "expert_combine_backward",
+    "LayernormArgs", "LayernormGradArgs", "gemm_layernorm", "gemm_layernorm_backward", "layernorm",
+    "layernorm_backward",
 ]
 
 STATUS = {
@@ -94,6 +96,33 @@ class RmsnormGradArgs(ctypes.Structure):
         ("residual_grad_type", ctypes.c_int),
         ("dh", ctypes.c_void_p), ("lddh", ctypes.c_int64), ("dh_type", ctypes.c_int),
         ("dweight", ctypes.c_void_p),
+    ]
+
+
+class LayernormArgs(ctypes.Structure):
+    """Mirror of gemm_layernorm_t (include/gemm12.h)."""
+    _fields_ = [
+        ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("x_type", ctypes.c_int),
+        ("residual", ctypes.c_void_p), ("ldr", ctypes.c_int64), ("residual_type", ctypes.c_int),
+        ("h", ctypes.c_void_p), ("ldh", ctypes.c_int64), ("h_type", ctypes.c_int),
+        ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("eps", ctypes.c_float),
+        ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64), ("y_type", ctypes.c_int),
+        ("q", ctypes.c_void_p), ("ldq", ctypes.c_int64), ("q_type", ctypes.c_int),
+        ("scales", ctypes.c_void_p), ("ld_scales", ctypes.c_int64),
+        ("mean", ctypes.c_void_p), ("rstd", ctypes.c_void_p),
+    ]
+
+
+class LayernormGradArgs(ctypes.Structure):
+    """Mirror of gemm_layernorm_grad_t (include/gemm12.h)."""
+    _fields_ = [
+        ("dy", ctypes.c_void_p), ("lddy", ctypes.c_int64), ("dy_type", ctypes.c_int),
+        ("h", ctypes.c_void_p), ("ldh", ctypes.c_int64), ("h_type", ctypes.c_int),
+        ("weight", ctypes.c_void_p), ("mean", ctypes.c_void_p), ("rstd", ctypes.c_void_p),
+        ("residual_grad", ctypes.c_void_p), ("ldrg", ctypes.c_int64),
+        ("residual_grad_type", ctypes.c_int),
+        ("dh", ctypes.c_void_p), ("lddh", ctypes.c_int64), ("dh_type", ctypes.c_int),
+        ("dweight", ctypes.c_void_p), ("dbias", ctypes.c_void_p),
     ]
 
 
@@ -193,6 +222,10 @@ def load_library(build_if_missing: bool = False):
         lib.gemm_bf16gemm_grouped_wgrad.argtypes = [i64, vp, i64, i64, i64, f32, vp, i64, vp, i64,
                                                     f32, vp, i64, i64, cint, vp]
         lib.gemm_bf16gemm_grouped_wgrad.restype = cint
+        lib.gemm_layernorm.argtypes = [i64, i64, ctypes.POINTER(LayernormArgs), vp]
+        lib.gemm_layernorm.restype = cint
+        lib.gemm_layernorm_backward.argtypes = [i64, i64, ctypes.POINTER(LayernormGradArgs), vp]
+        lib.gemm_layernorm_backward.restype = cint
         lib.gemm_expert_route.argtypes = [i64, i64, i64, vp, i64, cint, cint, vp, vp, vp]
         lib.gemm_expert_route.restype = cint
         lib.gemm_expert_route_backward.argtypes = [i64, i64, i64, vp, i64, cint, cint, vp, vp, vp, i64,
@@ -363,6 +396,16 @@ def gemm_rmsnorm(rows, dim, args: "RmsnormArgs", stream=0) -> int:
 def gemm_rmsnorm_backward(rows, dim, args: "RmsnormGradArgs", stream=0) -> int:
     """Its gradients (gemm_rmsnorm_grad_t). Returns the status."""
     return load_library().gemm_rmsnorm_backward(rows, dim, ctypes.byref(args), stream)
+
+
+def gemm_layernorm(rows, dim, args: "LayernormArgs", stream=0) -> int:
+    """Layer norm (gemm_layernorm_t). Returns the status."""
+    return load_library().gemm_layernorm(rows, dim, ctypes.byref(args), stream)
+
+
+def gemm_layernorm_backward(rows, dim, args: "LayernormGradArgs", stream=0) -> int:
+    """Its gradients (gemm_layernorm_grad_t). Returns the status."""
+    return load_library().gemm_layernorm_backward(rows, dim, ctypes.byref(args), stream)
 
 
 def gemm_fp8_quantize(rows, cols, x, ldx, x_type, block, transpose, q, ldq, scales, ld_scales,
@@ -607,6 +650,11 @@ def _torch_once():
     return _TORCH
 
 
+def _int8():
+    import torch
+    return torch.int8
+
+
 def _stream_of(dev, stream):
     if dev < 0:
         raise TypeError("all tensors must be CUDA tensors")
@@ -694,6 +742,68 @@ def rmsnorm_backward(dy, h, weight, rstd, dh, dweight=None, residual_grad=None, 
     st = load_library().gemm_rmsnorm_backward(rows, dim, ctypes.byref(a), handle)
     if st != 0:
         raise GemmError(st, "gemm_rmsnorm_backward")
+    return dh
+
+
+def layernorm(x, weight=None, bias=None, eps=1e-5, residual=None, h=None, y=None, q=None, scales=None,
+              mean=None, rstd=None, stream=None):
+    """h = x + residual; y = (h - mean) / sqrt(var + eps) * weight + bias over the last dimension of x
+    (rows, dim), into the given outputs: h, y (float32 or bfloat16), q with scales -- y in
+    float8_e4m3fn with scales (ceil(dim / 128), rows), or in int8 with scales (rows,) -- and mean,
+    rstd (rows,).  weight, bias and scales are float32.  h may be the residual itself, y x itself."""
+    _, f8, f32, _, _ = _torch_once()
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D")
+    shape, dev = x.shape, x.get_device()
+    rows, dim = shape
+    handle = _stream_of(dev, stream)
+    if (q is None) != (scales is None):
+        raise ValueError("q and scales come together")
+    none = (None, 0, 0)
+    if q is None:
+        eight = (None, 0, 0, None, 0)
+    elif q.dtype == f8:
+        eight = (*_array(q, shape, f8, dev, "q"), OUT["f8e4m3"],
+                 *_array(scales, (-(-dim // 128), rows), f32, dev, "scales"))
+    else:
+        eight = (*_array(q, shape, _int8(), dev, "q"), OUT["s8"],
+                 _vector(scales, rows, f32, dev, "scales"), 0)
+    a = LayernormArgs(
+        *_float_array(x, shape, dev, "x"),
+        *(none if residual is None else _float_array(residual, shape, dev, "residual")),
+        *(none if h is None else _float_array(h, shape, dev, "h")),
+        None if weight is None else _vector(weight, dim, f32, dev, "weight"),
+        None if bias is None else _vector(bias, dim, f32, dev, "bias"), eps,
+        *(none if y is None else _float_array(y, shape, dev, "y")), *eight,
+        None if mean is None else _vector(mean, rows, f32, dev, "mean"),
+        None if rstd is None else _vector(rstd, rows, f32, dev, "rstd"))
+    st = load_library().gemm_layernorm(rows, dim, ctypes.byref(a), handle)
+    if st != 0:
+        raise GemmError(st, "gemm_layernorm")
+
+
+def layernorm_backward(dy, h, weight, mean, rstd, dh, dweight=None, dbias=None, residual_grad=None,
+                       stream=None):
+    """Gradients of layernorm's y: dh <- the gradient with respect to h (and so x and the residual)
+    plus residual_grad, dweight and dbias (dim,) <- those of the weight (None: 1) and the bias."""
+    f32 = _torch_once()[2]
+    if dy.dim() != 2:
+        raise ValueError("dy must be 2-D")
+    shape, dev = dy.shape, dy.get_device()
+    rows, dim = shape
+    handle = _stream_of(dev, stream)
+    a = LayernormGradArgs(
+        *_float_array(dy, shape, dev, "dy"), *_float_array(h, shape, dev, "h"),
+        None if weight is None else _vector(weight, dim, f32, dev, "weight"),
+        _vector(mean, rows, f32, dev, "mean"), _vector(rstd, rows, f32, dev, "rstd"),
+        *((None, 0, 0) if residual_grad is None else
+          _float_array(residual_grad, shape, dev, "residual_grad")),
+        *_float_array(dh, shape, dev, "dh"),
+        None if dweight is None else _vector(dweight, dim, f32, dev, "dweight"),
+        None if dbias is None else _vector(dbias, dim, f32, dev, "dbias"))
+    st = load_library().gemm_layernorm_backward(rows, dim, ctypes.byref(a), handle)
+    if st != 0:
+        raise GemmError(st, "gemm_layernorm_backward")
     return dh
 
 

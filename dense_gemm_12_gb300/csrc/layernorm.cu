@@ -1,0 +1,704 @@
+// layernorm.cu -- layer norm with the residual's addition, its output in fp32,
+// bf16, fp8 with block scales or int8 with a scale per row, and its gradients.
+//
+//     h = x + r      m = mean_j h_j      s = (mean_j (h_j - m)^2 + eps)^-1/2
+//     y_j = (h_j - m) s w_j + b_j
+//
+// and, with dy the gradient of y, dr that of the stored h, xh = (h - m) s and
+// g = dy w:
+//
+//     dh = s (g - mean_j g_j - xh mean_j(g_j xh_j)) + dr
+//     dw = sum_rows dy xh        db = sum_rows dy
+//
+// Bound by memory: as in norm.cu, a row is read once, through the ring where
+// there are many, kept in registers over its sums, and written once.
+//
+// The squares are summed about the mean, never as mean(h^2) - m^2, which loses
+// everything when the mean is large.  The mean itself is only known to fp32's
+// rounding; what it is off by is the mean of the differences from it, which
+// comes with the second sum and is taken off both the squares' mean and the
+// values.
+#include "norm.cuh"
+
+namespace g12 {
+namespace {
+
+struct LnArgs {
+  int64_t rows;
+  int dim;
+  int tpr;
+  RingArgs ring;
+  gemm_layernorm_t p;
+};
+
+// Elements of chunk column c, and (not VEC) 16 i further, inside the row.
+template <bool VEC>
+__device__ __forceinline__ bool inside(int c, int i, int dim) {
+  return VEC || c + 16 * i < dim;
+}
+
+// y of one chunk from its differences from the mean; 0 where nothing is.
+template <bool VEC>
+__device__ __forceinline__ void affine(const float* weight, const float* bias, int c, int dim, bool in,
+                                       float rstd, float off, const float (&d)[8], float (&y)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = 0.0f;
+  if (!in) return;
+  float w[8], b[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    w[i] = 1.0f;
+    b[i] = 0.0f;
+  }
+  if (weight != nullptr) load_weight<VEC>(weight, c, dim, w);
+  if (bias != nullptr) load_weight<VEC>(bias, c, dim, b);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (inside<VEC>(c, i, dim)) y[i] = fmaf((d[i] - off) * rstd, w[i], b[i]);
+}
+
+__device__ __forceinline__ float chunk_amax(const float (&y)[8]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, finite_abs(y[i]));
+  return m;
+}
+
+// C > 0: a row in registers.  C == 0: rows longer than that are read three
+// times, and once more where their largest value is needed before the first is
+// written.  Nothing of a row is written before its last read.
+template <int C, bool VEC, int TX, int TR, bool RING = false>
+__global__ void __launch_bounds__(kMaxThreads, RING ? 2 : 1)
+    layernorm_kernel(const __grid_constant__ LnArgs a) {
+  __shared__ float red_mean[2][16], red_max[2][16];
+  __shared__ float2 red_var[2][16];
+  __shared__ Ring ring;
+  extern __shared__ uint4 dyn_smem[];
+  uint8_t* const stages = reinterpret_cast<uint8_t*>(dyn_smem);
+  const int stage_bytes = RING ? a.dim * (type_bytes(TX) + (TR < 0 ? 0 : type_bytes(TR))) : 0;
+  auto fetch = [&](int64_t row, int s) {
+    uint8_t* to = stages + s * stage_bytes;
+    mbar_arrive_expect_tx(&ring.full[s], static_cast<uint32_t>(stage_bytes));
+    bulk_load(to, static_cast<const uint8_t*>(a.p.x) + row * a.p.ldx * type_bytes(TX),
+              static_cast<uint32_t>(a.dim * type_bytes(TX)), &ring.full[s]);
+    if constexpr (TR >= 0)
+      bulk_load(to + a.dim * type_bytes(TX),
+                static_cast<const uint8_t*>(a.p.residual) + row * a.p.ldr * type_bytes(TR),
+                static_cast<uint32_t>(a.dim * type_bytes(TR)), &ring.full[s]);
+  };
+  if (RING) ring_init(ring, a.ring.stages);
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (RING && threadIdx.x == 0)
+    for (int s = 0; s < a.ring.stages; ++s) {
+      const int64_t row = blockIdx.x + static_cast<int64_t>(s) * gridDim.x;
+      if (row < a.rows) fetch(row, s);
+    }
+  int slot = 0;
+  uint32_t parity = 0;
+  const int tpr = a.tpr;
+  const int t = threadIdx.x % tpr;
+  const int per_cta = blockDim.x / tpr;
+  const int chunks = VEC ? a.dim / 8 : (a.dim + kFp8Block - 1) / kFp8Block * 16;
+  const float inv_dim = 1.0f / static_cast<float>(a.dim);
+  uint32_t turn_mean = 0, turn_var = 0, turn_max = 0;
+  const bool s8 = a.p.q != nullptr && a.p.q_type == GEMM_OUT_S8;
+  const bool f8 = a.p.q != nullptr && !s8;
+  // given the sums of the differences from `mean` and of their squares
+  auto statistics = [&](int64_t row, float mean, float2 sums, float& off, float& rstd) {
+    off = sums.x * inv_dim;
+    const float var = fmaf(sums.y, inv_dim, -off * off);
+    rstd = rsqrtf((var < 0.0f ? 0.0f : var) + a.p.eps);  // (NaN stays)
+    if (t == 0) {
+      if (a.p.mean != nullptr) a.p.mean[row] = mean + off;
+      if (a.p.rstd != nullptr) a.p.rstd[row] = rstd;
+    }
+  };
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * per_cta + threadIdx.x / tpr; row < a.rows;
+       row += static_cast<int64_t>(gridDim.x) * per_cta) {
+    float sum = 0.0f, off, rstd;
+    if constexpr (C > 0) {
+      Inputs<VEC, TX, TR> raw[C];
+      bool in[C];
+#pragma unroll
+      for (int k = 0; k < C; ++k) {
+        const int chunk = k * tpr + t;
+        const int c = chunk_col<VEC>(chunk);
+        in[k] = chunk < chunks && c < a.dim;
+        if constexpr (RING) {
+          if (k == 0) mbar_wait_late(&ring.full[slot], parity, &ring.abort_flag, a.ring.err);
+          raw[k].from_ring(a, stages + slot * stage_bytes, c, in[k]);
+        } else {
+          raw[k].load(a, row, c, in[k]);
+        }
+      }
+      float h[C][8];
+#pragma unroll
+      for (int k = 0; k < C; ++k) {
+        raw[k].sum(a, h[k]);  // zeros where nothing is
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum += h[k][i];
+        if (a.p.h != nullptr && in[k])
+          store8<VEC>(a.p.h, a.p.h_type, row * a.p.ldh, chunk_col<VEC>(k * tpr + t), a.dim, h[k]);
+      }
+      const float mean = row_sum(sum, tpr, red_mean, turn_mean) * inv_dim;
+      if constexpr (RING) {
+        // every thread has read the stage (row_sum's barrier): the next row
+        const int64_t next = row + static_cast<int64_t>(a.ring.stages) * gridDim.x;
+        if (threadIdx.x == 0 && next < a.rows && !*const_cast<volatile int*>(&ring.abort_flag))
+          fetch(next, slot);
+        if (++slot == a.ring.stages) {
+          slot = 0;
+          parity ^= 1u;
+        }
+      }
+      float2 sums = make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int k = 0; k < C; ++k) {
+        const int c = chunk_col<VEC>(k * tpr + t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          h[k][i] -= mean;
+          if (in[k] && inside<VEC>(c, i, a.dim)) {
+            sums.x += h[k][i];
+            sums.y = fmaf(h[k][i], h[k][i], sums.y);
+          }
+        }
+      }
+      statistics(row, mean, row_sums(sums, tpr, red_var, turn_var), off, rstd);
+      float amax = 0.0f;
+#pragma unroll
+      for (int k = 0; k < C; ++k) {
+        const int c = chunk_col<VEC>(k * tpr + t);
+        float y[8];
+        affine<VEC>(a.p.weight, a.p.bias, c, a.dim, in[k], rstd, off, h[k], y);
+        if (a.p.y != nullptr && in[k]) store8<VEC>(a.p.y, a.p.y_type, row * a.p.ldy, c, a.dim, y);
+        if (f8) write_fp8<VEC>(a.p.q, a.p.ldq, a.p.scales, a.p.ld_scales, row, c, a.dim, in[k], y);
+        if (s8) {
+          amax = fmaxf(amax, chunk_amax(y));
+#pragma unroll
+          for (int i = 0; i < 8; ++i) h[k][i] = y[i];
+        }
+      }
+      if (!s8) continue;
+      amax = row_max(amax, tpr, red_max, turn_max);
+      const float f = s8_factor(amax);
+#pragma unroll
+      for (int k = 0; k < C; ++k)
+        if (in[k]) write_s8<VEC>(a.p.q, a.p.ldq, row, chunk_col<VEC>(k * tpr + t), a.dim, f, h[k]);
+      if (t == 0) a.p.scales[row] = s8_scale(amax);
+    } else {
+      auto load = [&](int c, bool in, float (&h)[8]) {
+        Inputs<VEC, TX, TR> raw;
+        raw.load(a, row, c, in);
+        raw.sum(a, h);
+      };
+      for (int chunk = t; chunk < chunks; chunk += tpr) {
+        const int c = chunk_col<VEC>(chunk);
+        float h[8];
+        load(c, c < a.dim, h);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum += h[i];
+      }
+      const float mean = row_sum(sum, tpr, red_mean, turn_mean) * inv_dim;
+      float2 sums = make_float2(0.0f, 0.0f);
+      for (int chunk = t; chunk < chunks; chunk += tpr) {
+        const int c = chunk_col<VEC>(chunk);
+        float h[8];
+        load(c, c < a.dim, h);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (c < a.dim && inside<VEC>(c, i, a.dim)) {
+            const float d = h[i] - mean;
+            sums.x += d;
+            sums.y = fmaf(d, d, sums.y);
+          }
+      }
+      statistics(row, mean, row_sums(sums, tpr, red_var, turn_var), off, rstd);
+      float f = 0.0f;
+      if (s8) {
+        float amax = 0.0f;
+        for (int chunk = t; chunk < chunks; chunk += tpr) {
+          const int c = chunk_col<VEC>(chunk);
+          float h[8], y[8];
+          load(c, c < a.dim, h);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) h[i] -= mean;
+          affine<VEC>(a.p.weight, a.p.bias, c, a.dim, c < a.dim, rstd, off, h, y);
+          amax = fmaxf(amax, chunk_amax(y));
+        }
+        amax = row_max(amax, tpr, red_max, turn_max);
+        f = s8_factor(amax);
+        if (t == 0) a.p.scales[row] = s8_scale(amax);
+      }
+      for (int base = 0; base < chunks; base += tpr) {  // whole warps: write_fp8 shuffles
+        const int chunk = base + t;
+        const int c = chunk_col<VEC>(chunk);
+        const bool in = chunk < chunks && c < a.dim;
+        float h[8], y[8];
+        load(c, in, h);
+        if (in && a.p.h != nullptr) store8<VEC>(a.p.h, a.p.h_type, row * a.p.ldh, c, a.dim, h);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] -= mean;
+        affine<VEC>(a.p.weight, a.p.bias, c, a.dim, in, rstd, off, h, y);
+        if (in && a.p.y != nullptr) store8<VEC>(a.p.y, a.p.y_type, row * a.p.ldy, c, a.dim, y);
+        if (f8) write_fp8<VEC>(a.p.q, a.p.ldq, a.p.scales, a.p.ld_scales, row, c, a.dim, in, y);
+        if (s8 && in) write_s8<VEC>(a.p.q, a.p.ldq, row, c, a.dim, f, y);
+      }
+    }
+  }
+  if (RING && threadIdx.x == 0 && ring.abort_flag) drain(ring, a.ring.stages, slot, parity);
+}
+
+// ---------------------------------------------------------------- backward
+struct LnGradArgs {
+  int64_t rows;
+  int dim;
+  int tpr;
+  RingArgs ring;
+  gemm_layernorm_grad_t p;
+  float* part;  // partial sums of dw and db: a row of 2 dim floats per CTA, or nullptr
+};
+
+// Threads' worth of CTAs that an SM holds of an instance: one chunk a thread in
+// bf16 fits 64 registers, the others 91 to 128.
+constexpr int ln_grad_threads(bool ring, int chunks, int td, int th) {
+  if (!ring || chunks != 1) return kMaxThreads;
+  return td == GEMM_OUT_BF16 && th == GEMM_OUT_BF16 ? 1024 : 640;
+}
+
+// As norm_grad_kernel, with the two sums of a row taken together.
+template <int C, bool VEC, int TD, int TH, bool RING = false>
+__global__ void __launch_bounds__(ln_grad_threads(RING, C, TD, TH), 1)
+    layernorm_grad_kernel(const __grid_constant__ LnGradArgs a) {
+  __shared__ float2 red[2][16];
+  __shared__ Ring ring;
+  extern __shared__ uint4 dyn_smem[];  // the ring, or several rows' sums
+  uint8_t* const stages = reinterpret_cast<uint8_t*>(dyn_smem);
+  const int ring_dim = RING ? a.dim : 0;
+  const int bytes_d = ring_dim * type_bytes(TD), bytes_h = ring_dim * type_bytes(TH);
+  const int bytes_r = a.p.residual_grad == nullptr ? 0 : ring_dim * type_bytes(a.p.residual_grad_type);
+  const int stage_bytes = bytes_d + bytes_h + bytes_r;
+  auto fetch = [&](int64_t row, int s) {
+    uint8_t* to = stages + s * stage_bytes;
+    uint64_t* bar = &ring.full[s];
+    mbar_arrive_expect_tx(bar, static_cast<uint32_t>(stage_bytes));
+    bulk_load(to, static_cast<const uint8_t*>(a.p.dy) + row * a.p.lddy * type_bytes(TD), bytes_d, bar);
+    bulk_load(to + bytes_d, static_cast<const uint8_t*>(a.p.h) + row * a.p.ldh * type_bytes(TH),
+              bytes_h, bar);
+    if (bytes_r > 0)
+      bulk_load(to + bytes_d + bytes_h,
+                static_cast<const uint8_t*>(a.p.residual_grad) +
+                    row * a.p.ldrg * type_bytes(a.p.residual_grad_type),
+                bytes_r, bar);
+  };
+  if (RING) ring_init(ring, a.ring.stages);
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (RING && threadIdx.x == 0)
+    for (int s = 0; s < a.ring.stages; ++s) {
+      const int64_t row = blockIdx.x + static_cast<int64_t>(s) * gridDim.x;
+      if (row < a.rows) fetch(row, s);
+    }
+  int slot = 0;
+  uint32_t parity = 0;
+  const int tpr = a.tpr;
+  const int t = threadIdx.x % tpr;
+  const int sub = threadIdx.x / tpr;
+  const int per_cta = blockDim.x / tpr;
+  const int chunks = VEC ? a.dim / 8 : (a.dim + kFp8Block - 1) / kFp8Block * 16;
+  const float inv_dim = 1.0f / static_cast<float>(a.dim);
+  constexpr int CR = C > 0 ? C : 1;
+  float dw[CR][8], db[CR][8];
+#pragma unroll
+  for (int k = 0; k < CR; ++k)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[k][i] = db[k][i] = 0.0f;
+  uint32_t turn = 0;
+  const int64_t row_step = static_cast<int64_t>(gridDim.x) * per_cta;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * per_cta + sub;
+  auto weight = [&](int c, float (&w)[8]) {
+    if (a.p.weight != nullptr) {
+      load_weight<VEC>(a.p.weight, c, a.dim, w);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = 1.0f;
+    }
+  };
+  float next_rstd = row < a.rows ? a.p.rstd[row] : 0.0f;  // loaded a row ahead
+  float next_mean = row < a.rows ? a.p.mean[row] : 0.0f;
+  for (; row < a.rows; row += row_step) {
+    const float rstd = next_rstd, mean = next_mean;
+    if (row + row_step < a.rows) {
+      next_rstd = a.p.rstd[row + row_step];
+      next_mean = a.p.mean[row + row_step];
+    }
+    float2 sums = make_float2(0.0f, 0.0f);
+    if constexpr (C > 0) {
+      Raw8<TD> dy[C];
+      Raw8<TH> rh[C];
+      const uint8_t* from = stages + slot * stage_bytes;
+      if (RING) mbar_wait_late(&ring.full[slot], parity, &ring.abort_flag, a.ring.err);
+      auto get = [&](int k, int c, bool in) {
+        if constexpr (RING) {
+          dy[k] = {};
+          rh[k] = {};
+          if (!in) return;
+          dy[k] = load8_smem<TD>(from, c);
+          rh[k] = load8_smem<TH>(from + bytes_d, c);
+        } else {
+          dy[k] = load8<VEC, TD>(a.p.dy, a.p.dy_type, row * a.p.lddy, c, a.dim, in);
+          rh[k] = load8<VEC, TH>(a.p.h, a.p.h_type, row * a.p.ldh, c, a.dim, in);
+        }
+      };
+      auto has = [&](int k) {
+        const int chunk = k * tpr + t;
+        return chunk < chunks && chunk_col<VEC>(chunk) < a.dim;
+      };
+      if (!RING) {
+#pragma unroll
+        for (int k = 0; k < C; ++k) get(k, chunk_col<VEC>(k * tpr + t), has(k));
+      }
+#pragma unroll
+      for (int k = 0; k < C; ++k) {
+        const int c = chunk_col<VEC>(k * tpr + t);
+        if (RING) get(k, c, has(k));
+        if (!has(k)) continue;
+        float w[8], g[8], xh[8];
+        weight(c, w);
+        widen8<VEC, TD>(dy[k], a.p.dy_type, g);  // zeros past the row's end
+        widen8<VEC, TH>(rh[k], a.p.h_type, xh);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          xh[i] = (xh[i] - mean) * rstd;
+          db[k][i] += g[i];
+          dw[k][i] = fmaf(g[i], xh[i], dw[k][i]);
+          g[i] *= w[i];
+          sums.x += inside<VEC>(c, i, a.dim) ? g[i] : 0.0f;
+          sums.y = inside<VEC>(c, i, a.dim) ? fmaf(g[i], xh[i], sums.y) : sums.y;
+        }
+      }
+      sums = row_sums(sums, tpr, red, turn);
+      const float mean_g = sums.x * inv_dim, mean_x = sums.y * inv_dim;
+      if (RING && threadIdx.x == 0 && row >= static_cast<int64_t>(gridDim.x)) {
+        // every thread has left the previous row (row_sums' barrier)
+        const int64_t next = row + static_cast<int64_t>(a.ring.stages - 1) * gridDim.x;
+        if (next < a.rows && !*const_cast<volatile int*>(&ring.abort_flag))
+          fetch(next, slot == 0 ? a.ring.stages - 1 : slot - 1);
+      }
+#pragma unroll
+      for (int k = 0; k < C; ++k) {
+        const int c = chunk_col<VEC>(k * tpr + t);
+        if (!has(k)) continue;
+        if (RING) get(k, c, true);
+        float w[8], g[8], xh[8], r[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+        if (a.p.residual_grad != nullptr) {
+          const int type = a.p.residual_grad_type;
+          if constexpr (RING) {
+            const uint8_t* rg = from + bytes_d + bytes_h;
+            if (type == GEMM_OUT_BF16)
+              widen8<true, GEMM_OUT_BF16>(load8_smem<GEMM_OUT_BF16>(rg, c), type, r);
+            else
+              widen8<true, GEMM_OUT_F32>(load8_smem<GEMM_OUT_F32>(rg, c), type, r);
+          } else {
+            widen8<VEC, kAnyType>(load8<VEC, kAnyType>(a.p.residual_grad, type, row * a.p.ldrg, c,
+                                                       a.dim, true), type, r);
+          }
+        }
+        weight(c, w);
+        widen8<VEC, TD>(dy[k], a.p.dy_type, g);
+        widen8<VEC, TH>(rh[k], a.p.h_type, xh);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          r[i] = fmaf(rstd, fmaf(g[i], w[i], -mean_g) - (xh[i] - mean) * rstd * mean_x, r[i]);
+        store8<VEC>(a.p.dh, a.p.dh_type, row * a.p.lddh, c, a.dim, r);
+      }
+      if (RING && ++slot == a.ring.stages) {
+        slot = 0;
+        parity ^= 1u;
+      }
+    } else {
+      float mean_g = 0.0f, mean_x = 0.0f;
+      for (int half = 0; half < 2; ++half) {
+        if (half == 1) {
+          sums = row_sums(sums, tpr, red, turn);
+          mean_g = sums.x * inv_dim;
+          mean_x = sums.y * inv_dim;
+        }
+        for (int chunk = t; chunk < chunks; chunk += tpr) {
+          const int c = chunk_col<VEC>(chunk);
+          if (c >= a.dim) continue;
+          float w[8], g[8], xh[8], r[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+          const Raw8<TD> dy = load8<VEC, TD>(a.p.dy, a.p.dy_type, row * a.p.lddy, c, a.dim, true);
+          const Raw8<TH> rh = load8<VEC, TH>(a.p.h, a.p.h_type, row * a.p.ldh, c, a.dim, true);
+          if (half == 1 && a.p.residual_grad != nullptr)
+            widen8<VEC, kAnyType>(load8<VEC, kAnyType>(a.p.residual_grad, a.p.residual_grad_type,
+                                                       row * a.p.ldrg, c, a.dim, true),
+                                  a.p.residual_grad_type, r);
+          weight(c, w);
+          widen8<VEC, TD>(dy, a.p.dy_type, g);
+          widen8<VEC, TH>(rh, a.p.h_type, xh);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            xh[i] = (xh[i] - mean) * rstd;
+            g[i] *= w[i];
+            if (half == 1) {
+              r[i] = fmaf(rstd, g[i] - mean_g - xh[i] * mean_x, r[i]);
+            } else if (inside<VEC>(c, i, a.dim)) {
+              sums.x += g[i];
+              sums.y = fmaf(g[i], xh[i], sums.y);
+            }
+          }
+          if (half == 1) store8<VEC>(a.p.dh, a.p.dh_type, row * a.p.lddh, c, a.dim, r);
+        }
+      }
+    }
+  }
+  if (RING && threadIdx.x == 0 && ring.abort_flag) drain(ring, a.ring.stages, slot, parity);
+  if (C == 0 || a.part == nullptr) return;
+  // dw in the first dim columns of the CTA's row of `part`, db in the others
+  float* out = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.dim;
+  float* sums = reinterpret_cast<float*>(dyn_smem);
+#pragma unroll
+  for (int k = 0; k < CR; ++k) {
+    const int chunk = k * tpr + t;
+    const int c = chunk_col<VEC>(chunk);
+    if (chunk >= chunks || c >= a.dim) continue;
+    float* to = per_cta == 1 ? out : sums + static_cast<int64_t>(sub) * 2 * a.dim;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int col = VEC ? c + i : c + 16 * i;
+      if (col < a.dim) {
+        to[col] = dw[k][i];
+        to[a.dim + col] = db[k][i];
+      }
+    }
+  }
+  if (per_cta == 1) return;
+  __syncthreads();
+  for (int col = threadIdx.x; col < 2 * a.dim; col += blockDim.x) {
+    float s = 0.0f;
+    for (int r = 0; r < per_cta; ++r) s += sums[r * 2 * a.dim + col];
+    out[col] = s;
+  }
+}
+
+// dw and db of rows too long for layernorm_grad_kernel's registers: one column
+// per thread, the rows cut into gridDim.y parts, one row of `part` each.
+__global__ void __launch_bounds__(256) layernorm_dweight_kernel(const __grid_constant__ LnGradArgs a) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int64_t col = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (col >= a.dim) return;
+  float w = 0.0f, b = 0.0f;
+#pragma unroll 4
+  for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
+    const float dy = load1(a.p.dy, a.p.dy_type, row * a.p.lddy + col);
+    b += dy;
+    w = fmaf(dy, (load1(a.p.h, a.p.h_type, row * a.p.ldh + col) - a.p.mean[row]) * a.p.rstd[row], w);
+  }
+  float* out = a.part + blockIdx.y * 2 * static_cast<int64_t>(a.dim) + col;
+  out[0] = w;
+  out[a.dim] = b;
+}
+
+// Rows moved in vectors have an instance for each pair of input types; the
+// others look at the types as they go.
+template <bool VEC, int TX, int TR>
+cudaError_t launch_ln(const LnArgs& a, const RowPlan& p, int grid, cudaStream_t s) {
+  const dim3 g(static_cast<unsigned>(grid));
+  const int threads = p.tpr * p.per_cta;
+  if constexpr (VEC) {
+    if (a.ring.stages > 0) {  // more than one warp a row: two chunks a thread (plan_rows)
+      const size_t smem = static_cast<size_t>(a.ring.stages) * a.dim *
+                          (type_bytes(TX) + (TR < 0 ? 0 : type_bytes(TR)));
+      return ops_launch<layernorm_kernel<2, VEC, TX, TR, true>>(g, threads, smem, 1, s, a);
+    }
+  }
+  switch (p.chunks_per_thread) {
+    case 1: return ops_launch<layernorm_kernel<1, VEC, TX, TR>>(g, threads, 0, 1, s, a);
+    case 2: return ops_launch<layernorm_kernel<2, VEC, TX, TR>>(g, threads, 0, 1, s, a);
+    case 4: return ops_launch<layernorm_kernel<4, VEC, TX, TR>>(g, threads, 0, 1, s, a);
+    default: return ops_launch<layernorm_kernel<0, VEC, TX, TR>>(g, threads, 0, 1, s, a);
+  }
+}
+
+template <int TX>
+cudaError_t launch_ln_vec(const LnArgs& a, const RowPlan& p, int grid, cudaStream_t s) {
+  if (a.p.residual == nullptr) return launch_ln<true, TX, -1>(a, p, grid, s);
+  return a.p.residual_type == GEMM_OUT_BF16 ? launch_ln<true, TX, GEMM_OUT_BF16>(a, p, grid, s)
+                                            : launch_ln<true, TX, GEMM_OUT_F32>(a, p, grid, s);
+}
+
+cudaError_t launch_ln_any(const LnArgs& a, const RowPlan& p, bool vec, int grid, cudaStream_t s) {
+  if (vec)
+    return a.p.x_type == GEMM_OUT_BF16 ? launch_ln_vec<GEMM_OUT_BF16>(a, p, grid, s)
+                                       : launch_ln_vec<GEMM_OUT_F32>(a, p, grid, s);
+  return a.p.residual == nullptr ? launch_ln<false, kAnyType, -1>(a, p, grid, s)
+                                 : launch_ln<false, kAnyType, kAnyType>(a, p, grid, s);
+}
+
+template <bool VEC, int TD, int TH>
+cudaError_t launch_ln_grad(const LnGradArgs& a, const RowPlan& p, int grid, cudaStream_t s) {
+  const dim3 g(static_cast<unsigned>(grid));
+  const int threads = p.tpr * p.per_cta;
+  const size_t smem = p.per_cta > 1 ? sizeof(float) * 2 * p.per_cta * a.dim : 0;
+  if constexpr (VEC) {
+    if (a.ring.stages > 0) {
+      const int rg = a.p.residual_grad == nullptr ? 0 : type_bytes(a.p.residual_grad_type);
+      const size_t bytes = static_cast<size_t>(a.ring.stages) * a.dim * (type_bytes(TD) + type_bytes(TH) + rg);
+      if (p.chunks_per_thread == 1)
+        return ops_launch<layernorm_grad_kernel<1, VEC, TD, TH, true>>(g, threads, bytes, 1, s, a);
+      return ops_launch<layernorm_grad_kernel<2, VEC, TD, TH, true>>(g, threads, bytes, 1, s, a);
+    }
+  }
+  switch (p.chunks_per_thread) {
+    case 1: return ops_launch<layernorm_grad_kernel<1, VEC, TD, TH>>(g, threads, smem, 1, s, a);
+    case 2: return ops_launch<layernorm_grad_kernel<2, VEC, TD, TH>>(g, threads, smem, 1, s, a);
+    default: return ops_launch<layernorm_grad_kernel<0, VEC, TD, TH>>(g, threads, 0, 1, s, a);
+  }
+}
+
+cudaError_t launch_ln_grad_any(const LnGradArgs& a, const RowPlan& p, bool vec, int grid, cudaStream_t s) {
+  constexpr int B = GEMM_OUT_BF16, F = GEMM_OUT_F32;
+  if (!vec) return launch_ln_grad<false, kAnyType, kAnyType>(a, p, grid, s);
+  if (a.p.dy_type == B)
+    return a.p.h_type == B ? launch_ln_grad<true, B, B>(a, p, grid, s) : launch_ln_grad<true, B, F>(a, p, grid, s);
+  return a.p.h_type == B ? launch_ln_grad<true, F, B>(a, p, grid, s) : launch_ln_grad<true, F, F>(a, p, grid, s);
+}
+
+}  // namespace
+}  // namespace g12
+
+using namespace g12;
+
+extern "C" {
+
+gemm_status_t gemm_layernorm(int64_t rows, int64_t dim, const gemm_layernorm_t* args, void* stream) {
+  if (args == nullptr || rows < 0 || dim < 0 || rows > kOpsMaxDim || dim > (int64_t{1} << 30))
+    return GEMM_ERR_INVALID_VALUE;
+  if (rows == 0 || dim == 0) return GEMM_OK;
+  const gemm_layernorm_t& p = *args;
+  bool vec = dim % 8 == 0;
+  if (!array_ok(p.x, p.x_type, p.ldx, dim, true, vec) ||
+      !array_ok(p.residual, p.residual_type, p.ldr, dim, false, vec) ||
+      !array_ok(p.h, p.h_type, p.ldh, dim, false, vec) ||
+      !array_ok(p.y, p.y_type, p.ldy, dim, false, vec) ||
+      !array_ok(p.weight, GEMM_OUT_F32, dim, dim, false, vec) ||
+      !array_ok(p.bias, GEMM_OUT_F32, dim, dim, false, vec))
+    return GEMM_ERR_INVALID_VALUE;
+  if ((p.q == nullptr) != (p.scales == nullptr)) return GEMM_ERR_INVALID_VALUE;
+  if (p.q != nullptr) {
+    if ((p.q_type != GEMM_OUT_F8E4M3 && p.q_type != GEMM_OUT_S8) || p.ldq < dim || p.ldq > kOpsMaxDim ||
+        ops_misaligned(p.scales, 4) ||
+        (p.q_type == GEMM_OUT_F8E4M3 && (p.ld_scales < rows || p.ld_scales > kOpsMaxDim)))
+      return GEMM_ERR_INVALID_VALUE;
+    if (ops_misaligned(p.q, 8) || p.ldq % 8 != 0) vec = false;
+  }
+  if ((p.mean != nullptr && ops_misaligned(p.mean, 4)) || (p.rstd != nullptr && ops_misaligned(p.rstd, 4)))
+    return GEMM_ERR_INVALID_VALUE;
+  if (p.h == nullptr && p.y == nullptr && p.q == nullptr && p.mean == nullptr && p.rstd == nullptr)
+    return GEMM_OK;
+  int sms = 0;
+  uint32_t* err = nullptr;
+  const gemm_status_t st = abi_device(&sms, &err);
+  if (st != GEMM_OK) return st;
+  LnArgs a{};
+  a.rows = rows;
+  a.dim = static_cast<int>(dim);
+  a.p = p;
+  const int64_t chunks = vec ? dim / 8 : (dim + kFp8Block - 1) / kFp8Block * 16;
+  RowPlan pl = plan_rows(rows, chunks, sms, 4, 4);
+  a.tpr = pl.tpr;
+  a.ring.err = err;
+  int grid = row_grid(rows, pl, sms, 1024);
+  if (vec) {
+    const int64_t bytes = dim * (type_bytes(p.x_type) +
+                                 (p.residual == nullptr ? 0 : type_bytes(p.residual_type)));
+    const RowPlan pr = plan_rows(rows, chunks, sms, 2, 2);
+    const int ring_grid = plan_ring(pr, rows, bytes, sms, 1024, a.ring);
+    if (ring_grid > 0) {
+      grid = ring_grid;
+      pl = pr;
+      a.tpr = pl.tpr;
+    }
+  }
+  return abi_from_cuda(launch_ln_any(a, pl, vec, grid, static_cast<cudaStream_t>(stream)));
+}
+
+gemm_status_t gemm_layernorm_backward(int64_t rows, int64_t dim, const gemm_layernorm_grad_t* args,
+                                      void* stream) {
+  if (args == nullptr || rows < 0 || dim < 0 || rows > kOpsMaxDim || dim > (int64_t{1} << 30))
+    return GEMM_ERR_INVALID_VALUE;
+  if (dim == 0) return GEMM_OK;
+  const gemm_layernorm_grad_t& p = *args;
+  bool vec = dim % 8 == 0;
+  const bool some = rows > 0;
+  if (!array_ok(p.dy, p.dy_type, p.lddy, dim, some, vec) ||
+      !array_ok(p.h, p.h_type, p.ldh, dim, some, vec) ||
+      !array_ok(p.residual_grad, p.residual_grad_type, p.ldrg, dim, false, vec) ||
+      !array_ok(p.dh, p.dh_type, p.lddh, dim, some, vec) ||
+      !array_ok(p.weight, GEMM_OUT_F32, dim, dim, false, vec))
+    return GEMM_ERR_INVALID_VALUE;
+  if (some && (p.rstd == nullptr || ops_misaligned(p.rstd, 4) || p.mean == nullptr ||
+               ops_misaligned(p.mean, 4)))
+    return GEMM_ERR_INVALID_VALUE;
+  if ((p.dweight != nullptr && ops_misaligned(p.dweight, 4)) ||
+      (p.dbias != nullptr && ops_misaligned(p.dbias, 4)))
+    return GEMM_ERR_INVALID_VALUE;
+  const bool params = p.dweight != nullptr || p.dbias != nullptr;
+  if (!some && !params) return GEMM_OK;
+  int sms = 0;
+  uint32_t* err = nullptr;
+  gemm_status_t st = abi_device(&sms, &err);
+  if (st != GEMM_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (!some) {
+    cudaError_t e = cudaSuccess;
+    for (float* d : {p.dweight, p.dbias})
+      if (d != nullptr && e == cudaSuccess) e = cudaMemsetAsync(d, 0, sizeof(float) * dim, s);
+    return abi_from_cuda(e);
+  }
+  LnGradArgs a{};
+  a.rows = rows;
+  a.dim = static_cast<int>(dim);
+  a.p = p;
+  const int64_t chunks = vec ? dim / 8 : (dim + kFp8Block - 1) / kFp8Block * 16;
+  const bool two = vec && (chunks <= 64 || chunks > kMaxThreads);
+  const RowPlan pl = plan_rows(rows, chunks, sms, two ? 2 : 1, 2);
+  a.tpr = pl.tpr;
+  a.ring.err = err;
+  int grid = row_grid(rows, pl, sms, 512);
+  if (vec && pl.chunks_per_thread > 0) {
+    const int64_t bytes =
+        dim * (type_bytes(p.dy_type) + type_bytes(p.h_type) +
+               (p.residual_grad == nullptr ? 0 : type_bytes(p.residual_grad_type)));
+    const int fit = ln_grad_threads(true, pl.chunks_per_thread, p.dy_type, p.h_type);
+    const int ring_grid = plan_ring(pl, rows, bytes, sms, fit, a.ring);
+    if (ring_grid > 0) grid = ring_grid;
+  }
+  const bool by_column = pl.chunks_per_thread == 0;
+  int parts = grid;
+  if (by_column) {  // up to 64, of 256 MB together
+    parts = static_cast<int>(rows < 64 ? rows : 64);
+    while (parts > 1 && 2 * parts * dim > (int64_t{1} << 26)) parts /= 2;
+  }
+  std::unique_lock<std::mutex> lock;
+  if (params) {
+    st = abi_scratch(s, static_cast<int64_t>(parts) * 2 * dim, lock, &a.part);
+    if (st != GEMM_OK) return st;
+  }
+  cudaError_t e = cudaSuccess;
+  if (by_column && params) {  // first: dh may take the place of dy or h
+    const dim3 g(static_cast<unsigned>((dim + 255) / 256), static_cast<unsigned>(parts));
+    e = ops_launch<layernorm_dweight_kernel>(g, 256, 0, 1, s, a);
+  }
+  if (e == cudaSuccess) e = launch_ln_grad_any(a, pl, vec, grid, s);
+  if (e != cudaSuccess || !params) return abi_from_cuda(e);
+  const dim3 g(static_cast<unsigned>((dim + 31) / 32), 2);
+  const float* part = a.part;
+  return abi_from_cuda(ops_launch<add_parts_kernel>(g, 1024, 0, 1, s, part, parts, a.dim, 2 * dim,
+                                                    p.dweight, p.dbias));
+}
+
+}  // extern "C"

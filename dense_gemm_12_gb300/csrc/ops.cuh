@@ -145,6 +145,24 @@ __device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d
   return lo | (hi << 16);
 }
 
+// ------------------------------------------------------ int8 row scales
+constexpr float kS8Max = 127.0f;  // -128 is not used: the values are symmetric
+
+// Scale of a row whose largest finite magnitude is amax, and the factor that
+// its values are multiplied by before rounding (as for fp8).
+__device__ __forceinline__ float s8_scale(float amax) {
+  return fmaxf(__fdiv_rn(amax, kS8Max), kFp8ScaleMin);
+}
+__device__ __forceinline__ float s8_factor(float amax) {
+  return fminf(__fdiv_rn(kS8Max, amax), 1.0f / kFp8ScaleMin);
+}
+// Nearest whole number (ties to even) within +-127; NaN becomes 0.
+__device__ __forceinline__ int round_s8(float v) { return max(min(__float2int_rn(v), 127), -127); }
+__device__ __forceinline__ uint32_t pack_s8(float a, float b, float c, float d) {
+  return static_cast<uint32_t>(round_s8(a) & 0xff) | static_cast<uint32_t>(round_s8(b) & 0xff) << 8 |
+         static_cast<uint32_t>(round_s8(c) & 0xff) << 16 | static_cast<uint32_t>(round_s8(d)) << 24;
+}
+
 // ------------------------------------------------ eight elements of a row
 // A thread moves eight elements of a row at a time.  Vector form: they are
 // consecutive, 16-byte aligned.  Strided form (rows that cannot be moved in

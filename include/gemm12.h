@@ -543,9 +543,9 @@ gemm_status_t gemm_quantization(int64_t M, int64_t N, int64_t BM, int64_t BN,
  *  Sizes      Below 2^31, as at the top; what a product cuts into tiles (M or
  *             rows, N, and K of the bf16 products) at most 2^31 - 256, and
  *             the norm's dim at most 2^30.  More is GEMM_ERR_INVALID_VALUE.
- *  Memory     gemm_rmsnorm_backward keeps partial sums of the weight's
- *             gradient in the stream's scratch, gemm_expert_sort counters;
- *             operands of the products
+ *  Memory     gemm_rmsnorm_backward and gemm_layernorm_backward keep partial
+ *             sums of the parameters' gradients in the stream's scratch,
+ *             gemm_expert_sort counters; operands of the products
  *             that TMA cannot describe (base not 16-byte aligned, or a matrix
  *             stride, or the row pitch of more than one row, that is not a
  *             multiple of 16 bytes) are
@@ -637,6 +637,84 @@ typedef struct {
 
 gemm_status_t gemm_rmsnorm_backward(int64_t rows, int64_t dim, const gemm_rmsnorm_grad_t *args,
                                     void *stream);
+
+/*
+ * gemm_layernorm -- for each of `rows` rows of `dim` values (dim <= 2^30):
+ *
+ *     h = x + residual          (h = x without a residual)
+ *     mean = mean(h)            rstd = 1 / sqrt(mean((h - mean)^2) + eps)
+ *     y = (h - mean) * rstd * weight + bias
+ *
+ * in fp32, the squares about the mean, each output rounded once from there.
+ * weight NULL: 1; bias NULL: 0.  Every output is optional: h, y, mean and rstd
+ * (for the backward pass), and q with scales: y in 8 bits from its unrounded
+ * values, of q_type GEMM_OUT_F8E4M3 (GEMM_BLOCK_ROWS scales, as gemm_rmsnorm)
+ * or GEMM_OUT_S8 (one scale per row, as gemm_int8_quantize; ld_scales is not
+ * used).  Types, overlap and errors as gemm_rmsnorm; a q_type of neither kind
+ * is GEMM_ERR_INVALID_VALUE.  A row with a NaN or an infinity, or whose sum or
+ * sum of squares exceeds the fp32 range, has no finite statistics.
+ */
+typedef struct {
+    const void *x;          /* rows x dim                                        */
+    int64_t ldx;
+    int x_type;
+    const void *residual;   /* rows x dim, or NULL                               */
+    int64_t ldr;
+    int residual_type;
+    void *h;                /* rows x dim, or NULL                               */
+    int64_t ldh;
+    int h_type;
+    const float *weight;    /* dim, or NULL                                      */
+    const float *bias;      /* dim, or NULL                                      */
+    float eps;
+    void *y;                /* rows x dim, or NULL                               */
+    int64_t ldy;
+    int y_type;
+    void *q;                /* rows x dim fp8 or int8, or NULL                   */
+    int64_t ldq;
+    int q_type;
+    float *scales;          /* ceil(dim / 128) x rows (fp8) or rows (int8)       */
+    int64_t ld_scales;
+    float *mean;            /* rows, or NULL                                     */
+    float *rstd;            /* rows, or NULL                                     */
+} gemm_layernorm_t;
+
+gemm_status_t gemm_layernorm(int64_t rows, int64_t dim, const gemm_layernorm_t *args, void *stream);
+
+/*
+ * gemm_layernorm_backward -- the gradients of gemm_layernorm's y with respect
+ * to h (and so to x and to the residual), the weight and the bias, in fp32:
+ *
+ *     g = dy * weight       xh = (h - mean) * rstd
+ *     dh = rstd * (g - mean(g) - xh * mean(g * xh)) + residual_grad
+ *     dweight = sum over rows of dy * xh        dbias = sum over rows of dy
+ *
+ * h, mean and rstd are the forward pass's.  dweight and dbias (dim fp32 values
+ * each, overwritten; zeros for rows == 0) may be NULL; the rest as
+ * gemm_rmsnorm_backward.
+ */
+typedef struct {
+    const void *dy;             /* rows x dim                                    */
+    int64_t lddy;
+    int dy_type;
+    const void *h;              /* rows x dim                                    */
+    int64_t ldh;
+    int h_type;
+    const float *weight;        /* dim, or NULL                                  */
+    const float *mean;          /* rows                                          */
+    const float *rstd;          /* rows                                          */
+    const void *residual_grad;  /* rows x dim, or NULL                           */
+    int64_t ldrg;
+    int residual_grad_type;
+    void *dh;                   /* rows x dim                                    */
+    int64_t lddh;
+    int dh_type;
+    float *dweight;             /* dim, or NULL                                  */
+    float *dbias;               /* dim, or NULL                                  */
+} gemm_layernorm_grad_t;
+
+gemm_status_t gemm_layernorm_backward(int64_t rows, int64_t dim, const gemm_layernorm_grad_t *args,
+                                      void *stream);
 
 /*
  * gemm_fp8_quantize -- the rows x cols matrix x, or its transpose, in fp8 with
