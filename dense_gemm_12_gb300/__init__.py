@@ -35,7 +35,7 @@ __all__ = [
     "gemm_expert_combine", "gemm_expert_combine_backward", "expert_route", "expert_route_backward",
     "expert_sort", "expert_dispatch", "expert_combine", "expert_combine_backward",
     "LayernormArgs", "LayernormGradArgs", "gemm_layernorm", "gemm_layernorm_backward", "layernorm",
-    "layernorm_backward",
+    "layernorm_backward", "gemm_int8_quantize", "gemm_int8gemm", "int8_quantize", "int8gemm",
 ]
 
 STATUS = {
@@ -226,6 +226,11 @@ def load_library(build_if_missing: bool = False):
         lib.gemm_layernorm.restype = cint
         lib.gemm_layernorm_backward.argtypes = [i64, i64, ctypes.POINTER(LayernormGradArgs), vp]
         lib.gemm_layernorm_backward.restype = cint
+        lib.gemm_int8_quantize.argtypes = [i64, i64, vp, i64, cint, cint, vp, i64, vp, vp]
+        lib.gemm_int8_quantize.restype = cint
+        lib.gemm_int8gemm.argtypes = [i64, i64, i64, f32, vp, i64, vp, vp, i64, vp, vp, f32, vp, i64, cint,
+                                      vp]
+        lib.gemm_int8gemm.restype = cint
         lib.gemm_expert_route.argtypes = [i64, i64, i64, vp, i64, cint, cint, vp, vp, vp]
         lib.gemm_expert_route.restype = cint
         lib.gemm_expert_route_backward.argtypes = [i64, i64, i64, vp, i64, cint, cint, vp, vp, vp, i64,
@@ -420,6 +425,18 @@ def gemm_fp8gemm(M, N, K, alpha, A, lda, a_scales, ld_as, B, ldb, b_scales, ld_b
     """fp8 GEMM with block scales, B given as N x K. Returns the status."""
     return load_library().gemm_fp8gemm(M, N, K, alpha, A, lda, a_scales, ld_as, B, ldb, b_scales,
                                        ld_bs, b_block, beta, D, ldd, d_type, stream)
+
+
+def gemm_int8_quantize(rows, cols, x, ldx, x_type, transpose, q, ldq, scales, stream=0) -> int:
+    """A matrix or its transpose in int8 with row scales. Returns the status."""
+    return load_library().gemm_int8_quantize(rows, cols, x, ldx, x_type, transpose, q, ldq, scales, stream)
+
+
+def gemm_int8gemm(M, N, K, alpha, A, lda, a_scales, B, ldb, b_scales, bias, beta, D, ldd, d_type,
+                  stream=0) -> int:
+    """int8 GEMM with row scales, B given as N x K. Returns the status."""
+    return load_library().gemm_int8gemm(M, N, K, alpha, A, lda, a_scales, B, ldb, b_scales, bias, beta, D,
+                                        ldd, d_type, stream)
 
 
 def gemm_fp8gemm_grouped(G, offsets, rows, N, K, alpha, A, lda, a_scales, ld_as, B, ldb, stride_b,
@@ -883,6 +900,49 @@ def fp8gemm_grouped(A, a_scales, B, b_scales, offsets, D, alpha=1.0, beta=0.0, s
         ldd, code, handle)
     if st != 0:
         raise GemmError(st, "gemm_fp8gemm_grouped")
+    return D
+
+
+def int8_quantize(x, q, scales, transpose=False, stream=None):
+    """x (rows, cols), float32 or bfloat16, or its transpose, into q (int8) with one float32 scale for
+    each of q's rows."""
+    f32 = _torch_once()[2]
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D")
+    rows, cols = x.shape
+    dev = x.get_device()
+    handle = _stream_of(dev, stream)
+    shape = (cols, rows) if transpose else (rows, cols)
+    px, ldx, x_type = _float_array(x, x.shape, dev, "x")
+    pq, ldq = _array(q, shape, _int8(), dev, "q")
+    st = load_library().gemm_int8_quantize(rows, cols, px, ldx, x_type, 1 if transpose else 0, pq, ldq,
+                                           _vector(scales, shape[0], f32, dev, "scales"), handle)
+    if st != 0:
+        raise GemmError(st, "gemm_int8_quantize")
+    return q
+
+
+def int8gemm(A, a_scales, B, b_scales, D, alpha=1.0, beta=0.0, bias=None, stream=None):
+    """D <- alpha*(a_scales * A) @ (b_scales * B)^T + bias + beta*D in place: A (M, K) and B (N, K) int8
+    with a_scales (M,) and b_scales (N,), bias (N,) or None, D float32 or bfloat16.  The sums of
+    products are exact."""
+    f32 = _torch_once()[2]
+    if A.dim() != 2 or B.dim() != 2:
+        raise ValueError("A and B must be 2-D")
+    M, K = A.shape
+    N = B.shape[0]
+    dev = D.get_device()
+    handle = _stream_of(dev, stream)
+    s8 = _int8()
+    pa, lda = _array(A, (M, K), s8, dev, "A")
+    pb, ldb = _array(B, (N, K), s8, dev, "B")
+    pd, ldd, code = _float_array(D, (M, N), dev, "D")
+    st = load_library().gemm_int8gemm(
+        M, N, K, alpha, pa, lda, _vector(a_scales, M, f32, dev, "a_scales"), pb, ldb,
+        _vector(b_scales, N, f32, dev, "b_scales"),
+        None if bias is None else _vector(bias, N, f32, dev, "bias"), beta, pd, ldd, code, handle)
+    if st != 0:
+        raise GemmError(st, "gemm_int8gemm")
     return D
 
 

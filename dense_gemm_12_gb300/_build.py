@@ -20,7 +20,8 @@ LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["api.cu", "sgemm_simt.cu", "bf16_tc.cu", "bf16_decode.cu", "decode_noalloc.cu",
-           "norm.cu", "layernorm.cu", "fp8_quantize.cu", "fp8_tc.cu", "grouped_tc.cu", "experts.cu"]
+           "norm.cu", "layernorm.cu", "fp8_quantize.cu", "fp8_tc.cu", "grouped_tc.cu", "experts.cu",
+           "int8_quantize.cu", "int8_tc.cu", "bytes.cu"]
 HEADERS = ["ptx.cuh", "internal.h", "epilogue.cuh", "dispatch_table.inc", "ops.cuh", "groups.cuh", "norm.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -648,58 +648,6 @@ int choose_split(int64_t tiles, int num_kb, int num_sms, bool by_rows) {
   return best;
 }
 
-struct Operand {
-  const void* p;
-  int64_t rows, cols, ld;   // of each matrix
-  int64_t count, stride;    // matrices
-};
-
-// Row pitch in a tensor map.  A single row has none of its own: any will do.
-int64_t map_pitch(const Operand& o) { return o.rows == 1 ? (o.cols + 15) / 16 * 16 : o.ld; }
-
-bool tma_describes(const Operand& o) {
-  return !ops_misaligned(o.p, 16) && map_pitch(o) % 16 == 0 &&
-         (o.count == 1 || o.stride % 16 == 0);
-}
-
-// Bytes of the copies that TMA can describe (rows padded to 16 bytes).
-__global__ void stage_bytes_kernel(const uint8_t* src, int64_t ld, int64_t stride, uint8_t* dst,
-                                   int64_t ld2, int64_t rows, int64_t cols, int64_t count) {
-  grid_dependency_wait();
-  const int64_t pieces = ld2 / 16;
-  const int64_t total = count * rows * pieces;
-  for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int64_t line = i / pieces, c = (i - line * pieces) * 16;
-    const int64_t m = line / rows, r = line - m * rows;
-    const uint8_t* s = src + m * stride + r * ld + c;
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-      if (c + j < cols) w[j >> 2] |= static_cast<uint32_t>(s[j]) << (8 * (j & 3));
-    *reinterpret_cast<uint4*>(dst + line * ld2 + c) = make_uint4(w[0], w[1], w[2], w[3]);
-  }
-}
-
-cudaError_t stage(Operand& o, uint8_t* dst, int num_sms, cudaStream_t s) {
-  const int64_t ld2 = (o.cols + 15) / 16 * 16;
-  const int64_t total = o.count * o.rows * (ld2 / 16);
-  const int64_t want = (total + 255) / 256, fit = static_cast<int64_t>(num_sms) * 8;
-  const uint8_t* src = static_cast<const uint8_t*>(o.p);
-  const int64_t ld = o.ld, stride = o.stride, rows = o.rows, cols = o.cols, count = o.count;
-  const cudaError_t e = ops_launch<stage_bytes_kernel>(
-      dim3(static_cast<unsigned>(want < fit ? want : fit)), 256, 0, 1, s, src, ld, stride, dst, ld2,
-      rows, cols, count);
-  o.p = dst;
-  o.ld = ld2;
-  o.stride = o.rows * ld2;
-  return e;
-}
-
-int64_t staged_bytes(const Operand& o) {
-  return (o.count * o.rows * ((o.cols + 15) / 16 * 16) + 255) / 256 * 256;
-}
-
 template <bool CLUSTER>
 gemm_status_t launch(bool by_rows, int64_t ctas, int cluster, const Fp8Args& a,
                      const CUtensorMap& tmA, const CUtensorMap& tmB, cudaStream_t s) {
@@ -766,22 +714,22 @@ gemm_status_t run(int64_t G, const int32_t* offsets, int64_t M, int64_t N, int64
   std::unique_lock<std::mutex> lock;
   CUtensorMap tmA{}, tmB{};
   if (product) {
-    Operand oa{A, M, K, lda, 1, 0}, ob{B, N, K, ldb, G, stride_b};
-    const int64_t need_a = tma_describes(oa) ? 0 : staged_bytes(oa);
-    const int64_t need_b = tma_describes(ob) ? 0 : staged_bytes(ob);
+    ByteOperand oa{A, M, K, lda, 1, 0}, ob{B, N, K, ldb, G, stride_b};
+    const int64_t need_a = byte_tma_ok(oa) ? 0 : byte_staged(oa);
+    const int64_t need_b = byte_tma_ok(ob) ? 0 : byte_staged(ob);
     if (need_a + need_b > 0) {
       uint8_t* buf = nullptr;
       st = abi_stage(s, need_a + need_b, lock, &buf);
       if (st != GEMM_OK) return st;
-      cudaError_t e = need_a > 0 ? stage(oa, buf, sms, s) : cudaSuccess;
-      if (e == cudaSuccess && need_b > 0) e = stage(ob, buf + need_a, sms, s);
+      cudaError_t e = need_a > 0 ? byte_stage(oa, buf, sms, s) : cudaSuccess;
+      if (e == cudaSuccess && need_b > 0) e = byte_stage(ob, buf + need_a, sms, s);
       if (e != cudaSuccess) return abi_from_cuda(e);
     }
-    const int64_t da[2] = {K, M}, ta[1] = {map_pitch(oa)};
+    const int64_t da[2] = {K, M}, ta[1] = {byte_pitch(oa)};
     const uint32_t ba[2] = {BK, static_cast<uint32_t>(a.tile_rows)};
     // one matrix: any stride describes it
-    const int64_t db[3] = {K, N, G}, tb[2] = {map_pitch(ob),
-                                              G > 1 ? ob.stride : map_pitch(ob) * N};
+    const int64_t db[3] = {K, N, G}, tb[2] = {byte_pitch(ob),
+                                              G > 1 ? ob.stride : byte_pitch(ob) * N};
     const uint32_t bb[3] = {BK, BN, 1};
     if (!abi_encode_tiled(&tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, oa.p, da, ta, ba) ||
         !abi_encode_tiled(&tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, ob.p, db, tb, bb))

@@ -1,0 +1,590 @@
+// int8_tc.cu -- products of two int8 matrices with a scale for each row of both
+// (each token and each output channel), on the 5th-generation tensor cores:
+//
+//     D[i][j] = alpha sa[i] sb[j] sum_k A[i][k] B[j][k] + bias[j] + beta D[i][j]
+//
+// A is M x K and B is N x K, both contiguous along k.  The sum is exact.
+//
+// This GPU's tensor cores have no 8-bit integer kind (tcgen05.mma kind::i8 does
+// not exist for sm_103a), so the values are widened to fp16 on their way:
+// whole numbers up to 2048 are fp16 values, products of two int8 at most 2^14,
+// and 1024 of them add up to at most 2^24, below which fp32 holds every whole
+// number.  So an accumulator is exact over 1024 of k, and its sums are carried
+// on as 32-bit integers.
+//
+// The operands are swapped, D^T = B A^T: the MMA's rows are B's (the weights,
+// from TMEM) and its columns A's (the tokens, from shared memory).  A tile is
+// 256 weights by 16 to 128 tokens, so a decoding step's few tokens cost no
+// rows of an MMA, and a finished value of one token lies in one register of
+// every thread, 32 neighbouring channels to a warp: rows of D leave without
+// being turned around.
+//   * warp 0       TMA producer: 256 x 128 of B and up to 128 x 128 of A per
+//                  k-block, as int8, into a ring
+//   * warp 1       TMEM and MMAs (M = 128, K = 16): two halves of the weights
+//   * warps 4..11  widening, 128 values of k at a time: a thread takes one
+//                  weight row into its TMEM lane (tcgen05.st: shared memory,
+//                  which is what such a kernel runs out of, is not written or
+//                  read again for it) and its share of the tokens into shared
+//                  memory; two buffers of each.  Then, every 8 k-blocks, the
+//                  accumulator's 32 x (tokens) values per warp to integer sums
+//                  in registers, and at a tile's end to D.
+// Registers move from the first warpgroup to the other two for the sums.
+//
+// Few tiles: the CTAs of a cluster split a tile's k-blocks and add their sums
+// through distributed shared memory.
+#include <cstddef>
+
+#include "ops.cuh"
+
+namespace g12 {
+namespace {
+
+constexpr int WN = 256;        // weights per tile, two halves of 128
+constexpr int BK = 128;        // of k per block
+constexpr int kMaxTokens = 128;
+constexpr int kChunk = 8;      // k-blocks that an accumulator sums exactly
+constexpr int kMaxStages = 5;
+constexpr int kRawW = WN * BK;  // a stage's bytes of weights
+constexpr int kPool = 208 * 1024;  // the ring and the widened tokens
+constexpr int kThreads = 384;
+constexpr int kWorkThreads = 256;
+constexpr int kWorkWarps = kWorkThreads / 32;
+constexpr uint32_t kTmemCols = 512;
+// TMEM columns: sums of the two halves, then two buffers of widened weights
+constexpr uint32_t kSumCols = 128, kWideAt = 256, kWideCols = 128, kWideHalf = 64;
+// Registers of the warpgroups, few + 2 x many = 3 x 168: what compiles without
+// spills.
+constexpr int few_regs(int tm, bool cluster) { return tm < kMaxTokens ? 88 : (cluster ? 72 : 104); }
+constexpr int many_regs(int tm, bool cluster) { return (3 * 168 - few_regs(tm, cluster)) / 2; }
+// k-blocks of B that a CTA of a split tile asks L2 for early.
+constexpr int kEarlyBlocks = 4;
+
+constexpr int stage_bytes(int tm) { return kRawW + tm * BK; }
+constexpr int wide_bytes(int tm) { return tm * BK * 2; }  // one buffer of widened tokens
+constexpr int stages(int tm) {
+  const int n = (kPool - 2 * wide_bytes(tm)) / stage_bytes(tm);
+  return n < kMaxStages ? n : kMaxStages;
+}
+
+struct Int8Args {
+  int M, N;
+  int num_kb;          // k-blocks; 0: D <- bias + beta * D
+  float alpha, beta;
+  const float* sa;
+  const float* sb;
+  const float* bias;   // or nullptr
+  void* D;
+  int64_t ldd;
+  int d_type;
+  int cluster;         // > 1: CTAs that split one tile's k-blocks
+  uint32_t* err;
+};
+
+struct __align__(16) Tail {
+  uint64_t full[kMaxStages];   // raw operands are there
+  uint64_t empty[kMaxStages];  // ... have been read
+  uint64_t wide_full[2];       // widened operands are there
+  uint64_t wide_empty[2];      // ... have been used
+  uint64_t sum_full;           // an accumulator is finished
+  uint64_t sum_empty;          // ... has been read
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+constexpr size_t kSmemBytes = 1024 + kPool + sizeof(Tail);
+static_assert(kSmemBytes <= 227 * 1024, "int8 kernel shared memory");
+static_assert(stages(16) >= 2 && stages(kMaxTokens) >= 2, "stages");
+static_assert(kMaxTokens * WN * 4 <= kPool, "a cluster's sums fit in the ring");
+
+// Four int8 -> four fp16: with the sign bit turned over, a byte is its value +
+// 128, and as the low byte of 0x6400 it is the fp16 number 1024 + that.
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));  // 1152
+  const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+  const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), off);
+  const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
+  lo = *reinterpret_cast<const uint32_t*>(&x);
+  hi = *reinterpret_cast<const uint32_t*>(&y);
+}
+
+__device__ __forceinline__ uint4 ld_shared_u4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// Tile t of the order: bands of 8 column tiles, row tile by row tile within a
+// band (neighbouring CTAs share weights and tokens in L2).
+struct Tile {
+  int tn, tm;
+};
+__device__ __forceinline__ Tile tile_of(int t, int tiles_n, int tiles_m) {
+  const int per_band = 8 * tiles_m;
+  const int b = t / per_band;
+  const int wide = min(tiles_n - b * 8, 8);
+  const int in = t - b * per_band;
+  Tile r;
+  r.tm = in / wide;
+  r.tn = b * 8 + in - r.tm * wide;
+  return r;
+}
+
+// D of one value, given its integer sum.  cs: alpha times the channel's scale.
+__device__ __forceinline__ void finish(const Int8Args& p, int64_t at, int sum, float cs, float sa, float bias) {
+  float v = p.num_kb > 0 ? fmaf(static_cast<float>(sum) * sa, cs, bias) : bias;
+  if (p.beta != 0.0f) v = fmaf(p.beta, load1(p.D, p.d_type, at), v);
+  store1(p.D, p.d_type, at, v);
+}
+
+template <int TM, bool CLUSTER>
+__global__ void __launch_bounds__(kThreads, 1)
+    int8_kernel(const __grid_constant__ Int8Args p, const __grid_constant__ CUtensorMap tmA,
+                const __grid_constant__ CUtensorMap tmB) {
+  constexpr int STAGES = stages(TM), kStageBytes = stage_bytes(TM), kWideBytes = wide_bytes(TM);
+  constexpr uint32_t kIdesc = idesc_f16_f32(128, TM);
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = align_smem<1024>(smem_raw);
+  uint8_t* wide = smem + STAGES * kStageBytes;  // multiples of 1024
+  Tail* tail = reinterpret_cast<Tail*>(smem + kPool);
+  const uint32_t tail_at = smem_u32(tail);
+  const uint32_t abort_flag = tail_at + offsetof(Tail, abort_flag);
+  const uint32_t full_at = tail_at + offsetof(Tail, full), empty_at = tail_at + offsetof(Tail, empty);
+  const uint32_t wide_full_at = tail_at + offsetof(Tail, wide_full);
+  const uint32_t wide_empty_at = tail_at + offsetof(Tail, wide_empty);
+  const uint32_t sum_full_at = tail_at + offsetof(Tail, sum_full);
+  const uint32_t sum_empty_at = tail_at + offsetof(Tail, sum_empty);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&tail->full[s], 1);
+      mbar_init(&tail->empty[s], kWorkWarps);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tail->wide_full[b], kWorkWarps);
+      mbar_init(&tail->wide_empty[b], 1);
+    }
+    mbar_init(&tail->sum_full, 1);
+    mbar_init(&tail->sum_empty, kWorkWarps);
+    mbar_init(&tail->drain, 1);
+    tail->abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&tail->tmem_base, kTmemCols);
+    tmem_relinquish_alloc_permit();
+  }
+  const int tiles_n = (p.N + WN - 1) / WN, tiles_m = (p.M + TM - 1) / TM;
+  const int tiles = tiles_n * tiles_m;
+  const int split = CLUSTER ? p.cluster : 1;  // CTAs per tile
+  const int part = CLUSTER ? static_cast<int>(cluster_cta_rank()) : 0;
+  const int first = static_cast<int>(blockIdx.x) / split;
+  const int stride = static_cast<int>(gridDim.x);
+  const int kb0 = CLUSTER ? part * p.num_kb / split : 0;  // num_kb <= 2^10
+  const int kb1 = CLUSTER ? (part + 1) * p.num_kb / split : p.num_kb;
+  if (CLUSTER && warp == 0 && lane == 0) {
+    // The CTA's part of B may come to L2 while the previous kernel ends
+    // (nothing is read from it before the wait below).
+    const Tile w = tile_of(first, tiles_n, tiles_m);
+    for (int i = 0; i < kEarlyBlocks && kb0 + i < kb1; ++i)
+      tma_prefetch_l2_2d(&tmB, (kb0 + i) * BK, w.tn * WN);
+  }
+  grid_dependency_wait();
+  if (threadIdx.x == 0) grid_launch_dependents();
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem_base = tail->tmem_base;
+
+  if (warp < 4) {
+    regs_give_back<few_regs(TM, CLUSTER)>();
+    if (warp == 0) {
+      // ------------------------------------------------------ TMA producer
+      if (lane == 0) {
+        uint32_t it = 0;
+        bool ok = true;
+        for (int t = first; t < tiles && ok; t += stride) {
+          const Tile w = tile_of(t, tiles_n, tiles_m);
+          for (int kb = kb0; kb < kb1; ++kb, ++it) {
+            const uint32_t s = it % STAGES, round = it / STAGES;
+            if (!mbar_wait_at(empty_at + 8 * s, (round & 1u) ^ 1u, abort_flag, p.err)) {
+              ok = false;
+              break;
+            }
+            uint8_t* to = smem + s * kStageBytes;
+            mbar_arrive_expect_tx(&tail->full[s], kStageBytes);
+            tma_load_2d(to, &tmB, kb * BK, w.tn * WN, &tail->full[s]);
+            tma_load_2d(to + kRawW, &tmA, kb * BK, w.tm * TM, &tail->full[s]);
+          }
+          if (CLUSTER) break;  // one tile
+        }
+        if (!ok) {
+          for (uint32_t j = it > STAGES ? it - STAGES : 0u; j < it; ++j)
+            mbar_drain_wait(&tail->full[j % STAGES], (j / STAGES) & 1u);
+        }
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      // -------------------------------------------------------- MMA issuer
+      uint32_t it = 0, chunk = 0;
+      bool ok = true, issued = false;
+      // K-major, 64 of k to a row of 128 bytes: 8-row groups 1024 bytes apart
+      const uint64_t db0 = smem_desc_sw128(smem_u32(wide), 16, 1024);
+      for (int t = first; t < tiles && ok; t += stride) {
+        for (int kb = kb0; kb < kb1; ++kb, ++it) {
+          const uint32_t b = it & 1u;
+          const int in_chunk = (kb - kb0) % kChunk;
+          bool got = mbar_wait_at(wide_full_at + 8 * b, (it >> 1) & 1u, abort_flag, p.err);
+          if (in_chunk == 0)
+            got = got && mbar_wait_at(sum_empty_at, (chunk & 1u) ^ 1u, abort_flag, p.err);
+          if (__any_sync(0xffffffffu, !got)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const bool last = in_chunk == kChunk - 1 || kb + 1 == kb1;
+          if (elect_one()) {
+            const uint32_t at = tmem_base + kWideAt + b * kWideCols;
+            const uint64_t db = db0 + b * (kWideBytes >> 4);
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+              for (int kk = 0; kk < BK / 16; ++kk)
+                tc_mma_f16_ta(tmem_base + half * kSumCols, at + half * kWideHalf + kk * 8,
+                              db + (kk >> 2) * (TM * 128 >> 4) + (kk & 3) * 2, kIdesc,
+                              in_chunk != 0 || kk != 0 ? 1u : 0u);
+            tc_commit(&tail->wide_empty[b]);
+            if (last) tc_commit(&tail->sum_full);
+          }
+          __syncwarp();
+          issued = true;
+          if (last) ++chunk;
+        }
+        if (CLUSTER) break;
+      }
+      if (!ok && issued) {
+        if (elect_one()) tc_commit(&tail->drain);
+        __syncwarp();
+        mbar_drain_wait(&tail->drain, 0);
+      }
+      __syncwarp();
+    }
+    if (CLUSTER) {  // with the working warps' two barriers
+      __syncwarp();
+      cluster_sync();
+      cluster_sync();
+    }
+  } else {
+    // -------------------------------------------------- widening and sums
+    regs_take<many_regs(TM, CLUSTER)>();
+    const int tid = static_cast<int>(threadIdx.x) - 128;
+    const int quarter = warp & 3;      // TMEM lanes this warp may access
+    const int half = (warp - 4) >> 2;  // which 128 weights
+    const int wrow = half * 128 + quarter * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t sums_at = tmem_base + lanes + static_cast<uint32_t>(half) * kSumCols;
+    const uint32_t wide_at = tmem_base + lanes + kWideAt + static_cast<uint32_t>(half) * kWideHalf;
+    const uint32_t raw = smem_u32(smem), wide_smem = smem_u32(wide);
+    const uint32_t raw_w = raw + static_cast<uint32_t>(wrow) * BK;
+    constexpr int kPieces = TM * 8;  // 16-byte pieces of a block's tokens
+    constexpr int kMine = (kPieces + kWorkThreads - 1) / kWorkThreads;
+    uint32_t it = 0, chunk = 0;
+    int sum[TM];
+
+    // Widens k-block `it`; false if a wait ran out.
+    auto convert = [&]() -> bool {
+      const uint32_t s = it % STAGES, b = it & 1u;
+      if (!__all_sync(0xffffffffu, mbar_wait_at(full_at + 8 * s, (it / STAGES) & 1u, abort_flag, p.err)))
+        return false;
+      const uint32_t from = s * kStageBytes;
+      // 16-byte pieces on their way: half of the weights', then the others, then
+      // the tokens', each loaded before the last ones' stores
+      uint4 w[4], x[kMine];
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        w[c] = ld_shared_u4(raw_w + from + static_cast<uint32_t>((c ^ (wrow & 7)) * 16));
+      if (!__all_sync(0xffffffffu,
+                      mbar_wait_at(wide_empty_at + 8 * b, ((it >> 1) & 1u) ^ 1u, abort_flag, p.err)))
+        return false;
+      tc_fence_after_sync();
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t r[32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          widen4(w[c].x, r[c * 8], r[c * 8 + 1]);
+          widen4(w[c].y, r[c * 8 + 2], r[c * 8 + 3]);
+          widen4(w[c].z, r[c * 8 + 4], r[c * 8 + 5]);
+          widen4(w[c].w, r[c * 8 + 6], r[c * 8 + 7]);
+        }
+        if (h == 0) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            w[c] = ld_shared_u4(raw_w + from + static_cast<uint32_t>(((c + 4) ^ (wrow & 7)) * 16));
+        } else {
+#pragma unroll
+          for (int i = 0; i < kMine; ++i) {
+            const int q = tid + i * kWorkThreads, row = q >> 3, c = q & 7;
+            if (kPieces % kWorkThreads == 0 || q < kPieces)
+              x[i] = ld_shared_u4(raw + from + kRawW +
+                                  static_cast<uint32_t>(row * BK + ((c ^ (row & 7)) * 16)));
+          }
+        }
+        tmem_st_32x32b_x32(wide_at + b * kWideCols + h * 32, r);
+      }
+      const uint32_t to = wide_smem + b * kWideBytes;
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int q = tid + i * kWorkThreads, row = q >> 3, c = q & 7;
+        if (kPieces % kWorkThreads != 0 && q >= kPieces) continue;
+        uint32_t v[8];
+        widen4(x[i].x, v[0], v[1]);
+        widen4(x[i].y, v[2], v[3]);
+        widen4(x[i].z, v[4], v[5]);
+        widen4(x[i].w, v[6], v[7]);
+        // two 16-byte pieces of the row; pieces 4..7 of 8 lie in the other 64
+        // of k, at the same banks, so those lanes write theirs the other way round
+        const bool far = c >= 4;
+        const uint32_t base = to + (far ? TM * 128 : 0) + static_cast<uint32_t>(row) * 128;
+        const int c0 = 2 * (c & 3) + (far ? 1 : 0), c1 = c0 ^ 1;
+        const uint32_t a0 = base + static_cast<uint32_t>((c0 ^ (row & 7)) * 16);
+        const uint32_t a1 = base + static_cast<uint32_t>((c1 ^ (row & 7)) * 16);
+        st_shared_u4(a0, far ? v[4] : v[0], far ? v[5] : v[1], far ? v[6] : v[2], far ? v[7] : v[3]);
+        st_shared_u4(a1, far ? v[0] : v[4], far ? v[1] : v[5], far ? v[2] : v[6], far ? v[3] : v[7]);
+      }
+      tc_wait_st();
+      fence_proxy_async_smem();
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive_at(empty_at + 8 * s);
+        mbar_arrive_at(wide_full_at + 8 * b);
+      }
+      ++it;
+      return true;
+    };
+    // Adds the finished accumulator to the sums.
+    auto take = [&]() -> bool {
+      if (!__all_sync(0xffffffffu, mbar_wait_at(sum_full_at, chunk & 1u, abort_flag, p.err))) return false;
+      tc_fence_after_sync();
+      if constexpr (TM == 16) {
+        uint32_t r[16];
+        tmem_ld_32x32b_x16(sums_at, r);
+        tc_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sum[i] += __float2int_rn(__uint_as_float(r[i]));
+      } else {
+#pragma unroll
+        for (int j = 0; j < TM; j += 32) {
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(sums_at + j, r);
+          tmem_wait_ld(r);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) sum[j + i] += __float2int_rn(__uint_as_float(r[i]));
+        }
+      }
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_at(sum_empty_at);
+      ++chunk;
+      return true;
+    };
+
+    // This CTA's blocks of a tile.  The first block of a chunk is ready before
+    // the last chunk is taken.
+    auto sums = [&]() -> bool {
+#pragma unroll
+      for (int i = 0; i < TM; ++i) sum[i] = 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!convert()) return false;
+        if (kb > kb0 && (kb - kb0) % kChunk == 0 && !take()) return false;
+      }
+      return kb1 == kb0 || take();
+    };
+
+    for (int t = first; !CLUSTER && t < tiles; t += stride) {
+      if (!sums()) break;
+      const Tile w = tile_of(t, tiles_n, tiles_m);
+      const int n = w.tn * WN + wrow, row0 = w.tm * TM;
+      if (n < p.N) {
+        const float cs = p.num_kb > 0 ? p.alpha * p.sb[n] : 0.0f;
+        const float bias = p.bias != nullptr ? p.bias[n] : 0.0f;
+#pragma unroll
+        for (int j = 0; j < TM; ++j) {
+          if (row0 + j >= p.M) break;
+          const float sa = p.num_kb > 0 ? p.sa[row0 + j] : 0.0f;
+          finish(p, (row0 + j) * p.ldd + n, sum[j], cs, sa, bias);
+        }
+      }
+    }
+    if (CLUSTER) {
+      sums();
+      // This CTA's k-blocks are done, and with them every use of the ring: its
+      // sums go there, a token's 256 values to a row.
+      int* out = reinterpret_cast<int*>(smem) + wrow;
+#pragma unroll
+      for (int j = 0; j < TM; ++j) out[j * WN] = sum[j];
+      __syncwarp();
+      cluster_sync();  // every part's sums are in its shared memory
+      // after a wait ran out the sums are not complete; the error word says so
+      const Tile w = tile_of(first, tiles_n, tiles_m);
+      const int n = w.tn * WN + tid, row0 = w.tm * TM;
+      if (first < tiles && !ld_shared_volatile(abort_flag) && n < p.N) {
+        const float cs = p.alpha * p.sb[n];
+        const float bias = p.bias != nullptr ? p.bias[n] : 0.0f;
+        const int j1 = min((part + 1) * TM / split, p.M - row0);
+        const uint32_t mine = smem_u32(smem) + static_cast<uint32_t>(tid) * 4;
+        for (int j = part * TM / split; j < j1; ++j) {
+          int total = 0;
+          for (int src = 0; src < split; ++src)
+            total += __float_as_int(ld_shared_cluster_f32(
+                mapa_shared(mine + static_cast<uint32_t>(j) * (WN * 4), static_cast<uint32_t>(src))));
+          finish(p, (row0 + j) * p.ldd + n, total, cs, p.sa[row0 + j], bias);
+        }
+      }
+      __syncwarp();
+      cluster_sync();  // no CTA leaves while another may still read its shared memory
+    }
+  }
+
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  if (warp == 1) tmem_dealloc(tmem_base, kTmemCols);
+}
+
+// Clusters of S CTAs that can be resident at once on the current device; 0 if
+// unknown.
+int max_clusters(int S) {
+  static std::atomic<int> cache[64][9];
+  int dev = 0;
+  if (S < 2 || S > 8 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  const int known = cache[dev][S].load(std::memory_order_relaxed);
+  if (known != 0) return known;
+  int n = 0;
+  if (ops_allow_smem<int8_kernel<kMaxTokens, true>>(kSmemBytes) == cudaSuccess) {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(S);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(S));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, int8_kernel<kMaxTokens, true>, &cfg) != cudaSuccess) n = 0;
+  }
+  cudaGetLastError();
+  if (n > 0) cache[dev][S].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+// CTAs that split each tile's k-blocks, when all tiles fit in one round: the S
+// whose longest share of k-blocks plus the cost of adding S sums is least.
+int choose_split(int64_t tiles, int num_kb, int num_sms) {
+  int best = 1;
+  double cost = num_kb;
+  for (int s = 2; s <= 8 && s <= num_kb; ++s) {
+    if (tiles * s > num_sms || tiles > max_clusters(s)) continue;
+    const double c = (num_kb + s - 1) / s + 4.0;
+    if (c < cost) {
+      cost = c;
+      best = s;
+    }
+  }
+  return best;
+}
+
+template <int TM>
+cudaError_t launch(int64_t tiles, int num_sms, const Int8Args& a, const CUtensorMap& tmA,
+                   const CUtensorMap& tmB, cudaStream_t s) {
+  if (a.cluster > 1)
+    return ops_launch<int8_kernel<TM, true>>(dim3(static_cast<unsigned>(tiles * a.cluster)), kThreads,
+                                             kSmemBytes, a.cluster, s, a, tmA, tmB);
+  return ops_launch<int8_kernel<TM, false>>(dim3(static_cast<unsigned>(tiles < num_sms ? tiles : num_sms)),
+                                            kThreads, kSmemBytes, 1, s, a, tmA, tmB);
+}
+
+// Largest K whose sums fit 32 bits: K * 2^14 < 2^31.
+constexpr int64_t kMaxK = (int64_t{1} << 17) - 1;
+
+}  // namespace
+}  // namespace g12
+
+using namespace g12;
+
+extern "C" gemm_status_t gemm_int8gemm(int64_t M, int64_t N, int64_t K, float alpha, const int8_t* A,
+                                       int64_t lda, const float* a_scales, const int8_t* B, int64_t ldb,
+                                       const float* b_scales, const float* bias, float beta, void* D,
+                                       int64_t ldd, int d_type, void* stream) {
+  const int d_bytes = float_type_bytes(d_type);
+  if (M < 0 || N < 0 || K < 0 || M > kOpsMaxTiled || N > kOpsMaxTiled || K > kOpsMaxDim || d_bytes == 0)
+    return GEMM_ERR_INVALID_VALUE;
+  if (M == 0 || N == 0) return GEMM_OK;
+  const bool product = K > 0 && alpha != 0.0f;
+  if (D == nullptr || ldd < N || ldd > kOpsMaxDim || ops_misaligned(D, d_bytes) ||
+      (bias != nullptr && ops_misaligned(bias, 4)))
+    return GEMM_ERR_INVALID_VALUE;
+  if (product && (A == nullptr || B == nullptr || a_scales == nullptr || b_scales == nullptr || lda < K ||
+                  ldb < K || lda > kOpsMaxDim || ldb > kOpsMaxDim || ops_misaligned(a_scales, 4) ||
+                  ops_misaligned(b_scales, 4)))
+    return GEMM_ERR_INVALID_VALUE;
+  if (product && K > kMaxK) return GEMM_ERR_UNSUPPORTED;
+  int sms = 0;
+  uint32_t* err = nullptr;
+  gemm_status_t st = abi_device(&sms, &err);
+  if (st != GEMM_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  Int8Args a{};
+  a.M = static_cast<int>(M);
+  a.N = static_cast<int>(N);
+  a.num_kb = product ? static_cast<int>((K + BK - 1) / BK) : 0;
+  a.alpha = alpha;
+  a.beta = beta;
+  a.sa = a_scales;
+  a.sb = b_scales;
+  a.bias = bias;
+  a.D = D;
+  a.ldd = ldd;
+  a.d_type = d_type;
+  a.err = err;
+  const int tm = M > 64 ? 128 : (M > 32 ? 64 : (M > 16 ? 32 : 16));
+  std::unique_lock<std::mutex> lock;
+  CUtensorMap tmA{}, tmB{};
+  if (product) {
+    ByteOperand oa{A, M, K, lda, 1, 0}, ob{B, N, K, ldb, 1, 0};
+    const int64_t need_a = byte_tma_ok(oa) ? 0 : byte_staged(oa);
+    const int64_t need_b = byte_tma_ok(ob) ? 0 : byte_staged(ob);
+    if (need_a + need_b > 0) {
+      uint8_t* buf = nullptr;
+      st = abi_stage(s, need_a + need_b, lock, &buf);
+      if (st != GEMM_OK) return st;
+      cudaError_t e = need_a > 0 ? byte_stage(oa, buf, sms, s) : cudaSuccess;
+      if (e == cudaSuccess && need_b > 0) e = byte_stage(ob, buf + need_a, sms, s);
+      if (e != cudaSuccess) return abi_from_cuda(e);
+    }
+    const int64_t da[2] = {K, M}, ta[1] = {byte_pitch(oa)};
+    const int64_t db[2] = {K, N}, tb[1] = {byte_pitch(ob)};
+    const uint32_t ba[2] = {BK, static_cast<uint32_t>(tm)}, bb[2] = {BK, WN};
+    if (!abi_encode_tiled(&tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, oa.p, da, ta, ba) ||
+        !abi_encode_tiled(&tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, ob.p, db, tb, bb))
+      return GEMM_ERR_LAUNCH;
+  }
+  const int64_t tiles = ((N + WN - 1) / WN) * ((M + tm - 1) / tm);
+  if (tiles + sms > kOpsMaxDim) return GEMM_ERR_UNSUPPORTED;
+  a.cluster = choose_split(tiles, a.num_kb, sms);
+  switch (tm) {
+    case 16: return abi_from_cuda(launch<16>(tiles, sms, a, tmA, tmB, s));
+    case 32: return abi_from_cuda(launch<32>(tiles, sms, a, tmA, tmB, s));
+    case 64: return abi_from_cuda(launch<64>(tiles, sms, a, tmA, tmB, s));
+    default: return abi_from_cuda(launch<128>(tiles, sms, a, tmA, tmB, s));
+  }
+}

@@ -6,6 +6,7 @@
 
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
@@ -97,6 +98,25 @@ cudaError_t ops_launch(dim3 grid, int threads, size_t smem, int cluster, cudaStr
   const cudaError_t e = cudaLaunchKernelEx(&cfg, Kernel, args...);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
+
+// An operand of bytes (fp8, int8), contiguous along k, and its copy for TMA
+// where TMA cannot describe it as it is (bytes.cu).
+struct ByteOperand {
+  const void* p;
+  int64_t rows, cols, ld;   // of each matrix
+  int64_t count, stride;    // matrices
+};
+// Row pitch in a tensor map.  A single row has none of its own: any will do.
+inline int64_t byte_pitch(const ByteOperand& o) { return o.rows == 1 ? (o.cols + 15) / 16 * 16 : o.ld; }
+inline bool byte_tma_ok(const ByteOperand& o) {
+  return !ops_misaligned(o.p, 16) && byte_pitch(o) % 16 == 0 && (o.count == 1 || o.stride % 16 == 0);
+}
+// Bytes of a copy that TMA can describe (rows padded to 16 bytes).
+inline int64_t byte_staged(const ByteOperand& o) {
+  return (o.count * o.rows * ((o.cols + 15) / 16 * 16) + 255) / 256 * 256;
+}
+// Queues the copy to `dst` and points the operand there.
+cudaError_t byte_stage(ByteOperand& o, uint8_t* dst, int num_sms, cudaStream_t s);
 
 // ------------------------------------------------------- fp8 block scales
 constexpr float kFp8Max = 448.0f;             // largest finite E4M3 value
@@ -494,6 +514,40 @@ __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+
+// D[tmem] (+)= A[tmem] x B[smem], kind::f16, single CTA: lane i of A's columns is
+// row i, two values of k to a column.
+__device__ __forceinline__ void tc_mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                              uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Instruction descriptor of tcgen05.mma kind::f16 with fp16 (format 0) A and B,
+// both K-major, and an fp32 accumulator: fields as in idesc_bf16_f32.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(uint32_t M, uint32_t N) {
+  return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+// Each thread of the warp writes 32 consecutive columns of its own TMEM lane.
+__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+      "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+      "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tc_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
 // Instruction descriptor of tcgen05.mma kind::f8f6f4 with E4M3 A and B (format

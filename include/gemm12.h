@@ -545,7 +545,8 @@ gemm_status_t gemm_quantization(int64_t M, int64_t N, int64_t BM, int64_t BN,
  *             the norm's dim at most 2^30.  More is GEMM_ERR_INVALID_VALUE.
  *  Memory     gemm_rmsnorm_backward and gemm_layernorm_backward keep partial
  *             sums of the parameters' gradients in the stream's scratch,
- *             gemm_expert_sort counters; operands of the products
+ *             gemm_int8_quantize (transposed) columns' maxima, gemm_expert_sort
+ *             counters; operands of the products
  *             that TMA cannot describe (base not 16-byte aligned, or a matrix
  *             stride, or the row pitch of more than one row, that is not a
  *             multiple of 16 bytes) are
@@ -752,6 +753,38 @@ gemm_status_t gemm_fp8gemm(int64_t M, int64_t N, int64_t K, float alpha, const v
                            int64_t lda, const float *a_scales, int64_t ld_as, const void *B,
                            int64_t ldb, const float *b_scales, int64_t ld_bs, int b_block,
                            float beta, void *D, int64_t ldd, int d_type, void *stream);
+
+/*
+ * gemm_int8_quantize -- the rows x cols matrix x, or its transpose, in int8
+ * with a scale for each row of the result q (rows x cols, or with `transpose`
+ * cols x rows; ldq):
+ *
+ *     a = largest finite |x| of the row
+ *     scale = max(a / 127, 2^-126)      q = x / scale
+ *
+ * rounded half to even, within +-127; infinities become +-127 and NaN 0.  The
+ * quotient is formed as x * (127 / a) in fp32.  cols is at most 2^30 without
+ * `transpose`; with it the columns' maxima are in the stream's scratch.
+ *
+ * gemm_int8gemm -- for int8 A (M x K) and B (N x K), both contiguous along k,
+ * with one scale for each of A's rows (M fp32 values: tokens) and one for each
+ * of B's (N: output channels):
+ *
+ *     D[i][j] = alpha * a_scale[i] * b_scale[j] * sum_k A[i][k] * B[j][k]
+ *               + bias[j] + beta * D[i][j]
+ *
+ * The sum is exact (any int8 values, -128 included): K is at most 2^17 - 1
+ * (more is GEMM_ERR_UNSUPPORTED), the scales and the rest are fp32.  bias (N
+ * fp32 values) may be NULL.  D (ldd) is fp32 or bf16 and is not read when beta
+ * == 0.  K == 0 or alpha == 0: A, B and the scales are not read.  D must not
+ * overlap the operands.
+ */
+gemm_status_t gemm_int8_quantize(int64_t rows, int64_t cols, const void *x, int64_t ldx, int x_type,
+                                 int transpose, int8_t *q, int64_t ldq, float *scales, void *stream);
+gemm_status_t gemm_int8gemm(int64_t M, int64_t N, int64_t K, float alpha, const int8_t *A, int64_t lda,
+                            const float *a_scales, const int8_t *B, int64_t ldb, const float *b_scales,
+                            const float *bias, float beta, void *D, int64_t ldd, int d_type,
+                            void *stream);
 
 /*
  * Products grouped by expert.  Group g (0 <= g < G <= 1024) has the rows
