@@ -21,14 +21,14 @@
 //   * warp 0       TMA producer: 256 x 128 of B and up to 128 x 128 of A per
 //                  k-block, as int8, into a ring
 //   * warp 1       TMEM and MMAs (M = 128, K = 16): two halves of the weights
-//   * warps 4..11  widening, 128 values of k at a time: a thread takes one
-//                  weight row into its TMEM lane (tcgen05.st: shared memory,
-//                  which is what such a kernel runs out of, is not written or
-//                  read again for it) and its share of the tokens into shared
-//                  memory; two buffers of each.  Then, every 8 k-blocks, the
-//                  accumulator's 32 x (tokens) values per warp to integer sums
-//                  in registers, and at a tile's end to D.
-// Registers move from the first warpgroup to the other two for the sums.
+//   * warps 4..19  widening, 128 values of k at a time: a thread takes half of
+//                  a weight row into its TMEM lane (tcgen05.st: shared memory
+//                  is not written or read again for it) and its share of the
+//                  tokens into shared memory; two buffers of each.  Then, every
+//                  8 k-blocks, the accumulator's values of 32 weights and half
+//                  of the tokens per warp to integer sums in registers, and at
+//                  a tile's end to D.
+// Registers move from the first warpgroup to the other four for the sums.
 //
 // Few tiles: the CTAs of a cluster split a tile's k-blocks and add their sums
 // through distributed shared memory.
@@ -46,16 +46,14 @@ constexpr int kChunk = 8;      // k-blocks that an accumulator sums exactly
 constexpr int kMaxStages = 5;
 constexpr int kRawW = WN * BK;  // a stage's bytes of weights
 constexpr int kPool = 208 * 1024;  // the ring and the widened tokens
-constexpr int kThreads = 384;
-constexpr int kWorkThreads = 256;
+constexpr int kThreads = 640;
+constexpr int kWorkThreads = 512;
 constexpr int kWorkWarps = kWorkThreads / 32;
 constexpr uint32_t kTmemCols = 512;
 // TMEM columns: sums of the two halves, then two buffers of widened weights
 constexpr uint32_t kSumCols = 128, kWideAt = 256, kWideCols = 128, kWideHalf = 64;
-// Registers of the warpgroups, few + 2 x many = 3 x 168: what compiles without
-// spills.
-constexpr int few_regs(int tm, bool cluster) { return tm < kMaxTokens ? 88 : (cluster ? 72 : 104); }
-constexpr int many_regs(int tm, bool cluster) { return (3 * 168 - few_regs(tm, cluster)) / 2; }
+// 640 threads launch with 96 registers each; 64 + 4 x 104 = 5 x 96.
+constexpr int kFewRegs = 64, kManyRegs = 104;
 // k-blocks of B that a CTA of a split tile asks L2 for early.
 constexpr int kEarlyBlocks = 4;
 
@@ -203,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem_base = tail->tmem_base;
 
   if (warp < 4) {
-    regs_give_back<few_regs(TM, CLUSTER)>();
+    regs_give_back<kFewRegs>();
     if (warp == 0) {
       // ------------------------------------------------------ TMA producer
       if (lane == 0) {
@@ -282,20 +280,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // -------------------------------------------------- widening and sums
-    regs_take<many_regs(TM, CLUSTER)>();
+    regs_take<kManyRegs>();
     const int tid = static_cast<int>(threadIdx.x) - 128;
-    const int quarter = warp & 3;      // TMEM lanes this warp may access
-    const int half = (warp - 4) >> 2;  // which 128 weights
+    const int quarter = warp & 3;             // TMEM lanes this warp may access
+    const int half = ((warp - 4) >> 2) & 1;   // which 128 weights
+    const int side = (warp - 4) >> 3;         // which half of a block's k, and of the tokens' sums
     const int wrow = half * 128 + quarter * 32 + lane;
+    constexpr int kMySums = TM / 2;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t sums_at = tmem_base + lanes + static_cast<uint32_t>(half) * kSumCols;
-    const uint32_t wide_at = tmem_base + lanes + kWideAt + static_cast<uint32_t>(half) * kWideHalf;
+    const uint32_t sums_at = tmem_base + lanes + static_cast<uint32_t>(half) * kSumCols + side * kMySums;
+    const uint32_t wide_at = tmem_base + lanes + kWideAt + static_cast<uint32_t>(half) * kWideHalf + side * 32;
     const uint32_t raw = smem_u32(smem), wide_smem = smem_u32(wide);
     const uint32_t raw_w = raw + static_cast<uint32_t>(wrow) * BK;
+    const uint32_t turn = static_cast<uint32_t>((side * 4) ^ (wrow & 7)) * 16;
     constexpr int kPieces = TM * 8;  // 16-byte pieces of a block's tokens
     constexpr int kMine = (kPieces + kWorkThreads - 1) / kWorkThreads;
+    const uint32_t token = static_cast<uint32_t>(tid & (TM - 1));
+    const int piece0 = tid / TM;
+    const uint32_t raw_x = raw + kRawW + token * BK, turn_x = (token & 7) * 16;
     uint32_t it = 0, chunk = 0;
-    int sum[TM];
+    int sum[kMySums];
 
     // Widens k-block `it`; false if a wait ran out.
     auto convert = [&]() -> bool {
@@ -303,60 +307,50 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!__all_sync(0xffffffffu, mbar_wait_at(full_at + 8 * s, (it / STAGES) & 1u, abort_flag, p.err)))
         return false;
       const uint32_t from = s * kStageBytes;
-      // 16-byte pieces on their way: half of the weights', then the others, then
-      // the tokens', each loaded before the last ones' stores
-      uint4 w[4], x[kMine];
+      // 16-byte pieces, swizzled by their row: this side's four of the weight
+      // row, then the tokens'
+      uint4 w[2];
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        w[c] = ld_shared_u4(raw_w + from + static_cast<uint32_t>((c ^ (wrow & 7)) * 16));
+      for (int c = 0; c < 2; ++c) w[c] = ld_shared_u4(raw_w + from + (turn ^ (c * 16)));
       if (!__all_sync(0xffffffffu,
                       mbar_wait_at(wide_empty_at + 8 * b, ((it >> 1) & 1u) ^ 1u, abort_flag, p.err)))
         return false;
       tc_fence_after_sync();
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint32_t r[32];
+        uint32_t r[16];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          widen4(w[c].x, r[c * 8], r[c * 8 + 1]);
-          widen4(w[c].y, r[c * 8 + 2], r[c * 8 + 3]);
-          widen4(w[c].z, r[c * 8 + 4], r[c * 8 + 5]);
-          widen4(w[c].w, r[c * 8 + 6], r[c * 8 + 7]);
+        for (int c = 0; c < 2; ++c) {
+          const uint4 v = w[c];
+          widen4(v.x, r[c * 8], r[c * 8 + 1]);
+          widen4(v.y, r[c * 8 + 2], r[c * 8 + 3]);
+          widen4(v.z, r[c * 8 + 4], r[c * 8 + 5]);
+          widen4(v.w, r[c * 8 + 6], r[c * 8 + 7]);
         }
         if (h == 0) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            w[c] = ld_shared_u4(raw_w + from + static_cast<uint32_t>(((c + 4) ^ (wrow & 7)) * 16));
-        } else {
-#pragma unroll
-          for (int i = 0; i < kMine; ++i) {
-            const int q = tid + i * kWorkThreads, row = q >> 3, c = q & 7;
-            if (kPieces % kWorkThreads == 0 || q < kPieces)
-              x[i] = ld_shared_u4(raw + from + kRawW +
-                                  static_cast<uint32_t>(row * BK + ((c ^ (row & 7)) * 16)));
-          }
+          for (int c = 0; c < 2; ++c) w[c] = ld_shared_u4(raw_w + from + (turn ^ (c * 16 + 32)));
         }
-        tmem_st_32x32b_x32(wide_at + b * kWideCols + h * 32, r);
+        tmem_st_32x32b_x16(wide_at + b * kWideCols + h * 16, r);
       }
+      // Neighbouring threads take neighbouring tokens and the same piece, so that
+      // reads and writes of eight lanes fall in different banks.
       const uint32_t to = wide_smem + b * kWideBytes;
 #pragma unroll
       for (int i = 0; i < kMine; ++i) {
-        const int q = tid + i * kWorkThreads, row = q >> 3, c = q & 7;
-        if (kPieces % kWorkThreads != 0 && q >= kPieces) continue;
+        const int c = piece0 + i * (kWorkThreads / TM);
+        if (kPieces < kWorkThreads && c >= 8) continue;
+        const uint4 x = ld_shared_u4(raw_x + from + (static_cast<uint32_t>(c * 16) ^ turn_x));
         uint32_t v[8];
-        widen4(x[i].x, v[0], v[1]);
-        widen4(x[i].y, v[2], v[3]);
-        widen4(x[i].z, v[4], v[5]);
-        widen4(x[i].w, v[6], v[7]);
-        // two 16-byte pieces of the row; pieces 4..7 of 8 lie in the other 64
-        // of k, at the same banks, so those lanes write theirs the other way round
-        const bool far = c >= 4;
-        const uint32_t base = to + (far ? TM * 128 : 0) + static_cast<uint32_t>(row) * 128;
-        const int c0 = 2 * (c & 3) + (far ? 1 : 0), c1 = c0 ^ 1;
-        const uint32_t a0 = base + static_cast<uint32_t>((c0 ^ (row & 7)) * 16);
-        const uint32_t a1 = base + static_cast<uint32_t>((c1 ^ (row & 7)) * 16);
-        st_shared_u4(a0, far ? v[4] : v[0], far ? v[5] : v[1], far ? v[6] : v[2], far ? v[7] : v[3]);
-        st_shared_u4(a1, far ? v[0] : v[4], far ? v[1] : v[5], far ? v[2] : v[6], far ? v[3] : v[7]);
+        widen4(x.x, v[0], v[1]);
+        widen4(x.y, v[2], v[3]);
+        widen4(x.z, v[4], v[5]);
+        widen4(x.w, v[6], v[7]);
+        // two pieces of the first or the other 64 of k
+        const uint32_t at = to + (c >= 4 ? TM * 128 : 0) + token * 128;
+        const uint32_t first = static_cast<uint32_t>((c & 3) * 32) ^ turn_x;
+        st_shared_u4(at + first, v[0], v[1], v[2], v[3]);
+        st_shared_u4(at + (first ^ 16), v[4], v[5], v[6], v[7]);
       }
       tc_wait_st();
       fence_proxy_async_smem();
@@ -373,21 +367,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto take = [&]() -> bool {
       if (!__all_sync(0xffffffffu, mbar_wait_at(sum_full_at, chunk & 1u, abort_flag, p.err))) return false;
       tc_fence_after_sync();
-      if constexpr (TM == 16) {
-        uint32_t r[16];
-        tmem_ld_32x32b_x16(sums_at, r);
-        tc_wait_ld();
+      constexpr int kStep = kMySums < 16 ? kMySums : 16;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) sum[i] += __float2int_rn(__uint_as_float(r[i]));
-      } else {
+      for (int j = 0; j < kMySums; j += kStep) {
+        uint32_t r[kStep];
+        if constexpr (kStep == 8)
+          tmem_ld_32x32b_x8(sums_at + j, r);
+        else
+          tmem_ld_32x32b_x16(sums_at + j, r);
+        tmem_wait_ld(r);
 #pragma unroll
-        for (int j = 0; j < TM; j += 32) {
-          uint32_t r[32];
-          tmem_ld_32x32b_x32(sums_at + j, r);
-          tmem_wait_ld(r);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) sum[j + i] += __float2int_rn(__uint_as_float(r[i]));
-        }
+        for (int i = 0; i < kStep; ++i) sum[j + i] += __float2int_rn(__uint_as_float(r[i]));
       }
       tc_fence_before_sync();
       __syncwarp();
@@ -400,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the last chunk is taken.
     auto sums = [&]() -> bool {
 #pragma unroll
-      for (int i = 0; i < TM; ++i) sum[i] = 0;
+      for (int i = 0; i < kMySums; ++i) sum[i] = 0;
       for (int kb = kb0; kb < kb1; ++kb) {
         if (!convert()) return false;
         if (kb > kb0 && (kb - kb0) % kChunk == 0 && !take()) return false;
@@ -411,12 +401,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int t = first; !CLUSTER && t < tiles; t += stride) {
       if (!sums()) break;
       const Tile w = tile_of(t, tiles_n, tiles_m);
-      const int n = w.tn * WN + wrow, row0 = w.tm * TM;
+      const int n = w.tn * WN + wrow, row0 = w.tm * TM + side * kMySums;
       if (n < p.N) {
         const float cs = p.num_kb > 0 ? p.alpha * p.sb[n] : 0.0f;
         const float bias = p.bias != nullptr ? p.bias[n] : 0.0f;
 #pragma unroll
-        for (int j = 0; j < TM; ++j) {
+        for (int j = 0; j < kMySums; ++j) {
           if (row0 + j >= p.M) break;
           const float sa = p.num_kb > 0 ? p.sa[row0 + j] : 0.0f;
           finish(p, (row0 + j) * p.ldd + n, sum[j], cs, sa, bias);
@@ -427,20 +417,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       sums();
       // This CTA's k-blocks are done, and with them every use of the ring: its
       // sums go there, a token's 256 values to a row.
-      int* out = reinterpret_cast<int*>(smem) + wrow;
+      int* out = reinterpret_cast<int*>(smem) + side * kMySums * WN + wrow;
 #pragma unroll
-      for (int j = 0; j < TM; ++j) out[j * WN] = sum[j];
+      for (int j = 0; j < kMySums; ++j) out[j * WN] = sum[j];
       __syncwarp();
       cluster_sync();  // every part's sums are in its shared memory
       // after a wait ran out the sums are not complete; the error word says so
       const Tile w = tile_of(first, tiles_n, tiles_m);
-      const int n = w.tn * WN + tid, row0 = w.tm * TM;
+      // 512 threads: every other token each
+      const int n = w.tn * WN + (tid & (WN - 1)), row0 = w.tm * TM;
       if (first < tiles && !ld_shared_volatile(abort_flag) && n < p.N) {
         const float cs = p.alpha * p.sb[n];
         const float bias = p.bias != nullptr ? p.bias[n] : 0.0f;
         const int j1 = min((part + 1) * TM / split, p.M - row0);
-        const uint32_t mine = smem_u32(smem) + static_cast<uint32_t>(tid) * 4;
-        for (int j = part * TM / split; j < j1; ++j) {
+        const uint32_t mine = smem_u32(smem) + static_cast<uint32_t>(tid & (WN - 1)) * 4;
+        for (int j = part * TM / split + (tid >> 8); j < j1; j += 2) {
           int total = 0;
           for (int src = 0; src < split; ++src)
             total += __float_as_int(ld_shared_cluster_f32(
