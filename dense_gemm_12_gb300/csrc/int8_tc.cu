@@ -74,11 +74,13 @@ struct Int8Args {
   void* D;
   int64_t ldd;
   int d_type;
+  int d_pair;          // bf16, beta == 0: two channels can be written at once
   int cluster;         // > 1: CTAs that split one tile's k-blocks
   uint32_t* err;
 };
 
 struct __align__(16) Tail {
+  float scales[kWorkWarps][kMaxTokens / 2];  // of the tokens of a warp's sums
   uint64_t full[kMaxStages];   // raw operands are there
   uint64_t empty[kMaxStages];  // ... have been read
   uint64_t wide_full[2];       // widened operands are there
@@ -88,6 +90,8 @@ struct __align__(16) Tail {
   uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
+  int4 order;  // tiles, column tiles, row tiles, tiles to step: for the working
+               // warps, which have no registers to keep them in
 };
 
 constexpr size_t kSmemBytes = 1024 + kPool + sizeof(Tail);
@@ -106,6 +110,36 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
   lo = *reinterpret_cast<const uint32_t*>(&x);
   hi = *reinterpret_cast<const uint32_t*>(&y);
 }
+
+// Adds two whole numbers of at most 2^24, as fp32, to 32-bit integers, each with
+// kWholeOff on top.  Adding kRound leaves f rounded to a multiple of 2^13, which
+// its last bits then count; what is left, less than 2^13, is counted by the last
+// bits of its sum with 1.5 * 2^23 (the constants are chosen so that the second
+// and third sums are exact).  The conversion instruction, 16 a cycle, would take
+// as long as two k-blocks' MMAs for a tile's accumulator.
+constexpr float kRound = 103079215104.0f;               // 1.5 * 2^36
+constexpr float kRoundLeft = 103079215104.0f + 12582912.0f;  // and 1.5 * 2^23
+constexpr uint32_t kWholeOff = 0x51c00000u * 8192u + 0x4b400000u;  // their bits, as added below
+__device__ __forceinline__ void add_whole(uint32_t& a, uint32_t& b, uint32_t f, uint32_t g) {
+  uint32_t t0, t1, u0, u1;
+  asm("{\n\t.reg .b64 f, c, d, m, t, u;\n\t"
+      "mov.b64 f, {%4, %5};\n\t"
+      "mov.b64 c, {%6, %6};\n\t"
+      "mov.b64 d, {%7, %7};\n\t"
+      "mov.b64 m, {%8, %8};\n\t"
+      "add.rn.f32x2 t, f, c;\n\t"
+      "fma.rn.f32x2 u, t, m, d;\n\t"
+      "add.rn.f32x2 u, u, f;\n\t"
+      "mov.b64 {%0, %1}, t;\n\t"
+      "mov.b64 {%2, %3}, u;\n\t}"
+      : "=r"(t0), "=r"(t1), "=r"(u0), "=r"(u1)
+      : "r"(f), "r"(g), "f"(kRound), "f"(kRoundLeft), "f"(-1.0f));
+  a += (t0 << 13) + u0;
+  b += (t1 << 13) + u1;
+}
+// Which group of sums goes through the conversion instruction all the same: a
+// quarter, as long as the others take on the other units.
+__host__ __device__ constexpr bool by_unit(int j) { return j >= 48; }
 
 __device__ __forceinline__ uint4 ld_shared_u4(uint32_t addr) {
   uint4 v;
@@ -132,9 +166,12 @@ __device__ __forceinline__ Tile tile_of(int t, int tiles_n, int tiles_m) {
   return r;
 }
 
-// D of one value, given its integer sum.  cs: alpha times the channel's scale.
-__device__ __forceinline__ void finish(const Int8Args& p, int64_t at, int sum, float cs, float sa, float bias) {
-  float v = p.num_kb > 0 ? fmaf(static_cast<float>(sum) * sa, cs, bias) : bias;
+// A value of D without beta's part, given its integer sum.  cs: alpha times the
+// channel's scale.
+__device__ __forceinline__ float value(const Int8Args& p, uint32_t sum, float cs, float sa, float bias) {
+  return p.num_kb > 0 ? fmaf(static_cast<float>(static_cast<int>(sum)) * sa, cs, bias) : bias;
+}
+__device__ __forceinline__ void finish(const Int8Args& p, int64_t at, float v) {
   if (p.beta != 0.0f) v = fmaf(p.beta, load1(p.D, p.d_type, at), v);
   store1(p.D, p.d_type, at, v);
 }
@@ -172,6 +209,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&tail->sum_empty, kWorkWarps);
     mbar_init(&tail->drain, 1);
     tail->abort_flag = 0;
+    const int cols = (p.N + WN - 1) / WN, rows = (p.M + TM - 1) / TM;
+    tail->order = make_int4(cols * rows, cols, rows, static_cast<int>(gridDim.x));
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -287,6 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int side = (warp - 4) >> 3;         // which half of a block's k, and of the tokens' sums
     const int wrow = half * 128 + quarter * 32 + lane;
     constexpr int kMySums = TM / 2;
+    constexpr int kStep = kMySums == 16 || kMySums == 32 ? 16 : 8;  // sums per TMEM load
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t sums_at = tmem_base + lanes + static_cast<uint32_t>(half) * kSumCols + side * kMySums;
     const uint32_t wide_at = tmem_base + lanes + kWideAt + static_cast<uint32_t>(half) * kWideHalf + side * 32;
@@ -299,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int piece0 = tid / TM;
     const uint32_t raw_x = raw + kRawW + token * BK, turn_x = (token & 7) * 16;
     uint32_t it = 0, chunk = 0;
-    int sum[kMySums];
+    uint32_t sum[kMySums];
 
     // Widens k-block `it`; false if a wait ran out.
     auto convert = [&]() -> bool {
@@ -367,7 +407,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto take = [&]() -> bool {
       if (!__all_sync(0xffffffffu, mbar_wait_at(sum_full_at, chunk & 1u, abort_flag, p.err))) return false;
       tc_fence_after_sync();
-      constexpr int kStep = kMySums < 16 ? kMySums : 16;
 #pragma unroll
       for (int j = 0; j < kMySums; j += kStep) {
         uint32_t r[kStep];
@@ -376,8 +415,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
           tmem_ld_32x32b_x16(sums_at + j, r);
         tmem_wait_ld(r);
+        if (by_unit(j)) {
 #pragma unroll
-        for (int i = 0; i < kStep; ++i) sum[j + i] += __float2int_rn(__uint_as_float(r[i]));
+          for (int i = 0; i < kStep; ++i) sum[j + i] += static_cast<uint32_t>(__float2int_rn(__uint_as_float(r[i])));
+        } else {
+#pragma unroll
+          for (int i = 0; i < kStep; i += 2) add_whole(sum[j + i], sum[j + i + 1], r[i], r[i + 1]);
+        }
       }
       tc_fence_before_sync();
       __syncwarp();
@@ -389,8 +433,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // This CTA's blocks of a tile.  The first block of a chunk is ready before
     // the last chunk is taken.
     auto sums = [&]() -> bool {
+      const uint32_t start = 0u - kWholeOff * static_cast<uint32_t>((kb1 - kb0 + kChunk - 1) / kChunk);
 #pragma unroll
-      for (int i = 0; i < kMySums; ++i) sum[i] = 0;
+      for (int i = 0; i < kMySums; ++i) sum[i] = by_unit(i / kStep * kStep) ? 0u : start;
       for (int kb = kb0; kb < kb1; ++kb) {
         if (!convert()) return false;
         if (kb > kb0 && (kb - kb0) % kChunk == 0 && !take()) return false;
@@ -398,26 +443,62 @@ __global__ void __launch_bounds__(kThreads, 1)
       return kb1 == kb0 || take();
     };
 
-    for (int t = first; !CLUSTER && t < tiles; t += stride) {
+    const uint32_t my_scales = tail_at + offsetof(Tail, scales) +
+                               static_cast<uint32_t>(warp - 4) * sizeof(tail->scales[0]);
+    const uint32_t order_at = tail_at + offsetof(Tail, order);
+    for (int t = first; !CLUSTER && t < ld_shared_i4(order_at).x; t += ld_shared_i4(order_at).w) {
+      if (p.num_kb > 0) {
+        const int4 o = ld_shared_i4(order_at);
+        const int row0 = tile_of(t, o.y, o.z).tm * TM + side * kMySums;
+        for (int j = lane; j < kMySums; j += 32)
+          cp_async_4_at(my_scales + 4 * j, row0 + j < p.M ? p.sa + row0 + j : p.sa,
+                        row0 + j < p.M ? 4u : 0u);
+      }
       if (!sums()) break;
-      const Tile w = tile_of(t, tiles_n, tiles_m);
+      cp_async_wait_all();
+      __syncwarp();
+      const int4 o = ld_shared_i4(order_at);
+      const Tile w = tile_of(t, o.y, o.z);
       const int n = w.tn * WN + wrow, row0 = w.tm * TM + side * kMySums;
-      if (n < p.N) {
-        const float cs = p.num_kb > 0 ? p.alpha * p.sb[n] : 0.0f;
-        const float bias = p.bias != nullptr ? p.bias[n] : 0.0f;
+      const int rows = min(p.M - row0, kMySums);  // below 1: none
+      const bool in = n < p.N;
+      const float cs = in && p.num_kb > 0 ? p.alpha * p.sb[n] : 0.0f;
+      const float bias = in && p.bias != nullptr ? p.bias[n] : 0.0f;
+      const int64_t at = row0 * p.ldd + n;
+      if (p.d_pair && w.tn * WN + WN <= p.N && rows == kMySums) {
+        // Two tokens' values of a channel become two channels' of a token: even
+        // lanes take the first token's, odd ones the second's.
+        const bool odd = lane & 1;
+        __nv_bfloat16* d = static_cast<__nv_bfloat16*>(p.D) + at + (odd ? p.ldd - 1 : 0);
 #pragma unroll
-        for (int j = 0; j < kMySums; ++j) {
-          if (row0 + j >= p.M) break;
-          const float sa = p.num_kb > 0 ? p.sa[row0 + j] : 0.0f;
-          finish(p, (row0 + j) * p.ldd + n, sum[j], cs, sa, bias);
+        for (int j = 0; j < kMySums; j += 4) {
+          const float4 sa = ld_shared_v4(my_scales + 4 * j);
+          const float v0 = value(p, sum[j], cs, sa.x, bias), v1 = value(p, sum[j + 1], cs, sa.y, bias);
+          const float v2 = value(p, sum[j + 2], cs, sa.z, bias), v3 = value(p, sum[j + 3], cs, sa.w, bias);
+          const float x = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
+          const float y = __shfl_xor_sync(0xffffffffu, odd ? v2 : v3, 1);
+          *reinterpret_cast<uint32_t*>(d) = odd ? pack_bf16(x, v1) : pack_bf16(v0, x);
+          d += 2 * p.ldd;
+          *reinterpret_cast<uint32_t*>(d) = odd ? pack_bf16(y, v3) : pack_bf16(v2, y);
+          d += 2 * p.ldd;
+        }
+      } else if (in) {
+#pragma unroll
+        for (int j = 0; j < kMySums; j += 4) {
+          const float4 sa = ld_shared_v4(my_scales + 4 * j);
+          const float s4[4] = {sa.x, sa.y, sa.z, sa.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (j + i < rows) finish(p, at + (j + i) * p.ldd, value(p, sum[j + i], cs, s4[i], bias));
         }
       }
+      __syncwarp();  // the scales have been read
     }
     if (CLUSTER) {
       sums();
       // This CTA's k-blocks are done, and with them every use of the ring: its
       // sums go there, a token's 256 values to a row.
-      int* out = reinterpret_cast<int*>(smem) + side * kMySums * WN + wrow;
+      uint32_t* out = reinterpret_cast<uint32_t*>(smem) + side * kMySums * WN + wrow;
 #pragma unroll
       for (int j = 0; j < kMySums; ++j) out[j * WN] = sum[j];
       __syncwarp();
@@ -432,11 +513,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int j1 = min((part + 1) * TM / split, p.M - row0);
         const uint32_t mine = smem_u32(smem) + static_cast<uint32_t>(tid & (WN - 1)) * 4;
         for (int j = part * TM / split + (tid >> 8); j < j1; j += 2) {
-          int total = 0;
+          uint32_t total = 0;
           for (int src = 0; src < split; ++src)
-            total += __float_as_int(ld_shared_cluster_f32(
+            total += __float_as_uint(ld_shared_cluster_f32(
                 mapa_shared(mine + static_cast<uint32_t>(j) * (WN * 4), static_cast<uint32_t>(src))));
-          finish(p, (row0 + j) * p.ldd + n, total, cs, p.sa[row0 + j], bias);
+          finish(p, (row0 + j) * p.ldd + n, value(p, total, cs, p.sa[row0 + j], bias));
         }
       }
       __syncwarp();
@@ -546,6 +627,7 @@ extern "C" gemm_status_t gemm_int8gemm(int64_t M, int64_t N, int64_t K, float al
   a.D = D;
   a.ldd = ldd;
   a.d_type = d_type;
+  a.d_pair = d_type == GEMM_OUT_BF16 && beta == 0.0f && !ops_misaligned(D, 4) && (M == 1 || ldd % 2 == 0);
   a.err = err;
   const int tm = M > 64 ? 128 : (M > 32 ? 64 : (M > 16 ? 32 : 16));
   std::unique_lock<std::mutex> lock;
