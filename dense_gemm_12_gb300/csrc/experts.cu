@@ -22,6 +22,10 @@ __device__ __forceinline__ uint32_t logit_key(float l) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+__device__ __forceinline__ float key_value(uint32_t key) {
+  return __uint_as_float((key & 0x80000000u) ? (key & 0x7fffffffu) : ~key);
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int s = 16; s > 0; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
@@ -43,13 +47,14 @@ struct RouteArgs {
   float* weight;
 };
 
-// One warp per row, its logits in registers (lane l holds l, l + 32, ...): the
-// largest is taken `top` times.
+// One warp per row, its logits in registers (lane l holds l, l + 32, ...).
 template <int V>
 __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__ RouteArgs a) {
   grid_dependency_wait();
   grid_launch_dependents();
-  const int lane = threadIdx.x & 31;
+  __shared__ uint2 lists[V >= 4 ? kWarps : 1][V >= 4 ? 32 : 1];  // candidates
+  uint2* const list = lists[V >= 4 ? threadIdx.x >> 5 : 0];
+  const uint32_t lane = threadIdx.x & 31;
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); row < a.rows;
        row += static_cast<int64_t>(gridDim.x) * kWarps) {
     float l[V];
@@ -73,33 +78,81 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__
       for (int v = 0; v < V; ++v) sum += expf(l[v] - m);
       sum = warp_sum(sum);
     }
-    // lane j keeps choice j
-    int mine = -1;
+    // Lane j's choice: which of the `top` it is (place), its index and its value.
+    int mine = -1, place = lane;
     float value = -INFINITY;
-    for (int j = 0; j < a.top; ++j) {
-      uint32_t best = 0u;
+    uint32_t candidates = 33;
+    if constexpr (V >= 4) {
+      // The `top`-th largest of the lanes' own largest is a bound from below on
+      // the `top` largest of all.  What reaches it -- hardly more than `top` --
+      // goes to one lane each, in the order of the indexes, and counts how many
+      // come before it: half the instructions of a search for each choice
+      // (16384 rows of 256, 8 choices: 15.4 us that way).
+      uint32_t largest = 0u, bound = 1u;
 #pragma unroll
-      for (int v = 0; v < V; ++v) best = max(best, key[v]);
-      best = __reduce_max_sync(0xffffffffu, best);
-      if (best == 0u) break;
-      int at = V * 32;
+      for (int v = 0; v < V; ++v) largest = max(largest, key[v]);
+      for (int j = 0; j < a.top; ++j) {
+        const uint32_t best = __reduce_max_sync(0xffffffffu, largest);
+        if (best == 0u) {
+          bound = 1u;  // fewer than `top` lanes: all that are not masked
+          break;
+        }
+        bound = best;
+        if (largest == best) largest = 0u;
+      }
+      candidates = 0;
 #pragma unroll
-      for (int v = V - 1; v >= 0; --v)
-        if (key[v] == best) at = v * 32 + lane;
-      at = __reduce_min_sync(0xffffffffu, at);
+      for (int v = 0; v < V; ++v) {
+        const bool in = key[v] >= bound;
+        const uint32_t with = __ballot_sync(0xffffffffu, in);
+        const uint32_t at = candidates + __popc(with & ((1u << lane) - 1u));
+        if (in && at < 32u) list[at] = make_uint2(key[v], v * 32 + lane);
+        candidates += __popc(with);
+      }
+      if (candidates <= 32u) {
+        __syncwarp();
+        const uint2 c = list[lane];
+        const uint32_t k = lane < candidates ? c.x : 0u;
+        place = 0;
+        for (uint32_t i = 0; i < candidates; ++i) {
+          const uint32_t other = __shfl_sync(0xffffffffu, k, i);
+          place += other > k || (other == k && i < lane) ? 1 : 0;
+        }
+        if (lane < candidates && place < a.top) {
+          mine = static_cast<int>(c.y);
+          value = key_value(k);
+        } else if (lane >= candidates) {
+          place = lane;  // choices that cannot be made
+        }
+        __syncwarp();
+      }
+    }
+    if (candidates > 32u) {
+      for (int j = 0; j < a.top; ++j) {
+        uint32_t best = 0u;
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (at == v * 32 + lane) key[v] = 0u;
-      if (lane == j) {
-        mine = at;
-        value = __uint_as_float((best & 0x80000000u) ? (best & 0x7fffffffu) : ~best);
+        for (int v = 0; v < V; ++v) best = max(best, key[v]);
+        best = __reduce_max_sync(0xffffffffu, best);
+        if (best == 0u) break;
+        int at = V * 32;
+#pragma unroll
+        for (int v = V - 1; v >= 0; --v)
+          if (key[v] == best) at = v * 32 + lane;
+        at = __reduce_min_sync(0xffffffffu, at);
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          if (at == v * 32 + lane) key[v] = 0u;
+        if (lane == j) {
+          mine = at;
+          value = key_value(best);
+        }
       }
     }
     float e = mine < 0 ? 0.0f : expf(value - m);
     if (a.normalize) sum = warp_sum(e);
-    if (lane < a.top) {
-      a.expert[row * a.top + lane] = mine;
-      a.weight[row * a.top + lane] = mine < 0 ? 0.0f : e / sum;
+    if (place < a.top) {
+      a.expert[row * a.top + place] = mine;
+      a.weight[row * a.top + place] = mine < 0 ? 0.0f : e / sum;
     }
   }
 }
@@ -188,6 +241,7 @@ constexpr int kSortAhead = 8;  // rounds whose ids are loaded together
 struct SortArgs {
   int64_t n;
   int experts;
+  int bits;        // of experts + 1, which stands for lanes without a pair
   int64_t chunk;   // pairs per CTA, a multiple of 32 * kSortWarps
   const int32_t* expert;
   int32_t* slot;
@@ -195,6 +249,19 @@ struct SortArgs {
   int32_t* source;
   int32_t* counts;  // [CTA][experts + 1]; nullptr: one CTA
 };
+
+// Lanes of the warp with this lane's key (below 2^bits; all lanes call it).  By
+// a vote per bit: the instruction that compares all lanes takes some 300 cycles
+// where their keys differ (131072 pairs over 256 experts: 14.3 us against 6.9).
+__device__ __forceinline__ uint32_t same_key(int key, int bits) {
+  uint32_t same = 0xffffffffu;
+  for (int b = 0; b < bits; ++b) {
+    const bool one = (key >> b) & 1;
+    const uint32_t v = __ballot_sync(0xffffffffu, one);
+    same &= one ? v : ~v;
+  }
+  return same;
+}
 
 __device__ __forceinline__ int sort_key(const SortArgs& a, int64_t i) {
   const int e = a.expert[i];
@@ -246,42 +313,65 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const __grid_c
   const int64_t lo = blockIdx.x * a.chunk + warp * part, hi = min(lo + part, a.n);
   const uint32_t below = (1u << lane) - 1u;
 
-  for (int64_t base = lo; base < hi; base += 32 * kSortAhead) {
-    int key[kSortAhead];
+  // A part of one batch of rounds keeps its keys, and each pair's place within
+  // the part, for the second half; a longer one goes through its pairs again.
+  int key[kSortAhead], rank[kSortAhead];
+  auto load = [&](int64_t base) {
 #pragma unroll
     for (int u = 0; u < kSortAhead; ++u) {
       const int64_t i = base + u * 32 + lane;
-      key[u] = i < hi ? sort_key(a, i) : -1;
+      key[u] = i < hi ? sort_key(a, i) : buckets;
     }
+  };
+  // Places of a batch from `mine`, which moves on.  A whole batch runs without
+  // branches between its rounds.
+  auto count = [&](int64_t base) {
+    const bool whole = base + 32 * kSortAhead <= hi;
 #pragma unroll
     for (int u = 0; u < kSortAhead; ++u) {
-      const uint32_t same = __match_any_sync(0xffffffffu, key[u]);
-      if (key[u] >= 0 && (same & below) == 0u) mine[key[u]] += __popc(same);
+      if (!whole && base + u * 32 >= hi) break;
+      const uint32_t same = same_key(key[u], a.bits);
+      const bool in = key[u] < buckets;
+      rank[u] = in ? mine[key[u]] + __popc(same & below) : 0;
+      __syncwarp();
+      if (in && (same & below) == 0u) mine[key[u]] += __popc(same);
       __syncwarp();
     }
+  };
+  // What other chunks have of bucket g: in all, and before this one.
+  auto others = [&](int g, int& total, int& before) {
+    total = before = 0;
+    if (g >= buckets || a.counts == nullptr) return;
+    const int chunks = static_cast<int>(gridDim.x), me = static_cast<int>(blockIdx.x);
+#pragma unroll 16
+    for (int b = 0; b < chunks; ++b) {
+      const int c = __ldcg(a.counts + static_cast<int64_t>(b) * buckets + g);
+      if (b < me) before += c;
+      total += c;
+    }
+  };
+  const bool once = part <= 32 * kSortAhead;
+  int total, before;
+  others(static_cast<int>(threadIdx.x), total, before);
+  for (int64_t base = lo; base < hi; base += 32 * kSortAhead) {
+    load(base);
+    count(base);
   }
   __syncthreads();
   // Over the warps, and (several CTAs) over the chunks: what comes before.
   // Then the experts' first rows, 512 at a time.
   for (int g0 = 0; g0 < buckets; g0 += kSortThreads) {
     const int g = g0 + static_cast<int>(threadIdx.x);
-    int total = 0, before = 0;
+    if (g0 > 0) others(g, total, before);
     if (g < buckets) {
+      int run = 0;
+#pragma unroll
       for (int w = 0; w < kSortWarps; ++w) {
         const int c = cnt[w * buckets + g];
-        cnt[w * buckets + g] = total;
-        total += c;
+        cnt[w * buckets + g] = run;
+        run += c;
       }
-      if (a.counts != nullptr) {
-        total = 0;
-        const int chunks = static_cast<int>(gridDim.x), me = static_cast<int>(blockIdx.x);
-#pragma unroll 16
-        for (int b = 0; b < chunks; ++b) {
-          const int c = __ldcg(a.counts + static_cast<int64_t>(b) * buckets + g);
-          if (b < me) before += c;
-          total += c;
-        }
-      }
+      if (a.counts == nullptr) total = run;
     }
     int sum = total;
 #pragma unroll
@@ -303,22 +393,16 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const __grid_c
   }
 
   for (int64_t base = lo; base < hi; base += 32 * kSortAhead) {
-    int key[kSortAhead];
-#pragma unroll
-    for (int u = 0; u < kSortAhead; ++u) {
-      const int64_t i = base + u * 32 + lane;
-      key[u] = i < hi ? sort_key(a, i) : -1;
+    if (!once) {
+      load(base);
+      count(base);
     }
 #pragma unroll
     for (int u = 0; u < kSortAhead; ++u) {
       const int64_t i = base + u * 32 + lane;
-      const uint32_t same = __match_any_sync(0xffffffffu, key[u]);
-      const bool in = key[u] >= 0;
-      const int at = in ? first[key[u]] + mine[key[u]] + __popc(same & below) : 0;
-      __syncwarp();
-      if (in && (same & below) == 0u) mine[key[u]] += __popc(same);
-      __syncwarp();
-      if (!in) continue;
+      if (i >= hi) continue;
+      // (`once`: the part's first place was not in `mine` yet)
+      const int at = first[key[u]] + rank[u] + (once ? mine[key[u]] : 0);
       const bool real = key[u] < a.experts;
       a.slot[i] = real ? at : -1;
       if (a.source != nullptr) a.source[at] = real ? static_cast<int32_t>(i) : -1;
@@ -600,7 +684,7 @@ struct LaunchRouteGrad {
 
 // Pairs of a launch with one CTA, and pairs per CTA of one with several (as
 // many CTAs as kSortMostCtas).
-constexpr int64_t kSortSingle = 8192;
+constexpr int64_t kSortSingle = 4096;
 constexpr int64_t kSortChunk = 4096;
 constexpr int64_t kSortMostCtas = 256;
 
@@ -717,6 +801,7 @@ gemm_status_t gemm_expert_sort(int64_t n, int64_t G, const int32_t* expert, int3
     if (st != GEMM_OK) return st;
     a.counts = reinterpret_cast<int32_t*>(ws);
   }
+  while ((1 << a.bits) < a.experts + 2) ++a.bits;
   const int64_t unit = 32 * kSortWarps;
   a.chunk = ((n + ctas - 1) / ctas + unit - 1) / unit * unit;
   const dim3 grid(static_cast<unsigned>(ctas));

@@ -37,24 +37,71 @@ __device__ __forceinline__ bool inside(int c, int i, int dim) {
   return VEC || c + 16 * i < dim;
 }
 
-// y of one chunk from its differences from the mean; 0 where nothing is.
+__device__ __forceinline__ void to_pairs(const float (&v)[8], uint64_t (&p)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) p[i] = f32x2(v[2 * i], v[2 * i + 1]);
+}
+__device__ __forceinline__ void from_pairs(const uint64_t (&p)[4], float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = f32x2_parts(p[i]);
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+__device__ __forceinline__ float both(uint64_t p) {
+  const float2 f = f32x2_parts(p);
+  return f.x + f.y;
+}
+
+// A chunk's differences from the mean, zero where nothing is, and what they and
+// their squares add to the sums.
+template <bool VEC>
+__device__ __forceinline__ void center(uint64_t (&h)[4], uint64_t minus_mean, int c, int dim, bool in,
+                                       uint64_t& sum, uint64_t& squares) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    h[i] = add2(h[i], minus_mean);
+    if (!VEC) {
+      const float2 f = f32x2_parts(h[i]);
+      h[i] = f32x2(inside<VEC>(c, 2 * i, dim) ? f.x : 0.0f, inside<VEC>(c, 2 * i + 1, dim) ? f.y : 0.0f);
+    }
+    if (!in) h[i] = 0ull;
+    sum = add2(sum, h[i]);
+    squares = fma2(h[i], h[i], squares);
+  }
+}
+
+// y of one chunk from its differences d from the mean; 0 where nothing is.
 template <bool VEC>
 __device__ __forceinline__ void affine(const float* weight, const float* bias, int c, int dim, bool in,
-                                       float rstd, float off, const float (&d)[8], float (&y)[8]) {
+                                       float rstd, float off, const uint64_t (&d)[4], float (&y)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) y[i] = 0.0f;
   if (!in) return;
-  float w[8], b[8];
+  uint64_t p[4];
+  const float o = -off * rstd;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    w[i] = 1.0f;
-    b[i] = 0.0f;
+  for (int i = 0; i < 4; ++i) p[i] = fma2(d[i], f32x2(rstd, rstd), f32x2(o, o));
+  float v[8];
+  uint64_t q[4];
+  if (weight != nullptr) {
+    load_weight<VEC>(weight, c, dim, v);
+    to_pairs(v, q);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = mul2(p[i], q[i]);
   }
-  if (weight != nullptr) load_weight<VEC>(weight, c, dim, w);
-  if (bias != nullptr) load_weight<VEC>(bias, c, dim, b);
+  if (bias != nullptr) {
+    load_weight<VEC>(bias, c, dim, v);
+    to_pairs(v, q);
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (inside<VEC>(c, i, dim)) y[i] = fmaf((d[i] - off) * rstd, w[i], b[i]);
+    for (int i = 0; i < 4; ++i) p[i] = add2(p[i], q[i]);
+  }
+  from_pairs(p, y);
+  if (!VEC) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = inside<VEC>(c, i, dim) ? y[i] : 0.0f;
+  }
 }
 
 __device__ __forceinline__ float chunk_amax(const float (&y)[8]) {
@@ -101,7 +148,7 @@ __global__ void __launch_bounds__(kMaxThreads, RING ? 2 : 1)
   const int per_cta = blockDim.x / tpr;
   const int chunks = VEC ? a.dim / 8 : (a.dim + kFp8Block - 1) / kFp8Block * 16;
   const float inv_dim = 1.0f / static_cast<float>(a.dim);
-  uint32_t turn_mean = 0, turn_var = 0, turn_max = 0;
+  uint32_t turn = 0;  // of all three sums
   const bool s8 = a.p.q != nullptr && a.p.q_type == GEMM_OUT_S8;
   const bool f8 = a.p.q != nullptr && !s8;
   // given the sums of the differences from `mean` and of their squares
@@ -117,6 +164,8 @@ __global__ void __launch_bounds__(kMaxThreads, RING ? 2 : 1)
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * per_cta + threadIdx.x / tpr; row < a.rows;
        row += static_cast<int64_t>(gridDim.x) * per_cta) {
     float sum = 0.0f, off, rstd;
+    uint32_t turn_mean = turn, turn_var = turn, turn_max = turn;
+    ++turn;
     if constexpr (C > 0) {
       Inputs<VEC, TX, TR> raw[C];
       bool in[C];
@@ -132,15 +181,18 @@ __global__ void __launch_bounds__(kMaxThreads, RING ? 2 : 1)
           raw[k].load(a, row, c, in[k]);
         }
       }
-      float h[C][8];
+      uint64_t h[C][4], total = 0ull;
 #pragma unroll
       for (int k = 0; k < C; ++k) {
-        raw[k].sum(a, h[k]);  // zeros where nothing is
+        float v[8];
+        raw[k].sum(a, v);  // zeros where nothing is
+        to_pairs(v, h[k]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum += h[k][i];
+        for (int i = 0; i < 4; ++i) total = add2(total, h[k][i]);
         if (a.p.h != nullptr && in[k])
-          store8<VEC>(a.p.h, a.p.h_type, row * a.p.ldh, chunk_col<VEC>(k * tpr + t), a.dim, h[k]);
+          store8<VEC>(a.p.h, a.p.h_type, row * a.p.ldh, chunk_col<VEC>(k * tpr + t), a.dim, v);
       }
+      sum = both(total);
       const float mean = row_sum(sum, tpr, red_mean, turn_mean) * inv_dim;
       if constexpr (RING) {
         // every thread has read the stage (row_sum's barrier): the next row
@@ -152,20 +204,12 @@ __global__ void __launch_bounds__(kMaxThreads, RING ? 2 : 1)
           parity ^= 1u;
         }
       }
-      float2 sums = make_float2(0.0f, 0.0f);
+      uint64_t left = 0ull, squares = 0ull;
 #pragma unroll
-      for (int k = 0; k < C; ++k) {
-        const int c = chunk_col<VEC>(k * tpr + t);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          h[k][i] -= mean;
-          if (in[k] && inside<VEC>(c, i, a.dim)) {
-            sums.x += h[k][i];
-            sums.y = fmaf(h[k][i], h[k][i], sums.y);
-          }
-        }
-      }
-      statistics(row, mean, row_sums(sums, tpr, red_var, turn_var), off, rstd);
+      for (int k = 0; k < C; ++k)
+        center<VEC>(h[k], f32x2(-mean, -mean), chunk_col<VEC>(k * tpr + t), a.dim, in[k], left, squares);
+      statistics(row, mean, row_sums(make_float2(both(left), both(squares)), tpr, red_var, turn_var), off,
+                 rstd);
       float amax = 0.0f;
 #pragma unroll
       for (int k = 0; k < C; ++k) {
@@ -176,16 +220,18 @@ __global__ void __launch_bounds__(kMaxThreads, RING ? 2 : 1)
         if (f8) write_fp8<VEC>(a.p.q, a.p.ldq, a.p.scales, a.p.ld_scales, row, c, a.dim, in[k], y);
         if (s8) {
           amax = fmaxf(amax, chunk_amax(y));
-#pragma unroll
-          for (int i = 0; i < 8; ++i) h[k][i] = y[i];
+          to_pairs(y, h[k]);
         }
       }
       if (!s8) continue;
       amax = row_max(amax, tpr, red_max, turn_max);
       const float f = s8_factor(amax);
 #pragma unroll
-      for (int k = 0; k < C; ++k)
-        if (in[k]) write_s8<VEC>(a.p.q, a.p.ldq, row, chunk_col<VEC>(k * tpr + t), a.dim, f, h[k]);
+      for (int k = 0; k < C; ++k) {
+        float y[8];
+        from_pairs(h[k], y);
+        if (in[k]) write_s8<VEC>(a.p.q, a.p.ldq, row, chunk_col<VEC>(k * tpr + t), a.dim, f, y);
+      }
       if (t == 0) a.p.scales[row] = s8_scale(amax);
     } else {
       auto load = [&](int c, bool in, float (&h)[8]) {
@@ -201,30 +247,32 @@ __global__ void __launch_bounds__(kMaxThreads, RING ? 2 : 1)
         for (int i = 0; i < 8; ++i) sum += h[i];
       }
       const float mean = row_sum(sum, tpr, red_mean, turn_mean) * inv_dim;
-      float2 sums = make_float2(0.0f, 0.0f);
-      for (int chunk = t; chunk < chunks; chunk += tpr) {
-        const int c = chunk_col<VEC>(chunk);
+      const uint64_t minus_mean = f32x2(-mean, -mean);
+      uint64_t left = 0ull, squares = 0ull;
+      // the differences from the mean of one chunk
+      auto differences = [&](int c, bool in, uint64_t (&d)[4], uint64_t& s, uint64_t& ss) {
         float h[8];
-        load(c, c < a.dim, h);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (c < a.dim && inside<VEC>(c, i, a.dim)) {
-            const float d = h[i] - mean;
-            sums.x += d;
-            sums.y = fmaf(d, d, sums.y);
-          }
+        load(c, in, h);
+        to_pairs(h, d);
+        center<VEC>(d, minus_mean, c, a.dim, in, s, ss);
+      };
+      for (int chunk = t; chunk < chunks; chunk += tpr) {
+        uint64_t d[4];
+        const int c = chunk_col<VEC>(chunk);
+        differences(c, c < a.dim, d, left, squares);
       }
-      statistics(row, mean, row_sums(sums, tpr, red_var, turn_var), off, rstd);
+      statistics(row, mean, row_sums(make_float2(both(left), both(squares)), tpr, red_var, turn_var), off,
+                 rstd);
+      uint64_t unused = 0ull;
       float f = 0.0f;
       if (s8) {
         float amax = 0.0f;
         for (int chunk = t; chunk < chunks; chunk += tpr) {
           const int c = chunk_col<VEC>(chunk);
-          float h[8], y[8];
-          load(c, c < a.dim, h);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) h[i] -= mean;
-          affine<VEC>(a.p.weight, a.p.bias, c, a.dim, c < a.dim, rstd, off, h, y);
+          uint64_t d[4];
+          float y[8];
+          differences(c, c < a.dim, d, unused, unused);
+          affine<VEC>(a.p.weight, a.p.bias, c, a.dim, c < a.dim, rstd, off, d, y);
           amax = fmaxf(amax, chunk_amax(y));
         }
         amax = row_max(amax, tpr, red_max, turn_max);
@@ -238,9 +286,10 @@ __global__ void __launch_bounds__(kMaxThreads, RING ? 2 : 1)
         float h[8], y[8];
         load(c, in, h);
         if (in && a.p.h != nullptr) store8<VEC>(a.p.h, a.p.h_type, row * a.p.ldh, c, a.dim, h);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] -= mean;
-        affine<VEC>(a.p.weight, a.p.bias, c, a.dim, in, rstd, off, h, y);
+        uint64_t d[4];
+        to_pairs(h, d);
+        center<VEC>(d, minus_mean, c, a.dim, in, unused, unused);
+        affine<VEC>(a.p.weight, a.p.bias, c, a.dim, in, rstd, off, d, y);
         if (in && a.p.y != nullptr) store8<VEC>(a.p.y, a.p.y_type, row * a.p.ldy, c, a.dim, y);
         if (f8) write_fp8<VEC>(a.p.q, a.p.ldq, a.p.scales, a.p.ld_scales, row, c, a.dim, in, y);
         if (s8 && in) write_s8<VEC>(a.p.q, a.p.ldq, row, c, a.dim, f, y);
@@ -309,21 +358,43 @@ __global__ void __launch_bounds__(ln_grad_threads(RING, C, TD, TH), 1)
   const int chunks = VEC ? a.dim / 8 : (a.dim + kFp8Block - 1) / kFp8Block * 16;
   const float inv_dim = 1.0f / static_cast<float>(a.dim);
   constexpr int CR = C > 0 ? C : 1;
-  float dw[CR][8], db[CR][8];
+  uint64_t dw[CR][4], db[CR][4];
 #pragma unroll
   for (int k = 0; k < CR; ++k)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dw[k][i] = db[k][i] = 0.0f;
+    for (int i = 0; i < 4; ++i) dw[k][i] = db[k][i] = 0ull;
   uint32_t turn = 0;
   const int64_t row_step = static_cast<int64_t>(gridDim.x) * per_cta;
   int64_t row = static_cast<int64_t>(blockIdx.x) * per_cta + sub;
-  auto weight = [&](int c, float (&w)[8]) {
-    if (a.p.weight != nullptr) {
-      load_weight<VEC>(a.p.weight, c, a.dim, w);
-    } else {
+  // dy times the weight
+  auto weighted = [&](int c, uint64_t (&g)[4]) {
+    if (a.p.weight == nullptr) return;
+    float v[8];
+    uint64_t w[4];
+    load_weight<VEC>(a.p.weight, c, a.dim, v);
+    to_pairs(v, w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = 1.0f;
+    for (int i = 0; i < 4; ++i) g[i] = mul2(g[i], w[i]);
+  };
+  // (h - mean) * rstd, zero past the row's end; g is zero there
+  auto normal = [&](int c, float rstd, float mean, uint64_t (&xh)[4]) {
+    const uint64_t m = f32x2(-mean, -mean), s = f32x2(rstd, rstd);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      xh[i] = mul2(add2(xh[i], m), s);
+      if (!VEC) {
+        const float2 f = f32x2_parts(xh[i]);
+        xh[i] = f32x2(inside<VEC>(c, 2 * i, a.dim) ? f.x : 0.0f, inside<VEC>(c, 2 * i + 1, a.dim) ? f.y : 0.0f);
+      }
     }
+  };
+  // the gradient of h: r + rstd * (g - mean_g - xh * mean_x)
+  auto gradient = [&](const uint64_t (&g)[4], const uint64_t (&xh)[4], float rstd, float2 means, float (&r)[8]) {
+    float gv[8], xv[8];
+    from_pairs(g, gv);
+    from_pairs(xh, xv);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = fmaf(rstd, fmaf(-xv[i], means.y, gv[i] - means.x), r[i]);
   };
   float next_rstd = row < a.rows ? a.p.rstd[row] : 0.0f;  // loaded a row ahead
   float next_mean = row < a.rows ? a.p.mean[row] : 0.0f;
@@ -333,7 +404,7 @@ __global__ void __launch_bounds__(ln_grad_threads(RING, C, TD, TH), 1)
       next_rstd = a.p.rstd[row + row_step];
       next_mean = a.p.mean[row + row_step];
     }
-    float2 sums = make_float2(0.0f, 0.0f);
+    uint64_t sum_g = 0ull, sum_x = 0ull;  // of g, and of g xh
     if constexpr (C > 0) {
       Raw8<TD> dy[C];
       Raw8<TH> rh[C];
@@ -355,31 +426,38 @@ __global__ void __launch_bounds__(ln_grad_threads(RING, C, TD, TH), 1)
         const int chunk = k * tpr + t;
         return chunk < chunks && chunk_col<VEC>(chunk) < a.dim;
       };
-      if (!RING) {
+      // the registers hold both inputs but for two chunks loaded one by one
+      constexpr bool kHeld = !RING && (VEC || C == 1);
+      if (kHeld) {
 #pragma unroll
         for (int k = 0; k < C; ++k) get(k, chunk_col<VEC>(k * tpr + t), has(k));
       }
 #pragma unroll
       for (int k = 0; k < C; ++k) {
         const int c = chunk_col<VEC>(k * tpr + t);
-        if (RING) get(k, c, has(k));
+        if (!kHeld) get(k, c, has(k));
         if (!has(k)) continue;
-        float w[8], g[8], xh[8];
-        weight(c, w);
-        widen8<VEC, TD>(dy[k], a.p.dy_type, g);  // zeros past the row's end
-        widen8<VEC, TH>(rh[k], a.p.h_type, xh);
+        float v[8];
+        uint64_t g[4], xh[4];
+        widen8<VEC, TD>(dy[k], a.p.dy_type, v);  // zeros past the row's end
+        to_pairs(v, g);
+        widen8<VEC, TH>(rh[k], a.p.h_type, v);
+        to_pairs(v, xh);
+        normal(c, rstd, mean, xh);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          xh[i] = (xh[i] - mean) * rstd;
-          db[k][i] += g[i];
-          dw[k][i] = fmaf(g[i], xh[i], dw[k][i]);
-          g[i] *= w[i];
-          sums.x += inside<VEC>(c, i, a.dim) ? g[i] : 0.0f;
-          sums.y = inside<VEC>(c, i, a.dim) ? fmaf(g[i], xh[i], sums.y) : sums.y;
+        for (int i = 0; i < 4; ++i) {
+          db[k][i] = add2(db[k][i], g[i]);
+          dw[k][i] = fma2(g[i], xh[i], dw[k][i]);
+        }
+        weighted(c, g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          sum_g = add2(sum_g, g[i]);
+          sum_x = fma2(g[i], xh[i], sum_x);
         }
       }
-      sums = row_sums(sums, tpr, red, turn);
-      const float mean_g = sums.x * inv_dim, mean_x = sums.y * inv_dim;
+      float2 means = row_sums(make_float2(both(sum_g), both(sum_x)), tpr, red, turn);
+      means = make_float2(means.x * inv_dim, means.y * inv_dim);
       if (RING && threadIdx.x == 0 && row >= static_cast<int64_t>(gridDim.x)) {
         // every thread has left the previous row (row_sums' barrier)
         const int64_t next = row + static_cast<int64_t>(a.ring.stages - 1) * gridDim.x;
@@ -390,8 +468,8 @@ __global__ void __launch_bounds__(ln_grad_threads(RING, C, TD, TH), 1)
       for (int k = 0; k < C; ++k) {
         const int c = chunk_col<VEC>(k * tpr + t);
         if (!has(k)) continue;
-        if (RING) get(k, c, true);
-        float w[8], g[8], xh[8], r[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+        if (!kHeld) get(k, c, true);
+        float r[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
         if (a.p.residual_grad != nullptr) {
           const int type = a.p.residual_grad_type;
           if constexpr (RING) {
@@ -405,12 +483,15 @@ __global__ void __launch_bounds__(ln_grad_threads(RING, C, TD, TH), 1)
                                                        a.dim, true), type, r);
           }
         }
-        weight(c, w);
-        widen8<VEC, TD>(dy[k], a.p.dy_type, g);
-        widen8<VEC, TH>(rh[k], a.p.h_type, xh);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          r[i] = fmaf(rstd, fmaf(g[i], w[i], -mean_g) - (xh[i] - mean) * rstd * mean_x, r[i]);
+        float v[8];
+        uint64_t g[4], xh[4];
+        widen8<VEC, TD>(dy[k], a.p.dy_type, v);
+        to_pairs(v, g);
+        weighted(c, g);
+        widen8<VEC, TH>(rh[k], a.p.h_type, v);
+        to_pairs(v, xh);
+        normal(c, rstd, mean, xh);
+        gradient(g, xh, rstd, means, r);
         store8<VEC>(a.p.dh, a.p.dh_type, row * a.p.lddh, c, a.dim, r);
       }
       if (RING && ++slot == a.ring.stages) {
@@ -418,35 +499,36 @@ __global__ void __launch_bounds__(ln_grad_threads(RING, C, TD, TH), 1)
         parity ^= 1u;
       }
     } else {
-      float mean_g = 0.0f, mean_x = 0.0f;
+      float2 means = make_float2(0.0f, 0.0f);
       for (int half = 0; half < 2; ++half) {
         if (half == 1) {
-          sums = row_sums(sums, tpr, red, turn);
-          mean_g = sums.x * inv_dim;
-          mean_x = sums.y * inv_dim;
+          means = row_sums(make_float2(both(sum_g), both(sum_x)), tpr, red, turn);
+          means = make_float2(means.x * inv_dim, means.y * inv_dim);
         }
         for (int chunk = t; chunk < chunks; chunk += tpr) {
           const int c = chunk_col<VEC>(chunk);
           if (c >= a.dim) continue;
-          float w[8], g[8], xh[8], r[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+          float v[8], r[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+          uint64_t g[4], xh[4];
           const Raw8<TD> dy = load8<VEC, TD>(a.p.dy, a.p.dy_type, row * a.p.lddy, c, a.dim, true);
           const Raw8<TH> rh = load8<VEC, TH>(a.p.h, a.p.h_type, row * a.p.ldh, c, a.dim, true);
           if (half == 1 && a.p.residual_grad != nullptr)
             widen8<VEC, kAnyType>(load8<VEC, kAnyType>(a.p.residual_grad, a.p.residual_grad_type,
                                                        row * a.p.ldrg, c, a.dim, true),
                                   a.p.residual_grad_type, r);
-          weight(c, w);
-          widen8<VEC, TD>(dy, a.p.dy_type, g);
-          widen8<VEC, TH>(rh, a.p.h_type, xh);
+          widen8<VEC, TD>(dy, a.p.dy_type, v);
+          to_pairs(v, g);
+          weighted(c, g);
+          widen8<VEC, TH>(rh, a.p.h_type, v);
+          to_pairs(v, xh);
+          normal(c, rstd, mean, xh);
+          if (half == 1) {
+            gradient(g, xh, rstd, means, r);
+          } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            xh[i] = (xh[i] - mean) * rstd;
-            g[i] *= w[i];
-            if (half == 1) {
-              r[i] = fmaf(rstd, g[i] - mean_g - xh[i] * mean_x, r[i]);
-            } else if (inside<VEC>(c, i, a.dim)) {
-              sums.x += g[i];
-              sums.y = fmaf(g[i], xh[i], sums.y);
+            for (int i = 0; i < 4; ++i) {
+              sum_g = add2(sum_g, g[i]);
+              sum_x = fma2(g[i], xh[i], sum_x);
             }
           }
           if (half == 1) store8<VEC>(a.p.dh, a.p.dh_type, row * a.p.lddh, c, a.dim, r);
@@ -465,12 +547,15 @@ __global__ void __launch_bounds__(ln_grad_threads(RING, C, TD, TH), 1)
     const int c = chunk_col<VEC>(chunk);
     if (chunk >= chunks || c >= a.dim) continue;
     float* to = per_cta == 1 ? out : sums + static_cast<int64_t>(sub) * 2 * a.dim;
+    float w[8], b[8];
+    from_pairs(dw[k], w);
+    from_pairs(db[k], b);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int col = VEC ? c + i : c + 16 * i;
       if (col < a.dim) {
-        to[col] = dw[k][i];
-        to[a.dim + col] = db[k][i];
+        to[col] = w[i];
+        to[a.dim + col] = b[i];
       }
     }
   }

@@ -871,7 +871,7 @@ gemm_status_t gemm_expert_route_backward(int64_t rows, int64_t G, int64_t top, c
  * order: offsets (G + 1 values, for the grouped products) are the experts'
  * first rows, slot[i] is pair i's row, and source (NULL, or n values) the other
  * way round: source[slot[i]] = i.  Pairs whose id is outside 0 .. G - 1 have no
- * row: slot -1; source is -1 from row offsets[G] on.  More than 8192 pairs
+ * row: slot -1; source is -1 from row offsets[G] on.  More than 4096 pairs
  * need counters in the stream's scratch (see Memory).
  */
 gemm_status_t gemm_expert_sort(int64_t n, int64_t G, const int32_t *expert, int32_t *slot,
