@@ -10,8 +10,13 @@
 //     dh = s (g - mean_j g_j - xh mean_j(g_j xh_j)) + dr
 //     dw = sum_rows dy xh        db = sum_rows dy
 //
-// Bound by memory: as in norm.cu, a row is read once, through the ring where
-// there are many, kept in registers over its sums, and written once.
+// Bound by memory: a row is read once, kept in registers over its sums, and
+// written once.  Many rows come through rings in shared memory as in norm.cu,
+// but a CTA fills an SM: up to eight groups of threads, each with a row and a
+// ring of its own, around one copy of the weight and the bias.  Read anew for
+// each row those are as many bytes as the row itself, and with shared memory
+// full of rows they do not stay in L1 (8192 rows of 8192 in bf16: 104 us with a
+// group to a CTA and weights from L2).
 //
 // The squares are summed about the mean, never as mean(h^2) - m^2, which loses
 // everything when the mean is large.  The mean itself is only known to fp32's
@@ -23,6 +28,14 @@
 namespace g12 {
 namespace {
 
+constexpr int kMaxRings = 8;      // groups of a CTA
+constexpr int kLnCtaBytes = 6144;  // shared memory of a CTA besides weights and rings
+
+struct LnRings {
+  uint64_t full[kMaxRings * kMaxStages];
+  int abort_flag;
+};
+
 struct LnArgs {
   int64_t rows;
   int dim;
@@ -30,6 +43,64 @@ struct LnArgs {
   RingArgs ring;
   gemm_layernorm_t p;
 };
+
+// Sums (or largest) of N values over the tpr threads of a group.  red: two rows
+// of a value per warp, used in turn, one call a row.
+template <int N, bool MAX = false>
+__device__ __forceinline__ void over_row(float (&v)[N], int tpr, int group, float (*red)[16][N], uint32_t turn) {
+  auto join = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = join(v[i], __shfl_xor_sync(0xffffffffu, v[i], s));
+  if (tpr == 32) return;
+  const int lane = threadIdx.x & 31, warps = tpr >> 5;
+  float(*mine)[N] = red[turn & 1u];
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) mine[(threadIdx.x >> 5) % warps][i] = v[i];
+  }
+  asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(tpr) : "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = lane < warps ? mine[lane & 15][i] : 0.0f;  // (magnitudes: 0 too)
+#pragma unroll
+  for (int s = 8; s > 0; s >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = join(v[i], __shfl_xor_sync(0xffffffffu, v[i], s));
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, v[i], 0);
+}
+
+// After a wait ran out: a group's copies in flight land before the CTA leaves.
+__device__ __forceinline__ void drain_ring(uint64_t* full, int stages, int slot, uint32_t parity) {
+  for (int i = 0; i < stages; ++i) {
+    mbar_drain_wait(&full[slot], parity);
+    if (++slot == stages) {
+      slot = 0;
+      parity ^= 1u;
+    }
+  }
+}
+
+// The weight, and the bias behind it, to shared memory; all threads of the CTA.
+__device__ __forceinline__ void stage_weights(float* to, const float* weight, const float* bias, int dim,
+                                              bool with_bias) {
+  for (int i = threadIdx.x * 4; i < dim; i += blockDim.x * 4) {
+    *reinterpret_cast<float4*>(to + i) = weight != nullptr ? __ldg(reinterpret_cast<const float4*>(weight + i))
+                                                           : make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+    if (with_bias)
+      *reinterpret_cast<float4*>(to + dim + i) =
+          bias != nullptr ? __ldg(reinterpret_cast<const float4*>(bias + i)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  }
+}
+// Eight of them from there.
+__device__ __forceinline__ void staged_pairs(const float* from, uint64_t (&p)[4]) {
+  const float4 a = *reinterpret_cast<const float4*>(from), b = *reinterpret_cast<const float4*>(from + 4);
+  p[0] = f32x2(a.x, a.y);
+  p[1] = f32x2(a.z, a.w);
+  p[2] = f32x2(b.x, b.y);
+  p[3] = f32x2(b.z, b.w);
+}
 
 // Elements of chunk column c, and (not VEC) 16 i further, inside the row.
 template <bool VEC>
@@ -73,34 +144,48 @@ __device__ __forceinline__ void center(uint64_t (&h)[4], uint64_t minus_mean, in
 }
 
 // y of one chunk from its differences d from the mean; 0 where nothing is.
-template <bool VEC>
+// STAGED: weight and bias are in shared memory, one behind the other.
+template <bool VEC, bool STAGED = false>
 __device__ __forceinline__ void affine(const float* weight, const float* bias, int c, int dim, bool in,
                                        float rstd, float off, const uint64_t (&d)[4], float (&y)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) y[i] = 0.0f;
   if (!in) return;
-  uint64_t p[4];
   const float o = -off * rstd;
+  if constexpr (STAGED) {  // four elements at a time: registers
 #pragma unroll
-  for (int i = 0; i < 4; ++i) p[i] = fma2(d[i], f32x2(rstd, rstd), f32x2(o, o));
-  float v[8];
-  uint64_t q[4];
-  if (weight != nullptr) {
-    load_weight<VEC>(weight, c, dim, v);
-    to_pairs(v, q);
+    for (int i = 0; i < 2; ++i) {
+      const float4 w = *reinterpret_cast<const float4*>(weight + c + 4 * i);
+      const float4 b = *reinterpret_cast<const float4*>(weight + dim + c + 4 * i);
+      const float2 d0 = f32x2_parts(d[2 * i]), d1 = f32x2_parts(d[2 * i + 1]);
+      y[4 * i] = fmaf(fmaf(d0.x, rstd, o), w.x, b.x);
+      y[4 * i + 1] = fmaf(fmaf(d0.y, rstd, o), w.y, b.y);
+      y[4 * i + 2] = fmaf(fmaf(d1.x, rstd, o), w.z, b.z);
+      y[4 * i + 3] = fmaf(fmaf(d1.y, rstd, o), w.w, b.w);
+    }
+  } else {
+    uint64_t p[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = mul2(p[i], q[i]);
-  }
-  if (bias != nullptr) {
-    load_weight<VEC>(bias, c, dim, v);
-    to_pairs(v, q);
+    for (int i = 0; i < 4; ++i) p[i] = fma2(d[i], f32x2(rstd, rstd), f32x2(o, o));
+    float v[8];
+    uint64_t q[4];
+    if (weight != nullptr) {
+      load_weight<VEC>(weight, c, dim, v);
+      to_pairs(v, q);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = add2(p[i], q[i]);
-  }
-  from_pairs(p, y);
-  if (!VEC) {
+      for (int i = 0; i < 4; ++i) p[i] = mul2(p[i], q[i]);
+    }
+    if (bias != nullptr) {
+      load_weight<VEC>(bias, c, dim, v);
+      to_pairs(v, q);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = inside<VEC>(c, i, dim) ? y[i] : 0.0f;
+      for (int i = 0; i < 4; ++i) p[i] = add2(p[i], q[i]);
+    }
+    from_pairs(p, y);
+    if (!VEC) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = inside<VEC>(c, i, dim) ? y[i] : 0.0f;
+    }
   }
 }
 
@@ -114,90 +199,119 @@ __device__ __forceinline__ float chunk_amax(const float (&y)[8]) {
 // C > 0: a row in registers.  C == 0: rows longer than that are read three
 // times, and once more where their largest value is needed before the first is
 // written.  Nothing of a row is written before its last read.
-template <int C, bool VEC, int TX, int TR, bool RING = false>
-__global__ void __launch_bounds__(kMaxThreads, RING ? 2 : 1)
+// Q: the 8-bit output's type, kNoQ for none, or kAnyQ for one known at run time.
+constexpr int kNoQ = 0, kAnyQ = -1;
+
+template <int C, bool VEC, int TX, int TR, bool RING = false, int Q = kAnyQ>
+__global__ void __launch_bounds__(RING ? 1024 : kMaxThreads, 1)
     layernorm_kernel(const __grid_constant__ LnArgs a) {
-  __shared__ float red_mean[2][16], red_max[2][16];
-  __shared__ float2 red_var[2][16];
-  __shared__ Ring ring;
+  __shared__ float red_mean[kMaxRings][2][16][1], red_max[kMaxRings][2][16][1];
+  __shared__ float red_var[kMaxRings][2][16][2];
+  __shared__ LnRings ring;
   extern __shared__ uint4 dyn_smem[];
-  uint8_t* const stages = reinterpret_cast<uint8_t*>(dyn_smem);
+  float* const weights = reinterpret_cast<float*>(dyn_smem);  // RING: and the bias, then the rings
+  const int tpr = a.tpr;
+  const int t = threadIdx.x % tpr, group = threadIdx.x / tpr;
+  const int per_cta = blockDim.x / tpr;
+  const uint32_t rows = static_cast<uint32_t>(a.rows), row_step = gridDim.x * per_cta;  // below 2^31
+  const uint32_t row0 = blockIdx.x * per_cta + group;
   const int stage_bytes = RING ? a.dim * (type_bytes(TX) + (TR < 0 ? 0 : type_bytes(TR))) : 0;
-  auto fetch = [&](int64_t row, int s) {
-    uint8_t* to = stages + s * stage_bytes;
-    mbar_arrive_expect_tx(&ring.full[s], static_cast<uint32_t>(stage_bytes));
+  // offsets of the group's ring and barriers: short, for the registers
+  const int ring_off = RING ? 8 * a.dim + group * a.ring.stages * stage_bytes : 0;
+  const int bar_off = RING ? group * kMaxStages : 0;
+  auto stage = [&](int s) { return reinterpret_cast<uint8_t*>(dyn_smem) + ring_off + s * stage_bytes; };
+  // a group's first thread: copies `row` into stage s
+  auto fetch = [&](uint32_t at, int s) {
+    const int64_t row = at;
+    uint8_t* to = stage(s);
+    uint64_t* bar = &ring.full[bar_off + s];
+    mbar_arrive_expect_tx(bar, static_cast<uint32_t>(stage_bytes));
     bulk_load(to, static_cast<const uint8_t*>(a.p.x) + row * a.p.ldx * type_bytes(TX),
-              static_cast<uint32_t>(a.dim * type_bytes(TX)), &ring.full[s]);
+              static_cast<uint32_t>(a.dim * type_bytes(TX)), bar);
     if constexpr (TR >= 0)
       bulk_load(to + a.dim * type_bytes(TX),
                 static_cast<const uint8_t*>(a.p.residual) + row * a.p.ldr * type_bytes(TR),
-                static_cast<uint32_t>(a.dim * type_bytes(TR)), &ring.full[s]);
+                static_cast<uint32_t>(a.dim * type_bytes(TR)), bar);
   };
-  if (RING) ring_init(ring, a.ring.stages);
+  if (RING) {
+    if (t == 0) {
+      for (int s = 0; s < a.ring.stages; ++s) mbar_init(&ring.full[bar_off + s], 1);
+      if (group == 0) ring.abort_flag = 0;
+      fence_barrier_init();
+    }
+    __syncthreads();
+  }
   grid_dependency_wait();
   grid_launch_dependents();
-  if (RING && threadIdx.x == 0)
-    for (int s = 0; s < a.ring.stages; ++s) {
-      const int64_t row = blockIdx.x + static_cast<int64_t>(s) * gridDim.x;
-      if (row < a.rows) fetch(row, s);
-    }
+  if (RING) {
+    if (t == 0)
+      for (int s = 0; s < a.ring.stages; ++s)
+        if (row0 + s * row_step < rows) fetch(row0 + s * row_step, s);
+    stage_weights(weights, a.p.weight, a.p.bias, a.dim, true);
+    __syncthreads();
+  }
   int slot = 0;
   uint32_t parity = 0;
-  const int tpr = a.tpr;
-  const int t = threadIdx.x % tpr;
-  const int per_cta = blockDim.x / tpr;
   const int chunks = VEC ? a.dim / 8 : (a.dim + kFp8Block - 1) / kFp8Block * 16;
   const float inv_dim = 1.0f / static_cast<float>(a.dim);
   uint32_t turn = 0;  // of all three sums
-  const bool s8 = a.p.q != nullptr && a.p.q_type == GEMM_OUT_S8;
-  const bool f8 = a.p.q != nullptr && !s8;
-  // given the sums of the differences from `mean` and of their squares
-  auto statistics = [&](int64_t row, float mean, float2 sums, float& off, float& rstd) {
-    off = sums.x * inv_dim;
-    const float var = fmaf(sums.y, inv_dim, -off * off);
+  const bool s8 = Q == kAnyQ ? a.p.q != nullptr && a.p.q_type == GEMM_OUT_S8 : Q == GEMM_OUT_S8;
+  const bool f8 = Q == kAnyQ ? a.p.q != nullptr && !s8 : Q == GEMM_OUT_F8E4M3;
+  // given a thread's sums of the differences from `mean` and of their squares
+  auto statistics = [&](int64_t row, float mean, float left, float squares, float& off, float& rstd) {
+    float v[2] = {left, squares};
+    over_row<2>(v, tpr, group, red_var[RING ? group : 0], turn);
+    off = v[0] * inv_dim;
+    const float var = fmaf(v[1], inv_dim, -off * off);
     rstd = rsqrtf((var < 0.0f ? 0.0f : var) + a.p.eps);  // (NaN stays)
     if (t == 0) {
       if (a.p.mean != nullptr) a.p.mean[row] = mean + off;
       if (a.p.rstd != nullptr) a.p.rstd[row] = rstd;
     }
   };
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * per_cta + threadIdx.x / tpr; row < a.rows;
-       row += static_cast<int64_t>(gridDim.x) * per_cta) {
+  for (uint32_t at = row0; at < rows; at += row_step, ++turn) {
+    const int64_t row = at;
     float sum = 0.0f, off, rstd;
-    uint32_t turn_mean = turn, turn_var = turn, turn_max = turn;
-    ++turn;
+    auto mean_of = [&]() {
+      float v[1] = {sum};
+      over_row<1>(v, tpr, group, red_mean[RING ? group : 0], turn);
+      return v[0] * inv_dim;
+    };
+    auto largest_of = [&](float amax) {
+      float v[1] = {amax};
+      over_row<1, true>(v, tpr, group, red_max[RING ? group : 0], turn);
+      return v[0];
+    };
     if constexpr (C > 0) {
-      Inputs<VEC, TX, TR> raw[C];
+      // RING: a chunk at a time; else all chunks' loads are on their way together
+      Inputs<VEC, TX, TR> raw[RING ? 1 : C];
       bool in[C];
 #pragma unroll
       for (int k = 0; k < C; ++k) {
         const int chunk = k * tpr + t;
         const int c = chunk_col<VEC>(chunk);
         in[k] = chunk < chunks && c < a.dim;
-        if constexpr (RING) {
-          if (k == 0) mbar_wait_late(&ring.full[slot], parity, &ring.abort_flag, a.ring.err);
-          raw[k].from_ring(a, stages + slot * stage_bytes, c, in[k]);
-        } else {
-          raw[k].load(a, row, c, in[k]);
-        }
+        if constexpr (!RING) raw[k].load(a, row, c, in[k]);
       }
+      if constexpr (RING) mbar_wait_late(&ring.full[bar_off + slot], parity, &ring.abort_flag, a.ring.err);
       uint64_t h[C][4], total = 0ull;
 #pragma unroll
       for (int k = 0; k < C; ++k) {
+        const int c = chunk_col<VEC>(k * tpr + t);
         float v[8];
-        raw[k].sum(a, v);  // zeros where nothing is
+        if constexpr (RING) raw[0].from_ring(a, stage(slot), c, in[k]);
+        raw[RING ? 0 : k].sum(a, v);  // zeros where nothing is
         to_pairs(v, h[k]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) total = add2(total, h[k][i]);
-        if (a.p.h != nullptr && in[k])
-          store8<VEC>(a.p.h, a.p.h_type, row * a.p.ldh, chunk_col<VEC>(k * tpr + t), a.dim, v);
+        if (a.p.h != nullptr && in[k]) store8<VEC>(a.p.h, a.p.h_type, row * a.p.ldh, c, a.dim, v);
       }
       sum = both(total);
-      const float mean = row_sum(sum, tpr, red_mean, turn_mean) * inv_dim;
+      const float mean = mean_of();
       if constexpr (RING) {
-        // every thread has read the stage (row_sum's barrier): the next row
-        const int64_t next = row + static_cast<int64_t>(a.ring.stages) * gridDim.x;
-        if (threadIdx.x == 0 && next < a.rows && !*const_cast<volatile int*>(&ring.abort_flag))
+        // every thread has read the stage (the sum's barrier): the next row
+        const uint32_t next = at + a.ring.stages * row_step;
+        if (t == 0 && next < rows && !*const_cast<volatile int*>(&ring.abort_flag))
           fetch(next, slot);
         if (++slot == a.ring.stages) {
           slot = 0;
@@ -208,14 +322,13 @@ __global__ void __launch_bounds__(kMaxThreads, RING ? 2 : 1)
 #pragma unroll
       for (int k = 0; k < C; ++k)
         center<VEC>(h[k], f32x2(-mean, -mean), chunk_col<VEC>(k * tpr + t), a.dim, in[k], left, squares);
-      statistics(row, mean, row_sums(make_float2(both(left), both(squares)), tpr, red_var, turn_var), off,
-                 rstd);
+      statistics(row, mean, both(left), both(squares), off, rstd);
       float amax = 0.0f;
 #pragma unroll
       for (int k = 0; k < C; ++k) {
         const int c = chunk_col<VEC>(k * tpr + t);
         float y[8];
-        affine<VEC>(a.p.weight, a.p.bias, c, a.dim, in[k], rstd, off, h[k], y);
+        affine<VEC, RING>(RING ? weights : a.p.weight, a.p.bias, c, a.dim, in[k], rstd, off, h[k], y);
         if (a.p.y != nullptr && in[k]) store8<VEC>(a.p.y, a.p.y_type, row * a.p.ldy, c, a.dim, y);
         if (f8) write_fp8<VEC>(a.p.q, a.p.ldq, a.p.scales, a.p.ld_scales, row, c, a.dim, in[k], y);
         if (s8) {
@@ -224,7 +337,7 @@ __global__ void __launch_bounds__(kMaxThreads, RING ? 2 : 1)
         }
       }
       if (!s8) continue;
-      amax = row_max(amax, tpr, red_max, turn_max);
+      amax = largest_of(amax);
       const float f = s8_factor(amax);
 #pragma unroll
       for (int k = 0; k < C; ++k) {
@@ -246,7 +359,7 @@ __global__ void __launch_bounds__(kMaxThreads, RING ? 2 : 1)
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum += h[i];
       }
-      const float mean = row_sum(sum, tpr, red_mean, turn_mean) * inv_dim;
+      const float mean = mean_of();
       const uint64_t minus_mean = f32x2(-mean, -mean);
       uint64_t left = 0ull, squares = 0ull;
       // the differences from the mean of one chunk
@@ -261,8 +374,7 @@ __global__ void __launch_bounds__(kMaxThreads, RING ? 2 : 1)
         const int c = chunk_col<VEC>(chunk);
         differences(c, c < a.dim, d, left, squares);
       }
-      statistics(row, mean, row_sums(make_float2(both(left), both(squares)), tpr, red_var, turn_var), off,
-                 rstd);
+      statistics(row, mean, both(left), both(squares), off, rstd);
       uint64_t unused = 0ull;
       float f = 0.0f;
       if (s8) {
@@ -275,7 +387,7 @@ __global__ void __launch_bounds__(kMaxThreads, RING ? 2 : 1)
           affine<VEC>(a.p.weight, a.p.bias, c, a.dim, c < a.dim, rstd, off, d, y);
           amax = fmaxf(amax, chunk_amax(y));
         }
-        amax = row_max(amax, tpr, red_max, turn_max);
+        amax = largest_of(amax);
         f = s8_factor(amax);
         if (t == 0) a.p.scales[row] = s8_scale(amax);
       }
@@ -296,7 +408,7 @@ __global__ void __launch_bounds__(kMaxThreads, RING ? 2 : 1)
       }
     }
   }
-  if (RING && threadIdx.x == 0 && ring.abort_flag) drain(ring, a.ring.stages, slot, parity);
+  if (RING && t == 0 && ring.abort_flag) drain_ring(ring.full + bar_off, a.ring.stages, slot, parity);
 }
 
 // ---------------------------------------------------------------- backward
@@ -320,17 +432,24 @@ constexpr int ln_grad_threads(bool ring, int chunks, int td, int th) {
 template <int C, bool VEC, int TD, int TH, bool RING = false>
 __global__ void __launch_bounds__(ln_grad_threads(RING, C, TD, TH), 1)
     layernorm_grad_kernel(const __grid_constant__ LnGradArgs a) {
-  __shared__ float2 red[2][16];
-  __shared__ Ring ring;
-  extern __shared__ uint4 dyn_smem[];  // the ring, or several rows' sums
-  uint8_t* const stages = reinterpret_cast<uint8_t*>(dyn_smem);
+  __shared__ float red[kMaxRings][2][16][2];
+  __shared__ LnRings ring;
+  extern __shared__ uint4 dyn_smem[];  // the weight and the rings, or several rows' sums
+  float* const weights = reinterpret_cast<float*>(dyn_smem);
+  const int tpr = a.tpr;
+  const int t = threadIdx.x % tpr, group = threadIdx.x / tpr;
+  const int per_cta = blockDim.x / tpr;
+  const int64_t row_step = static_cast<int64_t>(gridDim.x) * per_cta;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * per_cta + group;
   const int ring_dim = RING ? a.dim : 0;
   const int bytes_d = ring_dim * type_bytes(TD), bytes_h = ring_dim * type_bytes(TH);
   const int bytes_r = a.p.residual_grad == nullptr ? 0 : ring_dim * type_bytes(a.p.residual_grad_type);
   const int stage_bytes = bytes_d + bytes_h + bytes_r;
+  uint8_t* const stages = reinterpret_cast<uint8_t*>(weights + ring_dim) + group * a.ring.stages * stage_bytes;
+  uint64_t* const full = ring.full + (RING ? group * kMaxStages : 0);
   auto fetch = [&](int64_t row, int s) {
     uint8_t* to = stages + s * stage_bytes;
-    uint64_t* bar = &ring.full[s];
+    uint64_t* bar = &full[s];
     mbar_arrive_expect_tx(bar, static_cast<uint32_t>(stage_bytes));
     bulk_load(to, static_cast<const uint8_t*>(a.p.dy) + row * a.p.lddy * type_bytes(TD), bytes_d, bar);
     bulk_load(to + bytes_d, static_cast<const uint8_t*>(a.p.h) + row * a.p.ldh * type_bytes(TH),
@@ -341,20 +460,25 @@ __global__ void __launch_bounds__(ln_grad_threads(RING, C, TD, TH), 1)
                     row * a.p.ldrg * type_bytes(a.p.residual_grad_type),
                 bytes_r, bar);
   };
-  if (RING) ring_init(ring, a.ring.stages);
+  if (RING) {
+    if (t == 0) {
+      for (int s = 0; s < a.ring.stages; ++s) mbar_init(&full[s], 1);
+      if (group == 0) ring.abort_flag = 0;
+      fence_barrier_init();
+    }
+    __syncthreads();
+  }
   grid_dependency_wait();
   grid_launch_dependents();
-  if (RING && threadIdx.x == 0)
-    for (int s = 0; s < a.ring.stages; ++s) {
-      const int64_t row = blockIdx.x + static_cast<int64_t>(s) * gridDim.x;
-      if (row < a.rows) fetch(row, s);
-    }
+  if (RING) {
+    if (t == 0)
+      for (int s = 0; s < a.ring.stages; ++s)
+        if (row + s * row_step < a.rows) fetch(row + s * row_step, s);
+    stage_weights(weights, a.p.weight, nullptr, a.dim, false);
+    __syncthreads();
+  }
   int slot = 0;
   uint32_t parity = 0;
-  const int tpr = a.tpr;
-  const int t = threadIdx.x % tpr;
-  const int sub = threadIdx.x / tpr;
-  const int per_cta = blockDim.x / tpr;
   const int chunks = VEC ? a.dim / 8 : (a.dim + kFp8Block - 1) / kFp8Block * 16;
   const float inv_dim = 1.0f / static_cast<float>(a.dim);
   constexpr int CR = C > 0 ? C : 1;
@@ -364,15 +488,17 @@ __global__ void __launch_bounds__(ln_grad_threads(RING, C, TD, TH), 1)
 #pragma unroll
     for (int i = 0; i < 4; ++i) dw[k][i] = db[k][i] = 0ull;
   uint32_t turn = 0;
-  const int64_t row_step = static_cast<int64_t>(gridDim.x) * per_cta;
-  int64_t row = static_cast<int64_t>(blockIdx.x) * per_cta + sub;
   // dy times the weight
   auto weighted = [&](int c, uint64_t (&g)[4]) {
-    if (a.p.weight == nullptr) return;
     float v[8];
     uint64_t w[4];
-    load_weight<VEC>(a.p.weight, c, a.dim, v);
-    to_pairs(v, w);
+    if constexpr (RING) {
+      staged_pairs(weights + c, w);
+    } else {
+      if (a.p.weight == nullptr) return;
+      load_weight<VEC>(a.p.weight, c, a.dim, v);
+      to_pairs(v, w);
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) g[i] = mul2(g[i], w[i]);
   };
@@ -398,7 +524,13 @@ __global__ void __launch_bounds__(ln_grad_threads(RING, C, TD, TH), 1)
   };
   float next_rstd = row < a.rows ? a.p.rstd[row] : 0.0f;  // loaded a row ahead
   float next_mean = row < a.rows ? a.p.mean[row] : 0.0f;
-  for (; row < a.rows; row += row_step) {
+  // the row's means of g and of g xh, given a thread's sums
+  auto means_of = [&](uint64_t sum_g, uint64_t sum_x) {
+    float v[2] = {both(sum_g), both(sum_x)};
+    over_row<2>(v, tpr, group, red[RING ? group : 0], turn);
+    return make_float2(v[0] * inv_dim, v[1] * inv_dim);
+  };
+  for (; row < a.rows; row += row_step, ++turn) {
     const float rstd = next_rstd, mean = next_mean;
     if (row + row_step < a.rows) {
       next_rstd = a.p.rstd[row + row_step];
@@ -409,7 +541,7 @@ __global__ void __launch_bounds__(ln_grad_threads(RING, C, TD, TH), 1)
       Raw8<TD> dy[C];
       Raw8<TH> rh[C];
       const uint8_t* from = stages + slot * stage_bytes;
-      if (RING) mbar_wait_late(&ring.full[slot], parity, &ring.abort_flag, a.ring.err);
+      if (RING) mbar_wait_late(&full[slot], parity, &ring.abort_flag, a.ring.err);
       auto get = [&](int k, int c, bool in) {
         if constexpr (RING) {
           dy[k] = {};
@@ -456,11 +588,10 @@ __global__ void __launch_bounds__(ln_grad_threads(RING, C, TD, TH), 1)
           sum_x = fma2(g[i], xh[i], sum_x);
         }
       }
-      float2 means = row_sums(make_float2(both(sum_g), both(sum_x)), tpr, red, turn);
-      means = make_float2(means.x * inv_dim, means.y * inv_dim);
-      if (RING && threadIdx.x == 0 && row >= static_cast<int64_t>(gridDim.x)) {
-        // every thread has left the previous row (row_sums' barrier)
-        const int64_t next = row + static_cast<int64_t>(a.ring.stages - 1) * gridDim.x;
+      const float2 means = means_of(sum_g, sum_x);
+      if (RING && t == 0 && turn > 0) {
+        // every thread has left the previous row (the sums' barrier)
+        const int64_t next = row + (a.ring.stages - 1) * row_step;
         if (next < a.rows && !*const_cast<volatile int*>(&ring.abort_flag))
           fetch(next, slot == 0 ? a.ring.stages - 1 : slot - 1);
       }
@@ -501,10 +632,7 @@ __global__ void __launch_bounds__(ln_grad_threads(RING, C, TD, TH), 1)
     } else {
       float2 means = make_float2(0.0f, 0.0f);
       for (int half = 0; half < 2; ++half) {
-        if (half == 1) {
-          means = row_sums(make_float2(both(sum_g), both(sum_x)), tpr, red, turn);
-          means = make_float2(means.x * inv_dim, means.y * inv_dim);
-        }
+        if (half == 1) means = means_of(sum_g, sum_x);
         for (int chunk = t; chunk < chunks; chunk += tpr) {
           const int c = chunk_col<VEC>(chunk);
           if (c >= a.dim) continue;
@@ -536,8 +664,9 @@ __global__ void __launch_bounds__(ln_grad_threads(RING, C, TD, TH), 1)
       }
     }
   }
-  if (RING && threadIdx.x == 0 && ring.abort_flag) drain(ring, a.ring.stages, slot, parity);
+  if (RING && t == 0 && ring.abort_flag) drain_ring(full, a.ring.stages, slot, parity);
   if (C == 0 || a.part == nullptr) return;
+  if (RING && per_cta > 1) __syncthreads();  // the rings make room for the sums
   // dw in the first dim columns of the CTA's row of `part`, db in the others
   float* out = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.dim;
   float* sums = reinterpret_cast<float*>(dyn_smem);
@@ -546,7 +675,7 @@ __global__ void __launch_bounds__(ln_grad_threads(RING, C, TD, TH), 1)
     const int chunk = k * tpr + t;
     const int c = chunk_col<VEC>(chunk);
     if (chunk >= chunks || c >= a.dim) continue;
-    float* to = per_cta == 1 ? out : sums + static_cast<int64_t>(sub) * 2 * a.dim;
+    float* to = per_cta == 1 ? out : sums + static_cast<int64_t>(group) * 2 * a.dim;
     float w[8], b[8];
     from_pairs(dw[k], w);
     from_pairs(db[k], b);
@@ -587,6 +716,27 @@ __global__ void __launch_bounds__(256) layernorm_dweight_kernel(const __grid_con
   out[a.dim] = b;
 }
 
+// Groups per CTA (p.per_cta), CTAs per SM (the return value; 0: no rings) and
+// stages of each group's ring of rows of `bytes`, next to `weights` bytes of
+// weights, if there are enough rows.  sm_threads: what the instance's registers
+// let an SM hold.  Groups need a barrier each, so short rows take two CTAs.
+int plan_groups(RowPlan& p, int64_t rows, int64_t bytes, int64_t weights, int num_sms, int sm_threads,
+                RingArgs& ring) {
+  if (p.per_cta != 1 || p.chunks_per_thread == 0 || p.tpr == 32) return 0;
+  const int per_sm = 2 * kMaxRings * p.tpr <= sm_threads ? 2 : 1;
+  int groups = sm_threads / per_sm / p.tpr;
+  if (groups > kMaxRings) groups = kMaxRings;
+  for (; groups >= 1; --groups) {
+    const int64_t stages = (kSmBytes / per_sm - kLnCtaBytes - weights) / (groups * bytes);
+    if (stages < 2) continue;
+    if (rows < 2 * static_cast<int64_t>(per_sm) * num_sms * groups) return 0;
+    ring.stages = static_cast<int>(stages < kMaxStages ? stages : kMaxStages);
+    p.per_cta = groups;
+    return per_sm;
+  }
+  return 0;
+}
+
 // Rows moved in vectors have an instance for each pair of input types; the
 // others look at the types as they go.
 template <bool VEC, int TX, int TR>
@@ -595,9 +745,12 @@ cudaError_t launch_ln(const LnArgs& a, const RowPlan& p, int grid, cudaStream_t 
   const int threads = p.tpr * p.per_cta;
   if constexpr (VEC) {
     if (a.ring.stages > 0) {  // more than one warp a row: two chunks a thread (plan_rows)
-      const size_t smem = static_cast<size_t>(a.ring.stages) * a.dim *
-                          (type_bytes(TX) + (TR < 0 ? 0 : type_bytes(TR)));
-      return ops_launch<layernorm_kernel<2, VEC, TX, TR, true>>(g, threads, smem, 1, s, a);
+      const size_t row = static_cast<size_t>(a.dim) * (type_bytes(TX) + (TR < 0 ? 0 : type_bytes(TR)));
+      const size_t smem = 8 * static_cast<size_t>(a.dim) + p.per_cta * a.ring.stages * row;
+      if (a.p.q == nullptr) return ops_launch<layernorm_kernel<2, VEC, TX, TR, true, kNoQ>>(g, threads, smem, 1, s, a);
+      if (a.p.q_type == GEMM_OUT_S8)
+        return ops_launch<layernorm_kernel<2, VEC, TX, TR, true, GEMM_OUT_S8>>(g, threads, smem, 1, s, a);
+      return ops_launch<layernorm_kernel<2, VEC, TX, TR, true, GEMM_OUT_F8E4M3>>(g, threads, smem, 1, s, a);
     }
   }
   switch (p.chunks_per_thread) {
@@ -631,7 +784,8 @@ cudaError_t launch_ln_grad(const LnGradArgs& a, const RowPlan& p, int grid, cuda
   if constexpr (VEC) {
     if (a.ring.stages > 0) {
       const int rg = a.p.residual_grad == nullptr ? 0 : type_bytes(a.p.residual_grad_type);
-      const size_t bytes = static_cast<size_t>(a.ring.stages) * a.dim * (type_bytes(TD) + type_bytes(TH) + rg);
+      const size_t row = static_cast<size_t>(a.dim) * (type_bytes(TD) + type_bytes(TH) + rg);
+      const size_t bytes = 4 * static_cast<size_t>(a.dim) + p.per_cta * a.ring.stages * row;
       if (p.chunks_per_thread == 1)
         return ops_launch<layernorm_grad_kernel<1, VEC, TD, TH, true>>(g, threads, bytes, 1, s, a);
       return ops_launch<layernorm_grad_kernel<2, VEC, TD, TH, true>>(g, threads, bytes, 1, s, a);
@@ -700,10 +854,10 @@ gemm_status_t gemm_layernorm(int64_t rows, int64_t dim, const gemm_layernorm_t* 
   if (vec) {
     const int64_t bytes = dim * (type_bytes(p.x_type) +
                                  (p.residual == nullptr ? 0 : type_bytes(p.residual_type)));
-    const RowPlan pr = plan_rows(rows, chunks, sms, 2, 2);
-    const int ring_grid = plan_ring(pr, rows, bytes, sms, 1024, a.ring);
-    if (ring_grid > 0) {
-      grid = ring_grid;
+    RowPlan pr = plan_rows(rows, chunks, sms, 2, 2);
+    const int per_sm = plan_groups(pr, rows, bytes, 8 * dim, sms, 1024, a.ring);
+    if (per_sm > 0) {
+      grid = per_sm * sms;
       pl = pr;
       a.tpr = pl.tpr;
     }
@@ -750,7 +904,7 @@ gemm_status_t gemm_layernorm_backward(int64_t rows, int64_t dim, const gemm_laye
   a.p = p;
   const int64_t chunks = vec ? dim / 8 : (dim + kFp8Block - 1) / kFp8Block * 16;
   const bool two = vec && (chunks <= 64 || chunks > kMaxThreads);
-  const RowPlan pl = plan_rows(rows, chunks, sms, two ? 2 : 1, 2);
+  RowPlan pl = plan_rows(rows, chunks, sms, two ? 2 : 1, 2);
   a.tpr = pl.tpr;
   a.ring.err = err;
   int grid = row_grid(rows, pl, sms, 512);
@@ -759,8 +913,8 @@ gemm_status_t gemm_layernorm_backward(int64_t rows, int64_t dim, const gemm_laye
         dim * (type_bytes(p.dy_type) + type_bytes(p.h_type) +
                (p.residual_grad == nullptr ? 0 : type_bytes(p.residual_grad_type)));
     const int fit = ln_grad_threads(true, pl.chunks_per_thread, p.dy_type, p.h_type);
-    const int ring_grid = plan_ring(pl, rows, bytes, sms, fit, a.ring);
-    if (ring_grid > 0) grid = ring_grid;
+    const int per_sm = plan_groups(pl, rows, bytes, 4 * dim, sms, fit, a.ring);
+    if (per_sm > 0) grid = per_sm * sms;
   }
   const bool by_column = pl.chunks_per_thread == 0;
   int parts = grid;

@@ -73,28 +73,6 @@ __device__ __forceinline__ float row_sum(float v, int tpr, float (*red)[16], uin
   return __shfl_sync(0xffffffffu, v, 0);
 }
 
-// The same for two values at once.
-__device__ __forceinline__ float2 row_sums(float2 v, int tpr, float2 (*red)[16], uint32_t& turn) {
-#pragma unroll
-  for (int s = 16; s > 0; s >>= 1) {
-    v.x += __shfl_xor_sync(0xffffffffu, v.x, s);
-    v.y += __shfl_xor_sync(0xffffffffu, v.y, s);
-  }
-  if (tpr == 32) return v;
-  float2* mine = red[turn & 1u];
-  ++turn;
-  const int lane = threadIdx.x & 31;
-  if (lane == 0) mine[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = lane < (tpr >> 5) ? mine[lane] : make_float2(0.0f, 0.0f);
-#pragma unroll
-  for (int s = 8; s > 0; s >>= 1) {
-    v.x += __shfl_xor_sync(0xffffffffu, v.x, s);
-    v.y += __shfl_xor_sync(0xffffffffu, v.y, s);
-  }
-  return make_float2(__shfl_sync(0xffffffffu, v.x, 0), __shfl_sync(0xffffffffu, v.y, 0));
-}
-
 // Their largest.
 __device__ __forceinline__ float row_max(float v, int tpr, float (*red)[16], uint32_t& turn) {
 #pragma unroll

@@ -62,7 +62,8 @@ ROWS_DIM = [(1, 1), (1, 128), (3, 127), (5, 129), (1, 4096), (7, 1000), (33, 512
             (700, 200), (1000, 1024), (330, 4096), (320, 5000), (2, 8192), (3, 12288), (2, 16384),
             (3, 16385), (2, 20000), (310, 16392), (40, 33000)]
 # rows through the ring: several to a CTA, stages of two to four places
-STAGED = [(4000, 1024), (2500, 4096), (1300, 8192), (5000, 520)]
+STAGED = [(4000, 1024), (2500, 4096), (1300, 8192), (5000, 520), (6001, 2048), (9001, 1032), (2431, 4104),
+          (3001, 6144), (9000, 576)]
 
 
 def forward(rows, dim, xt, rt, out, pad, mean=0.0, weight=True, bias=True):
