@@ -30,7 +30,7 @@ struct Int8QuantArgs {
 // and no loop: the next row's CTA is there while this one waits.
 template <int C, bool VEC, int T>
 __global__ void __launch_bounds__(kMaxThreads) int8_rows_kernel(const __grid_constant__ Int8QuantArgs a) {
-  __shared__ float red[2][16];
+  __shared__ uint32_t red[2][16], red_finite[2][16];
   grid_dependency_wait();
   grid_launch_dependents();
   const int tpr = a.tpr;
@@ -39,19 +39,19 @@ __global__ void __launch_bounds__(kMaxThreads) int8_rows_kernel(const __grid_con
   if (row >= a.rows) return;  // whole warps: rows share no warp
   const int dim = static_cast<int>(a.cols);
   const int chunks = VEC ? dim / 8 : (dim + kFp8Block - 1) / kFp8Block * 16;
-  uint32_t turn = 0;
-  float amax = 0.0f;
-  auto largest = [&](const Raw8<T>& raw) {
+  // a chunk's largest magnitude; `only_finite`: infinities and NaN left out
+  auto largest = [&](const Raw8<T>& raw, uint32_t& m, bool only_finite) {
     float v[8];
     widen8<VEC, T>(raw, a.x_type, v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, finite_abs(v[i]));
+    for (int i = 0; i < 8; ++i) m = max(m, only_finite ? __float_as_uint(finite_abs(v[i])) : abs_bits(v[i]));
   };
-  auto write = [&](const Raw8<T>& raw, int c, float f) {
+  auto write = [&](const Raw8<T>& raw, int c, float f, bool finite) {
     float v[8];
     widen8<VEC, T>(raw, a.x_type, v);
-    write_s8<VEC>(a.q, a.ldq, row, c, dim, f, v);
+    write_s8<VEC>(a.q, a.ldq, row, c, dim, f, finite, v);
   };
+  uint32_t amax = 0u;
   if constexpr (C > 0) {
     Raw8<T> raw[C];
     bool in[C];
@@ -62,25 +62,38 @@ __global__ void __launch_bounds__(kMaxThreads) int8_rows_kernel(const __grid_con
       raw[k] = load8<VEC, T>(a.x, a.x_type, row * a.ldx, c, dim, in[k]);
     }
 #pragma unroll
-    for (int k = 0; k < C; ++k) largest(raw[k]);
-    amax = row_max(amax, tpr, red, turn);
-    const float f = s8_factor(amax);
+    for (int k = 0; k < C; ++k) largest(raw[k], amax, false);
+    amax = row_max_bits(amax, tpr, 0, red, 0);
+    const bool finite = amax < kInfBits;
+    if (!finite) {
+      amax = 0u;
+#pragma unroll
+      for (int k = 0; k < C; ++k) largest(raw[k], amax, true);
+      amax = row_max_bits(amax, tpr, 0, red_finite, 0);
+    }
+    const float f = s8_factor(__uint_as_float(amax));
 #pragma unroll
     for (int k = 0; k < C; ++k)
-      if (in[k]) write(raw[k], chunk_col<VEC>(k * tpr + t), f);
+      if (in[k]) write(raw[k], chunk_col<VEC>(k * tpr + t), f, finite);
   } else {
+    auto search = [&](bool only_finite) {
+      uint32_t m = 0u;
+      for (int chunk = t; chunk < chunks; chunk += tpr) {
+        const int c = chunk_col<VEC>(chunk);
+        largest(load8<VEC, T>(a.x, a.x_type, row * a.ldx, c, dim, c < dim), m, only_finite);
+      }
+      return m;
+    };
+    amax = row_max_bits(search(false), tpr, 0, red, 0);
+    const bool finite = amax < kInfBits;
+    if (!finite) amax = row_max_bits(search(true), tpr, 0, red_finite, 0);
+    const float f = s8_factor(__uint_as_float(amax));
     for (int chunk = t; chunk < chunks; chunk += tpr) {
       const int c = chunk_col<VEC>(chunk);
-      largest(load8<VEC, T>(a.x, a.x_type, row * a.ldx, c, dim, c < dim));
-    }
-    amax = row_max(amax, tpr, red, turn);
-    const float f = s8_factor(amax);
-    for (int chunk = t; chunk < chunks; chunk += tpr) {
-      const int c = chunk_col<VEC>(chunk);
-      if (c < dim) write(load8<VEC, T>(a.x, a.x_type, row * a.ldx, c, dim, true), c, f);
+      if (c < dim) write(load8<VEC, T>(a.x, a.x_type, row * a.ldx, c, dim, true), c, f, finite);
     }
   }
-  if (t == 0) a.scales[row] = s8_scale(amax);
+  if (t == 0) a.scales[row] = s8_scale(__uint_as_float(amax));
 }
 
 // Transposed, first: the largest magnitudes of 256 columns over every
@@ -165,8 +178,10 @@ __global__ void __launch_bounds__(256) int8_turn_kernel(const __grid_constant__ 
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float f = factor[VEC ? c + j : c + 16 * j];
-        piece[j] = make_uint2(pack_s8(v[0][j] * f, v[1][j] * f, v[2][j] * f, v[3][j] * f),
-                              pack_s8(v[4][j] * f, v[5][j] * f, v[6][j] * f, v[7][j] * f));
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = static_cast<uint32_t>(round_s8(v[i][j] * f));
+        piece[j] = make_uint2(low_bytes(w[0], w[1], w[2], w[3]), low_bytes(w[4], w[5], w[6], w[7]));
       }
     }
 #pragma unroll

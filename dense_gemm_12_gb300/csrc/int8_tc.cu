@@ -57,11 +57,19 @@ constexpr int kFewRegs = 64, kManyRegs = 104;
 // k-blocks of B that a CTA of a split tile asks L2 for early.
 constexpr int kEarlyBlocks = 4;
 
-constexpr int stage_bytes(int tm) { return kRawW + tm * BK; }
-constexpr int wide_bytes(int tm) { return tm * BK * 2; }  // one buffer of widened tokens
-constexpr int stages(int tm) {
-  const int n = (kPool - 2 * wide_bytes(tm)) / stage_bytes(tm);
-  return n < kMaxStages ? n : kMaxStages;
+// kSplit: the CTAs of a cluster split a tile's k-blocks.  kWide: the tokens come
+// in fp16, widened by a kernel of their own; TMA writes them where the MMAs read
+// them.
+enum Mode : int { kSingle = 0, kSplit = 1, kWide = 2 };
+
+constexpr int wide_bytes(int tm) { return tm * BK * 2; }  // a block's tokens, widened
+// Buffers of them: the threads' two, or a ring as deep as the weights'.
+constexpr int wide_buffers(int mode) { return mode == kWide ? 3 : 2; }
+constexpr int stage_bytes(int tm, int mode) { return kRawW + (mode == kWide ? 0 : tm * BK); }
+constexpr int stages(int tm, int mode) {
+  const int n = (kPool - wide_buffers(mode) * wide_bytes(tm)) / stage_bytes(tm, mode);
+  const int most = mode == kWide ? 3 : kMaxStages;
+  return n < most ? n : most;
 }
 
 struct Int8Args {
@@ -85,6 +93,8 @@ struct __align__(16) Tail {
   uint64_t empty[kMaxStages];  // ... have been read
   uint64_t wide_full[2];       // widened operands are there
   uint64_t wide_empty[2];      // ... have been used
+  uint64_t x_full[3];          // kWide: tokens are there
+  uint64_t x_empty[3];         // ... have been used
   uint64_t sum_full;           // an accumulator is finished
   uint64_t sum_empty;          // ... has been read
   uint64_t drain;
@@ -96,7 +106,8 @@ struct __align__(16) Tail {
 
 constexpr size_t kSmemBytes = 1024 + kPool + sizeof(Tail);
 static_assert(kSmemBytes <= 227 * 1024, "int8 kernel shared memory");
-static_assert(stages(16) >= 2 && stages(kMaxTokens) >= 2, "stages");
+static_assert(stages(16, kSingle) >= 2 && stages(kMaxTokens, kSingle) >= 2 && stages(kMaxTokens, kWide) == 3,
+              "stages");
 static_assert(kMaxTokens * WN * 4 <= kPool, "a cluster's sums fit in the ring");
 
 // Four int8 -> four fp16: with the sign bit turned over, a byte is its value +
@@ -176,11 +187,13 @@ __device__ __forceinline__ void finish(const Int8Args& p, int64_t at, float v) {
   store1(p.D, p.d_type, at, v);
 }
 
-template <int TM, bool CLUSTER>
+template <int TM, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     int8_kernel(const __grid_constant__ Int8Args p, const __grid_constant__ CUtensorMap tmA,
                 const __grid_constant__ CUtensorMap tmB) {
-  constexpr int STAGES = stages(TM), kStageBytes = stage_bytes(TM), kWideBytes = wide_bytes(TM);
+  constexpr bool CLUSTER = MODE == kSplit, WIDE = MODE == kWide;
+  constexpr int STAGES = stages(TM, MODE), kStageBytes = stage_bytes(TM, MODE), kWideBytes = wide_bytes(TM);
+  constexpr int kXBuffers = wide_buffers(MODE);
   constexpr uint32_t kIdesc = idesc_f16_f32(128, TM);
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = align_smem<1024>(smem_raw);
@@ -191,6 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t full_at = tail_at + offsetof(Tail, full), empty_at = tail_at + offsetof(Tail, empty);
   const uint32_t wide_full_at = tail_at + offsetof(Tail, wide_full);
   const uint32_t wide_empty_at = tail_at + offsetof(Tail, wide_empty);
+  const uint32_t x_full_at = tail_at + offsetof(Tail, x_full), x_empty_at = tail_at + offsetof(Tail, x_empty);
   const uint32_t sum_full_at = tail_at + offsetof(Tail, sum_full);
   const uint32_t sum_empty_at = tail_at + offsetof(Tail, sum_empty);
   const int warp = threadIdx.x >> 5;
@@ -204,6 +218,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tail->wide_full[b], kWorkWarps);
       mbar_init(&tail->wide_empty[b], 1);
+    }
+    for (int b = 0; WIDE && b < kXBuffers; ++b) {
+      mbar_init(&tail->x_full[b], 1);
+      mbar_init(&tail->x_empty[b], 1);
     }
     mbar_init(&tail->sum_full, 1);
     mbar_init(&tail->sum_empty, kWorkWarps);
@@ -257,13 +275,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint8_t* to = smem + s * kStageBytes;
             mbar_arrive_expect_tx(&tail->full[s], kStageBytes);
             tma_load_2d(to, &tmB, kb * BK, w.tn * WN, &tail->full[s]);
-            tma_load_2d(to + kRawW, &tmA, kb * BK, w.tm * TM, &tail->full[s]);
+            if (!WIDE) {
+              tma_load_2d(to + kRawW, &tmA, kb * BK, w.tm * TM, &tail->full[s]);
+              continue;
+            }
+            const uint32_t x = it % kXBuffers;
+            if (!mbar_wait_at(x_empty_at + 8 * x, ((it / kXBuffers) & 1u) ^ 1u, abort_flag, p.err)) {
+              ok = false;
+              ++it;  // the weights are on their way
+              break;
+            }
+            mbar_arrive_expect_tx(&tail->x_full[x], kWideBytes);
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+              tma_load_2d(wide + x * kWideBytes + half * (TM * 128), &tmA, kb * BK + half * 64, w.tm * TM,
+                          &tail->x_full[x]);
           }
           if (CLUSTER) break;  // one tile
         }
         if (!ok) {
           for (uint32_t j = it > STAGES ? it - STAGES : 0u; j < it; ++j)
             mbar_drain_wait(&tail->full[j % STAGES], (j / STAGES) & 1u);
+          // (of the last block perhaps only the weights: that wait runs out)
+          for (uint32_t j = it > kXBuffers ? it - kXBuffers : 0u; WIDE && j < it; ++j)
+            mbar_drain_wait(&tail->x_full[j % kXBuffers], (j / kXBuffers) & 1u);
         }
       }
       __syncwarp();
@@ -280,6 +315,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           bool got = mbar_wait_at(wide_full_at + 8 * b, (it >> 1) & 1u, abort_flag, p.err);
           if (in_chunk == 0)
             got = got && mbar_wait_at(sum_empty_at, (chunk & 1u) ^ 1u, abort_flag, p.err);
+          const uint32_t x = WIDE ? it % kXBuffers : b;  // buffer of tokens
+          if (WIDE) got = got && mbar_wait_at(x_full_at + 8 * x, (it / kXBuffers) & 1u, abort_flag, p.err);
           if (__any_sync(0xffffffffu, !got)) {
             ok = false;
             break;
@@ -288,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool last = in_chunk == kChunk - 1 || kb + 1 == kb1;
           if (elect_one()) {
             const uint32_t at = tmem_base + kWideAt + b * kWideCols;
-            const uint64_t db = db0 + b * (kWideBytes >> 4);
+            const uint64_t db = db0 + x * (kWideBytes >> 4);
 #pragma unroll 1
             for (int half = 0; half < 2; ++half)
 #pragma unroll
@@ -297,6 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                               db + (kk >> 2) * (TM * 128 >> 4) + (kk & 3) * 2, kIdesc,
                               in_chunk != 0 || kk != 0 ? 1u : 0u);
             tc_commit(&tail->wide_empty[b]);
+            if (WIDE) tc_commit(&tail->x_empty[x]);
             if (last) tc_commit(&tail->sum_full);
           }
           __syncwarp();
@@ -330,14 +368,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t sums_at = tmem_base + lanes + static_cast<uint32_t>(half) * kSumCols + side * kMySums;
     const uint32_t wide_at = tmem_base + lanes + kWideAt + static_cast<uint32_t>(half) * kWideHalf + side * 32;
-    const uint32_t raw = smem_u32(smem), wide_smem = smem_u32(wide);
-    const uint32_t raw_w = raw + static_cast<uint32_t>(wrow) * BK;
+    const uint32_t raw_w = smem_u32(smem) + static_cast<uint32_t>(wrow) * BK;
     const uint32_t turn = static_cast<uint32_t>((side * 4) ^ (wrow & 7)) * 16;
     constexpr int kPieces = TM * 8;  // 16-byte pieces of a block's tokens
     constexpr int kMine = (kPieces + kWorkThreads - 1) / kWorkThreads;
+    static_assert(kMine <= 2, "a thread's second piece lies in the other 64 of k");
     const uint32_t token = static_cast<uint32_t>(tid & (TM - 1));
-    const int piece0 = tid / TM;
-    const uint32_t raw_x = raw + kRawW + token * BK, turn_x = (token & 7) * 16;
+    const int piece = tid / TM;  // the first; the second is piece + 4
+    const bool has_piece = kPieces >= kWorkThreads || piece < 8;
+    // where it lies, and the first of its two widened pieces (the other: ^ 16)
+    const uint32_t x_from = smem_u32(smem) + kRawW + token * BK +
+                            (static_cast<uint32_t>(piece * 16) ^ ((token & 7) * 16));
+    const uint32_t x_to = smem_u32(wide) + (piece >= 4 ? TM * 128 : 0) + token * 128 +
+                          (static_cast<uint32_t>((piece & 3) * 32) ^ ((token & 7) * 16));
     uint32_t it = 0, chunk = 0;
     uint32_t sum[kMySums];
 
@@ -375,25 +418,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // Neighbouring threads take neighbouring tokens and the same piece, so that
       // reads and writes of eight lanes fall in different banks.
-      const uint32_t to = wide_smem + b * kWideBytes;
+      // Neighbouring threads take neighbouring tokens and the same piece, so that
+      // reads and writes of eight lanes fall in different banks.
+      if (!WIDE && has_piece) {
 #pragma unroll
-      for (int i = 0; i < kMine; ++i) {
-        const int c = piece0 + i * (kWorkThreads / TM);
-        if (kPieces < kWorkThreads && c >= 8) continue;
-        const uint4 x = ld_shared_u4(raw_x + from + (static_cast<uint32_t>(c * 16) ^ turn_x));
-        uint32_t v[8];
-        widen4(x.x, v[0], v[1]);
-        widen4(x.y, v[2], v[3]);
-        widen4(x.z, v[4], v[5]);
-        widen4(x.w, v[6], v[7]);
-        // two pieces of the first or the other 64 of k
-        const uint32_t at = to + (c >= 4 ? TM * 128 : 0) + token * 128;
-        const uint32_t first = static_cast<uint32_t>((c & 3) * 32) ^ turn_x;
-        st_shared_u4(at + first, v[0], v[1], v[2], v[3]);
-        st_shared_u4(at + (first ^ 16), v[4], v[5], v[6], v[7]);
+        for (int i = 0; i < kMine; ++i) {
+          const uint4 x = ld_shared_u4((x_from ^ (i * 64)) + from);
+          uint32_t v[8];
+          widen4(x.x, v[0], v[1]);
+          widen4(x.y, v[2], v[3]);
+          widen4(x.z, v[4], v[5]);
+          widen4(x.w, v[6], v[7]);
+          const uint32_t to = x_to + b * kWideBytes + i * (TM * 128);
+          st_shared_u4(to, v[0], v[1], v[2], v[3]);
+          st_shared_u4(to ^ 16, v[4], v[5], v[6], v[7]);
+        }
       }
       tc_wait_st();
-      fence_proxy_async_smem();
+      if (!WIDE) fence_proxy_async_smem();
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) {
@@ -531,6 +573,36 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc(tmem_base, kTmemCols);
 }
 
+// int8 rows -> fp16 rows of pitch ld2 (a multiple of 8; what is behind a row's
+// end is zero).  16 values a thread.
+__global__ void __launch_bounds__(256) widen_rows_kernel(const int8_t* src, int64_t ld, uint16_t* dst,
+                                                         int64_t ld2, int64_t rows, int64_t cols, int vec) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int64_t pieces = (ld2 + 15) / 16, total = rows * pieces;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * 256;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += step) {
+    const int64_t r = total < (int64_t{1} << 31) ? static_cast<uint32_t>(i) / static_cast<uint32_t>(pieces) : i / pieces;
+    const int64_t c = (i - r * pieces) * 16;
+    const int8_t* s = src + r * ld + c;
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+    if (vec && c + 16 <= cols) {
+      const uint4 v = __ldcs(reinterpret_cast<const uint4*>(s));
+      w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (c + j < cols) w[j >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(s[j])) << (8 * (j & 3));
+    }
+    uint32_t v[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) widen4(w[j], v[2 * j], v[2 * j + 1]);
+    uint4* d = reinterpret_cast<uint4*>(dst + r * ld2 + c);
+    d[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    if (c + 8 < ld2) d[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
+
 // Clusters of S CTAs that can be resident at once on the current device; 0 if
 // unknown.
 int max_clusters(int S) {
@@ -540,7 +612,7 @@ int max_clusters(int S) {
   const int known = cache[dev][S].load(std::memory_order_relaxed);
   if (known != 0) return known;
   int n = 0;
-  if (ops_allow_smem<int8_kernel<kMaxTokens, true>>(kSmemBytes) == cudaSuccess) {
+  if (ops_allow_smem<int8_kernel<kMaxTokens, kSplit>>(kSmemBytes) == cudaSuccess) {
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -552,7 +624,7 @@ int max_clusters(int S) {
     cfg.dynamicSmemBytes = kSmemBytes;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, int8_kernel<kMaxTokens, true>, &cfg) != cudaSuccess) n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, int8_kernel<kMaxTokens, kSplit>, &cfg) != cudaSuccess) n = 0;
   }
   cudaGetLastError();
   if (n > 0) cache[dev][S].store(n, std::memory_order_relaxed);
@@ -579,9 +651,9 @@ template <int TM>
 cudaError_t launch(int64_t tiles, int num_sms, const Int8Args& a, const CUtensorMap& tmA,
                    const CUtensorMap& tmB, cudaStream_t s) {
   if (a.cluster > 1)
-    return ops_launch<int8_kernel<TM, true>>(dim3(static_cast<unsigned>(tiles * a.cluster)), kThreads,
+    return ops_launch<int8_kernel<TM, kSplit>>(dim3(static_cast<unsigned>(tiles * a.cluster)), kThreads,
                                              kSmemBytes, a.cluster, s, a, tmA, tmB);
-  return ops_launch<int8_kernel<TM, false>>(dim3(static_cast<unsigned>(tiles < num_sms ? tiles : num_sms)),
+  return ops_launch<int8_kernel<TM, kSingle>>(dim3(static_cast<unsigned>(tiles < num_sms ? tiles : num_sms)),
                                             kThreads, kSmemBytes, 1, s, a, tmA, tmB);
 }
 
@@ -630,30 +702,52 @@ extern "C" gemm_status_t gemm_int8gemm(int64_t M, int64_t N, int64_t K, float al
   a.d_pair = d_type == GEMM_OUT_BF16 && beta == 0.0f && !ops_misaligned(D, 4) && (M == 1 || ldd % 2 == 0);
   a.err = err;
   const int tm = M > 64 ? 128 : (M > 32 ? 64 : (M > 16 ? 32 : 16));
-  std::unique_lock<std::mutex> lock;
-  CUtensorMap tmA{}, tmB{};
-  if (product) {
-    ByteOperand oa{A, M, K, lda, 1, 0}, ob{B, N, K, ldb, 1, 0};
-    const int64_t need_a = byte_tma_ok(oa) ? 0 : byte_staged(oa);
-    const int64_t need_b = byte_tma_ok(ob) ? 0 : byte_staged(ob);
-    if (need_a + need_b > 0) {
-      uint8_t* buf = nullptr;
-      st = abi_stage(s, need_a + need_b, lock, &buf);
-      if (st != GEMM_OK) return st;
-      cudaError_t e = need_a > 0 ? byte_stage(oa, buf, sms, s) : cudaSuccess;
-      if (e == cudaSuccess && need_b > 0) e = byte_stage(ob, buf + need_a, sms, s);
-      if (e != cudaSuccess) return abi_from_cuda(e);
-    }
-    const int64_t da[2] = {K, M}, ta[1] = {byte_pitch(oa)};
-    const int64_t db[2] = {K, N}, tb[1] = {byte_pitch(ob)};
-    const uint32_t ba[2] = {BK, static_cast<uint32_t>(tm)}, bb[2] = {BK, WN};
-    if (!abi_encode_tiled(&tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, oa.p, da, ta, ba) ||
-        !abi_encode_tiled(&tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, ob.p, db, tb, bb))
-      return GEMM_ERR_LAUNCH;
-  }
   const int64_t tiles = ((N + WN - 1) / WN) * ((M + tm - 1) / tm);
   if (tiles + sms > kOpsMaxDim) return GEMM_ERR_UNSUPPORTED;
   a.cluster = choose_split(tiles, a.num_kb, sms);
+  std::unique_lock<std::mutex> lock;
+  CUtensorMap tmA{}, tmB{};
+  bool wide = false;
+  if (product) {
+    ByteOperand oa{A, M, K, lda, 1, 0}, ob{B, N, K, ldb, 1, 0};
+    const int64_t need_b = byte_tma_ok(ob) ? 0 : byte_staged(ob);
+    const int64_t ld2 = (K + 7) / 8 * 8, wide_a = (2 * M * ld2 + 255) / 256 * 256;
+    uint8_t* buf = nullptr;
+    // The tokens widened by themselves, if there are enough tiles to share them
+    // and memory for them.
+    if (tm == kMaxTokens && tiles > sms) {
+      st = abi_stage(s, wide_a + need_b, lock, &buf);
+      wide = st == GEMM_OK;
+      if (!wide) lock = std::unique_lock<std::mutex>();
+    }
+    const int64_t need_a = wide || byte_tma_ok(oa) ? 0 : byte_staged(oa);
+    if (!wide && need_a + need_b > 0) {
+      st = abi_stage(s, need_a + need_b, lock, &buf);
+      if (st != GEMM_OK) return st;
+    }
+    cudaError_t e = cudaSuccess;
+    if (wide) {
+      const int64_t want = (M * ((ld2 + 15) / 16) + 255) / 256, fit = static_cast<int64_t>(sms) * 16;
+      uint16_t* to = reinterpret_cast<uint16_t*>(buf);
+      const int vec = !ops_misaligned(A, 16) && (M == 1 || lda % 16 == 0);
+      e = ops_launch<widen_rows_kernel>(dim3(static_cast<unsigned>(want < fit ? want : fit)), 256, 0, 1, s, A,
+                                        lda, to, ld2, M, K, vec);
+    } else if (need_a > 0) {
+      e = byte_stage(oa, buf, sms, s);
+    }
+    if (e == cudaSuccess && need_b > 0) e = byte_stage(ob, buf + (wide ? wide_a : need_a), sms, s);
+    if (e != cudaSuccess) return abi_from_cuda(e);
+    const int64_t da[2] = {K, M}, ta[1] = {wide ? 2 * ld2 : byte_pitch(oa)};
+    const int64_t db[2] = {K, N}, tb[1] = {byte_pitch(ob)};
+    const uint32_t ba[2] = {wide ? 64u : static_cast<uint32_t>(BK), static_cast<uint32_t>(tm)}, bb[2] = {BK, WN};
+    if (!abi_encode_tiled(&tmA, wide ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+                          wide ? buf : oa.p, da, ta, ba) ||
+        !abi_encode_tiled(&tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, ob.p, db, tb, bb))
+      return GEMM_ERR_LAUNCH;
+  }
+  if (wide)
+    return abi_from_cuda(ops_launch<int8_kernel<kMaxTokens, kWide>>(dim3(static_cast<unsigned>(sms)), kThreads,
+                                                                    kSmemBytes, 1, s, a, tmA, tmB));
   switch (tm) {
     case 16: return abi_from_cuda(launch<16>(tiles, sms, a, tmA, tmB, s));
     case 32: return abi_from_cuda(launch<32>(tiles, sms, a, tmA, tmB, s));

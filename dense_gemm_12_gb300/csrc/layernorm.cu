@@ -44,15 +44,14 @@ struct LnArgs {
   gemm_layernorm_t p;
 };
 
-// Sums (or largest) of N values over the tpr threads of a group.  red: two rows
+// Sums of N values over the tpr threads of a group.  red: two rows
 // of a value per warp, used in turn, one call a row.
-template <int N, bool MAX = false>
+template <int N>
 __device__ __forceinline__ void over_row(float (&v)[N], int tpr, int group, float (*red)[16][N], uint32_t turn) {
-  auto join = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
 #pragma unroll
   for (int s = 16; s > 0; s >>= 1)
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = join(v[i], __shfl_xor_sync(0xffffffffu, v[i], s));
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], s);
   if (tpr == 32) return;
   const int lane = threadIdx.x & 31, warps = tpr >> 5;
   float(*mine)[N] = red[turn & 1u];
@@ -62,11 +61,11 @@ __device__ __forceinline__ void over_row(float (&v)[N], int tpr, int group, floa
   }
   asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(tpr) : "memory");
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = lane < warps ? mine[lane & 15][i] : 0.0f;  // (magnitudes: 0 too)
+  for (int i = 0; i < N; ++i) v[i] = lane < warps ? mine[lane & 15][i] : 0.0f;
 #pragma unroll
   for (int s = 8; s > 0; s >>= 1)
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = join(v[i], __shfl_xor_sync(0xffffffffu, v[i], s));
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], s);
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, v[i], 0);
 }
@@ -189,11 +188,18 @@ __device__ __forceinline__ void affine(const float* weight, const float* bias, i
   }
 }
 
-__device__ __forceinline__ float chunk_amax(const float (&y)[8]) {
+__device__ __forceinline__ uint32_t chunk_max(const float (&y)[8]) {
+  uint32_t m = 0u;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, abs_bits(y[i]));
+  return m;
+}
+// The same over the finite values only.
+__device__ __forceinline__ uint32_t chunk_finite_max(const float (&y)[8]) {
   float m = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = fmaxf(m, finite_abs(y[i]));
-  return m;
+  return __float_as_uint(m);
 }
 
 // C > 0: a row in registers.  C == 0: rows longer than that are read three
@@ -205,7 +211,8 @@ constexpr int kNoQ = 0, kAnyQ = -1;
 template <int C, bool VEC, int TX, int TR, bool RING = false, int Q = kAnyQ>
 __global__ void __launch_bounds__(RING ? 1024 : kMaxThreads, 1)
     layernorm_kernel(const __grid_constant__ LnArgs a) {
-  __shared__ float red_mean[kMaxRings][2][16][1], red_max[kMaxRings][2][16][1];
+  __shared__ float red_mean[kMaxRings][2][16][1];
+  __shared__ uint32_t red_max[kMaxRings][2][16], red_finite[kMaxRings][2][16];
   __shared__ float red_var[kMaxRings][2][16][2];
   __shared__ LnRings ring;
   extern __shared__ uint4 dyn_smem[];
@@ -277,10 +284,11 @@ __global__ void __launch_bounds__(RING ? 1024 : kMaxThreads, 1)
       over_row<1>(v, tpr, group, red_mean[RING ? group : 0], turn);
       return v[0] * inv_dim;
     };
-    auto largest_of = [&](float amax) {
-      float v[1] = {amax};
-      over_row<1, true>(v, tpr, group, red_max[RING ? group : 0], turn);
-      return v[0];
+    auto largest_of = [&](uint32_t m) {
+      return row_max_bits(m, tpr, group, red_max[RING ? group : 0], turn);
+    };
+    auto largest_finite_of = [&](uint32_t m) {
+      return row_max_bits(m, tpr, group, red_finite[RING ? group : 0], turn);
     };
     if constexpr (C > 0) {
       // RING: a chunk at a time; else all chunks' loads are on their way together
@@ -323,7 +331,7 @@ __global__ void __launch_bounds__(RING ? 1024 : kMaxThreads, 1)
       for (int k = 0; k < C; ++k)
         center<VEC>(h[k], f32x2(-mean, -mean), chunk_col<VEC>(k * tpr + t), a.dim, in[k], left, squares);
       statistics(row, mean, both(left), both(squares), off, rstd);
-      float amax = 0.0f;
+      uint32_t amax = 0u;
 #pragma unroll
       for (int k = 0; k < C; ++k) {
         const int c = chunk_col<VEC>(k * tpr + t);
@@ -332,20 +340,31 @@ __global__ void __launch_bounds__(RING ? 1024 : kMaxThreads, 1)
         if (a.p.y != nullptr && in[k]) store8<VEC>(a.p.y, a.p.y_type, row * a.p.ldy, c, a.dim, y);
         if (f8) write_fp8<VEC>(a.p.q, a.p.ldq, a.p.scales, a.p.ld_scales, row, c, a.dim, in[k], y);
         if (s8) {
-          amax = fmaxf(amax, chunk_amax(y));
+          amax = max(amax, chunk_max(y));
           to_pairs(y, h[k]);
         }
       }
       if (!s8) continue;
       amax = largest_of(amax);
-      const float f = s8_factor(amax);
+      const bool finite = amax < kInfBits;
+      if (!finite) {
+        amax = 0u;
+#pragma unroll
+        for (int k = 0; k < C; ++k) {
+          float y[8];
+          from_pairs(h[k], y);
+          amax = max(amax, chunk_finite_max(y));
+        }
+        amax = largest_finite_of(amax);
+      }
+      const float f = s8_factor(__uint_as_float(amax));
 #pragma unroll
       for (int k = 0; k < C; ++k) {
         float y[8];
         from_pairs(h[k], y);
-        if (in[k]) write_s8<VEC>(a.p.q, a.p.ldq, row, chunk_col<VEC>(k * tpr + t), a.dim, f, y);
+        if (in[k]) write_s8<VEC>(a.p.q, a.p.ldq, row, chunk_col<VEC>(k * tpr + t), a.dim, f, finite, y);
       }
-      if (t == 0) a.p.scales[row] = s8_scale(amax);
+      if (t == 0) a.p.scales[row] = s8_scale(__uint_as_float(amax));
     } else {
       auto load = [&](int c, bool in, float (&h)[8]) {
         Inputs<VEC, TX, TR> raw;
@@ -377,19 +396,26 @@ __global__ void __launch_bounds__(RING ? 1024 : kMaxThreads, 1)
       statistics(row, mean, both(left), both(squares), off, rstd);
       uint64_t unused = 0ull;
       float f = 0.0f;
+      bool finite = true;
       if (s8) {
-        float amax = 0.0f;
-        for (int chunk = t; chunk < chunks; chunk += tpr) {
-          const int c = chunk_col<VEC>(chunk);
-          uint64_t d[4];
-          float y[8];
-          differences(c, c < a.dim, d, unused, unused);
-          affine<VEC>(a.p.weight, a.p.bias, c, a.dim, c < a.dim, rstd, off, d, y);
-          amax = fmaxf(amax, chunk_amax(y));
-        }
-        amax = largest_of(amax);
-        f = s8_factor(amax);
-        if (t == 0) a.p.scales[row] = s8_scale(amax);
+        uint32_t amax = 0u;
+        auto search = [&](bool only_finite) {
+          uint32_t m = 0u;
+          for (int chunk = t; chunk < chunks; chunk += tpr) {
+            const int c = chunk_col<VEC>(chunk);
+            uint64_t d[4];
+            float y[8];
+            differences(c, c < a.dim, d, unused, unused);
+            affine<VEC>(a.p.weight, a.p.bias, c, a.dim, c < a.dim, rstd, off, d, y);
+            m = max(m, only_finite ? chunk_finite_max(y) : chunk_max(y));
+          }
+          return m;
+        };
+        amax = largest_of(search(false));
+        finite = amax < kInfBits;
+        if (!finite) amax = largest_finite_of(search(true));
+        f = s8_factor(__uint_as_float(amax));
+        if (t == 0) a.p.scales[row] = s8_scale(__uint_as_float(amax));
       }
       for (int base = 0; base < chunks; base += tpr) {  // whole warps: write_fp8 shuffles
         const int chunk = base + t;
@@ -404,7 +430,7 @@ __global__ void __launch_bounds__(RING ? 1024 : kMaxThreads, 1)
         affine<VEC>(a.p.weight, a.p.bias, c, a.dim, in, rstd, off, d, y);
         if (in && a.p.y != nullptr) store8<VEC>(a.p.y, a.p.y_type, row * a.p.ldy, c, a.dim, y);
         if (f8) write_fp8<VEC>(a.p.q, a.p.ldq, a.p.scales, a.p.ld_scales, row, c, a.dim, in, y);
-        if (s8 && in) write_s8<VEC>(a.p.q, a.p.ldq, row, c, a.dim, f, y);
+        if (s8 && in) write_s8<VEC>(a.p.q, a.p.ldq, row, c, a.dim, f, finite, y);
       }
     }
   }
@@ -421,16 +447,9 @@ struct LnGradArgs {
   float* part;  // partial sums of dw and db: a row of 2 dim floats per CTA, or nullptr
 };
 
-// Threads' worth of CTAs that an SM holds of an instance: one chunk a thread in
-// bf16 fits 64 registers, the others 91 to 128.
-constexpr int ln_grad_threads(bool ring, int chunks, int td, int th) {
-  if (!ring || chunks != 1) return kMaxThreads;
-  return td == GEMM_OUT_BF16 && th == GEMM_OUT_BF16 ? 1024 : 640;
-}
-
 // As norm_grad_kernel, with the two sums of a row taken together.
 template <int C, bool VEC, int TD, int TH, bool RING = false>
-__global__ void __launch_bounds__(ln_grad_threads(RING, C, TD, TH), 1)
+__global__ void __launch_bounds__(kMaxThreads, 1)
     layernorm_grad_kernel(const __grid_constant__ LnGradArgs a) {
   __shared__ float red[kMaxRings][2][16][2];
   __shared__ LnRings ring;
@@ -786,8 +805,6 @@ cudaError_t launch_ln_grad(const LnGradArgs& a, const RowPlan& p, int grid, cuda
       const int rg = a.p.residual_grad == nullptr ? 0 : type_bytes(a.p.residual_grad_type);
       const size_t row = static_cast<size_t>(a.dim) * (type_bytes(TD) + type_bytes(TH) + rg);
       const size_t bytes = 4 * static_cast<size_t>(a.dim) + p.per_cta * a.ring.stages * row;
-      if (p.chunks_per_thread == 1)
-        return ops_launch<layernorm_grad_kernel<1, VEC, TD, TH, true>>(g, threads, bytes, 1, s, a);
       return ops_launch<layernorm_grad_kernel<2, VEC, TD, TH, true>>(g, threads, bytes, 1, s, a);
     }
   }
@@ -903,17 +920,17 @@ gemm_status_t gemm_layernorm_backward(int64_t rows, int64_t dim, const gemm_laye
   a.dim = static_cast<int>(dim);
   a.p = p;
   const int64_t chunks = vec ? dim / 8 : (dim + kFp8Block - 1) / kFp8Block * 16;
-  const bool two = vec && (chunks <= 64 || chunks > kMaxThreads);
-  RowPlan pl = plan_rows(rows, chunks, sms, two ? 2 : 1, 2);
+  // Two chunks a thread in vectors (one and twice the threads: 8192 x 4096 66 us
+  // against 61, 16384 x 1024 41 against 36).
+  RowPlan pl = plan_rows(rows, chunks, sms, vec ? 2 : 1, 2);
   a.tpr = pl.tpr;
   a.ring.err = err;
   int grid = row_grid(rows, pl, sms, 512);
-  if (vec && pl.chunks_per_thread > 0) {
+  if (vec && pl.chunks_per_thread == 2) {
     const int64_t bytes =
         dim * (type_bytes(p.dy_type) + type_bytes(p.h_type) +
                (p.residual_grad == nullptr ? 0 : type_bytes(p.residual_grad_type)));
-    const int fit = ln_grad_threads(true, pl.chunks_per_thread, p.dy_type, p.h_type);
-    const int per_sm = plan_groups(pl, rows, bytes, 4 * dim, sms, fit, a.ring);
+    const int per_sm = plan_groups(pl, rows, bytes, 4 * dim, sms, kMaxThreads, a.ring);
     if (per_sm > 0) grid = per_sm * sms;
   }
   const bool by_column = pl.chunks_per_thread == 0;

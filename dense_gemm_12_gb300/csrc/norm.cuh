@@ -73,20 +73,21 @@ __device__ __forceinline__ float row_sum(float v, int tpr, float (*red)[16], uin
   return __shfl_sync(0xffffffffu, v, 0);
 }
 
-// Their largest.
-__device__ __forceinline__ float row_max(float v, int tpr, float (*red)[16], uint32_t& turn) {
-#pragma unroll
-  for (int s = 16; s > 0; s >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, s));
-  if (tpr == 32) return v;
-  float* mine = red[turn & 1u];
-  ++turn;
-  const int lane = threadIdx.x & 31;
-  if (lane == 0) mine[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = lane < (tpr >> 5) ? mine[lane] : 0.0f;  // magnitudes
-#pragma unroll
-  for (int s = 8; s > 0; s >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, s));
-  return __shfl_sync(0xffffffffu, v, 0);
+// Bits of |v|: they order like the values, infinities and NaN above all.
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+constexpr uint32_t kInfBits = 0x7f800000u;
+
+// Largest of the bits over the tpr threads of a row, which are group `group` of
+// the CTA's.  red: two rows of a value per warp, used in turn, one call a row.
+__device__ __forceinline__ uint32_t row_max_bits(uint32_t m, int tpr, int group, uint32_t (*red)[16],
+                                                 uint32_t turn) {
+  m = __reduce_max_sync(0xffffffffu, m);
+  if (tpr == 32) return m;
+  const int lane = threadIdx.x & 31, warps = tpr >> 5;
+  uint32_t* mine = red[turn & 1u];
+  if (lane == 0) mine[(threadIdx.x >> 5) % warps] = m;
+  asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(tpr) : "memory");
+  return __reduce_max_sync(0xffffffffu, lane < warps ? mine[lane & 15] : 0u);
 }
 
 // Where the eight elements of chunk `chunk` lie: consecutive (VEC), or every
@@ -131,19 +132,25 @@ __device__ __forceinline__ void write_fp8(void* q_rows, int64_t ldq, float* scal
   if ((threadIdx.x & 15) == 0) scales[(c >> 7) * ld_scales + row] = fp8_scale(amax);
 }
 
-// A chunk of a row in int8, given the factor of the row.
+// A chunk of a row in int8, given the factor of the row.  finite: neither
+// infinities nor NaN in the row.  Its products then lie within +-127.001, and
+// one fused operation with 1.5 * 2^23 on top rounds them to whole numbers in the
+// last bits, two's complement (the conversion instruction takes 16 a cycle).
 template <bool VEC>
 __device__ __forceinline__ void write_s8(void* q_rows, int64_t ldq, int64_t row, int c, int dim, float f,
-                                         const float (&y)[8]) {
+                                         bool finite, const float (&y)[8]) {
   int8_t* q = static_cast<int8_t*>(q_rows) + row * ldq;
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    w[i] = finite ? __float_as_uint(fmaf(y[i], f, 12582912.0f)) : static_cast<uint32_t>(round_s8(y[i] * f));
   if (VEC) {
-    *reinterpret_cast<uint2*>(q + c) =
-        make_uint2(pack_s8(y[0] * f, y[1] * f, y[2] * f, y[3] * f),
-                   pack_s8(y[4] * f, y[5] * f, y[6] * f, y[7] * f));
+    *reinterpret_cast<uint2*>(q + c) = make_uint2(low_bytes(w[0], w[1], w[2], w[3]),
+                                                  low_bytes(w[4], w[5], w[6], w[7]));
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (c + 16 * i < dim) q[c + 16 * i] = static_cast<int8_t>(round_s8(y[i] * f));
+      if (c + 16 * i < dim) q[c + 16 * i] = static_cast<int8_t>(w[i]);
   }
 }
 

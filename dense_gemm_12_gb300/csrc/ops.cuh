@@ -178,9 +178,9 @@ __device__ __forceinline__ float s8_factor(float amax) {
 }
 // Nearest whole number (ties to even) within +-127; NaN becomes 0.
 __device__ __forceinline__ int round_s8(float v) { return max(min(__float2int_rn(v), 127), -127); }
-__device__ __forceinline__ uint32_t pack_s8(float a, float b, float c, float d) {
-  return static_cast<uint32_t>(round_s8(a) & 0xff) | static_cast<uint32_t>(round_s8(b) & 0xff) << 8 |
-         static_cast<uint32_t>(round_s8(c) & 0xff) << 16 | static_cast<uint32_t>(round_s8(d)) << 24;
+// Their last bytes, the first one lowest.
+__device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
 // ------------------------------------------------ eight elements of a row
