@@ -21,8 +21,9 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["api.cu", "sgemm_simt.cu", "bf16_tc.cu", "bf16_decode.cu", "decode_noalloc.cu",
            "norm.cu", "layernorm.cu", "fp8_quantize.cu", "fp8_tc.cu", "grouped_tc.cu", "experts.cu",
-           "int8_quantize.cu", "int8_tc.cu", "bytes.cu"]
-HEADERS = ["ptx.cuh", "internal.h", "epilogue.cuh", "dispatch_table.inc", "ops.cuh", "groups.cuh", "norm.cuh"]
+           "int8_quantize.cu", "int8_tc.cu", "int8_wide.cu", "bytes.cu"]
+HEADERS = ["ptx.cuh", "internal.h", "epilogue.cuh", "dispatch_table.inc", "ops.cuh", "groups.cuh", "norm.cuh",
+           "int8.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",

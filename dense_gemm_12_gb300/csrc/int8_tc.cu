@@ -31,10 +31,15 @@
 // Registers move from the first warpgroup to the other four for the sums.
 //
 // Few tiles: the CTAs of a cluster split a tile's k-blocks and add their sums
-// through distributed shared memory.
+// through distributed shared memory.  Many tiles: int8_wide.cu, if the stream's
+// buffer can hold both operands widened.
+//
+// Measured: 16 x 12288 x 4096 13.7 us (the weights at 3.7 TB/s: 96 CTAs have a
+// half of a tile's k each, and a k-block takes 460 ns from its copy to its MMA),
+// 64 x 12288 x 4096 21.3, 128 x 4096 x 4096 18.3, 1024 x 4096 x 4096 36.
 #include <cstddef>
 
-#include "ops.cuh"
+#include "int8.cuh"
 
 namespace g12 {
 namespace {
@@ -57,35 +62,12 @@ constexpr int kFewRegs = 64, kManyRegs = 104;
 // k-blocks of B that a CTA of a split tile asks L2 for early.
 constexpr int kEarlyBlocks = 4;
 
-// kSplit: the CTAs of a cluster split a tile's k-blocks.  kWide: the tokens come
-// in fp16, widened by a kernel of their own; TMA writes them where the MMAs read
-// them.
-enum Mode : int { kSingle = 0, kSplit = 1, kWide = 2 };
-
-constexpr int wide_bytes(int tm) { return tm * BK * 2; }  // a block's tokens, widened
-// Buffers of them: the threads' two, or a ring as deep as the weights'.
-constexpr int wide_buffers(int mode) { return mode == kWide ? 3 : 2; }
-constexpr int stage_bytes(int tm, int mode) { return kRawW + (mode == kWide ? 0 : tm * BK); }
-constexpr int stages(int tm, int mode) {
-  const int n = (kPool - wide_buffers(mode) * wide_bytes(tm)) / stage_bytes(tm, mode);
-  const int most = mode == kWide ? 3 : kMaxStages;
-  return n < most ? n : most;
+constexpr int stage_bytes(int tm) { return kRawW + tm * BK; }
+constexpr int wide_bytes(int tm) { return tm * BK * 2; }  // one buffer of widened tokens
+constexpr int stages(int tm) {
+  const int n = (kPool - 2 * wide_bytes(tm)) / stage_bytes(tm);
+  return n < kMaxStages ? n : kMaxStages;
 }
-
-struct Int8Args {
-  int M, N;
-  int num_kb;          // k-blocks; 0: D <- bias + beta * D
-  float alpha, beta;
-  const float* sa;
-  const float* sb;
-  const float* bias;   // or nullptr
-  void* D;
-  int64_t ldd;
-  int d_type;
-  int d_pair;          // bf16, beta == 0: two channels can be written at once
-  int cluster;         // > 1: CTAs that split one tile's k-blocks
-  uint32_t* err;
-};
 
 struct __align__(16) Tail {
   float scales[kWorkWarps][kMaxTokens / 2];  // of the tokens of a warp's sums
@@ -93,8 +75,6 @@ struct __align__(16) Tail {
   uint64_t empty[kMaxStages];  // ... have been read
   uint64_t wide_full[2];       // widened operands are there
   uint64_t wide_empty[2];      // ... have been used
-  uint64_t x_full[3];          // kWide: tokens are there
-  uint64_t x_empty[3];         // ... have been used
   uint64_t sum_full;           // an accumulator is finished
   uint64_t sum_empty;          // ... has been read
   uint64_t drain;
@@ -106,51 +86,8 @@ struct __align__(16) Tail {
 
 constexpr size_t kSmemBytes = 1024 + kPool + sizeof(Tail);
 static_assert(kSmemBytes <= 227 * 1024, "int8 kernel shared memory");
-static_assert(stages(16, kSingle) >= 2 && stages(kMaxTokens, kSingle) >= 2 && stages(kMaxTokens, kWide) == 3,
-              "stages");
+static_assert(stages(16) >= 2 && stages(kMaxTokens) >= 2, "stages");
 static_assert(kMaxTokens * WN * 4 <= kPool, "a cluster's sums fit in the ring");
-
-// Four int8 -> four fp16: with the sign bit turned over, a byte is its value +
-// 128, and as the low byte of 0x6400 it is the fp16 number 1024 + that.
-__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  const uint32_t u = w ^ 0x80808080u;
-  const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));  // 1152
-  const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-  const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), off);
-  const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
-  lo = *reinterpret_cast<const uint32_t*>(&x);
-  hi = *reinterpret_cast<const uint32_t*>(&y);
-}
-
-// Adds two whole numbers of at most 2^24, as fp32, to 32-bit integers, each with
-// kWholeOff on top.  Adding kRound leaves f rounded to a multiple of 2^13, which
-// its last bits then count; what is left, less than 2^13, is counted by the last
-// bits of its sum with 1.5 * 2^23 (the constants are chosen so that the second
-// and third sums are exact).  The conversion instruction, 16 a cycle, would take
-// as long as two k-blocks' MMAs for a tile's accumulator.
-constexpr float kRound = 103079215104.0f;               // 1.5 * 2^36
-constexpr float kRoundLeft = 103079215104.0f + 12582912.0f;  // and 1.5 * 2^23
-constexpr uint32_t kWholeOff = 0x51c00000u * 8192u + 0x4b400000u;  // their bits, as added below
-__device__ __forceinline__ void add_whole(uint32_t& a, uint32_t& b, uint32_t f, uint32_t g) {
-  uint32_t t0, t1, u0, u1;
-  asm("{\n\t.reg .b64 f, c, d, m, t, u;\n\t"
-      "mov.b64 f, {%4, %5};\n\t"
-      "mov.b64 c, {%6, %6};\n\t"
-      "mov.b64 d, {%7, %7};\n\t"
-      "mov.b64 m, {%8, %8};\n\t"
-      "add.rn.f32x2 t, f, c;\n\t"
-      "fma.rn.f32x2 u, t, m, d;\n\t"
-      "add.rn.f32x2 u, u, f;\n\t"
-      "mov.b64 {%0, %1}, t;\n\t"
-      "mov.b64 {%2, %3}, u;\n\t}"
-      : "=r"(t0), "=r"(t1), "=r"(u0), "=r"(u1)
-      : "r"(f), "r"(g), "f"(kRound), "f"(kRoundLeft), "f"(-1.0f));
-  a += (t0 << 13) + u0;
-  b += (t1 << 13) + u1;
-}
-// Which group of sums goes through the conversion instruction all the same: a
-// quarter, as long as the others take on the other units.
-__host__ __device__ constexpr bool by_unit(int j) { return j >= 48; }
 
 __device__ __forceinline__ uint4 ld_shared_u4(uint32_t addr) {
   uint4 v;
@@ -177,23 +114,11 @@ __device__ __forceinline__ Tile tile_of(int t, int tiles_n, int tiles_m) {
   return r;
 }
 
-// A value of D without beta's part, given its integer sum.  cs: alpha times the
-// channel's scale.
-__device__ __forceinline__ float value(const Int8Args& p, uint32_t sum, float cs, float sa, float bias) {
-  return p.num_kb > 0 ? fmaf(static_cast<float>(static_cast<int>(sum)) * sa, cs, bias) : bias;
-}
-__device__ __forceinline__ void finish(const Int8Args& p, int64_t at, float v) {
-  if (p.beta != 0.0f) v = fmaf(p.beta, load1(p.D, p.d_type, at), v);
-  store1(p.D, p.d_type, at, v);
-}
-
-template <int TM, int MODE>
+template <int TM, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, 1)
     int8_kernel(const __grid_constant__ Int8Args p, const __grid_constant__ CUtensorMap tmA,
                 const __grid_constant__ CUtensorMap tmB) {
-  constexpr bool CLUSTER = MODE == kSplit, WIDE = MODE == kWide;
-  constexpr int STAGES = stages(TM, MODE), kStageBytes = stage_bytes(TM, MODE), kWideBytes = wide_bytes(TM);
-  constexpr int kXBuffers = wide_buffers(MODE);
+  constexpr int STAGES = stages(TM), kStageBytes = stage_bytes(TM), kWideBytes = wide_bytes(TM);
   constexpr uint32_t kIdesc = idesc_f16_f32(128, TM);
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = align_smem<1024>(smem_raw);
@@ -204,7 +129,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t full_at = tail_at + offsetof(Tail, full), empty_at = tail_at + offsetof(Tail, empty);
   const uint32_t wide_full_at = tail_at + offsetof(Tail, wide_full);
   const uint32_t wide_empty_at = tail_at + offsetof(Tail, wide_empty);
-  const uint32_t x_full_at = tail_at + offsetof(Tail, x_full), x_empty_at = tail_at + offsetof(Tail, x_empty);
   const uint32_t sum_full_at = tail_at + offsetof(Tail, sum_full);
   const uint32_t sum_empty_at = tail_at + offsetof(Tail, sum_empty);
   const int warp = threadIdx.x >> 5;
@@ -218,10 +142,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tail->wide_full[b], kWorkWarps);
       mbar_init(&tail->wide_empty[b], 1);
-    }
-    for (int b = 0; WIDE && b < kXBuffers; ++b) {
-      mbar_init(&tail->x_full[b], 1);
-      mbar_init(&tail->x_empty[b], 1);
     }
     mbar_init(&tail->sum_full, 1);
     mbar_init(&tail->sum_empty, kWorkWarps);
@@ -275,30 +195,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint8_t* to = smem + s * kStageBytes;
             mbar_arrive_expect_tx(&tail->full[s], kStageBytes);
             tma_load_2d(to, &tmB, kb * BK, w.tn * WN, &tail->full[s]);
-            if (!WIDE) {
-              tma_load_2d(to + kRawW, &tmA, kb * BK, w.tm * TM, &tail->full[s]);
-              continue;
-            }
-            const uint32_t x = it % kXBuffers;
-            if (!mbar_wait_at(x_empty_at + 8 * x, ((it / kXBuffers) & 1u) ^ 1u, abort_flag, p.err)) {
-              ok = false;
-              ++it;  // the weights are on their way
-              break;
-            }
-            mbar_arrive_expect_tx(&tail->x_full[x], kWideBytes);
-#pragma unroll
-            for (int half = 0; half < 2; ++half)
-              tma_load_2d(wide + x * kWideBytes + half * (TM * 128), &tmA, kb * BK + half * 64, w.tm * TM,
-                          &tail->x_full[x]);
+            tma_load_2d(to + kRawW, &tmA, kb * BK, w.tm * TM, &tail->full[s]);
           }
           if (CLUSTER) break;  // one tile
         }
         if (!ok) {
           for (uint32_t j = it > STAGES ? it - STAGES : 0u; j < it; ++j)
             mbar_drain_wait(&tail->full[j % STAGES], (j / STAGES) & 1u);
-          // (of the last block perhaps only the weights: that wait runs out)
-          for (uint32_t j = it > kXBuffers ? it - kXBuffers : 0u; WIDE && j < it; ++j)
-            mbar_drain_wait(&tail->x_full[j % kXBuffers], (j / kXBuffers) & 1u);
         }
       }
       __syncwarp();
@@ -315,8 +218,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           bool got = mbar_wait_at(wide_full_at + 8 * b, (it >> 1) & 1u, abort_flag, p.err);
           if (in_chunk == 0)
             got = got && mbar_wait_at(sum_empty_at, (chunk & 1u) ^ 1u, abort_flag, p.err);
-          const uint32_t x = WIDE ? it % kXBuffers : b;  // buffer of tokens
-          if (WIDE) got = got && mbar_wait_at(x_full_at + 8 * x, (it / kXBuffers) & 1u, abort_flag, p.err);
           if (__any_sync(0xffffffffu, !got)) {
             ok = false;
             break;
@@ -325,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool last = in_chunk == kChunk - 1 || kb + 1 == kb1;
           if (elect_one()) {
             const uint32_t at = tmem_base + kWideAt + b * kWideCols;
-            const uint64_t db = db0 + x * (kWideBytes >> 4);
+            const uint64_t db = db0 + b * (kWideBytes >> 4);
 #pragma unroll 1
             for (int half = 0; half < 2; ++half)
 #pragma unroll
@@ -334,7 +235,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                               db + (kk >> 2) * (TM * 128 >> 4) + (kk & 3) * 2, kIdesc,
                               in_chunk != 0 || kk != 0 ? 1u : 0u);
             tc_commit(&tail->wide_empty[b]);
-            if (WIDE) tc_commit(&tail->x_empty[x]);
             if (last) tc_commit(&tail->sum_full);
           }
           __syncwarp();
@@ -368,19 +268,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t sums_at = tmem_base + lanes + static_cast<uint32_t>(half) * kSumCols + side * kMySums;
     const uint32_t wide_at = tmem_base + lanes + kWideAt + static_cast<uint32_t>(half) * kWideHalf + side * 32;
-    const uint32_t raw_w = smem_u32(smem) + static_cast<uint32_t>(wrow) * BK;
+    const uint32_t raw = smem_u32(smem), wide_smem = smem_u32(wide);
+    const uint32_t raw_w = raw + static_cast<uint32_t>(wrow) * BK;
     const uint32_t turn = static_cast<uint32_t>((side * 4) ^ (wrow & 7)) * 16;
     constexpr int kPieces = TM * 8;  // 16-byte pieces of a block's tokens
     constexpr int kMine = (kPieces + kWorkThreads - 1) / kWorkThreads;
-    static_assert(kMine <= 2, "a thread's second piece lies in the other 64 of k");
     const uint32_t token = static_cast<uint32_t>(tid & (TM - 1));
-    const int piece = tid / TM;  // the first; the second is piece + 4
-    const bool has_piece = kPieces >= kWorkThreads || piece < 8;
-    // where it lies, and the first of its two widened pieces (the other: ^ 16)
-    const uint32_t x_from = smem_u32(smem) + kRawW + token * BK +
-                            (static_cast<uint32_t>(piece * 16) ^ ((token & 7) * 16));
-    const uint32_t x_to = smem_u32(wide) + (piece >= 4 ? TM * 128 : 0) + token * 128 +
-                          (static_cast<uint32_t>((piece & 3) * 32) ^ ((token & 7) * 16));
+    const int piece0 = tid / TM;
+    const uint32_t raw_x = raw + kRawW + token * BK, turn_x = (token & 7) * 16;
     uint32_t it = 0, chunk = 0;
     uint32_t sum[kMySums];
 
@@ -418,24 +313,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // Neighbouring threads take neighbouring tokens and the same piece, so that
       // reads and writes of eight lanes fall in different banks.
-      // Neighbouring threads take neighbouring tokens and the same piece, so that
-      // reads and writes of eight lanes fall in different banks.
-      if (!WIDE && has_piece) {
+      const uint32_t to = wide_smem + b * kWideBytes;
 #pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-          const uint4 x = ld_shared_u4((x_from ^ (i * 64)) + from);
-          uint32_t v[8];
-          widen4(x.x, v[0], v[1]);
-          widen4(x.y, v[2], v[3]);
-          widen4(x.z, v[4], v[5]);
-          widen4(x.w, v[6], v[7]);
-          const uint32_t to = x_to + b * kWideBytes + i * (TM * 128);
-          st_shared_u4(to, v[0], v[1], v[2], v[3]);
-          st_shared_u4(to ^ 16, v[4], v[5], v[6], v[7]);
-        }
+      for (int i = 0; i < kMine; ++i) {
+        const int c = piece0 + i * (kWorkThreads / TM);
+        if (kPieces < kWorkThreads && c >= 8) continue;
+        const uint4 x = ld_shared_u4(raw_x + from + (static_cast<uint32_t>(c * 16) ^ turn_x));
+        uint32_t v[8];
+        widen4(x.x, v[0], v[1]);
+        widen4(x.y, v[2], v[3]);
+        widen4(x.z, v[4], v[5]);
+        widen4(x.w, v[6], v[7]);
+        // two pieces of the first or the other 64 of k
+        const uint32_t at = to + (c >= 4 ? TM * 128 : 0) + token * 128;
+        const uint32_t first = static_cast<uint32_t>((c & 3) * 32) ^ turn_x;
+        st_shared_u4(at + first, v[0], v[1], v[2], v[3]);
+        st_shared_u4(at + (first ^ 16), v[4], v[5], v[6], v[7]);
       }
       tc_wait_st();
-      if (!WIDE) fence_proxy_async_smem();
+      fence_proxy_async_smem();
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) {
@@ -491,49 +387,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int t = first; !CLUSTER && t < ld_shared_i4(order_at).x; t += ld_shared_i4(order_at).w) {
       if (p.num_kb > 0) {
         const int4 o = ld_shared_i4(order_at);
-        const int row0 = tile_of(t, o.y, o.z).tm * TM + side * kMySums;
-        for (int j = lane; j < kMySums; j += 32)
-          cp_async_4_at(my_scales + 4 * j, row0 + j < p.M ? p.sa + row0 + j : p.sa,
-                        row0 + j < p.M ? 4u : 0u);
+        fetch_scales<kMySums>(p, my_scales, tile_of(t, o.y, o.z).tm * TM + side * kMySums);
       }
       if (!sums()) break;
       cp_async_wait_all();
       __syncwarp();
       const int4 o = ld_shared_i4(order_at);
       const Tile w = tile_of(t, o.y, o.z);
-      const int n = w.tn * WN + wrow, row0 = w.tm * TM + side * kMySums;
-      const int rows = min(p.M - row0, kMySums);  // below 1: none
-      const bool in = n < p.N;
-      const float cs = in && p.num_kb > 0 ? p.alpha * p.sb[n] : 0.0f;
-      const float bias = in && p.bias != nullptr ? p.bias[n] : 0.0f;
-      const int64_t at = row0 * p.ldd + n;
-      if (p.d_pair && w.tn * WN + WN <= p.N && rows == kMySums) {
-        // Two tokens' values of a channel become two channels' of a token: even
-        // lanes take the first token's, odd ones the second's.
-        const bool odd = lane & 1;
-        __nv_bfloat16* d = static_cast<__nv_bfloat16*>(p.D) + at + (odd ? p.ldd - 1 : 0);
-#pragma unroll
-        for (int j = 0; j < kMySums; j += 4) {
-          const float4 sa = ld_shared_v4(my_scales + 4 * j);
-          const float v0 = value(p, sum[j], cs, sa.x, bias), v1 = value(p, sum[j + 1], cs, sa.y, bias);
-          const float v2 = value(p, sum[j + 2], cs, sa.z, bias), v3 = value(p, sum[j + 3], cs, sa.w, bias);
-          const float x = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
-          const float y = __shfl_xor_sync(0xffffffffu, odd ? v2 : v3, 1);
-          *reinterpret_cast<uint32_t*>(d) = odd ? pack_bf16(x, v1) : pack_bf16(v0, x);
-          d += 2 * p.ldd;
-          *reinterpret_cast<uint32_t*>(d) = odd ? pack_bf16(y, v3) : pack_bf16(v2, y);
-          d += 2 * p.ldd;
-        }
-      } else if (in) {
-#pragma unroll
-        for (int j = 0; j < kMySums; j += 4) {
-          const float4 sa = ld_shared_v4(my_scales + 4 * j);
-          const float s4[4] = {sa.x, sa.y, sa.z, sa.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (j + i < rows) finish(p, at + (j + i) * p.ldd, value(p, sum[j + i], cs, s4[i], bias));
-        }
-      }
+      write_channel<kMySums>(p, sum, my_scales, w.tn * WN + wrow, w.tm * TM + side * kMySums);
       __syncwarp();  // the scales have been read
     }
     if (CLUSTER) {
@@ -573,36 +434,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc(tmem_base, kTmemCols);
 }
 
-// int8 rows -> fp16 rows of pitch ld2 (a multiple of 8; what is behind a row's
-// end is zero).  16 values a thread.
-__global__ void __launch_bounds__(256) widen_rows_kernel(const int8_t* src, int64_t ld, uint16_t* dst,
-                                                         int64_t ld2, int64_t rows, int64_t cols, int vec) {
-  grid_dependency_wait();
-  grid_launch_dependents();
-  const int64_t pieces = (ld2 + 15) / 16, total = rows * pieces;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * 256;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += step) {
-    const int64_t r = total < (int64_t{1} << 31) ? static_cast<uint32_t>(i) / static_cast<uint32_t>(pieces) : i / pieces;
-    const int64_t c = (i - r * pieces) * 16;
-    const int8_t* s = src + r * ld + c;
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-    if (vec && c + 16 <= cols) {
-      const uint4 v = __ldcs(reinterpret_cast<const uint4*>(s));
-      w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-    } else {
-#pragma unroll
-      for (int j = 0; j < 16; ++j)
-        if (c + j < cols) w[j >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(s[j])) << (8 * (j & 3));
-    }
-    uint32_t v[8];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) widen4(w[j], v[2 * j], v[2 * j + 1]);
-    uint4* d = reinterpret_cast<uint4*>(dst + r * ld2 + c);
-    d[0] = make_uint4(v[0], v[1], v[2], v[3]);
-    if (c + 8 < ld2) d[1] = make_uint4(v[4], v[5], v[6], v[7]);
-  }
-}
-
 // Clusters of S CTAs that can be resident at once on the current device; 0 if
 // unknown.
 int max_clusters(int S) {
@@ -612,7 +443,7 @@ int max_clusters(int S) {
   const int known = cache[dev][S].load(std::memory_order_relaxed);
   if (known != 0) return known;
   int n = 0;
-  if (ops_allow_smem<int8_kernel<kMaxTokens, kSplit>>(kSmemBytes) == cudaSuccess) {
+  if (ops_allow_smem<int8_kernel<kMaxTokens, true>>(kSmemBytes) == cudaSuccess) {
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -624,7 +455,7 @@ int max_clusters(int S) {
     cfg.dynamicSmemBytes = kSmemBytes;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, int8_kernel<kMaxTokens, kSplit>, &cfg) != cudaSuccess) n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, int8_kernel<kMaxTokens, true>, &cfg) != cudaSuccess) n = 0;
   }
   cudaGetLastError();
   if (n > 0) cache[dev][S].store(n, std::memory_order_relaxed);
@@ -651,9 +482,9 @@ template <int TM>
 cudaError_t launch(int64_t tiles, int num_sms, const Int8Args& a, const CUtensorMap& tmA,
                    const CUtensorMap& tmB, cudaStream_t s) {
   if (a.cluster > 1)
-    return ops_launch<int8_kernel<TM, kSplit>>(dim3(static_cast<unsigned>(tiles * a.cluster)), kThreads,
+    return ops_launch<int8_kernel<TM, true>>(dim3(static_cast<unsigned>(tiles * a.cluster)), kThreads,
                                              kSmemBytes, a.cluster, s, a, tmA, tmB);
-  return ops_launch<int8_kernel<TM, kSingle>>(dim3(static_cast<unsigned>(tiles < num_sms ? tiles : num_sms)),
+  return ops_launch<int8_kernel<TM, false>>(dim3(static_cast<unsigned>(tiles < num_sms ? tiles : num_sms)),
                                             kThreads, kSmemBytes, 1, s, a, tmA, tmB);
 }
 
@@ -706,48 +537,34 @@ extern "C" gemm_status_t gemm_int8gemm(int64_t M, int64_t N, int64_t K, float al
   if (tiles + sms > kOpsMaxDim) return GEMM_ERR_UNSUPPORTED;
   a.cluster = choose_split(tiles, a.num_kb, sms);
   std::unique_lock<std::mutex> lock;
+  if (product && tm == kMaxTokens && int8_wide_pays(M, N, K, tiles, a.cluster, sms)) {
+    // without the memory (inside a capture, say) the way below: the same sums
+    uint8_t* buf = nullptr;
+    st = abi_stage(s, int8_wide_bytes(M, N, K), lock, &buf);
+    if (st == GEMM_OK) return int8_wide(a, K, A, lda, B, ldb, buf, sms, s);
+    if (st != GEMM_ERR_NO_MEMORY) return st;
+    lock = std::unique_lock<std::mutex>();
+  }
   CUtensorMap tmA{}, tmB{};
-  bool wide = false;
   if (product) {
     ByteOperand oa{A, M, K, lda, 1, 0}, ob{B, N, K, ldb, 1, 0};
+    const int64_t need_a = byte_tma_ok(oa) ? 0 : byte_staged(oa);
     const int64_t need_b = byte_tma_ok(ob) ? 0 : byte_staged(ob);
-    const int64_t ld2 = (K + 7) / 8 * 8, wide_a = (2 * M * ld2 + 255) / 256 * 256;
-    uint8_t* buf = nullptr;
-    // The tokens widened by themselves, if there are enough tiles to share them
-    // and memory for them.
-    if (tm == kMaxTokens && tiles > sms) {
-      st = abi_stage(s, wide_a + need_b, lock, &buf);
-      wide = st == GEMM_OK;
-      if (!wide) lock = std::unique_lock<std::mutex>();
-    }
-    const int64_t need_a = wide || byte_tma_ok(oa) ? 0 : byte_staged(oa);
-    if (!wide && need_a + need_b > 0) {
+    if (need_a + need_b > 0) {
+      uint8_t* buf = nullptr;
       st = abi_stage(s, need_a + need_b, lock, &buf);
       if (st != GEMM_OK) return st;
+      cudaError_t e = need_a > 0 ? byte_stage(oa, buf, sms, s) : cudaSuccess;
+      if (e == cudaSuccess && need_b > 0) e = byte_stage(ob, buf + need_a, sms, s);
+      if (e != cudaSuccess) return abi_from_cuda(e);
     }
-    cudaError_t e = cudaSuccess;
-    if (wide) {
-      const int64_t want = (M * ((ld2 + 15) / 16) + 255) / 256, fit = static_cast<int64_t>(sms) * 16;
-      uint16_t* to = reinterpret_cast<uint16_t*>(buf);
-      const int vec = !ops_misaligned(A, 16) && (M == 1 || lda % 16 == 0);
-      e = ops_launch<widen_rows_kernel>(dim3(static_cast<unsigned>(want < fit ? want : fit)), 256, 0, 1, s, A,
-                                        lda, to, ld2, M, K, vec);
-    } else if (need_a > 0) {
-      e = byte_stage(oa, buf, sms, s);
-    }
-    if (e == cudaSuccess && need_b > 0) e = byte_stage(ob, buf + (wide ? wide_a : need_a), sms, s);
-    if (e != cudaSuccess) return abi_from_cuda(e);
-    const int64_t da[2] = {K, M}, ta[1] = {wide ? 2 * ld2 : byte_pitch(oa)};
+    const int64_t da[2] = {K, M}, ta[1] = {byte_pitch(oa)};
     const int64_t db[2] = {K, N}, tb[1] = {byte_pitch(ob)};
-    const uint32_t ba[2] = {wide ? 64u : static_cast<uint32_t>(BK), static_cast<uint32_t>(tm)}, bb[2] = {BK, WN};
-    if (!abi_encode_tiled(&tmA, wide ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
-                          wide ? buf : oa.p, da, ta, ba) ||
+    const uint32_t ba[2] = {BK, static_cast<uint32_t>(tm)}, bb[2] = {BK, WN};
+    if (!abi_encode_tiled(&tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, oa.p, da, ta, ba) ||
         !abi_encode_tiled(&tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, ob.p, db, tb, bb))
       return GEMM_ERR_LAUNCH;
   }
-  if (wide)
-    return abi_from_cuda(ops_launch<int8_kernel<kMaxTokens, kWide>>(dim3(static_cast<unsigned>(sms)), kThreads,
-                                                                    kSmemBytes, 1, s, a, tmA, tmB));
   switch (tm) {
     case 16: return abi_from_cuda(launch<16>(tiles, sms, a, tmA, tmB, s));
     case 32: return abi_from_cuda(launch<32>(tiles, sms, a, tmA, tmB, s));

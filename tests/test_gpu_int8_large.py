@@ -1,0 +1,143 @@
+"""gemm_int8gemm at sizes where both operands are widened beforehand, against sums in 64 bits: the same
+bounds as for the smaller products (exact sums; six roundings of 2^-24 and the output's half step)."""
+import pytest
+import torch
+
+import dense_gemm_12_gb300 as g
+from gpu_helpers import check_device_error
+from ops_ref import DTYPE, U32, UBF, Guarded, randn
+from test_gpu_int8 import ints, near, sums64
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib(gemm_lib, cuda_device):
+    yield
+
+
+def kernels(run):
+    """The names of the kernels that `run` launches; the profiler may miss the first ones of a process."""
+    for _ in range(3):
+        with torch.profiler.profile(activities=[torch.profiler.ProfilerActivity.CUDA]) as prof:
+            run()
+            torch.cuda.synchronize()
+        names = " ".join(e.key for e in prof.key_averages())
+        if "int8" in names:
+            break
+    return names
+
+
+# whole and partial tiles of 256 x 256; less than a k-block of 64, one, a chunk of 1024 and around it
+SHAPES = [(2304, 2560, 64), (2100, 2500, 5), (2305, 2049, 1025), (2100, 2500, 1023), (2048, 4096, 512),
+          (4097, 1031, 2048), (1031, 6000, 2113), (3000, 5000, 1999), (2561, 2560, 8200)]
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES)
+@pytest.mark.parametrize("pad,off", [(0, 0), (5, 3), (16, 16)])
+def test_sums_scales_bias_and_beta(M, N, K, pad, off):
+    A, B = ints(M, K, 1, pad=pad, off=off), ints(N, K, 2, pad=pad, off=off)
+    sums = sums64(A.t, B.t)
+    if K <= 1024:
+        D = Guarded((M, N), torch.float32, 3)
+        g.int8gemm(A.t, torch.ones(M, device="cuda"), B.t, torch.ones(N, device="cuda"), D.t)
+        check_device_error()
+        assert torch.equal(D.t.double(), sums)
+        assert D.clean_outside()
+    sa, sb, bias = randn(M, seed=3).exp(), randn(N, seed=4).exp(), randn(N, seed=5, scale=100.0)
+    prod = -0.75 * sums * sa.double()[:, None] * sb.double()
+    for out, beta, ld in (("f32", 0.5, 1), ("bf16", 0.5, 1), ("bf16", 0.0, 2)):
+        D = Guarded((M, N), DTYPE[out], ld).set(randn(M, N, seed=6, scale=1000.0))
+        old = beta * D.t.double()
+        g.int8gemm(A.t, sa, B.t, sb, D.t, alpha=-0.75, beta=beta, bias=bias)
+        check_device_error()
+        near(D.t, prod + bias.double() + old, prod.abs() + bias.double().abs() + old.abs())
+        assert D.clean_outside()
+
+
+def test_which_way_a_product_goes():
+    def names(M, N, K):
+        A, B = ints(M, K, 1).t, ints(N, K, 2).t
+        D = torch.empty(M, N, device="cuda")
+        return kernels(lambda: g.int8gemm(A, torch.ones(M, device="cuda"), B, torch.ones(N, device="cuda"), D))
+
+    assert {s: "int8_wide_kernel" in names(*s) for s in SHAPES} == dict.fromkeys(SHAPES, True)
+    small = [(16, 4096, 1024), (128, 4096, 1024), (256, 256, 4096), (1, 20000, 512)]
+    assert {s: "int8_wide_kernel" in names(*s) for s in small} == dict.fromkeys(small, False)
+
+
+@pytest.mark.parametrize("a,b", [(-128, -128), (127, -128), (127, 127)])
+@pytest.mark.parametrize("K", [1024, 1025, 16400])
+def test_largest_sums(K, a, b):
+    # every product the same: a chunk's sums reach 2^24
+    M, N = 2304, 2304
+    pitch = -(-K // 16) * 16
+    A, B = (torch.full((n, pitch), v, dtype=torch.int8, device="cuda")[:, :K] for n, v in ((M, a), (N, b)))
+    A[:, 0] = 1   # and an odd number in between
+    A[M // 2:, K - 1] = 3
+    ones = torch.ones(M, device="cuda")
+    D = torch.empty(M, N, device="cuda")
+    g.int8gemm(A, ones, B, ones[:N], D)
+    check_device_error()
+    assert torch.equal(D, sums64(A, B).float())   # the conversion, to nearest even, is the only rounding
+
+
+def test_the_same_bits_in_a_capture_on_streams_and_with_the_smaller_tiles():
+    M, N, K = 2100, 2500, 704
+    A, B = ints(M, K, 1).t, ints(N, K, 2).t
+    sa, sb = randn(M, seed=3).exp(), randn(N, seed=4).exp()
+
+    def run(D):
+        g.int8gemm(A, sa, B, sb, D)
+
+    want = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    run(want)
+    # row blocks of 128 tokens take the other way: the same sums, finished alike
+    parts = torch.empty_like(want)
+    for i in range(0, M, 128):
+        g.int8gemm(A[i:i + 128], sa[i:i + 128], B, sb, parts[i:i + 128])
+    assert torch.equal(parts, want)
+    torch.cuda.synchronize()
+    # a stream without a buffer: a capture cannot have one
+    for warm in (False, True):
+        s = torch.cuda.Stream()
+        D, E = torch.empty_like(want), torch.empty_like(want)
+        if warm:
+            with torch.cuda.stream(s):
+                run(E)
+            s.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            run(D)
+        D.zero_()
+        E.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            graph.replay()
+            run(E)          # behind the replay, in the same buffer
+            graph.replay()
+        s.synchronize()
+        check_device_error()
+        assert torch.equal(D, want) and torch.equal(E, want)
+    # two streams at once, each with a buffer of its own
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [torch.empty_like(want) for _ in range(2)]
+    for _ in range(4):
+        for s, D in zip(streams, outs):
+            with torch.cuda.stream(s):
+                run(D)
+    torch.cuda.synchronize()
+    assert all(torch.equal(D, want) for D in outs)
+
+
+def test_row_blocks_and_nothing_behind_them():
+    # rows behind the last token and columns behind the last channel keep their bytes
+    M, N, K = 2101, 2503, 130
+    A, B = ints(M, K, 1, pad=14).t, ints(N, K, 2, pad=14).t
+    for dtype in (torch.float32, torch.bfloat16):
+        D = torch.full((M + 40, N + 61), 7.0, dtype=dtype, device="cuda")
+        g.int8gemm(A, torch.ones(M, device="cuda"), B, torch.ones(N, device="cuda"), D[:M, :N])
+        check_device_error()
+        mag = sums64(A, B)
+        assert bool(((D[:M, :N].double() - mag).abs() <= (UBF if dtype == torch.bfloat16 else U32) * mag.abs()).all())
+        assert bool((D[M:] == 7).all()) and bool((D[:, N:] == 7).all())
