@@ -3,13 +3,15 @@
     python examples/expert_layer.py
 
 Serving (``forward``): h = x + residual and its norm in fp8 (``rmsnorm``), router logits
-(``bf16gemm``), the rows gathered expert by expert, both of the experts' products in fp8
+(``bf16gemm``), each token's experts and their weights (``expert_route``), the rows gathered expert
+by expert (``expert_sort``, ``expert_dispatch``), both of the experts' products in fp8
 (``fp8gemm_grouped``, weights quantised once with ``fp8_quantize``, the hidden values quantised in
-between), and an output projection of the combined rows (``fp8gemm``).
+between), the rows added up again (``expert_combine``) and an output projection (``fp8gemm``).
 
 Training (``gradients``): the experts' products in bf16 (``bf16gemm_grouped``), their gradients
-with respect to rows and weights (the transposed product and ``bf16gemm_grouped_wgrad``) and the
-norm's (``rmsnorm_backward``).
+with respect to rows and weights (the transposed product and ``bf16gemm_grouped_wgrad``), those of
+the weights of a token's experts and of the router (``expert_combine_backward``,
+``expert_route_backward``) and the norm's (``rmsnorm_backward``).
 
 No call waits for the GPU: which rows an expert has is only ever known there.
 """
@@ -62,52 +64,53 @@ class ExpertLayer:
         self.out_q = out_q[0], out_s[0]
 
     def route(self, y):
-        """(place of each gathered row's token, its weight, the experts' offsets)."""
+        """y (rows, dim) -> the router's logits, each token's experts and their weights (rows, top), the
+        rows of its pairs among the gathered ones (rows, top) and the experts' offsets."""
         rows = y.shape[0]
         logits = torch.empty(rows, self.experts, device="cuda")
         g.bf16gemm(y, self.router, logits)
-        weight, expert = logits.softmax(-1).topk(self.top, dim=-1)
-        expert, order = expert.reshape(-1).sort(stable=True)
-        counts = (expert[:, None] == torch.arange(self.experts, device="cuda")).sum(0)
-        offsets = torch.nn.functional.pad(counts.cumsum(0), (1, 0)).to(torch.int32)
-        return order // self.top, weight.reshape(-1)[order], offsets
-
-    def combine(self, rows, token, weight, n):
-        return torch.zeros(n, self.dim, device="cuda").index_add_(0, token, rows.float() * weight[:, None])
+        expert = torch.empty(rows, self.top, dtype=torch.int32, device="cuda")
+        slot, weight = torch.empty_like(expert), torch.empty(rows, self.top, device="cuda")
+        offsets = torch.empty(self.experts + 1, dtype=torch.int32, device="cuda")
+        g.expert_route(logits, expert, weight)
+        g.expert_sort(expert, slot, offsets)
+        return logits, expert, weight, slot, offsets
 
     def forward(self, x, residual):
         """x, residual (rows, dim) bf16 -> (the layer's output, the new residual h)."""
         rows = x.shape[0]
+        n = rows * self.top
         h, y = torch.empty_like(residual), torch.empty_like(x)
         q, s = empty_fp8(rows, self.dim), torch.empty(blocks(self.dim), rows, device="cuda")
         g.rmsnorm(x, self.norm, eps=self.eps, residual=residual, h=h, y=y, q=q, scales=s)
-        token, weight, offsets = self.route(y)
-        n = token.shape[0]
-        a = empty_fp8(n, self.dim)
-        # (rows of fp8 are gathered as bytes)
-        a.view(torch.uint8).copy_(q.view(torch.uint8)[token])
+        _, _, weight, slot, offsets = self.route(y)
+        a, a_s = empty_fp8(n, self.dim), torch.empty(blocks(self.dim), n, device="cuda")
+        g.expert_dispatch(q, slot, a, x_scales=s, a_scales=a_s)
         hid = torch.empty(n, self.hidden, dtype=torch.bfloat16, device="cuda")
-        g.fp8gemm_grouped(a, s[:, token].contiguous(), *self.up_q, offsets, hid)
+        g.fp8gemm_grouped(a, a_s, *self.up_q, offsets, hid)
         hid = torch.nn.functional.gelu(hid)
         hq, hs = empty_fp8(n, self.hidden), torch.empty(blocks(self.hidden), n, device="cuda")
         g.fp8_quantize(hid, hq, hs)
         back = torch.empty(n, self.dim, dtype=torch.bfloat16, device="cuda")
         g.fp8gemm_grouped(hq, hs, *self.down_q, offsets, back)
-        both = self.combine(back, token, weight, rows)
+        both = torch.empty(rows, self.dim, device="cuda")
+        g.expert_combine(back, slot, both, weight)
         g.fp8_quantize(both, q, s)
         out = torch.empty(rows, self.dim, dtype=torch.bfloat16, device="cuda")
         g.fp8gemm(q, s, *self.out_q, out)
         return out, h
 
     def gradients(self, x, residual, grad):
-        """Loss sum(grad * experts(norm(x + residual))) for a fixed routing: the experts' output
-        and the gradients of h, the norm's weight, and both weights."""
+        """Loss sum(grad * experts(norm(x + residual))): the experts' output and the gradients of h,
+        the norm's weight, the router and both of the experts' weights (which experts a token has is
+        fixed, how much each counts is not)."""
         rows = x.shape[0]
+        n = rows * self.top
         h, y, rstd = torch.empty_like(residual), torch.empty_like(x), torch.empty(rows, device="cuda")
         g.rmsnorm(x, self.norm, eps=self.eps, residual=residual, h=h, y=y, rstd=rstd)
-        token, weight, offsets = self.route(y)
-        n = token.shape[0]
-        a = y[token]
+        logits, expert, weight, slot, offsets = self.route(y)
+        a = torch.zeros(n, self.dim, dtype=torch.bfloat16, device="cuda")
+        g.expert_dispatch(y, slot, a)
         pre = torch.empty(n, self.hidden, dtype=torch.bfloat16, device="cuda")
         g.bf16gemm_grouped(a, self.up, offsets, pre)
         with torch.enable_grad():
@@ -116,9 +119,11 @@ class ExpertLayer:
         mid = act.detach().to(torch.bfloat16)
         back = torch.empty(n, self.dim, dtype=torch.bfloat16, device="cuda")
         g.bf16gemm_grouped(mid, self.down, offsets, back)
-        out = self.combine(back, token, weight, rows)
+        out = torch.empty(rows, self.dim, device="cuda")
+        g.expert_combine(back, slot, out, weight)
 
-        d_back = (grad.float()[token] * weight[:, None]).to(torch.bfloat16)
+        d_back, d_weight = torch.empty_like(back), torch.empty_like(weight)
+        g.expert_combine_backward(grad, back, slot, weight, da=d_back, dweight=d_weight)
         d_down = torch.empty(self.down.shape, device="cuda")
         g.bf16gemm_grouped_wgrad(mid, d_back, offsets, d_down)
         d_mid = torch.empty_like(mid)
@@ -129,21 +134,29 @@ class ExpertLayer:
         g.bf16gemm_grouped_wgrad(a, d_pre, offsets, d_up)
         d_a = torch.empty_like(a)
         g.bf16gemm_grouped(d_pre, self.up, offsets, d_a, transpose_b=True)
-        d_y = torch.zeros(rows, self.dim, device="cuda").index_add_(0, token, d_a.float())
+        d_y = torch.empty(rows, self.dim, device="cuda")
+        g.expert_combine(d_a, slot, d_y)
+        # the router: one group of all the rows
+        d_logits = torch.empty(rows, self.experts, dtype=torch.bfloat16, device="cuda")
+        g.expert_route_backward(logits, expert, d_weight, d_logits)
+        all_rows = torch.arange(2, dtype=torch.int32, device="cuda") * rows
+        d_router = torch.empty(1, self.dim, self.experts, device="cuda")
+        g.bf16gemm_grouped_wgrad(y, d_logits, all_rows, d_router)
+        g.bf16gemm_grouped(d_logits, self.router[None], all_rows, d_y, beta=1.0, transpose_b=True)
         d_h, d_norm = torch.empty_like(h), torch.empty_like(self.norm)
         g.rmsnorm_backward(d_y, h, self.norm, rstd, d_h, d_norm)
-        return out, {"h": d_h, "norm": d_norm, "up": d_up, "down": d_down}
+        return out, {"h": d_h, "norm": d_norm, "router": d_router[0], "up": d_up, "down": d_down}
 
     def plain(self, x, residual, project=True):
         """The same layer in fp32 torch operations on the bf16 weights (differentiable)."""
         h = x.float() + residual.float()
         y = h * (h.square().mean(-1, keepdim=True) + self.eps).rsqrt() * self.norm
-        token, weight, offsets = self.route(y.detach().to(torch.bfloat16))
-        expert = torch.bucketize(torch.arange(token.shape[0], device="cuda"), offsets[1:], right=True)
-        a = y[token]
+        expert = self.route(y.detach().to(torch.bfloat16))[1].long()
+        weight = (y @ self.router.float()).softmax(-1).gather(1, expert)
+        a, expert = y.repeat_interleave(self.top, 0), expert.reshape(-1)
         mid = torch.nn.functional.gelu(torch.einsum("nk,nkf->nf", a, self.up.float()[expert]))
         back = torch.einsum("nf,nfk->nk", mid, self.down.float()[expert])
-        out = torch.zeros_like(y).index_add(0, token, back * weight[:, None])
+        out = (back.unflatten(0, weight.shape) * weight[..., None]).sum(1)
         return out @ self.out.float() if project else out
 
 
@@ -160,16 +173,17 @@ def main(rows=96, dim=512, hidden=384, experts=8):
         out, _ = layer.forward(x, residual)
         served = relative(out, layer.plain(x, residual))
         got, grads = layer.gradients(x, residual, grad)
-    up, down, norm = layer.up, layer.down, layer.norm
+    up, down, norm, router = layer.up, layer.down, layer.norm, layer.router
     h = (x.float() + residual.float()).requires_grad_()
     layer.up, layer.down = (w.float().requires_grad_() for w in (up, down))
-    layer.norm = norm.clone().requires_grad_()
+    layer.norm, layer.router = norm.clone().requires_grad_(), router.clone().requires_grad_()
     want = layer.plain(h, torch.zeros_like(h), project=False)
     (want * grad.float()).sum().backward()
     errors = {"output": relative(got, want.detach()), "h": relative(grads["h"], h.grad),
               "norm": relative(grads["norm"], layer.norm.grad),
+              "router": relative(grads["router"], layer.router.grad),
               "up": relative(grads["up"], layer.up.grad), "down": relative(grads["down"], layer.down.grad)}
-    layer.up, layer.down, layer.norm = up, down, norm
+    layer.up, layer.down, layer.norm, layer.router = up, down, norm, router
     status = g.gemm_check_device_error(torch.cuda.current_stream().cuda_stream)
     if status != 0:
         raise g.GemmError(status, "expert_layer")
