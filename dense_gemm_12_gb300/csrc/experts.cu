@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kThreads) route_grad_kernel(const __grid_const
 // without an expert count as one more expert behind the last.
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortAhead = 8;  // rounds whose ids are loaded together
+constexpr int kSortAhead = 8;  // rounds whose ids are loaded together, at most
 
 struct SortArgs {
   int64_t n;
@@ -252,7 +252,7 @@ struct SortArgs {
 
 // Lanes of the warp with this lane's key (below 2^bits; all lanes call it).  By
 // a vote per bit: the instruction that compares all lanes takes some 300 cycles
-// where their keys differ (131072 pairs over 256 experts: 14.3 us against 6.9).
+// where their keys differ (131072 pairs over 256 experts: 14.3 us against 8.0).
 __device__ __forceinline__ uint32_t same_key(int key, int bits) {
   uint32_t same = 0xffffffffu;
   for (int b = 0; b < bits; ++b) {
@@ -294,7 +294,9 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const __grid_c
     a.counts[static_cast<int64_t>(blockIdx.x) * buckets + g] = cnt[g];
 }
 
-// Shared memory: first[experts + 1], then counts [warp][experts + 1].
+// Shared memory: first[experts + 1], then counts [warp][experts + 1].  AHEAD:
+// rounds taken together, so that a whole part needs no branch between them.
+template <int AHEAD>
 __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const __grid_constant__ SortArgs a) {
   extern __shared__ uint4 dyn_smem[];
   __shared__ int warp_total[kSortWarps];
@@ -315,10 +317,10 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const __grid_c
 
   // A part of one batch of rounds keeps its keys, and each pair's place within
   // the part, for the second half; a longer one goes through its pairs again.
-  int key[kSortAhead], rank[kSortAhead];
+  int key[AHEAD], rank[AHEAD];
   auto load = [&](int64_t base) {
 #pragma unroll
-    for (int u = 0; u < kSortAhead; ++u) {
+    for (int u = 0; u < AHEAD; ++u) {
       const int64_t i = base + u * 32 + lane;
       key[u] = i < hi ? sort_key(a, i) : buckets;
     }
@@ -326,9 +328,9 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const __grid_c
   // Places of a batch from `mine`, which moves on.  A whole batch runs without
   // branches between its rounds.
   auto count = [&](int64_t base) {
-    const bool whole = base + 32 * kSortAhead <= hi;
+    const bool whole = base + 32 * AHEAD <= hi;
 #pragma unroll
-    for (int u = 0; u < kSortAhead; ++u) {
+    for (int u = 0; u < AHEAD; ++u) {
       if (!whole && base + u * 32 >= hi) break;
       const uint32_t same = same_key(key[u], a.bits);
       const bool in = key[u] < buckets;
@@ -350,10 +352,10 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const __grid_c
       total += c;
     }
   };
-  const bool once = part <= 32 * kSortAhead;
+  const bool once = part <= 32 * AHEAD;
   int total, before;
   others(static_cast<int>(threadIdx.x), total, before);
-  for (int64_t base = lo; base < hi; base += 32 * kSortAhead) {
+  for (int64_t base = lo; base < hi; base += 32 * AHEAD) {
     load(base);
     count(base);
   }
@@ -392,13 +394,13 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const __grid_c
     __syncthreads();
   }
 
-  for (int64_t base = lo; base < hi; base += 32 * kSortAhead) {
+  for (int64_t base = lo; base < hi; base += 32 * AHEAD) {
     if (!once) {
       load(base);
       count(base);
     }
 #pragma unroll
-    for (int u = 0; u < kSortAhead; ++u) {
+    for (int u = 0; u < AHEAD; ++u) {
       const int64_t i = base + u * 32 + lane;
       if (i >= hi) continue;
       // (`once`: the part's first place was not in `mine` yet)
@@ -683,9 +685,11 @@ struct LaunchRouteGrad {
 };
 
 // Pairs of a launch with one CTA, and pairs per CTA of one with several (as
-// many CTAs as kSortMostCtas).
+// many CTAs as kSortMostCtas).  Chunks of 1024 and 4096 instead: 131072 pairs
+// over 256 experts 9.8 and 8.0 us against 6.7, 32768 over 64 5.2 and 8.3
+// against 5.2.
 constexpr int64_t kSortSingle = 4096;
-constexpr int64_t kSortChunk = 4096;
+constexpr int64_t kSortChunk = 2048;
 constexpr int64_t kSortMostCtas = 256;
 
 template <typename T>
@@ -809,7 +813,9 @@ gemm_status_t gemm_expert_sort(int64_t n, int64_t G, const int32_t* expert, int3
     const cudaError_t e = ops_launch<sort_count_kernel>(grid, kSortThreads, sizeof(int) * buckets, 1, s, a);
     if (e != cudaSuccess) return abi_from_cuda(e);
   }
-  return abi_from_cuda(ops_launch<sort_place_kernel>(grid, kSortThreads, smem, 1, s, a));
+  if (a.chunk <= 4 * unit)
+    return abi_from_cuda(ops_launch<sort_place_kernel<4>>(grid, kSortThreads, smem, 1, s, a));
+  return abi_from_cuda(ops_launch<sort_place_kernel<kSortAhead>>(grid, kSortThreads, smem, 1, s, a));
 }
 
 gemm_status_t gemm_expert_dispatch(int64_t rows, int64_t top, int64_t n, int64_t dim, int elem_bytes,
