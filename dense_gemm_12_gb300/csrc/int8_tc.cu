@@ -405,22 +405,43 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int j = 0; j < kMySums; ++j) out[j * WN] = sum[j];
       __syncwarp();
-      cluster_sync();  // every part's sums are in its shared memory
-      // after a wait ran out the sums are not complete; the error word says so
       const Tile w = tile_of(first, tiles_n, tiles_m);
       // 512 threads: every other token each
       const int n = w.tn * WN + (tid & (WN - 1)), row0 = w.tm * TM;
-      if (first < tiles && !ld_shared_volatile(abort_flag) && n < p.N) {
-        const float cs = p.alpha * p.sb[n];
-        const float bias = p.bias != nullptr ? p.bias[n] : 0.0f;
+      const bool in = first < tiles && n < p.N;
+      const float cs = in ? p.alpha * p.sb[n] : 0.0f;
+      const float bias = in && p.bias != nullptr ? p.bias[n] : 0.0f;
+      cluster_sync();  // every part's sums are in its shared memory
+      // after a wait ran out the sums are not complete; the error word says so
+      if (in && !ld_shared_volatile(abort_flag)) {
         const int j1 = min((part + 1) * TM / split, p.M - row0);
         const uint32_t mine = smem_u32(smem) + static_cast<uint32_t>(tid & (WN - 1)) * 4;
-        for (int j = part * TM / split + (tid >> 8); j < j1; j += 2) {
-          uint32_t total = 0;
-          for (int src = 0; src < split; ++src)
-            total += __float_as_uint(ld_shared_cluster_f32(
-                mapa_shared(mine + static_cast<uint32_t>(j) * (WN * 4), static_cast<uint32_t>(src))));
-          finish(p, (row0 + j) * p.ldd + n, value(p, total, cs, p.sa[row0 + j], bias));
+        // Other CTAs' values are on their way for a microsecond: those of four
+        // tokens and four parts at once.
+        for (int j0 = part * TM / split + (tid >> 8); j0 < j1; j0 += 8) {
+          float sa[4];
+          uint32_t total[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+          for (int u = 0; u < 4; ++u) sa[u] = j0 + 2 * u < j1 ? p.sa[row0 + j0 + 2 * u] : 0.0f;
+          for (int src = 0; src < split; src += 4) {
+            uint32_t v[4][4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t from = mapa_shared(mine, static_cast<uint32_t>(min(src + q, split - 1)));
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                v[q][u] = 0u;
+                if (src + q < split && j0 + 2 * u < j1)
+                  v[q][u] = __float_as_uint(ld_shared_cluster_f32(from + static_cast<uint32_t>(j0 + 2 * u) * (WN * 4)));
+              }
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) total[u] += v[0][u] + v[1][u] + v[2][u] + v[3][u];
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (j0 + 2 * u < j1)
+              finish(p, (row0 + j0 + 2 * u) * p.ldd + n, value(p, total[u], cs, sa[u], bias));
         }
       }
       __syncwarp();
