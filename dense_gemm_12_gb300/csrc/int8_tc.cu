@@ -34,9 +34,9 @@
 // through distributed shared memory.  Many tiles: int8_wide.cu, if the stream's
 // buffer can hold both operands widened.
 //
-// Measured: 16 x 12288 x 4096 13.7 us (the weights at 3.7 TB/s: 96 CTAs have a
-// half of a tile's k each, and a k-block takes 460 ns from its copy to its MMA),
-// 64 x 12288 x 4096 21.3, 128 x 4096 x 4096 18.3, 1024 x 4096 x 4096 36.
+// Measured: 16 x 12288 x 4096 13.5 us (96 CTAs take 6.1 TB/s of weights between
+// a start and an end of 5.7 us together), 16 x 38912 x 4096 29.2 (HBM: 6.8 TB/s
+// between them), 64 x 12288 x 4096 18.3, 128 x 4096 x 4096 16.1.
 #include <cstddef>
 
 #include "int8.cuh"
@@ -57,6 +57,10 @@ constexpr int kWorkWarps = kWorkThreads / 32;
 constexpr uint32_t kTmemCols = 512;
 // TMEM columns: sums of the two halves, then two buffers of widened weights
 constexpr uint32_t kSumCols = 128, kWideAt = 256, kWideCols = 128, kWideHalf = 64;
+// 64 tokens: half of the warps widen a block, the others the next one (64 x
+// 12288 x 4096 18.3 us against 19.1, 64 x 20000 x 2048 14.7 against 15.5; with 32
+// tokens 14.7 against 14.5, with 128 the MMAs are slower than the warps).
+constexpr bool in_turn(int tm) { return tm == 64; }
 // 640 threads launch with 96 registers each; 64 + 4 x 104 = 5 x 96.
 constexpr int kFewRegs = 64, kManyRegs = 104;
 // k-blocks of B that a CTA of a split tile asks L2 for early.
@@ -120,6 +124,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const __grid_constant__ CUtensorMap tmB) {
   constexpr int STAGES = stages(TM), kStageBytes = stage_bytes(TM), kWideBytes = wide_bytes(TM);
   constexpr uint32_t kIdesc = idesc_f16_f32(128, TM);
+  constexpr bool TURN = in_turn(TM);
+  constexpr int kBlockWarps = TURN ? kWorkWarps / 2 : kWorkWarps;  // that widen a block
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = align_smem<1024>(smem_raw);
   uint8_t* wide = smem + STAGES * kStageBytes;  // multiples of 1024
@@ -137,10 +143,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&tail->full[s], 1);
-      mbar_init(&tail->empty[s], kWorkWarps);
+      mbar_init(&tail->empty[s], kBlockWarps);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&tail->wide_full[b], kWorkWarps);
+      mbar_init(&tail->wide_full[b], kBlockWarps);
       mbar_init(&tail->wide_empty[b], 1);
     }
     mbar_init(&tail->sum_full, 1);
@@ -261,20 +267,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = static_cast<int>(threadIdx.x) - 128;
     const int quarter = warp & 3;             // TMEM lanes this warp may access
     const int half = ((warp - 4) >> 2) & 1;   // which 128 weights
-    const int side = (warp - 4) >> 3;         // which half of a block's k, and of the tokens' sums
+    const int side = (warp - 4) >> 3;         // which half of the tokens' sums, and
+    const int part_k = TURN ? 0 : side;       // ... of a block's k, or every other block
     const int wrow = half * 128 + quarter * 32 + lane;
     constexpr int kMySums = TM / 2;
     constexpr int kStep = kMySums == 16 || kMySums == 32 ? 16 : 8;  // sums per TMEM load
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t sums_at = tmem_base + lanes + static_cast<uint32_t>(half) * kSumCols + side * kMySums;
-    const uint32_t wide_at = tmem_base + lanes + kWideAt + static_cast<uint32_t>(half) * kWideHalf + side * 32;
+    const uint32_t wide_at = tmem_base + lanes + kWideAt + static_cast<uint32_t>(half) * kWideHalf + part_k * 32;
     const uint32_t raw = smem_u32(smem), wide_smem = smem_u32(wide);
     const uint32_t raw_w = raw + static_cast<uint32_t>(wrow) * BK;
-    const uint32_t turn = static_cast<uint32_t>((side * 4) ^ (wrow & 7)) * 16;
+    const uint32_t turn = static_cast<uint32_t>((part_k * 4) ^ (wrow & 7)) * 16;
+    constexpr int kRounds = TURN ? 4 : 2;  // of 32 of k
     constexpr int kPieces = TM * 8;  // 16-byte pieces of a block's tokens
-    constexpr int kMine = (kPieces + kWorkThreads - 1) / kWorkThreads;
+    constexpr int kBlockThreads = kBlockWarps * 32;
+    constexpr int kMine = (kPieces + kBlockThreads - 1) / kBlockThreads;
     const uint32_t token = static_cast<uint32_t>(tid & (TM - 1));
-    const int piece0 = tid / TM;
+    const int piece0 = (tid & (kBlockThreads - 1)) / TM;
     const uint32_t raw_x = raw + kRawW + token * BK, turn_x = (token & 7) * 16;
     uint32_t it = 0, chunk = 0;
     uint32_t sum[kMySums];
@@ -295,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return false;
       tc_fence_after_sync();
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < kRounds; ++h) {
         uint32_t r[16];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
@@ -305,9 +314,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           widen4(v.z, r[c * 8 + 4], r[c * 8 + 5]);
           widen4(v.w, r[c * 8 + 6], r[c * 8 + 7]);
         }
-        if (h == 0) {
+        if (h + 1 < kRounds) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) w[c] = ld_shared_u4(raw_w + from + (turn ^ (c * 16 + 32)));
+          for (int c = 0; c < 2; ++c) w[c] = ld_shared_u4(raw_w + from + (turn ^ (c * 16 + (h + 1) * 32)));
         }
         tmem_st_32x32b_x16(wide_at + b * kWideCols + h * 16, r);
       }
@@ -316,8 +325,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t to = wide_smem + b * kWideBytes;
 #pragma unroll
       for (int i = 0; i < kMine; ++i) {
-        const int c = piece0 + i * (kWorkThreads / TM);
-        if (kPieces < kWorkThreads && c >= 8) continue;
+        const int c = piece0 + i * (kBlockThreads / TM);
+        if (kPieces < kBlockThreads && c >= 8) continue;
         const uint4 x = ld_shared_u4(raw_x + from + (static_cast<uint32_t>(c * 16) ^ turn_x));
         uint32_t v[8];
         widen4(x.x, v[0], v[1]);
@@ -368,15 +377,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       return true;
     };
 
-    // This CTA's blocks of a tile.  The first block of a chunk is ready before
-    // the last chunk is taken.
+    // This CTA's blocks of a tile.  A warp's first block of a chunk is ready
+    // before it takes the last chunk.
     auto sums = [&]() -> bool {
       const uint32_t start = 0u - kWholeOff * static_cast<uint32_t>((kb1 - kb0 + kChunk - 1) / kChunk);
 #pragma unroll
       for (int i = 0; i < kMySums; ++i) sum[i] = by_unit(i / kStep * kStep) ? 0u : start;
+      int left = (kb1 - kb0 + kChunk - 1) / kChunk;  // chunks to take
       for (int kb = kb0; kb < kb1; ++kb) {
+        if (TURN && (it & 1u) != static_cast<uint32_t>(side)) {
+          ++it;
+          continue;
+        }
         if (!convert()) return false;
-        if (kb > kb0 && (kb - kb0) % kChunk == 0 && !take()) return false;
+        if (kb - kb0 >= kChunk && (kb - kb0) % kChunk < (TURN ? 2 : 1)) {
+          if (!take()) return false;
+          if (TURN) --left;
+        }
+      }
+      if constexpr (TURN) {  // (the last chunk may have had no block for this warp)
+        for (; left > 0; --left)
+          if (!take()) return false;
+        return true;
       }
       return kb1 == kb0 || take();
     };
