@@ -4,6 +4,8 @@
 //
 // Everything here is bound by memory or by latency; nothing waits on the host,
 // and every sum has a fixed order.
+#include <cfloat>
+
 #include "ops.cuh"
 #include "groups.cuh"
 
@@ -47,7 +49,23 @@ struct RouteArgs {
   float* weight;
 };
 
-// One warp per row, its logits in registers (lane l holds l, l + 32, ...).
+// A lane's logits of a row (lane l holds l, l + 32, ...).
+template <int V>
+__device__ __forceinline__ void load_logits(const void* logits, int type, int64_t at, int experts, float (&l)[V]) {
+  const int lane = threadIdx.x & 31;
+  if (type == GEMM_OUT_F32) {
+    const float* from = static_cast<const float*>(logits) + at;
+#pragma unroll
+    for (int v = 0; v < V; ++v) l[v] = v * 32 + lane < experts ? from[v * 32 + lane] : -INFINITY;
+  } else {
+    const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(logits) + at;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      l[v] = v * 32 + lane < experts ? __bfloat162float(from[v * 32 + lane]) : -INFINITY;
+  }
+}
+
+// One warp per row, its logits in registers.
 template <int V>
 __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__ RouteArgs a) {
   grid_dependency_wait();
@@ -58,26 +76,13 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); row < a.rows;
        row += static_cast<int64_t>(gridDim.x) * kWarps) {
     float l[V];
-    uint32_t key[V];
+    load_logits(a.logits, a.type, row * a.ld, a.experts, l);
+    float most = -INFINITY;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int i = v * 32 + lane;
-      l[v] = i < a.experts ? load1(a.logits, a.type, row * a.ld + i) : -INFINITY;
-    }
-    float m = -INFINITY;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      key[v] = logit_key(l[v]);
-      m = fmaxf(m, l[v]);  // passes over NaN
-    }
-    m = warp_max(m);
-    if (m == -INFINITY) m = 0.0f;
-    float sum = 0.0f;
-    if (!a.normalize) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) sum += expf(l[v] - m);
-      sum = warp_sum(sum);
-    }
+    for (int v = 0; v < V; ++v) most = fmaxf(most, l[v]);  // passes over NaN
+    uint32_t largest = logit_key(most);
+    const uint32_t first = __reduce_max_sync(0xffffffffu, largest);
+    const float m = first == 0u ? 0.0f : key_value(first);
     // Lane j's choice: which of the `top` it is (place), its index and its value.
     int mine = -1, place = lane;
     float value = -INFINITY;
@@ -88,31 +93,26 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__
       // goes to one lane each, in the order of the indexes, and counts how many
       // come before it: half the instructions of a search for each choice
       // (16384 rows of 256, 8 choices: 15.4 us that way).
-      uint32_t largest = 0u, bound = 1u;
-#pragma unroll
-      for (int v = 0; v < V; ++v) largest = max(largest, key[v]);
-      for (int j = 0; j < a.top; ++j) {
-        const uint32_t best = __reduce_max_sync(0xffffffffu, largest);
-        if (best == 0u) {
-          bound = 1u;  // fewer than `top` lanes: all that are not masked
-          break;
-        }
-        bound = best;
+      uint32_t best = first;
+      for (int j = 1; j < a.top && best != 0u; ++j) {
         if (largest == best) largest = 0u;
+        best = __reduce_max_sync(0xffffffffu, largest);
       }
+      // fewer than `top` lanes: all that are not masked
+      const float bound = best == 0u ? -FLT_MAX : key_value(best);
       candidates = 0;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const bool in = key[v] >= bound;
+        const bool in = l[v] >= bound;
         const uint32_t with = __ballot_sync(0xffffffffu, in);
         const uint32_t at = candidates + __popc(with & ((1u << lane) - 1u));
-        if (in && at < 32u) list[at] = make_uint2(key[v], v * 32 + lane);
+        if (in && at < 32u) list[at] = make_uint2(__float_as_uint(l[v]), v * 32 + lane);
         candidates += __popc(with);
       }
       if (candidates <= 32u) {
         __syncwarp();
         const uint2 c = list[lane];
-        const uint32_t k = lane < candidates ? c.x : 0u;
+        const uint32_t k = lane < candidates ? logit_key(__uint_as_float(c.x)) : 0u;
         place = 0;
         for (uint32_t i = 0; i < candidates; ++i) {
           const uint32_t other = __shfl_sync(0xffffffffu, k, i);
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__
         }
         if (lane < candidates && place < a.top) {
           mine = static_cast<int>(c.y);
-          value = key_value(k);
+          value = __uint_as_float(c.x);
         } else if (lane >= candidates) {
           place = lane;  // choices that cannot be made
         }
@@ -128,6 +128,9 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__
       }
     }
     if (candidates > 32u) {
+      uint32_t key[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) key[v] = logit_key(l[v]);
       for (int j = 0; j < a.top; ++j) {
         uint32_t best = 0u;
 #pragma unroll
@@ -148,8 +151,14 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__
         }
       }
     }
-    float e = mine < 0 ? 0.0f : expf(value - m);
-    if (a.normalize) sum = warp_sum(e);
+    const float e = mine < 0 ? 0.0f : expf(value - m);
+    float sum = e;
+    if (!a.normalize) {
+      sum = 0.0f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) sum += expf(l[v] - m);
+    }
+    sum = warp_sum(sum);
     if (place < a.top) {
       a.expert[row * a.top + place] = mine;
       a.weight[row * a.top + place] = mine < 0 ? 0.0f : e / sum;
@@ -174,11 +183,7 @@ __global__ void __launch_bounds__(kThreads) route_grad_kernel(const __grid_const
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); row < a.rows;
        row += static_cast<int64_t>(gridDim.x) * kWarps) {
     float l[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int i = v * 32 + lane;
-      l[v] = i < a.experts ? load1(a.logits, a.type, row * a.ld + i) : -INFINITY;
-    }
+    load_logits(a.logits, a.type, row * a.ld, a.experts, l);
     int e = -1;
     float dw = 0.0f, chosen = 0.0f;
     if (lane < a.top) {
@@ -827,8 +832,9 @@ gemm_status_t gemm_expert_dispatch(int64_t rows, int64_t top, int64_t n, int64_t
       (elem_bytes != 1 && elem_bytes != 2 && elem_bytes != 4))
     return GEMM_ERR_INVALID_VALUE;
   if (rows == 0 || top == 0 || n == 0 || dim == 0) return GEMM_OK;
-  if ((x_scales == nullptr) != (a_scales == nullptr) || x == nullptr || a == nullptr || !ids_ok(slot) || ldx < dim || lda < dim || ldx > kOpsMaxDim ||
-      lda > kOpsMaxDim || ops_misaligned(x, elem_bytes) || ops_misaligned(a, elem_bytes))
+  if ((x_scales == nullptr) != (a_scales == nullptr) || x == nullptr || a == nullptr || !ids_ok(slot) ||
+      ldx < dim || lda < dim || ldx > kOpsMaxDim || lda > kOpsMaxDim || ops_misaligned(x, elem_bytes) ||
+      ops_misaligned(a, elem_bytes))
     return GEMM_ERR_INVALID_VALUE;
   if (x_scales != nullptr && (ld_xs < rows || ld_as < n || ld_xs > kOpsMaxDim || ld_as > kOpsMaxDim ||
                               ops_misaligned(x_scales, 4) || ops_misaligned(a_scales, 4)))
