@@ -34,12 +34,6 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int s = 16; s > 0; s >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, s));
-  return v;
-}
-
 // ------------------------------------------------------------------ router
 struct RouteArgs {
   int64_t rows, ld;
@@ -70,8 +64,8 @@ template <int V>
 __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__ RouteArgs a) {
   grid_dependency_wait();
   grid_launch_dependents();
-  __shared__ uint2 lists[V >= 4 ? kWarps : 1][V >= 4 ? 32 : 1];  // candidates
-  uint2* const list = lists[V >= 4 ? threadIdx.x >> 5 : 0];
+  __shared__ uint2 lists[V >= 2 ? kWarps : 1][V >= 2 ? 32 : 1];  // candidates
+  uint2* const list = lists[V >= 2 ? threadIdx.x >> 5 : 0];
   const uint32_t lane = threadIdx.x & 31;
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); row < a.rows;
        row += static_cast<int64_t>(gridDim.x) * kWarps) {
@@ -87,7 +81,7 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__
     int mine = -1, place = lane;
     float value = -INFINITY;
     uint32_t candidates = 33;
-    if constexpr (V >= 4) {
+    if constexpr (V >= 2) {
       // The `top`-th largest of the lanes' own largest is a bound from below on
       // the `top` largest of all.  What reaches it -- hardly more than `top` --
       // goes to one lane each, in the order of the indexes, and counts how many
@@ -182,10 +176,8 @@ __global__ void __launch_bounds__(kThreads) route_grad_kernel(const __grid_const
   const int lane = threadIdx.x & 31;
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); row < a.rows;
        row += static_cast<int64_t>(gridDim.x) * kWarps) {
-    float l[V];
-    load_logits(a.logits, a.type, row * a.ld, a.experts, l);
     int e = -1;
-    float dw = 0.0f, chosen = 0.0f;
+    float dw = 0.0f, chosen = -INFINITY;
     if (lane < a.top) {
       e = a.expert[row * a.top + lane];
       if (e < 0 || e >= a.experts) e = -1;
@@ -194,16 +186,19 @@ __global__ void __launch_bounds__(kThreads) route_grad_kernel(const __grid_const
       dw = a.dweight[row * a.top + lane];
       chosen = load1(a.logits, a.type, row * a.ld + e);
     }
-    float m = -INFINITY;
+    // the shares of the chosen ones: of themselves alone no other logit is read
+    float l[V], most = chosen;
+    if (!a.normalize) {
+      load_logits(a.logits, a.type, row * a.ld, a.experts, l);
 #pragma unroll
-    for (int v = 0; v < V; ++v) m = fmaxf(m, l[v]);
-    m = warp_max(m);
-    if (m == -INFINITY) m = 0.0f;
+      for (int v = 0; v < V; ++v) most = fmaxf(most, l[v]);
+    }
+    const uint32_t largest = __reduce_max_sync(0xffffffffu, logit_key(most));
+    const float m = largest == 0u ? 0.0f : key_value(largest);
     chosen = e >= 0 ? expf(chosen - m) : 0.0f;
-    float sum = 0.0f;
-    if (a.normalize) {
-      sum = chosen;
-    } else {
+    float sum = chosen;
+    if (!a.normalize) {
+      sum = 0.0f;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         l[v] = expf(l[v] - m);
@@ -218,12 +213,20 @@ __global__ void __launch_bounds__(kThreads) route_grad_kernel(const __grid_const
 #pragma unroll
     for (int v = 0; v < V; ++v) g[v] = a.normalize ? 0.0f : -dot * (l[v] * inv);
     const float mine = (a.normalize ? dw - dot : dw) * (chosen * inv);
+    // the choices among them, hardly ever more than two, in their order
+    uint32_t todo = 0u;
     for (int j = 0; j < a.top; ++j) {
+      const int ej = __shfl_sync(0xffffffffu, e, j);
+      if (ej >= 0 && (ej & 31) == lane) todo |= 1u << j;
+    }
+    while (__any_sync(0xffffffffu, todo != 0u)) {
+      const int j = todo != 0u ? __ffs(todo) - 1 : 0;
       const int ej = __shfl_sync(0xffffffffu, e, j);
       const float gj = __shfl_sync(0xffffffffu, mine, j);
 #pragma unroll
       for (int v = 0; v < V; ++v)
-        if (ej == v * 32 + lane) g[v] += gj;
+        if (todo != 0u && ej == v * 32 + lane) g[v] += gj;
+      todo &= todo - 1u;
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
