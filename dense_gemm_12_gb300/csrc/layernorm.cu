@@ -583,13 +583,19 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
 #pragma unroll
         for (int k = 0; k < C; ++k) get(k, chunk_col<VEC>(k * tpr + t), has(k));
       }
+      // From a ring of bf16 rows, the first pass's g and xh stay for the second
+      // (8192 x 4096 55.5 us against 61.7 with the rows read again); in fp32 those
+      // registers cost more than the reads (106 us against 98).
+      constexpr bool kKept = RING && TD == GEMM_OUT_BF16 && TH == GEMM_OUT_BF16;
+      uint64_t gs[kKept ? C : 1][4], xs[kKept ? C : 1][4];
 #pragma unroll
       for (int k = 0; k < C; ++k) {
         const int c = chunk_col<VEC>(k * tpr + t);
         if (!kHeld) get(k, c, has(k));
         if (!has(k)) continue;
         float v[8];
-        uint64_t g[4], xh[4];
+        uint64_t(&g)[4] = gs[kKept ? k : 0];
+        uint64_t(&xh)[4] = xs[kKept ? k : 0];
         widen8<VEC, TD>(dy[k], a.p.dy_type, v);  // zeros past the row's end
         to_pairs(v, g);
         widen8<VEC, TH>(rh[k], a.p.h_type, v);
@@ -618,7 +624,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
       for (int k = 0; k < C; ++k) {
         const int c = chunk_col<VEC>(k * tpr + t);
         if (!has(k)) continue;
-        if (!kHeld) get(k, c, true);
+        if (!kHeld && !kKept) get(k, c, true);
         float r[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
         if (a.p.residual_grad != nullptr) {
           const int type = a.p.residual_grad_type;
@@ -633,14 +639,17 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
                                                        a.dim, true), type, r);
           }
         }
-        float v[8];
-        uint64_t g[4], xh[4];
-        widen8<VEC, TD>(dy[k], a.p.dy_type, v);
-        to_pairs(v, g);
-        weighted(c, g);
-        widen8<VEC, TH>(rh[k], a.p.h_type, v);
-        to_pairs(v, xh);
-        normal(c, rstd, mean, xh);
+        uint64_t(&g)[4] = gs[kKept ? k : 0];
+        uint64_t(&xh)[4] = xs[kKept ? k : 0];
+        if (!kKept) {
+          float v[8];
+          widen8<VEC, TD>(dy[k], a.p.dy_type, v);
+          to_pairs(v, g);
+          weighted(c, g);
+          widen8<VEC, TH>(rh[k], a.p.h_type, v);
+          to_pairs(v, xh);
+          normal(c, rstd, mean, xh);
+        }
         gradient(g, xh, rstd, means, r);
         store8<VEC>(a.p.dh, a.p.dh_type, row * a.p.lddh, c, a.dim, r);
       }
