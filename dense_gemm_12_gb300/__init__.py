@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 from . import _build
@@ -126,6 +127,19 @@ class LayernormGradArgs(ctypes.Structure):
     ]
 
 
+def _packer(mirror):
+    """Packs a mirror's fields, in their order, into bytes (None is not taken: 0).  A quarter of the
+    time that the mirror's constructor takes, and a call of a small norm is mostly that."""
+    codes = {ctypes.c_void_p: "P", ctypes.c_int64: "q", ctypes.c_int: "i", ctypes.c_float: "f"}
+    layout = struct.Struct("@" + "".join(codes[t] for _, t in mirror._fields_))
+    assert layout.size == ctypes.sizeof(mirror)
+    return layout.pack
+
+
+_pack_layernorm = _packer(LayernormArgs)
+_pack_layernorm_grad = _packer(LayernormGradArgs)
+
+
 KERNELS = {"auto": 0, "single_cta": 1, "cta_pair": 2, "wide": 3}
 # gemm_config_t.split value for the stream-K tail (fp32 only): GEMM_SPLIT_STREAM.
 SPLIT_STREAM = -1
@@ -226,6 +240,11 @@ def load_library(build_if_missing: bool = False):
         lib.gemm_layernorm.restype = cint
         lib.gemm_layernorm_backward.argtypes = [i64, i64, ctypes.POINTER(LayernormGradArgs), vp]
         lib.gemm_layernorm_backward.restype = cint
+        # the same entry points, for arguments packed as bytes
+        for name in ("gemm_layernorm", "gemm_layernorm_backward"):
+            packed = lib[name]
+            packed.argtypes, packed.restype = [i64, i64, vp, vp], cint
+            setattr(lib, name + "_packed", packed)
         lib.gemm_int8_quantize.argtypes = [i64, i64, vp, i64, cint, cint, vp, i64, vp, vp]
         lib.gemm_int8_quantize.restype = cint
         lib.gemm_int8gemm.argtypes = [i64, i64, i64, f32, vp, i64, vp, vp, i64, vp, vp, f32, vp, i64, cint,
@@ -680,7 +699,7 @@ def _stream_of(dev, stream):
 
 def _array(t, shape, dtype, dev, name):
     """(address, leading dimension) of a row-major matrix (or of each of a batch), checked."""
-    if t.dtype != dtype or t.get_device() != dev:
+    if t.dtype is not dtype or t.get_device() != dev:
         raise TypeError("%s must be a %s tensor on the other operands' device" % (name, dtype))
     if t.shape != shape:
         raise ValueError("%s must have shape %s, not %s" % (name, tuple(shape), tuple(t.shape)))
@@ -695,14 +714,17 @@ def _float_array(t, shape, dev, name):
     code = _FLOAT_CODES.get(t.dtype)
     if code is None:
         raise TypeError("%s must be a float32 or bfloat16 tensor" % name)
-    return (*_array(t, shape, t.dtype, dev, name), code)
+    strides = t.stride()
+    if t.get_device() != dev or t.shape != shape or (strides[-1] != 1 and shape[-1] > 1):
+        return (*_array(t, shape, t.dtype, dev, name), code)  # which says what is wrong
+    return t.data_ptr(), strides[-2] if shape[-2] > 1 else max(shape[-1], 1), code
 
 
 def _vector(t, n, dtype, dev, name):
     """Address of a contiguous vector of n values."""
-    if t.dtype != dtype or t.get_device() != dev:
+    if t.dtype is not dtype or t.get_device() != dev:
         raise TypeError("%s must be a %s tensor on the other operands' device" % (name, dtype))
-    if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
+    if t.dim() != 1 or t.numel() != n or not t.is_contiguous():
         raise ValueError("%s must be a contiguous vector of %d values" % (name, n))
     return t.data_ptr()
 
@@ -776,25 +798,25 @@ def layernorm(x, weight=None, bias=None, eps=1e-5, residual=None, h=None, y=None
     handle = _stream_of(dev, stream)
     if (q is None) != (scales is None):
         raise ValueError("q and scales come together")
-    none = (None, 0, 0)
+    none = (0, 0, 0)
     if q is None:
-        eight = (None, 0, 0, None, 0)
+        eight = (0, 0, 0, 0, 0)
     elif q.dtype == f8:
         eight = (*_array(q, shape, f8, dev, "q"), OUT["f8e4m3"],
                  *_array(scales, (-(-dim // 128), rows), f32, dev, "scales"))
     else:
         eight = (*_array(q, shape, _int8(), dev, "q"), OUT["s8"],
                  _vector(scales, rows, f32, dev, "scales"), 0)
-    a = LayernormArgs(
+    a = _pack_layernorm(
         *_float_array(x, shape, dev, "x"),
         *(none if residual is None else _float_array(residual, shape, dev, "residual")),
         *(none if h is None else _float_array(h, shape, dev, "h")),
-        None if weight is None else _vector(weight, dim, f32, dev, "weight"),
-        None if bias is None else _vector(bias, dim, f32, dev, "bias"), eps,
+        0 if weight is None else _vector(weight, dim, f32, dev, "weight"),
+        0 if bias is None else _vector(bias, dim, f32, dev, "bias"), eps,
         *(none if y is None else _float_array(y, shape, dev, "y")), *eight,
-        None if mean is None else _vector(mean, rows, f32, dev, "mean"),
-        None if rstd is None else _vector(rstd, rows, f32, dev, "rstd"))
-    st = load_library().gemm_layernorm(rows, dim, ctypes.byref(a), handle)
+        0 if mean is None else _vector(mean, rows, f32, dev, "mean"),
+        0 if rstd is None else _vector(rstd, rows, f32, dev, "rstd"))
+    st = load_library().gemm_layernorm_packed(rows, dim, a, handle)
     if st != 0:
         raise GemmError(st, "gemm_layernorm")
 
@@ -809,16 +831,16 @@ def layernorm_backward(dy, h, weight, mean, rstd, dh, dweight=None, dbias=None, 
     shape, dev = dy.shape, dy.get_device()
     rows, dim = shape
     handle = _stream_of(dev, stream)
-    a = LayernormGradArgs(
+    a = _pack_layernorm_grad(
         *_float_array(dy, shape, dev, "dy"), *_float_array(h, shape, dev, "h"),
-        None if weight is None else _vector(weight, dim, f32, dev, "weight"),
+        0 if weight is None else _vector(weight, dim, f32, dev, "weight"),
         _vector(mean, rows, f32, dev, "mean"), _vector(rstd, rows, f32, dev, "rstd"),
-        *((None, 0, 0) if residual_grad is None else
+        *((0, 0, 0) if residual_grad is None else
           _float_array(residual_grad, shape, dev, "residual_grad")),
         *_float_array(dh, shape, dev, "dh"),
-        None if dweight is None else _vector(dweight, dim, f32, dev, "dweight"),
-        None if dbias is None else _vector(dbias, dim, f32, dev, "dbias"))
-    st = load_library().gemm_layernorm_backward(rows, dim, ctypes.byref(a), handle)
+        0 if dweight is None else _vector(dweight, dim, f32, dev, "dweight"),
+        0 if dbias is None else _vector(dbias, dim, f32, dev, "dbias"))
+    st = load_library().gemm_layernorm_backward_packed(rows, dim, a, handle)
     if st != 0:
         raise GemmError(st, "gemm_layernorm_backward")
     return dh
@@ -992,7 +1014,7 @@ def bf16gemm_grouped_wgrad(A, dD, offsets, dB, alpha=1.0, beta=0.0, stream=None)
 
 def _dense(t, shape, dtype, dev, name):
     """Address of a contiguous array of this shape."""
-    if t.dtype != dtype or t.get_device() != dev:
+    if t.dtype is not dtype or t.get_device() != dev:
         raise TypeError("%s must be a %s tensor on the other operands' device" % (name, dtype))
     if t.shape != shape or not t.is_contiguous():
         raise ValueError("%s must be contiguous, of shape %s" % (name, tuple(shape)))

@@ -546,14 +546,15 @@ gemm_status_t gemm_quantization(int64_t M, int64_t N, int64_t BM, int64_t BN,
  *  Memory     gemm_rmsnorm_backward and gemm_layernorm_backward keep partial
  *             sums of the parameters' gradients in the stream's scratch,
  *             gemm_int8_quantize (transposed) columns' maxima, gemm_expert_sort
- *             counters; operands of the products
- *             that TMA cannot describe (base not 16-byte aligned, or a matrix
- *             stride, or the row pitch of more than one row, that is not a
- *             multiple of 16 bytes) are
+ *             counters; operands of the products that TMA cannot describe
+ *             (base not 16-byte aligned, or a matrix stride, or the row pitch
+ *             of more than one row, that is not a multiple of 16 bytes) are
  *             always copied into the stream's staging buffer.  Where that
  *             memory cannot be had (inside a stream capture on a stream
  *             whose buffer is too small, or out of memory) the call returns
- *             GEMM_ERR_NO_MEMORY and queues nothing.
+ *             GEMM_ERR_NO_MEMORY and queues nothing.  Large gemm_int8gemm calls
+ *             keep both operands there in fp16 (twice their bytes, up to 1 GiB);
+ *             without that memory they take a slower way to the same bits.
  *  Order      Sums are always added in the same order: the same call gives
  *             the same bits.
  */

@@ -102,3 +102,11 @@ def test_tensor_helpers_refuse_wrong_tensors(gemm_lib, cuda_device):
     for error, call in bad:
         with pytest.raises(error):
             call()
+
+
+def test_packed_arguments_are_the_mirrors(gemm_lib):
+    g = gemm_lib
+    for mirror, pack in ((g.LayernormArgs, g._pack_layernorm), (g.LayernormGradArgs, g._pack_layernorm_grad)):
+        values = [0.5 if name == "eps" else 1000 + i for i, (name, _) in enumerate(mirror._fields_)]
+        a = mirror.from_buffer_copy(pack(*values))
+        assert [getattr(a, name) for name, _ in mirror._fields_] == values
