@@ -121,10 +121,10 @@ __device__ __forceinline__ void fetch_scales(const Int8Args& p, uint32_t to, int
 }
 
 // The product with both operands widened to fp16 beforehand (int8_wide.cu): the
-// bytes of the widened copies, and whether that is the faster way than `tiles`
-// of 128 tokens, each of `split` CTAs; then the product, the copies in `buf`.
+// bytes of the widened copies, and whether that takes less than `us`
+// microseconds; then the product, with the copies in `buf`.
 int64_t int8_wide_bytes(int64_t M, int64_t N, int64_t K);
-bool int8_wide_pays(int64_t M, int64_t N, int64_t K, int64_t tiles, int split, int num_sms);
+bool int8_wide_pays(int64_t M, int64_t N, int64_t K, double us);
 gemm_status_t int8_wide(const Int8Args& a, int64_t K, const int8_t* A, int64_t lda, const int8_t* B,
                         int64_t ldb, uint8_t* buf, int num_sms, cudaStream_t s);
 

@@ -36,7 +36,8 @@
 //
 // Measured: 16 x 12288 x 4096 13.5 us (96 CTAs take 6.1 TB/s of weights between
 // a start and an end of 5.7 us together), 16 x 38912 x 4096 29.2 (HBM: 6.8 TB/s
-// between them), 64 x 12288 x 4096 18.3, 128 x 4096 x 4096 16.1.
+// between them), 64 x 12288 x 4096 17.1, 128 x 4096 x 4096 12.9 (tiles of 64),
+// 128 x 12288 x 4096 23.6.
 #include <cstddef>
 
 #include "int8.cuh"
@@ -428,42 +429,65 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < kMySums; ++j) out[j * WN] = sum[j];
       __syncwarp();
       const Tile w = tile_of(first, tiles_n, tiles_m);
-      // 512 threads: every other token each
-      const int n = w.tn * WN + (tid & (WN - 1)), row0 = w.tm * TM;
-      const bool in = first < tiles && n < p.N;
-      const float cs = in ? p.alpha * p.sb[n] : 0.0f;
-      const float bias = in && p.bias != nullptr ? p.bias[n] : 0.0f;
+      // four channels of every eighth token to a thread
+      const int n = w.tn * WN + (tid & 63) * 4, row0 = w.tm * TM;
+      const int in = first < tiles ? min(p.N - n, 4) : 0;  // channels
+      float cs[4], bias[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        cs[i] = i < in ? p.alpha * p.sb[n + i] : 0.0f;
+        bias[i] = i < in && p.bias != nullptr ? p.bias[n + i] : 0.0f;
+      }
       cluster_sync();  // every part's sums are in its shared memory
       // after a wait ran out the sums are not complete; the error word says so
-      if (in && !ld_shared_volatile(abort_flag)) {
+      if (in > 0 && !ld_shared_volatile(abort_flag)) {
         const int j1 = min((part + 1) * TM / split, p.M - row0);
-        const uint32_t mine = smem_u32(smem) + static_cast<uint32_t>(tid & (WN - 1)) * 4;
-        // Other CTAs' values are on their way for a microsecond: those of four
+        const uint32_t mine = smem_u32(smem) + static_cast<uint32_t>(tid & 63) * 16;
+        // Other CTAs' values are on their way for a microsecond: those of two
         // tokens and four parts at once.
-        for (int j0 = part * TM / split + (tid >> 8); j0 < j1; j0 += 8) {
-          float sa[4];
-          uint32_t total[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-          for (int u = 0; u < 4; ++u) sa[u] = j0 + 2 * u < j1 ? p.sa[row0 + j0 + 2 * u] : 0.0f;
+        for (int j0 = part * TM / split + (tid >> 6); j0 < j1; j0 += 16) {
+          const bool two = j0 + 8 < j1;
+          const float sa[2] = {p.sa[row0 + j0], two ? p.sa[row0 + j0 + 8] : 0.0f};
+          uint32_t total[2][4] = {};
           for (int src = 0; src < split; src += 4) {
-            uint32_t v[4][4];
+            float4 v[4][2];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const uint32_t from = mapa_shared(mine, static_cast<uint32_t>(min(src + q, split - 1)));
 #pragma unroll
-              for (int u = 0; u < 4; ++u) {
-                v[q][u] = 0u;
-                if (src + q < split && j0 + 2 * u < j1)
-                  v[q][u] = __float_as_uint(ld_shared_cluster_f32(from + static_cast<uint32_t>(j0 + 2 * u) * (WN * 4)));
+              for (int u = 0; u < 2; ++u) {
+                v[q][u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (src + q < split && (u == 0 || two))
+                  v[q][u] = ld_shared_cluster_v4(from + static_cast<uint32_t>(j0 + 8 * u) * (WN * 4));
               }
             }
 #pragma unroll
-            for (int u = 0; u < 4; ++u) total[u] += v[0][u] + v[1][u] + v[2][u] + v[3][u];
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                total[u][0] += __float_as_uint(v[q][u].x);
+                total[u][1] += __float_as_uint(v[q][u].y);
+                total[u][2] += __float_as_uint(v[q][u].z);
+                total[u][3] += __float_as_uint(v[q][u].w);
+              }
           }
 #pragma unroll
-          for (int u = 0; u < 4; ++u)
-            if (j0 + 2 * u < j1)
-              finish(p, (row0 + j0 + 2 * u) * p.ldd + n, value(p, total[u], cs, sa[u], bias));
+          for (int u = 0; u < 2; ++u) {
+            if (u == 1 && !two) continue;
+            float d[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) d[i] = value(p, total[u][i], cs[i], sa[u], bias[i]);
+            const int64_t at = (row0 + j0 + 8 * u) * p.ldd + n;
+            if (p.d_pair && in == 4) {
+              uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.D) + at);
+              to[0] = pack_bf16(d[0], d[1]);
+              to[1] = pack_bf16(d[2], d[3]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (i < in) finish(p, at + i, d[i]);
+            }
+          }
         }
       }
       __syncwarp();
@@ -521,6 +545,35 @@ int choose_split(int64_t tiles, int num_kb, int num_sms) {
   return best;
 }
 
+// A call's tiles of tm tokens, the CTAs that share each, and its time in
+// microseconds by what was measured: a tile's start and end, its k-blocks, and
+// the parts' sums.
+struct Plan {
+  int tm, split;
+  int64_t tiles;
+  double us;
+};
+Plan plan_for(int tm, int64_t M, int64_t N, int num_kb, int num_sms) {
+  Plan p;
+  p.tm = tm;
+  p.tiles = ((N + WN - 1) / WN) * ((M + tm - 1) / tm);
+  p.split = choose_split(p.tiles, num_kb, num_sms);
+  const int64_t rounds = (p.tiles * p.split + num_sms - 1) / num_sms;
+  const int share = (num_kb + p.split - 1) / p.split;
+  p.us = static_cast<double>(rounds) * (tm > 64 ? 0.96 * share + 5.5 : 0.65 * share + 4.4) +
+         (p.split == 1 ? 0.0 : (tm > 64 ? 4.0 : 2.7));
+  return p;
+}
+// 128 tokens to a tile widen each weight for the most of them; 64, where that
+// makes tiles for more CTAs (us, 64 / 128: 128 x 4096 x 4096 12.9 / 16.5, 512 x
+// 1024 x 4096 12.9 / 16.5, 256 x 4096 x 1024 9.5 / 12.2, 512 x 4096 x 4096 25.4 /
+// 24.0, 768 x 4096 x 4096 48.6 / 35.9).
+Plan choose_plan(int64_t M, int64_t N, int num_kb, int num_sms) {
+  if (M <= 64) return plan_for(M > 32 ? 64 : (M > 16 ? 32 : 16), M, N, num_kb, num_sms);
+  const Plan a = plan_for(64, M, N, num_kb, num_sms), b = plan_for(128, M, N, num_kb, num_sms);
+  return a.us < b.us ? a : b;
+}
+
 template <int TM>
 cudaError_t launch(int64_t tiles, int num_sms, const Int8Args& a, const CUtensorMap& tmA,
                    const CUtensorMap& tmB, cudaStream_t s) {
@@ -575,12 +628,11 @@ extern "C" gemm_status_t gemm_int8gemm(int64_t M, int64_t N, int64_t K, float al
   a.d_type = d_type;
   a.d_pair = d_type == GEMM_OUT_BF16 && beta == 0.0f && !ops_misaligned(D, 4) && (M == 1 || ldd % 2 == 0);
   a.err = err;
-  const int tm = M > 64 ? 128 : (M > 32 ? 64 : (M > 16 ? 32 : 16));
-  const int64_t tiles = ((N + WN - 1) / WN) * ((M + tm - 1) / tm);
-  if (tiles + sms > kOpsMaxDim) return GEMM_ERR_UNSUPPORTED;
-  a.cluster = choose_split(tiles, a.num_kb, sms);
+  const Plan plan = choose_plan(M, N, a.num_kb, sms);
+  if (plan.tiles + sms > kOpsMaxDim) return GEMM_ERR_UNSUPPORTED;
+  a.cluster = plan.split;
   std::unique_lock<std::mutex> lock;
-  if (product && tm == kMaxTokens && int8_wide_pays(M, N, K, tiles, a.cluster, sms)) {
+  if (product && M > 64 && int8_wide_pays(M, N, K, plan.us)) {
     // without the memory (inside a capture, say) the way below: the same sums
     uint8_t* buf = nullptr;
     st = abi_stage(s, int8_wide_bytes(M, N, K), lock, &buf);
@@ -603,15 +655,15 @@ extern "C" gemm_status_t gemm_int8gemm(int64_t M, int64_t N, int64_t K, float al
     }
     const int64_t da[2] = {K, M}, ta[1] = {byte_pitch(oa)};
     const int64_t db[2] = {K, N}, tb[1] = {byte_pitch(ob)};
-    const uint32_t ba[2] = {BK, static_cast<uint32_t>(tm)}, bb[2] = {BK, WN};
+    const uint32_t ba[2] = {BK, static_cast<uint32_t>(plan.tm)}, bb[2] = {BK, WN};
     if (!abi_encode_tiled(&tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, oa.p, da, ta, ba) ||
         !abi_encode_tiled(&tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, ob.p, db, tb, bb))
       return GEMM_ERR_LAUNCH;
   }
-  switch (tm) {
-    case 16: return abi_from_cuda(launch<16>(tiles, sms, a, tmA, tmB, s));
-    case 32: return abi_from_cuda(launch<32>(tiles, sms, a, tmA, tmB, s));
-    case 64: return abi_from_cuda(launch<64>(tiles, sms, a, tmA, tmB, s));
-    default: return abi_from_cuda(launch<128>(tiles, sms, a, tmA, tmB, s));
+  switch (plan.tm) {
+    case 16: return abi_from_cuda(launch<16>(plan.tiles, sms, a, tmA, tmB, s));
+    case 32: return abi_from_cuda(launch<32>(plan.tiles, sms, a, tmA, tmB, s));
+    case 64: return abi_from_cuda(launch<64>(plan.tiles, sms, a, tmA, tmB, s));
+    default: return abi_from_cuda(launch<128>(plan.tiles, sms, a, tmA, tmB, s));
   }
 }

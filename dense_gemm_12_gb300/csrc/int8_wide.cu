@@ -334,21 +334,21 @@ constexpr int64_t kMostBytes = int64_t{1} << 30;
 
 int64_t int8_wide_bytes(int64_t M, int64_t N, int64_t K) { return copy_bytes(M, K) + copy_bytes(N, K); }
 
-bool int8_wide_pays(int64_t M, int64_t N, int64_t K, int64_t tiles, int split, int num_sms) {
+bool int8_wide_pays(int64_t M, int64_t N, int64_t K, double us) {
   const int64_t bytes = int8_wide_bytes(M, N, K);
   const int pairs = max_pairs();
   if (bytes > kMostBytes || pairs <= 0) return false;
-  // Nanoseconds: rounds of tiles here (64 of k in 280) after the widening (3
-  // bytes a value at 5 TB/s, and a launch), and there (128 of k in 980).  Both
-  // sides, us here / there: 256 x 4096 x 4096 31 / 20, 1024 x 4096 x 4096 36 /
-  // 36, 2048 x 4096 x 512 15.7 / 17.6, 2048 x 4096 x 4096 55 / 70, 4096^3 96 /
-  // 138, 8192 x 8192 x 128 56 / 77, 8192^3 609 / 907.
-  const int64_t mine = ((N + 255) / 256) * ((M + 255) / 256);
-  const double here = static_cast<double>((mine + pairs - 1) / pairs) * (280.0 * ((K + 63) / 64) + 1500.0) +
-                      0.75 * static_cast<double>(bytes) / 2500.0 + 2500.0;
-  const int64_t rounds = (tiles * split + num_sms - 1) / num_sms;
-  const double there = static_cast<double>(rounds) * (980.0 * ((K + 127) / 128) / split + 3000.0);
-  return here < there;
+  // Rounds of tiles (64 of k in 280 ns, or the time of an end, where that is
+  // more), the last tile's end, the widening (3 bytes a value at 7 TB/s) and its
+  // launch.  Both sides, us here / there: 256 x 4096 x 4096 31 / 17, 512 x 4096 x
+  // 4096 31 / 24, 1024 x 4096 x 1024 14.4 / 13.2, 768 x 4096 x 4096 32 / 36, 2048 x
+  // 4096 x 512 15.9 / 17.6, 4096^3 96 / 138, 8192 x 8192 x 128 56 / 77, 8192^3 605 /
+  // 907.
+  const int64_t tiles = ((N + 255) / 256) * ((M + 255) / 256);
+  const double blocks = 0.28 * static_cast<double>((K + 63) / 64) + 0.85;
+  const double here = static_cast<double>((tiles + pairs - 1) / pairs) * (blocks < 4.0 ? 4.0 : blocks) + 3.5 +
+                      1.5e-6 * static_cast<double>(bytes) / 7.0 + 2.5;
+  return here < us;
 }
 
 gemm_status_t int8_wide(const Int8Args& args, int64_t K, const int8_t* A, int64_t lda, const int8_t* B,

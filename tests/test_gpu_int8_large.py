@@ -29,7 +29,7 @@ def kernels(run):
 
 
 # whole and partial tiles of 256 x 256; less than a k-block of 64, one, a chunk of 1024 and around it
-SHAPES = [(2304, 2560, 64), (2100, 2500, 5), (2305, 2049, 1025), (2100, 2500, 1023), (2048, 4096, 512),
+SHAPES = [(4096, 4352, 64), (4100, 4099, 5), (2305, 2049, 1025), (2100, 2500, 1023), (2048, 4096, 512),
           (4097, 1031, 2048), (1031, 6000, 2113), (3000, 5000, 1999), (2561, 2560, 8200)]
 
 
@@ -141,3 +141,33 @@ def test_row_blocks_and_nothing_behind_them():
         mag = sums64(A, B)
         assert bool(((D[:M, :N].double() - mag).abs() <= (UBF if dtype == torch.bfloat16 else U32) * mag.abs()).all())
         assert bool((D[M:] == 7).all()) and bool((D[:, N:] == 7).all())
+
+
+# tiles of 128 tokens that widen as they go: split over a cluster, one and several tiles a CTA
+@pytest.mark.parametrize("M,N,K,name", [
+    (120, 12200, 4000, "<128, true>"), (128, 12288, 4097, "<128, true>"), (100, 20000, 512, "<128, false>"),
+    (127, 24001, 300, "<128, false>"), (100, 50000, 140, "<128, false>"), (200, 30000, 1100, "<128, false>")])
+def test_tiles_of_128_tokens(M, N, K, name):
+    A, B = ints(M, K, 1, pad=-K % 16), ints(N, K, 2, pad=-K % 16)
+    sa, sb, bias = randn(M, seed=3).exp(), randn(N, seed=4).exp(), randn(N, seed=5, scale=100.0)
+    prod = sums64(A.t, B.t) * sa.double()[:, None] * sb.double()
+    for out, beta, pad in (("f32", 0.5, 3), ("bf16", 0.0, N % 2), ("bf16", 0.0, 1 - N % 2)):
+        D = Guarded((M, N), DTYPE[out], pad).set(randn(M, N, seed=6, scale=1000.0))
+        old = beta * D.t.double()
+        assert "int8_kernel" + name in kernels(lambda: g.int8gemm(A.t, sa, B.t, sb, D.t, beta=0.0, bias=bias))
+        D.set(randn(M, N, seed=6, scale=1000.0))
+        g.int8gemm(A.t, sa, B.t, sb, D.t, beta=beta, bias=bias)
+        check_device_error()
+        near(D.t, prod + bias.double() + old, prod.abs() + bias.double().abs() + old.abs())
+        assert D.clean_outside()
+
+
+# 64 tokens to a tile though there are more: one tile a CTA and split ones
+@pytest.mark.parametrize("M,N,K", [(128, 4096, 4096), (100, 1000, 999), (500, 4000, 1000), (513, 1000, 2100)])
+def test_tiles_of_64_of_more_tokens(M, N, K):
+    A, B = ints(M, K, 1, pad=-K % 16), ints(N, K, 2, pad=-K % 16)
+    D = torch.empty(M, N, device="cuda")
+    one = torch.ones(max(M, N), device="cuda")
+    assert "int8_kernel<64" in kernels(lambda: g.int8gemm(A.t, one[:M], B.t, one[:N], D))
+    check_device_error()
+    assert torch.equal(D, sums64(A.t, B.t).float())
