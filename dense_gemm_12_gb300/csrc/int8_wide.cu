@@ -7,15 +7,15 @@
 // MMAs' reads, 1536 cycles of it per 1024 cycles of MMAs, and the accumulator
 // fills TMEM together with the widened weights, so the MMAs stand still while it
 // is read (8192^3 904 us, of which 590 at the rate of the MMAs).  Measured here:
-// 8192^3 605 us, 38 of them the widening (1.94 PFLOP/s after it), 4096^3 96 (four
-// rounds of tiles for 3.4), 3000 x 5000 x 1999 58.
-//   * CTA pairs take 256 weights x 256 tokens (cta_group::2, M = 256, N = 256):
-//     each CTA holds 128 of both, 32 KB a k-block of 64, in a ring of six stages
+// 8192^3 605 us, 38 of them the widening (1.94 PFLOP/s after it), 4096^3 91 (four
+// full rounds), 3000 x 5000 x 1999 53 (3.7 of four rounds).
+//   * CTA pairs take 256 weights x 256 or 224 tokens (cta_group::2, M = 256): each
+//     CTA holds half of both, 30 or 32 KB a k-block of 64, in a ring of six stages
 //   * warp 0 is the TMA producer, warp 1 of the even CTA the MMA issuer, into two
-//     accumulators in turn (256 columns each: all of TMEM)
+//     accumulators in turn (up to 256 columns each: all of TMEM)
 //   * warps 4..11 carry an accumulator's sums on as integers every 1024 of k, and
 //     write a finished tile, while the MMAs fill the other: a thread has one
-//     channel and 128 tokens in registers (moved from the first warpgroup).
+//     channel and half of the tokens in registers (moved from the first warpgroup).
 #include <cstddef>
 
 #include "int8.cuh"
@@ -23,20 +23,20 @@
 namespace g12 {
 namespace {
 
-constexpr int BM = 128, BN = 256, BK = 64;   // a CTA's weights, a pair's tokens
+constexpr int BM = 128, BK = 64;   // a CTA's weights; the pair's tokens are BN
 constexpr int STAGES = 6;
-constexpr int kStageBytesA = BM * BK * 2, kStageBytes = 2 * kStageBytesA;  // 32 KB
-constexpr int kRingBytes = STAGES * kStageBytes;
 constexpr int kChunk = 1024 / BK;  // k-blocks that an accumulator sums exactly
 constexpr int kThreads = 384;
 constexpr int kSumWarps = 8;
-constexpr int kSums = BN / 2;  // tokens of a thread
-constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kIdesc = idesc_f16_f32(2 * BM, BN);
+constexpr uint32_t kTmemCols = 512, kSumCols = 256;
 constexpr int kFewRegs = 40, kManyRegs = 232;  // 40 + 2 x 232 = 3 x 168
 
+constexpr int kStageBytesA = BM * BK * 2;
+constexpr int stage_bytes(int bn) { return kStageBytesA + bn / 2 * BK * 2; }  // multiples of 1024
+
+template <int BN>
 struct __align__(16) Tail {
-  float scales[kSumWarps][kSums];
+  float scales[kSumWarps][BN / 2];
   uint64_t full[STAGES];
   uint64_t empty[STAGES];
   uint64_t sum_full[2];
@@ -46,8 +46,10 @@ struct __align__(16) Tail {
   int abort_flag;
 };
 
-constexpr size_t kSmemBytes = 1024 + kRingBytes + sizeof(Tail);
-static_assert(kSmemBytes <= 227 * 1024, "int8 wide kernel shared memory");
+constexpr size_t smem_bytes(int bn) {
+  return 1024 + STAGES * stage_bytes(bn) + (bn == 256 ? sizeof(Tail<256>) : sizeof(Tail<224>));
+}
+static_assert(smem_bytes(256) <= 227 * 1024, "int8 wide kernel shared memory");
 
 // Tile t: bands of 8 column tiles, row tile by row tile within a band.
 struct Tile {
@@ -64,13 +66,19 @@ __device__ __forceinline__ Tile tile_of(int t, int tiles_n, int tiles_m) {
   return r;
 }
 
-// tmW: the weights (N x K), tmX: the tokens (M x K), boxes of 64 x 128.
+// tmW: the weights (N x K), tmX: the tokens (M x K), boxes of 64 x 128 and 64 x
+// BN / 2.
+template <int BN>
 __global__ void __launch_bounds__(kThreads, 1)
     int8_wide_kernel(const __grid_constant__ Int8Args p, const __grid_constant__ CUtensorMap tmW,
                      const __grid_constant__ CUtensorMap tmX) {
+  using Tail = Tail<BN>;
+  constexpr int kStageBytes = stage_bytes(BN);
+  constexpr int kSums = BN / 2;  // tokens of a thread
+  constexpr uint32_t kIdesc = idesc_f16_f32(2 * BM, BN);
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = align_smem<1024>(smem_raw);
-  Tail* tail = reinterpret_cast<Tail*>(smem + kRingBytes);
+  Tail* tail = reinterpret_cast<Tail*>(smem + STAGES * kStageBytes);
   const uint32_t tail_at = smem_u32(tail);
   const uint32_t abort_flag = tail_at + offsetof(Tail, abort_flag);
   const uint32_t full_at = tail_at + offsetof(Tail, full), empty_at = tail_at + offsetof(Tail, empty);
@@ -166,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < BK / 16; ++kk)
-              tc_mma_f16_pair(tmem_base + ab * BN, da0 + step + kk * 2, db0 + step + kk * 2, kIdesc,
+              tc_mma_f16_pair(tmem_base + ab * kSumCols, da0 + step + kk * 2, db0 + step + kk * 2, kIdesc,
                               in_chunk != 0 || kk != 0 ? 1u : 0u);
             tc_commit_pair_multicast(&tail->empty[s], 0x3);
             if (last) tc_commit_pair_multicast(&tail->sum_full[ab], 0x3);
@@ -216,12 +224,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after_sync();
         // eight at a time, the next ones on their way
         uint32_t r[2][8];
-        tmem_ld_32x32b_x8(from + ab * BN, r[0]);
+        tmem_ld_32x32b_x8(from + ab * kSumCols, r[0]);
 #pragma unroll
         for (int j = 0; j < kSums; j += 8) {
           const int cur = (j >> 3) & 1;
           tmem_wait_ld(r[cur]);
-          if (j + 8 < kSums) tmem_ld_32x32b_x8(from + ab * BN + j + 8, r[cur ^ 1]);
+          if (j + 8 < kSums) tmem_ld_32x32b_x8(from + ab * kSumCols + j + 8, r[cur ^ 1]);
 #pragma unroll
           for (int i = 0; i < 8; i += 2) {
             if (by_unit(j)) {
@@ -305,7 +313,7 @@ int max_pairs() {
   const int known = cache[dev].load(std::memory_order_relaxed);
   if (known != 0) return known;
   int n = 0;
-  if (ops_allow_smem<int8_wide_kernel>(kSmemBytes) == cudaSuccess) {
+  if (ops_allow_smem<int8_wide_kernel<256>>(smem_bytes(256)) == cudaSuccess) {
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -314,10 +322,10 @@ int max_pairs() {
     attr[0].val.clusterDim.z = 1;
     cfg.gridDim = dim3(2);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.dynamicSmemBytes = smem_bytes(256);
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, int8_wide_kernel, &cfg) != cudaSuccess) n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, int8_wide_kernel<256>, &cfg) != cudaSuccess) n = 0;
   }
   cudaGetLastError();
   if (n > 0) cache[dev].store(n, std::memory_order_relaxed);
@@ -326,6 +334,23 @@ int max_pairs() {
 
 int64_t pitch_of(int64_t K) { return (K + 7) / 8 * 8; }
 int64_t copy_bytes(int64_t rows, int64_t K) { return (2 * rows * pitch_of(K) + 255) / 256 * 256; }
+
+// Microseconds of all rounds of tiles of bn tokens: 64 of k in 280 ns for 256 of
+// them, or the time of a tile's end, where that is more.
+double tiles_us(int bn, int64_t M, int64_t N, int64_t K, int pairs) {
+  const int64_t tiles = ((N + 2 * BM - 1) / (2 * BM)) * ((M + bn - 1) / bn);
+  const double us = (bn == 256 ? 0.28 : 0.252) * static_cast<double>((K + BK - 1) / BK) + 0.85;
+  return static_cast<double>((tiles + pairs - 1) / pairs) * (us < 4.0 ? 4.0 : us);
+}
+// Tokens of a tile: 224 where that makes better rounds, and does not compute
+// many more rows than 256 without a token in them (us, 224 / 256: 3000 x 5000 x
+// 1999 52.7 / 58.0, 3000 x 4096 x 4096 71 / 84, 2000 x 8192 x 2048 53 / 60, 4096^3 91 /
+// 96, but 4096 x 4096 x 2048 52.3 / 51.0 and x 1024 33.9 / 30.2).
+int tokens_of(int64_t M, int64_t N, int64_t K, int pairs) {
+  const double few = static_cast<double>((M + 223) / 224 * 224), many = static_cast<double>((M + 255) / 256 * 256);
+  const double more = few > many ? few / many - 1.0 : 0.0;
+  return tiles_us(224, M, N, K, pairs) < tiles_us(256, M, N, K, pairs) * (1.0 - 2.4 * more) ? 224 : 256;
+}
 
 // The widened copies take at most this much of the stream's buffer.
 constexpr int64_t kMostBytes = int64_t{1} << 30;
@@ -338,17 +363,13 @@ bool int8_wide_pays(int64_t M, int64_t N, int64_t K, double us) {
   const int64_t bytes = int8_wide_bytes(M, N, K);
   const int pairs = max_pairs();
   if (bytes > kMostBytes || pairs <= 0) return false;
-  // Rounds of tiles (64 of k in 280 ns, or the time of an end, where that is
-  // more), the last tile's end, the widening (3 bytes a value at 7 TB/s) and its
-  // launch.  Both sides, us here / there: 256 x 4096 x 4096 31 / 17, 512 x 4096 x
-  // 4096 31 / 24, 1024 x 4096 x 1024 14.4 / 13.2, 768 x 4096 x 4096 32 / 36, 2048 x
-  // 4096 x 512 15.9 / 17.6, 4096^3 96 / 138, 8192 x 8192 x 128 56 / 77, 8192^3 605 /
-  // 907.
-  const int64_t tiles = ((N + 255) / 256) * ((M + 255) / 256);
-  const double blocks = 0.28 * static_cast<double>((K + 63) / 64) + 0.85;
-  const double here = static_cast<double>((tiles + pairs - 1) / pairs) * (blocks < 4.0 ? 4.0 : blocks) + 3.5 +
-                      1.5e-6 * static_cast<double>(bytes) / 7.0 + 2.5;
-  return here < us;
+  // The tiles, the last one's end, the widening (3 bytes a value at 7 TB/s) and
+  // its launch.  Both sides, us here / there: 256 x 4096 x 4096 31 / 17, 512 x
+  // 4096 x 4096 31 / 24, 1024 x 4096 x 1024 14.4 / 13.2, 768 x 4096 x 4096 32 / 36,
+  // 2048 x 4096 x 512 15.9 / 17.6, 4096^3 96 / 138, 8192 x 8192 x 128 56 / 77,
+  // 8192^3 605 / 907.
+  return tiles_us(tokens_of(M, N, K, pairs), M, N, K, pairs) + 3.5 +
+             1.5e-6 * static_cast<double>(bytes) / 7.0 + 2.5 < us;
 }
 
 gemm_status_t int8_wide(const Int8Args& args, int64_t K, const int8_t* A, int64_t lda, const int8_t* B,
@@ -372,17 +393,21 @@ gemm_status_t int8_wide(const Int8Args& args, int64_t K, const int8_t* A, int64_
   const cudaError_t e =
       ops_launch<widen_kernel>(dim3(static_cast<unsigned>(want < fit ? want : fit)), 256, 0, 1, s, w);
   if (e != cudaSuccess) return abi_from_cuda(e);
+  const int pairs = max_pairs(), bn = tokens_of(p.M, p.N, K, pairs);
   CUtensorMap tm[2];
   for (int i = 0; i < 2; ++i) {
     const int64_t dims[2] = {K, w.rows[i]}, pitch[1] = {2 * w.ld2};
-    const uint32_t box[2] = {BK, BM};
+    const uint32_t box[2] = {BK, static_cast<uint32_t>(i == 0 ? BM : bn / 2)};
     if (!abi_encode_tiled(&tm[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, w.dst[i], dims, pitch, box))
       return GEMM_ERR_LAUNCH;
   }
-  const int64_t tiles = ((p.N + int64_t{255}) / 256) * ((p.M + int64_t{255}) / 256);
-  const int pairs = max_pairs();
-  return abi_from_cuda(ops_launch<int8_wide_kernel>(dim3(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs))),
-                                                    kThreads, kSmemBytes, 2, s, p, tm[0], tm[1]));
+  const int64_t tiles = ((p.N + int64_t{2 * BM - 1}) / (2 * BM)) * ((p.M + bn - int64_t{1}) / bn);
+  const dim3 grid(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs)));
+  if (bn == 224)
+    return abi_from_cuda(
+        ops_launch<int8_wide_kernel<224>>(grid, kThreads, smem_bytes(224), 2, s, p, tm[0], tm[1]));
+  return abi_from_cuda(
+      ops_launch<int8_wide_kernel<256>>(grid, kThreads, smem_bytes(256), 2, s, p, tm[0], tm[1]));
 }
 
 }  // namespace g12

@@ -61,7 +61,10 @@ def test_which_way_a_product_goes():
         D = torch.empty(M, N, device="cuda")
         return kernels(lambda: g.int8gemm(A, torch.ones(M, device="cuda"), B, torch.ones(N, device="cuda"), D))
 
-    assert {s: "int8_wide_kernel" in names(*s) for s in SHAPES} == dict.fromkeys(SHAPES, True)
+    found = {s: names(*s) for s in SHAPES}
+    assert {s: "int8_wide_kernel" in n for s, n in found.items()} == dict.fromkeys(SHAPES, True)
+    for tokens in (224, 256):   # to a tile, whichever makes the better rounds
+        assert any("int8_wide_kernel<%d>" % tokens in n for n in found.values())
     small = [(16, 4096, 1024), (128, 4096, 1024), (256, 256, 4096), (1, 20000, 512)]
     assert {s: "int8_wide_kernel" in names(*s) for s in small} == dict.fromkeys(small, False)
 
@@ -80,6 +83,19 @@ def test_largest_sums(K, a, b):
     g.int8gemm(A, ones, B, ones[:N], D)
     check_device_error()
     assert torch.equal(D, sums64(A, B).float())   # the conversion, to nearest even, is the only rounding
+
+
+def test_longest_rows():
+    # K = 2^17 - 1, all products 2^14: just below 2^31
+    K, n = 131071, 2000
+    A, B = (torch.full((n, K + 1), -128, dtype=torch.int8, device="cuda")[:, :K] for _ in range(2))
+    A[:, 1] = torch.arange(n, device="cuda") % 256 - 128
+    D = torch.empty(n, n, device="cuda")
+    one = torch.ones(n, device="cuda")
+    assert "int8_wide_kernel" in kernels(lambda: g.int8gemm(A, one, B, one, D))
+    check_device_error()
+    want = 2.0 ** 14 * (K - 1) - 128 * A[:, 1].double()
+    assert torch.equal(D, want[:, None].expand(n, n).float())
 
 
 def test_the_same_bits_in_a_capture_on_streams_and_with_the_smaller_tiles():
