@@ -900,8 +900,8 @@ gemm_status_t gemm_expert_sort(int64_t n, int64_t G, const int32_t *expert, int3
  *     dweight[r][j] = sum over the row of dout[r] * a[slot[r][j]]
  *
  * (0 for a pair without a row).  Either may be NULL; `a` is read for dweight
- * only, and da may take its place (same type and ld).  The residual's gradient
- * is dout itself.
+ * only, and da may take its place (same type and ld; no row may be named twice
+ * then).  The residual's gradient is dout itself.
  */
 gemm_status_t gemm_expert_dispatch(int64_t rows, int64_t top, int64_t n, int64_t dim, int elem_bytes,
                                    const void *x, int64_t ldx, const int32_t *slot, void *a, int64_t lda,
