@@ -775,8 +775,8 @@ gemm_status_t gemm_fp8gemm(int64_t M, int64_t N, int64_t K, float alpha, const v
  *               + bias[j] + beta * D[i][j]
  *
  * The sum is exact (any int8 values, -128 included): K is at most 2^17 - 1
- * (more is GEMM_ERR_UNSUPPORTED), the scales and the rest are fp32.  bias (N
- * fp32 values) may be NULL.  D (ldd) is fp32 or bf16 and is not read when beta
+ * (more is GEMM_ERR_UNSUPPORTED); the rest is fp32, (sum * a_scale) * (alpha *
+ * b_scale) in this order.  bias (N fp32 values) may be NULL.  D (ldd) is fp32 or bf16 and is not read when beta
  * == 0.  K == 0 or alpha == 0: A, B and the scales are not read.  D must not
  * overlap the operands.
  */
