@@ -34,9 +34,9 @@
 // through distributed shared memory.  Many tiles: int8_wide.cu, if the stream's
 // buffer can hold both operands widened.
 //
-// Measured: 16 x 12288 x 4096 13.5 us (96 CTAs take 6.1 TB/s of weights, at the
-// rate of the widening -- 3300 warp instructions in the 1000 cycles of a block;
-// half of the MMAs gain 0.5 us -- between a start and an end of 5.7 us together), 16 x 38912 x 4096 29.2 (HBM: 6.8 TB/s
+// Measured: 16 x 12288 x 4096 13.5 us (96 CTAs take 6.1 TB/s of weights -- more
+// buffers and half of the MMAs change little -- between a start and an end of
+// 5.7 us together), 16 x 38912 x 4096 29.2 (HBM: 6.8 TB/s
 // between them), 64 x 12288 x 4096 17.1, 128 x 4096 x 4096 12.9 (tiles of 64),
 // 128 x 12288 x 4096 23.6.
 #include <cstddef>
