@@ -443,15 +443,14 @@ struct DispatchArgs {
   const int32_t* slot;
 };
 
-// T: what a thread moves at a time.  Each row is read once and written `top`
-// times.
-constexpr int kCopyAhead = 4;
-
-template <typename T>
+// T: what a thread moves at a time, AHEAD of them on their way together.  Each
+// row is read once and written `top` times.
+template <typename T, int AHEAD>
 __global__ void __launch_bounds__(kThreads) dispatch_kernel(const __grid_constant__ DispatchArgs p) {
   grid_dependency_wait();
   grid_launch_dependents();
   if (blockIdx.x >= p.row_ctas) {  // scales: consecutive threads on consecutive rows
+    if (blockIdx.y > 0) return;
     const int64_t total = p.kb * p.rows;
     const int64_t step = (static_cast<int64_t>(gridDim.x) - p.row_ctas) * kThreads;
     for (int64_t i = (blockIdx.x - p.row_ctas) * kThreads + threadIdx.x; i < total; i += step) {
@@ -470,17 +469,18 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(const __grid_constan
        row += p.row_ctas * per_cta) {
     const T* from = reinterpret_cast<const T*>(p.x + row * p.x_pitch);
     const int32_t* slot = p.slot + row * p.top;
-    for (int64_t c = t; c < p.pieces; c += static_cast<int64_t>(p.tpr) * kCopyAhead) {
-      T v[kCopyAhead];
+    const int64_t wide = static_cast<int64_t>(p.tpr) * AHEAD;
+    for (int64_t c = blockIdx.y * wide + t; c < p.pieces; c += gridDim.y * wide) {
+      T v[AHEAD];
 #pragma unroll
-      for (int u = 0; u < kCopyAhead; ++u)
+      for (int u = 0; u < AHEAD; ++u)
         if (c + u * p.tpr < p.pieces) v[u] = __ldcs(from + c + u * p.tpr);
       for (int j = 0; j < p.top; ++j) {
         const int64_t at = slot[j];
         if (at < 0 || at >= p.n) continue;
         T* to = reinterpret_cast<T*>(p.a + at * p.a_pitch);
 #pragma unroll
-        for (int u = 0; u < kCopyAhead; ++u)
+        for (int u = 0; u < AHEAD; ++u)
           if (c + u * p.tpr < p.pieces) to[c + u * p.tpr] = v[u];
       }
     }
@@ -705,8 +705,12 @@ constexpr int64_t kSortMostCtas = 256;
 template <typename T>
 cudaError_t launch_dispatch(DispatchArgs& p, int64_t row_bytes, int num_sms, cudaStream_t s) {
   p.pieces = row_bytes / static_cast<int64_t>(sizeof(T));
+  // Few pieces: one a thread, rows cut into several CTAs (16 x 4096 bf16, eight
+  // choices each 2.1 us, 3.5 with four a thread).
+  const bool few = p.rows * p.pieces <= static_cast<int64_t>(num_sms) * kThreads;
+  const int ahead = few ? 1 : 4;
   p.tpr = 32;
-  while (p.tpr < kThreads && p.pieces > static_cast<int64_t>(p.tpr) * kCopyAhead) p.tpr *= 2;
+  while (p.tpr < kThreads && p.pieces > static_cast<int64_t>(p.tpr) * ahead) p.tpr *= 2;
   const int64_t per_cta = kThreads / p.tpr;
   const int64_t want = (p.rows + per_cta - 1) / per_cta, fit = static_cast<int64_t>(num_sms) * 64;
   p.row_ctas = want < fit ? want : fit;
@@ -715,8 +719,11 @@ cudaError_t launch_dispatch(DispatchArgs& p, int64_t row_bytes, int num_sms, cud
     scale_ctas = (p.kb * p.rows + kThreads - 1) / kThreads;
     if (scale_ctas > fit) scale_ctas = fit;
   }
-  return ops_launch<dispatch_kernel<T>>(dim3(static_cast<unsigned>(p.row_ctas + scale_ctas)), kThreads, 0,
-                                        1, s, p);
+  const unsigned ctas = static_cast<unsigned>(p.row_ctas + scale_ctas);
+  if (few)
+    return ops_launch<dispatch_kernel<T, 1>>(dim3(ctas, static_cast<unsigned>((p.pieces + p.tpr - 1) / p.tpr)),
+                                             kThreads, 0, 1, s, p);
+  return ops_launch<dispatch_kernel<T, 4>>(dim3(ctas), kThreads, 0, 1, s, p);
 }
 
 template <bool VEC, int TA>
