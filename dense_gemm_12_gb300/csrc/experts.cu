@@ -581,7 +581,10 @@ __global__ void __launch_bounds__(kThreads) combine_grad_kernel(const __grid_con
   const int chunks = VEC ? p.dim / 8 : (p.dim + kFp8Block - 1) / kFp8Block * 16;
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * per_cta + threadIdx.x / p.tpr; row < p.rows;
        row += static_cast<int64_t>(gridDim.x) * per_cta) {
-    for (int j0 = 0; j0 < p.top; j0 += CHOICES) {
+    // (one at a time: those of a row may be in CTAs of their own)
+    const int first = CHOICES == 1 ? static_cast<int>(blockIdx.y) : 0;
+    const int step = CHOICES == 1 ? static_cast<int>(gridDim.y) : CHOICES;
+    for (int j0 = first; j0 < p.top; j0 += step) {
       int64_t at[CHOICES];
       float w[CHOICES], dot[CHOICES];
 #pragma unroll
@@ -749,12 +752,21 @@ cudaError_t launch_combine(CombineArgs& p, cudaStream_t s) {
 template <bool VEC, int TD, int TA>
 cudaError_t launch_combine_grad(CombineGradArgs& p, int num_sms, cudaStream_t s) {
   const int64_t chunks = VEC ? p.dim / 8 : (p.dim + kFp8Block - 1) / kFp8Block * 16;
-  p.tpr = chunks <= 256 ? 32 : kThreads;
+  // A warp a row up to 1024 elements, and to 2048 if there are enough rows (a CTA
+  // and a warp a row: 1024 x 2048 bf16, eight choices 10.8 and 18.8 us, 2048 x 1024,
+  // four 8.5 and 5.5).
+  const bool warp = chunks <= 128 || (chunks <= 256 && p.rows > static_cast<int64_t>(num_sms) * 2 * kWarps);
+  p.tpr = warp ? 32 : kThreads;
   const int64_t per_cta = kThreads / p.tpr;
   const int64_t want = (p.rows + per_cta - 1) / per_cta, fit = static_cast<int64_t>(num_sms) * 64;
   const dim3 grid(static_cast<unsigned>(want < fit ? want : fit));
   if constexpr (VEC) {
-    if (p.top == 1) return ops_launch<combine_grad_kernel<VEC, TD, TA, 1>>(grid, kThreads, 0, 1, s, p);
+    // Few rows: every choice for itself (16 x 4096 bf16, eight choices 2.5 us, 4.8
+    // four at a time).
+    const bool few = p.top > 4 && p.rows * p.top <= static_cast<int64_t>(num_sms) * 4 * per_cta;
+    if (few || p.top == 1)
+      return ops_launch<combine_grad_kernel<VEC, TD, TA, 1>>(
+          dim3(grid.x, static_cast<unsigned>(few ? p.top : 1)), kThreads, 0, 1, s, p);
     if (p.top == 2) return ops_launch<combine_grad_kernel<VEC, TD, TA, 2>>(grid, kThreads, 0, 1, s, p);
   }
   return ops_launch<combine_grad_kernel<VEC, TD, TA, 4>>(grid, kThreads, 0, 1, s, p);

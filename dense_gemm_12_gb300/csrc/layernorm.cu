@@ -749,8 +749,9 @@ __global__ void __launch_bounds__(256) layernorm_dweight_kernel(const __grid_con
 // stages of each group's ring of rows of `bytes`, next to `weights` bytes of
 // weights, if there are enough rows.  sm_threads: what the instance's registers
 // let an SM hold.  Groups need a barrier each, so short rows take two CTAs.
+// fewer: fewer groups than that where there are too few rows for them.
 int plan_groups(RowPlan& p, int64_t rows, int64_t bytes, int64_t weights, int num_sms, int sm_threads,
-                RingArgs& ring) {
+                bool fewer, RingArgs& ring) {
   if (p.per_cta != 1 || p.chunks_per_thread == 0 || p.tpr == 32) return 0;
   const int per_sm = 2 * kMaxRings * p.tpr <= sm_threads ? 2 : 1;
   int groups = sm_threads / per_sm / p.tpr;
@@ -758,7 +759,10 @@ int plan_groups(RowPlan& p, int64_t rows, int64_t bytes, int64_t weights, int nu
   for (; groups >= 1; --groups) {
     const int64_t stages = (kSmBytes / per_sm - kLnCtaBytes - weights) / (groups * bytes);
     if (stages < 2) continue;
-    if (rows < 2 * static_cast<int64_t>(per_sm) * num_sms * groups) return 0;
+    if (rows < 2 * static_cast<int64_t>(per_sm) * num_sms * groups) {
+      if (fewer) continue;
+      return 0;
+    }
     ring.stages = static_cast<int>(stages < kMaxStages ? stages : kMaxStages);
     p.per_cta = groups;
     return per_sm;
@@ -882,7 +886,7 @@ gemm_status_t gemm_layernorm(int64_t rows, int64_t dim, const gemm_layernorm_t* 
     const int64_t bytes = dim * (type_bytes(p.x_type) +
                                  (p.residual == nullptr ? 0 : type_bytes(p.residual_type)));
     RowPlan pr = plan_rows(rows, chunks, sms, 2, 2);
-    const int per_sm = plan_groups(pr, rows, bytes, 8 * dim, sms, 1024, a.ring);
+    const int per_sm = plan_groups(pr, rows, bytes, 8 * dim, sms, 1024, false, a.ring);
     if (per_sm > 0) {
       grid = per_sm * sms;
       pl = pr;
@@ -930,19 +934,22 @@ gemm_status_t gemm_layernorm_backward(int64_t rows, int64_t dim, const gemm_laye
   a.dim = static_cast<int>(dim);
   a.p = p;
   const int64_t chunks = vec ? dim / 8 : (dim + kFp8Block - 1) / kFp8Block * 16;
-  // Two chunks a thread in vectors (one and twice the threads: 8192 x 4096 66 us
-  // against 61, 16384 x 1024 41 against 36).
+  // From rings, and where a row takes one warp, two chunks a thread (one and twice
+  // the threads: 8192 x 4096 66 us against 61, 16384 x 1024 41 against 36, 3000 x 512
+  // 16 against 9), else one.  Rings even with fewer groups (1000 x 1024 10 us, 18
+  // without, 2000 x 1024 11 and 22; the forward pass is faster without).
   RowPlan pl = plan_rows(rows, chunks, sms, vec ? 2 : 1, 2);
-  a.tpr = pl.tpr;
   a.ring.err = err;
-  int grid = row_grid(rows, pl, sms, 512);
+  int per_sm = 0;
   if (vec && pl.chunks_per_thread == 2) {
     const int64_t bytes =
         dim * (type_bytes(p.dy_type) + type_bytes(p.h_type) +
                (p.residual_grad == nullptr ? 0 : type_bytes(p.residual_grad_type)));
-    const int per_sm = plan_groups(pl, rows, bytes, 4 * dim, sms, kMaxThreads, a.ring);
-    if (per_sm > 0) grid = per_sm * sms;
+    per_sm = plan_groups(pl, rows, bytes, 4 * dim, sms, kMaxThreads, true, a.ring);
   }
+  if (per_sm == 0 && pl.tpr > 32) pl = plan_rows(rows, chunks, sms, 1, 2);
+  a.tpr = pl.tpr;
+  const int grid = per_sm > 0 ? per_sm * sms : row_grid(rows, pl, sms, 512);
   const bool by_column = pl.chunks_per_thread == 0;
   int parts = grid;
   if (by_column) {  // up to 64, of 256 MB together
