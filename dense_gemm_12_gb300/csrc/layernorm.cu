@@ -16,7 +16,7 @@
 // ring of its own, around one copy of the weight and the bias.  Read anew for
 // each row those are as many bytes as the row itself, and with shared memory
 // full of rows they do not stay in L1 (8192 rows of 8192 in bf16: 104 us with a
-// group to a CTA and weights from L2, 87 here, 6.2 TB/s; into int8 111; the
+// group to a CTA and weights from L2, 87 here, 6.2 TB/s; into int8 107; the
 // gradient of 8192 rows of 4096 54, 5.0 TB/s).
 //
 // The squares are summed about the mean, never as mean(h^2) - m^2, which loses

@@ -134,16 +134,30 @@ __device__ __forceinline__ void write_fp8(void* q_rows, int64_t ldq, float* scal
 
 // A chunk of a row in int8, given the factor of the row.  finite: neither
 // infinities nor NaN in the row.  Its products then lie within +-127.001, and
-// one fused operation with 1.5 * 2^23 on top rounds them to whole numbers in the
-// last bits, two's complement (the conversion instruction takes 16 a cycle).
+// adding 1.5 * 2^23 rounds them to whole numbers in the last bits, two's
+// complement (the conversion instruction takes 16 a cycle).  The product is
+// rounded before that, as round_s8's is: a value's byte is the same whatever else
+// is in its row, and whichever kernel makes it.  Both in one fused operation
+// would decide ties by the factor's own rounding, and half of a row's largest
+// value, 63.5 steps, is common in bf16; so the product is __fmul_rn's, which is
+// never joined to an addition (see mul2).
 template <bool VEC>
 __device__ __forceinline__ void write_s8(void* q_rows, int64_t ldq, int64_t row, int c, int dim, float f,
                                          bool finite, const float (&y)[8]) {
   int8_t* q = static_cast<int8_t*>(q_rows) + row * ldq;
   uint32_t w[8];
+  if (finite) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    w[i] = finite ? __float_as_uint(fmaf(y[i], f, 12582912.0f)) : static_cast<uint32_t>(round_s8(y[i] * f));
+    for (int i = 0; i < 8; i += 2) {
+      const uint64_t p = f32x2(__fmul_rn(y[i], f), __fmul_rn(y[i + 1], f));
+      const float2 r = f32x2_parts(add2(p, f32x2(12582912.0f, 12582912.0f)));
+      w[i] = __float_as_uint(r.x);
+      w[i + 1] = __float_as_uint(r.y);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = static_cast<uint32_t>(round_s8(y[i] * f));
+  }
   if (VEC) {
     *reinterpret_cast<uint2*>(q + c) = make_uint2(low_bytes(w[0], w[1], w[2], w[3]),
                                                   low_bytes(w[4], w[5], w[6], w[7]));

@@ -602,7 +602,10 @@ __device__ __forceinline__ float2 f32x2_parts(uint64_t v) {
   return f;
 }
 
-// Two fp32 operations in one instruction.
+// Two fp32 operations in one instruction.  A product and the addition behind it
+// may come out as one fused operation (they do, .rn or not: an int8 rounding made
+// of mul2 and add2 gave fma2's bytes): where the product itself has to be rounded,
+// take __fmul_rn.
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));

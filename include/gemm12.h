@@ -764,8 +764,10 @@ gemm_status_t gemm_fp8gemm(int64_t M, int64_t N, int64_t K, float alpha, const v
  *     scale = max(a / 127, 2^-126)      q = x / scale
  *
  * rounded half to even, within +-127; infinities become +-127 and NaN 0.  The
- * quotient is formed as x * (127 / a).  cols is at most 2^30 without
- * `transpose`; with it the columns' maxima are in the stream's scratch.
+ * quotient is formed as x * (127 / a), the factor and the product each rounded
+ * to fp32, so that a value's byte depends on itself and a alone.  cols is at
+ * most 2^30 without `transpose`; with it the columns' maxima are in the stream's
+ * scratch.
  *
  * gemm_int8gemm -- for int8 A (M x K) and B (N x K), both contiguous along k,
  * with one scale for each of A's rows (M fp32 values: tokens) and one for each
