@@ -1085,7 +1085,8 @@ def expert_sort(expert, slot, offsets, source=None, stream=None):
 def expert_dispatch(x, slot, a, x_scales=None, a_scales=None, stream=None):
     """a[slot[r, j]] <- x[r] for each token r and choice j: x (rows, dim), slot (rows, top) int32 from
     expert_sort, a (n, dim) of x's dtype (float32, bfloat16, float8_e4m3fn or int8).  With scales: x's
-    fp8 scales (ceil(dim / 128), rows) to a's (ceil(dim / 128), n).  Other rows of a stay."""
+    fp8 scales (ceil(dim / 128), rows) to a's (ceil(dim / 128), n), or int8 rows' (rows,) to (n,).
+    Other rows of a stay."""
     f32, i32 = _torch_once()[2], _torch_once()[4]
     shape = _pairs(slot, "slot")
     if x.dim() != 2 or a.dim() != 2 or x.shape[0] != shape[0]:
@@ -1098,12 +1099,16 @@ def expert_dispatch(x, slot, a, x_scales=None, a_scales=None, stream=None):
     n, dev = a.shape[0], x.get_device()
     handle = _stream_of(dev, stream)
     kb = -(-dim // 128)
-    none = (None, 0)
+    if x_scales is None:
+        scales = (None, 0, None, 0)
+    elif x.dtype == _int8() and x_scales.dim() == 1:
+        scales = (_vector(x_scales, rows, f32, dev, "x_scales"), 0, _vector(a_scales, n, f32, dev, "a_scales"), 0)
+    else:
+        scales = (*_array(x_scales, (kb, rows), f32, dev, "x_scales"),
+                  *_array(a_scales, (kb, n), f32, dev, "a_scales"))
     st = load_library().gemm_expert_dispatch(
         rows, shape[1], n, dim, _ROW_BYTES[x.dtype], *_array(x, (rows, dim), x.dtype, dev, "x"),
-        _dense(slot, shape, i32, dev, "slot"), *_array(a, (n, dim), x.dtype, dev, "a"),
-        *(none if x_scales is None else _array(x_scales, (kb, rows), f32, dev, "x_scales")),
-        *(none if x_scales is None else _array(a_scales, (kb, n), f32, dev, "a_scales")), handle)
+        _dense(slot, shape, i32, dev, "slot"), *_array(a, (n, dim), x.dtype, dev, "a"), *scales, handle)
     if st != 0:
         raise GemmError(st, "gemm_expert_dispatch")
     return a

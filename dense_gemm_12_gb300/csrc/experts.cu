@@ -873,8 +873,11 @@ gemm_status_t gemm_expert_dispatch(int64_t rows, int64_t top, int64_t n, int64_t
       ldx < dim || lda < dim || ldx > kOpsMaxDim || lda > kOpsMaxDim || ops_misaligned(x, elem_bytes) ||
       ops_misaligned(a, elem_bytes))
     return GEMM_ERR_INVALID_VALUE;
-  if (x_scales != nullptr && (ld_xs < rows || ld_as < n || ld_xs > kOpsMaxDim || ld_as > kOpsMaxDim ||
-                              ops_misaligned(x_scales, 4) || ops_misaligned(a_scales, 4)))
+  const bool one = x_scales != nullptr && ld_xs == 0 && ld_as == 0;  // scale for each row
+  if (x_scales != nullptr && (ops_misaligned(x_scales, 4) || ops_misaligned(a_scales, 4)))
+    return GEMM_ERR_INVALID_VALUE;
+  if (x_scales != nullptr && !one &&
+      (ld_xs < rows || ld_as < n || ld_xs > kOpsMaxDim || ld_as > kOpsMaxDim))
     return GEMM_ERR_INVALID_VALUE;
   if (top > kMaxTop) return GEMM_ERR_UNSUPPORTED;
   int sms = 0;
@@ -889,7 +892,7 @@ gemm_status_t gemm_expert_dispatch(int64_t rows, int64_t top, int64_t n, int64_t
   p.x_pitch = ldx * elem_bytes;
   p.a = static_cast<uint8_t*>(a);
   p.a_pitch = lda * elem_bytes;
-  p.kb = (dim + kFp8Block - 1) / kFp8Block;
+  p.kb = one ? 1 : (dim + kFp8Block - 1) / kFp8Block;
   p.xs = x_scales;
   p.ld_xs = ld_xs;
   p.as = a_scales;

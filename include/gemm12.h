@@ -884,8 +884,9 @@ gemm_status_t gemm_expert_sort(int64_t n, int64_t G, const int32_t *expert, int3
  * gemm_expert_dispatch -- a[slot[r][j]] = x[r]: each token's row (of `dim`
  * elements of elem_bytes = 1, 2 or 4) to its places among the n rows of `a`.
  * x_scales and a_scales, both or neither: the rows' fp8 scales, ceil(dim / 128)
- * x rows and x n, moved likewise.  Here and below a slot outside 0 .. n - 1 is
- * no row, and rows of `a` that no slot names are not written.  A slot that
+ * x rows and x n, moved likewise; with ld_xs == ld_as == 0 one scale for each row
+ * (rows and n values), as int8 rows have.  Here and below a slot outside 0 .. n - 1
+ * is no row, and rows of `a` that no slot names are not written.  A slot that
  * names a row twice leaves one of the two there.
  *
  * gemm_expert_combine -- back again:
