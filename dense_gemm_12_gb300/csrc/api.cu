@@ -233,6 +233,16 @@ gemm_status_t release(Scratch& sc, cudaStream_t stream) {
   return result;
 }
 
+// The buffers of `stream`, none at first; nullptr where the host has no memory
+// for the entry (no exception leaves an entry point).
+Scratch* buffers_of(DeviceState& st, cudaStream_t stream) {
+  try {
+    return &st.scratch[static_cast<void*>(stream)];
+  } catch (const std::bad_alloc&) {
+    return nullptr;
+  }
+}
+
 // The scratch area of `stream` on this device, grown to at least the given
 // sizes (new counters start at zero).  Growth is stream-ordered on `stream`
 // and never blocks the host.  Inside a stream capture nothing is allocated:
@@ -240,7 +250,9 @@ gemm_status_t release(Scratch& sc, cudaStream_t stream) {
 // the launch without one.  Caller holds st.ws_mutex.
 gemm_status_t ensure_scratch(DeviceState& st, cudaStream_t stream, int64_t floats,
                              int64_t counters, Scratch** out) {
-  Scratch& sc = st.scratch[static_cast<void*>(stream)];
+  Scratch* const found = buffers_of(st, stream);
+  if (found == nullptr) return GEMM_ERR_NO_MEMORY;
+  Scratch& sc = *found;
   *out = &sc;
   const bool in_graph = capturing(stream);
   const int64_t need[2] = {floats * static_cast<int64_t>(sizeof(float)),
@@ -266,7 +278,9 @@ gemm_status_t ensure_scratch(DeviceState& st, cudaStream_t stream, int64_t float
 // `bytes` (stream-ordered, as ensure_scratch; nothing is allocated inside a
 // stream capture).  Caller holds st.ws_mutex.
 gemm_status_t ensure_stage(DeviceState& st, cudaStream_t stream, int64_t bytes, uint8_t** out) {
-  Scratch& sc = st.scratch[static_cast<void*>(stream)];
+  Scratch* const found = buffers_of(st, stream);
+  if (found == nullptr) return GEMM_ERR_NO_MEMORY;
+  Scratch& sc = *found;
   const bool in_graph = capturing(stream);
   if (sc.buf[kStage].bytes < bytes) {
     if (in_graph) return GEMM_ERR_NO_MEMORY;
