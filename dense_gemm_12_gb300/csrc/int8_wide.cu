@@ -7,8 +7,8 @@
 // MMAs' reads, 1536 cycles of it per 1024 cycles of MMAs, and the accumulator
 // fills TMEM together with the widened weights, so the MMAs stand still while it
 // is read (8192^3 904 us, of which 590 at the rate of the MMAs).  Measured here:
-// 8192^3 605 us, 38 of them the widening (1.94 PFLOP/s after it), 4096^3 91 (four
-// full rounds), 3000 x 5000 x 1999 53 (3.7 of four rounds).
+// 8192^3 605 to 620 us, 38 of them the widening (1.9 PFLOP/s after it), 4096^3 91
+// (four full rounds), 3000 x 5000 x 1999 53 (3.7 of four rounds).
 //   * CTA pairs take 256 weights x 256 or 224 tokens (cta_group::2, M = 256): each
 //     CTA holds half of both, 30 or 32 KB a k-block of 64, in a ring of six stages
 //   * warp 0 is the TMA producer, warp 1 of the even CTA the MMA issuer, into two

@@ -16,8 +16,11 @@
 // ring of its own, around one copy of the weight and the bias.  Read anew for
 // each row those are as many bytes as the row itself, and with shared memory
 // full of rows they do not stay in L1 (8192 rows of 8192 in bf16: 104 us with a
-// group to a CTA and weights from L2, 87 here, 6.2 TB/s; into int8 107; the
-// gradient of 8192 rows of 4096 54, 5.0 TB/s).
+// group to a CTA and weights from L2, 87 here, 6.2 TB/s; into fp8 106, int8 107; the
+// gradient of 8192 rows of 4096 54, 5.0 TB/s).  Rows that 16-byte pieces do not fit
+// come element by element, one to a CTA's turn: 8000 x 1999 46 us (2.8 TB/s), the
+// gradient 65.  Rows too long for the registers are read three times, by the
+// gradient too: 2048 x 20000 156 us, the gradient of 2048 x 16384 212.
 //
 // The squares are summed about the mean, never as mean(h^2) - m^2, which loses
 // everything when the mean is large.  The mean itself is only known to fp32's
@@ -924,8 +927,11 @@ gemm_status_t gemm_layernorm(int64_t rows, int64_t dim, const gemm_layernorm_t* 
   a.dim = static_cast<int>(dim);
   a.p = p;
   const int64_t chunks = vec ? dim / 8 : (dim + kFp8Block - 1) / kFp8Block * 16;
-  // Four chunks a thread, but one where that leaves 33 to 64 threads a row (2000 x
-  // 2048 9.1 us against 12.5, 2000 x 1999 13.2 against 20.9; 2000 x 1024 7.2 against 4.5).
+  // Four chunks a thread, but one where four leave 33 to 64 threads a row, 1025 to
+  // 2048 elements (us, one / four: 400 x 1032 2.9 / 3.9, 1000 x 1280 5.0 / 6.7, 1000 x
+  // 2048 5.8 / 7.5, 2400 x 1536 11.3 / 12.1, 2400 x 2048 10.0 / 13.0, ragged 1000 x 1100
+  // 6.3 / 10.3, 8000 x 1999 46 / 66; 150 x 1032 to 2048 alike; shorter rows fit a warp:
+  // 2000 x 1024 7.2 / 4.5).
   RowPlan pl = plan_rows(rows, chunks, sms, chunks > 128 && chunks <= 256 ? 1 : 4, 4);
   a.tpr = pl.tpr;
   a.ring.err = err;
